@@ -456,6 +456,126 @@ int spc_mla_decode_attn(const void* q, const void* Wuk, const void* Wuv, const s
                         float scale, float* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged 4-bit KV cache: from request lengths to the decode step's attention.
+ * The pages take the caches as given; these calls place requests in a block
+ * pool, write a prompt's rows into it in 4 bits, attend over the prompt, and
+ * attend over the 4-bit cache for one new token per request, over the whole
+ * context or over the positions the retrieval head selected.
+ *
+ * Record (SPC_KV4_RECORD = 144 bytes): one position of one KV head,
+ *   bytes   0 ..  63  K codes, two e2m1 values a byte (element 2i in the low
+ *                     nibble of byte i, 2i + 1 in the high one)
+ *   bytes  64 .. 127  V codes
+ *   bytes 128 .. 135  K scales, e4m3, one per 16 consecutive values
+ *   bytes 136 .. 143  V scales
+ * Value = code * scale of its group; every such product is exact in bf16.
+ * Cache: uint8 [num_blocks][n_kv][block_size][144], 16-byte aligned,
+ * block_size in {16, 32, 64, 128}, num_blocks * block_size < 2^31. Slot s is
+ * position s % block_size of block s / block_size. A block table row
+ * int32 [max_blocks] names the block of each block_size positions of one
+ * request; max_blocks * block_size <= SPC_MAX_CAP.
+ * ---------------------------------------------------------------------- */
+#define SPC_KV4_RECORD 144
+#define SPC_KV4_GROUP 16
+
+/* Block tables and slot maps from request lengths. Request b holds L0 =
+ * len[b] positions in ceil(L0 / block_size) blocks and shall hold L1 =
+ * len_next[b]. Blocks a shrinking request no longer needs (L1 < L0; 0 ends
+ * it) go onto the free stack, in request and block order; then the blocks a
+ * growing request needs are taken from the top of the stack, in request and
+ * block order, and written into its table row.
+ *   cu_new[b]   = number of new positions (max(0, L1 - L0)) of requests < b
+ *   slot_map[cu_new[b] + i] = slot of position L0 + i of request b
+ *   slot_map[t] = -1 for cu_new[B] <= t < n_slots
+ * Table entries that are not needed (any more) are left as they were.
+ * len, len_next int32 [B]; block_table int32 [B][max_blocks]; free_list int32
+ * [num_blocks], its first n_free[0] entries the stack; n_free_next int32 [1],
+ * the stack's new height (not the same address as n_free); cu_new int32
+ * [B + 1], the cu_seqlens of the new tokens; slot_map int32 [n_slots];
+ * status int32 [1], zeroed by the caller. If a length is outside [0,
+ * max_blocks * block_size], the stack has too few blocks (or would pass
+ * num_blocks), or the new positions pass n_slots, the status word becomes
+ * SPC_ERR_OVERFLOW, tables and stack stay as they were, n_free_next = n_free,
+ * cu_new = 0 and slot_map = -1, so that a store of these slots writes nothing.
+ * Inputs other than the table and the stack are not written: calling it again
+ * with the same lengths and n_free gives the same result.
+ * Limits: 1 <= B <= 64, 1 <= n_slots, 4-byte aligned addresses. */
+int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_table, int32_t* free_list,
+                  const int32_t* n_free, int32_t* n_free_next, int32_t* cu_new, int32_t* slot_map,
+                  int32_t* status, int B, int max_blocks, int block_size, int num_blocks, int n_slots,
+                  void* stream);
+
+/* Rows into the cache. For t < T with 0 <= slot_map[t] < num_blocks *
+ * block_size (others are skipped), every KV head and K and V alike, each 16
+ * consecutive values x become
+ *   s = e4m3(min(max|x| / 6, 448)),  code = e2m1(x / s)  (0 where s = 0),
+ * both rounded to nearest, ties to even, of the exact quotients. Values beyond
+ * 6 * 448 saturate (infinities too); a NaN makes its group's scale NaN.
+ * k, v      bf16, row t at k + t * k_stride elements: [n_kv][d], 16-byte
+ *           aligned; strides are multiples of 8 elements, at least n_kv * d.
+ * slot_map  int32 [T]; a slot that occurs twice ends up with bytes of either row.
+ * Limits: d = 128, 0 <= T <= 2^24, 1 <= n_kv <= 1024. */
+int spc_kv4_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                  void* cache, int T, int n_kv, int d, int num_blocks, int block_size, void* stream);
+
+/* Rows out of the cache: k[t], v[t] = the values of slot slot_map[t], exact in
+ * bf16; rows whose slot is outside the cache are left as they were. Arguments
+ * and limits as spc_kv4_store. */
+int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, int64_t k_stride,
+                 int64_t v_stride, int T, int n_kv, int d, int num_blocks, int block_size, void* stream);
+
+/* Decode attention over the paged 4-bit cache, one query token per request.
+ * For request b, query head h (g = h / G):
+ *   R = { p : 0 <= p < len[b] }                       (selected = NULL)
+ *     = { selected[b,g,i] : 0 <= . < len[b] }         (otherwise; a position
+ *                                  that occurs twice counts twice)
+ *   out[b,h,:] = sum_{p in R} softmax_p(scale * q[b,h] . K[g,p]) V[g,p]
+ * Positions whose table entry is outside [0, num_blocks) are left out; zeros
+ * where nothing is left.
+ * q          bf16 [B][n_q][d], 16-byte aligned.
+ * block_table int32 [B][max_blocks]; len int32 [B] (at most max_blocks *
+ *            block_size positions count).
+ * selected   int32 [B][n_kv][budget], or NULL with budget 0.
+ * out        bf16 [B][n_q][d], 16-byte aligned.
+ * workspace  spc_kv4_decode_attn_workspace_size() bytes, 256-byte aligned,
+ *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
+ *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
+ *            that may overlap must use distinct workspaces.
+ * Limits: d = 128, G in {1,2,4,8,16,32,64}, 1 <= B <= 64, n_kv <= 1024,
+ *         budget <= 4096, scale > 0. */
+size_t spc_kv4_decode_attn_workspace_size(int B, int n_q, int n_kv, int d, int max_blocks, int block_size,
+                                          int budget);
+
+int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                        const int32_t* selected, int B, int n_q, int n_kv, int d, int num_blocks,
+                        int block_size, int max_blocks, int budget, float scale, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Causal attention over whole prompts, packed one behind the other. Sequence
+ * b is rows [cu_seqlens[b], cu_seqlens[b + 1]); for its row i, query head h
+ * (g = h / G):
+ *   out[i,h,:] = sum_{j <= i, j in the sequence} softmax_j(scale * q[i,h] . k[j,g]) v[j,g]
+ * Rows outside every sequence are left as they were. What a row does not see
+ * (later rows, other sequences) does not reach it, NaN and infinities included.
+ * q, k, v    bf16, row t at q + t * q_stride elements: [n_q][d] (k, v: [n_kv][d]),
+ *            16-byte aligned; strides are multiples of 8 elements, at least the
+ *            row's size (the three may lie in one fused projection's output).
+ * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are an
+ *            empty sequence.
+ * out        bf16 [T][n_q][d], 16-byte aligned; must not overlap q, k or v.
+ * workspace  spc_prompt_attn_workspace_size() bytes, 256-byte aligned,
+ *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
+ *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
+ *            that may overlap must use distinct workspaces.
+ * Limits: d = 128, G in {1,2,4,8,16,32,64}, n_q <= 1024, 1 <= B <= 64,
+ *         0 <= T <= 2^24, at most SPC_MAX_CAP rows a sequence, scale > 0. */
+size_t spc_prompt_attn_workspace_size(int T, int B, int n_q, int n_kv, int d);
+
+int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int T, int B,
+                    int n_q, int n_kv, int d, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                    float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Helpers (no counterpart on the pages).
  * ---------------------------------------------------------------------- */
 

@@ -58,6 +58,14 @@ SIGNATURES = {
     "spc_mla_score_select": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
                                   ctypes.c_size_t, _P, _I]),
     "spc_mla_gather": (_I, [_P, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "spc_block_map": (_I, [_P] * 9 + [_I] * 5 + [_P]),
+    "spc_kv4_store": (_I, [_P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "spc_kv4_load": (_I, [_P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, _I, _I, _I, _I, _I, _P]),
+    "spc_kv4_decode_attn_workspace_size": (ctypes.c_size_t, [_I] * 7),
+    "spc_kv4_decode_attn": (_I, [_P] * 5 + [_I] * 8 + [ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "spc_prompt_attn_workspace_size": (ctypes.c_size_t, [_I] * 5),
+    "spc_prompt_attn": (_I, [_P] * 4 + [_I] * 5 + [ctypes.c_int64] * 3 + [ctypes.c_float, _P, _P, ctypes.c_size_t,
+                                                                         _P]),
     "spc_mla_decode_attn_workspace_size": (ctypes.c_size_t, [_I] * 3),
     "spc_mla_decode_attn": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t,
                                  _P]),
@@ -273,6 +281,130 @@ def spc_mla_decode_attn(q, Wuk, Wuv, views, selected, slot_pos, n_layers, B, bud
     _check("spc_mla_decode_attn", lib().spc_mla_decode_attn(
         _ptr(q), _ptr(Wuk), _ptr(Wuv), _ptr(views), _ptr(selected), _ptr(slot_pos), n_layers, B, budget,
         float(scale), _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged 4-bit cache
+SPC_KV4_RECORD, SPC_KV4_GROUP = 144, 16
+
+_BF16 = ("torch.bfloat16", "torch.int16", "torch.uint16")
+_I32 = ("torch.int32",)
+_BYTES = ("torch.uint8", "torch.int8")
+
+
+def _dev(name, t, dtypes, numel):
+    """Pointer of a contiguous device tensor of at least `numel` elements (an
+    int is taken as a device address, None stays None)."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(dtypes)}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    _on_current_device(name, t)
+    return t.data_ptr()
+
+
+def _on_current_device(name, t):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: tensor is on {t.device}, expected a CUDA device")
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(name, t, T, n, d, stride):
+    """(pointer, row stride in elements) of bf16 rows [T][n][d] whose rows may
+    lie `stride` elements apart."""
+    if t is None or isinstance(t, int):
+        return t, n * d if stride is None else int(stride)
+    if str(t.dtype) not in _BF16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected bf16 values or bit patterns")
+    if t.dim() != 3 or t.shape[0] < T or t.shape[1] != n or t.shape[2] != d:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}][{n}][{d}]")
+    s0, s1, s2 = t.stride()
+    # a dimension of one element may carry any stride
+    if (s2 != 1 and d > 1) or (s1 != d and n > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if t.shape[0] <= 1:
+        s0 = max(s0, n * d) // 8 * 8
+    if stride is not None and stride != s0:
+        raise ValueError(f"{name}: stride {stride} given for a tensor of row stride {s0}")
+    _on_current_device(name, t)
+    return t.data_ptr(), s0
+
+
+def spc_block_map(len, len_next, block_table, free_list, n_free, n_free_next, cu_new, slot_map, status, B, max_blocks,
+                  block_size, num_blocks, n_slots, stream=None) -> None:
+    """Block tables, free stack and slot map of the requests' next lengths."""
+    _check("spc_block_map", lib().spc_block_map(
+        _dev("len", len, _I32, B), _dev("len_next", len_next, _I32, B),
+        _dev("block_table", block_table, _I32, B * max_blocks), _dev("free_list", free_list, _I32, num_blocks),
+        _dev("n_free", n_free, _I32, 1), _dev("n_free_next", n_free_next, _I32, 1),
+        _dev("cu_new", cu_new, _I32, B + 1), _dev("slot_map", slot_map, _I32, n_slots),
+        _dev("status", status, _I32, 1), B, max_blocks, block_size, num_blocks, n_slots, _stream(stream)))
+
+
+def spc_kv4_store(k, v, slot_map, cache, T, n_kv, d, num_blocks, block_size, k_stride=None, v_stride=None,
+                  stream=None) -> None:
+    """Rows of K and V into the slots of the 4-bit cache. The row strides are
+    the tensors' own; they are given only with plain addresses."""
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    _check("spc_kv4_store", lib().spc_kv4_store(
+        k, v, k_stride, v_stride, _dev("slot_map", slot_map, _I32, T),
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD), T, n_kv, d, num_blocks,
+        block_size, _stream(stream)))
+
+
+def spc_kv4_load(cache, slot_map, k, v, T, n_kv, d, num_blocks, block_size, k_stride=None, v_stride=None,
+                 stream=None) -> None:
+    """Rows of the 4-bit cache's slots as bf16 (exact)."""
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    _check("spc_kv4_load", lib().spc_kv4_load(
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD),
+        _dev("slot_map", slot_map, _I32, T), k, v, k_stride, v_stride, T, n_kv, d, num_blocks, block_size,
+        _stream(stream)))
+
+
+def spc_kv4_decode_attn_workspace_size(B, n_q, n_kv, d, max_blocks, block_size, budget) -> int:
+    return int(lib().spc_kv4_decode_attn_workspace_size(B, n_q, n_kv, d, max_blocks, block_size, budget))
+
+
+def spc_kv4_decode_attn(q, cache, block_table, len, selected, B, n_q, n_kv, d, num_blocks, block_size, max_blocks,
+                        budget, scale, out, workspace, workspace_bytes=None, stream=None) -> None:
+    """Decode attention over the paged 4-bit cache: the whole context, or
+    (selected, budget) the positions kept per KV head."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check("spc_kv4_decode_attn", lib().spc_kv4_decode_attn(
+        _dev("q", q, _BF16, B * n_q * d),
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD),
+        _dev("block_table", block_table, _I32, B * max_blocks), _dev("len", len, _I32, B),
+        _dev("selected", selected, _I32, B * n_kv * budget), B, n_q, n_kv, d, num_blocks, block_size, max_blocks,
+        budget, float(scale), _dev("out", out, _BF16, B * n_q * d), _dev("workspace", workspace, _BYTES, 0),
+        workspace_bytes, _stream(stream)))
+
+
+def spc_prompt_attn_workspace_size(T, B, n_q, n_kv, d) -> int:
+    return int(lib().spc_prompt_attn_workspace_size(T, B, n_q, n_kv, d))
+
+
+def spc_prompt_attn(q, k, v, cu_seqlens, T, B, n_q, n_kv, d, scale, out, workspace, workspace_bytes=None,
+                    q_stride=None, k_stride=None, v_stride=None, stream=None) -> None:
+    """Causal attention over B packed prompts. The row strides are the
+    tensors' own; they are given only with plain addresses."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    q, q_stride = _rows("q", q, T, n_q, d, q_stride)
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    _check("spc_prompt_attn", lib().spc_prompt_attn(
+        q, k, v, _dev("cu_seqlens", cu_seqlens, _I32, B + 1), T, B, n_q, n_kv, d, q_stride, k_stride, v_stride,
+        float(scale), _dev("out", out, _BF16, T * n_q * d), _dev("workspace", workspace, _BYTES, 0), workspace_bytes,
+        _stream(stream)))
 
 
 def spc_device_sm_count() -> int:

@@ -398,6 +398,142 @@ int spc_mla_decode_attn(const void* q, const void* Wuk, const void* Wuv, const s
                          stream);
 }
 
+static int block_shift_of(int block_size) {
+  return block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : block_size == 128 ? 7 : -1;
+}
+static bool pool_ok(int num_blocks, int block_size) {
+  return num_blocks >= 1 && block_shift_of(block_size) > 0 && (long long)num_blocks * block_size < (1ll << 31);
+}
+static bool table_ok(int max_blocks, int block_size) {
+  return max_blocks >= 1 && (long long)max_blocks * block_size <= SPC_MAX_CAP;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+constexpr int kMaxRows = 1 << 24;
+
+int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_table, int32_t* free_list,
+                  const int32_t* n_free, int32_t* n_free_next, int32_t* cu_new, int32_t* slot_map, int32_t* status,
+                  int B, int max_blocks, int block_size, int num_blocks, int n_slots, void* stream) {
+  if (!len || !len_next || !block_table || !free_list || !n_free || !n_free_next || !cu_new || !slot_map || !status)
+    return SPC_ERR_INVALID_ARG;
+  if (n_free == n_free_next) return SPC_ERR_INVALID_ARG;
+  if (!aligned4(len) || !aligned4(len_next) || !aligned4(block_table) || !aligned4(free_list) || !aligned4(n_free) ||
+      !aligned4(n_free_next) || !aligned4(cu_new) || !aligned4(slot_map) || !aligned4(status))
+    return SPC_ERR_INVALID_ARG;
+  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size) || !table_ok(max_blocks, block_size))
+    return SPC_ERR_SHAPE;
+  if (n_slots < 1 || n_slots > kMaxRows) return SPC_ERR_SHAPE;
+  BlockMapCall c{};
+  c.len = len; c.len_next = len_next; c.table = block_table; c.free_list = free_list; c.n_free = n_free;
+  c.n_free_next = n_free_next; c.cu_new = cu_new; c.slot_map = slot_map; c.status = status;
+  c.B = B; c.max_blocks = max_blocks; c.block_shift = block_shift_of(block_size); c.num_blocks = num_blocks;
+  c.n_slots = n_slots;
+  return block_map_launch(c, stream);
+}
+
+static int kv4_rows_check(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                          const void* cache, int T, int n_kv, int d, int num_blocks, int block_size) {
+  if (d != SPC_HEAD_DIM || n_kv < 1 || n_kv > 1024 || T < 0 || T > kMaxRows || !pool_ok(num_blocks, block_size))
+    return SPC_ERR_SHAPE;
+  if (T == 0) return SPC_OK;
+  if (!k || !v || !slot_map || !cache) return SPC_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slot_map)) return SPC_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)n_kv * d;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (1ll << 40) ||
+      v_stride > (1ll << 40))
+    return SPC_ERR_SHAPE;
+  return SPC_OK;
+}
+
+static Kv4RowsCall kv4_rows_call(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                 const int32_t* slot_map, const void* cache, int T, int n_kv, int num_blocks,
+                                 int block_size) {
+  Kv4RowsCall c{};
+  c.k = static_cast<const uint16_t*>(k); c.v = static_cast<const uint16_t*>(v);
+  c.k_stride = k_stride; c.v_stride = v_stride; c.slot_map = slot_map;
+  c.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  c.T = T; c.n_kv = n_kv; c.block_shift = block_shift_of(block_size); c.n_cache_slots = num_blocks * block_size;
+  return c;
+}
+
+int spc_kv4_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                  void* cache, int T, int n_kv, int d, int num_blocks, int block_size, void* stream) {
+  const int bad = kv4_rows_check(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, d, num_blocks, block_size);
+  if (bad != SPC_OK || T == 0) return bad;
+  return kv4_store_launch(kv4_rows_call(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, num_blocks, block_size),
+                          stream);
+}
+
+int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, int64_t k_stride, int64_t v_stride,
+                 int T, int n_kv, int d, int num_blocks, int block_size, void* stream) {
+  const int bad = kv4_rows_check(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, d, num_blocks, block_size);
+  if (bad != SPC_OK || T == 0) return bad;
+  return kv4_load_launch(kv4_rows_call(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, num_blocks, block_size),
+                         stream);
+}
+
+size_t spc_kv4_decode_attn_workspace_size(int B, int n_q, int n_kv, int d, int max_blocks, int block_size,
+                                          int budget) {
+  if (B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > 1024 ||
+      block_shift_of(block_size) < 0 || !table_ok(max_blocks, block_size) || budget < 0 || budget > SPC_MAX_BUDGET)
+    return 0;
+  return kv4_attn_workspace(B, n_q, n_kv, max_blocks, block_size, budget);
+}
+
+int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                        const int32_t* selected, int B, int n_q, int n_kv, int d, int num_blocks, int block_size,
+                        int max_blocks, int budget, float scale, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  if (!q || !cache || !block_table || !len || !out) return SPC_ERR_INVALID_ARG;
+  if ((selected == nullptr) != (budget == 0)) return SPC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned4(block_table) || !aligned4(len) ||
+      !aligned4(selected))
+    return SPC_ERR_INVALID_ARG;
+  if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > 1024) return SPC_ERR_SHAPE;
+  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size) || !table_ok(max_blocks, block_size))
+    return SPC_ERR_SHAPE;
+  if (budget < 0 || budget > SPC_MAX_BUDGET) return SPC_ERR_SHAPE;
+  if (!(scale > 0.f) || scale > 3e38f) return SPC_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < kv4_attn_workspace(B, n_q, n_kv, max_blocks, block_size, budget))
+    return SPC_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
+  Kv4AttnCall c{};
+  c.q = static_cast<const uint16_t*>(q); c.cache = static_cast<const uint8_t*>(cache); c.table = block_table;
+  c.len = len; c.selected = selected; c.out = static_cast<uint16_t*>(out);
+  c.B = B; c.n_q = n_q; c.n_kv = n_kv; c.num_blocks = num_blocks; c.block_shift = block_shift_of(block_size);
+  c.max_blocks = max_blocks; c.budget = budget; c.scale2 = scale * kLog2e;
+  return kv4_attn_launch(c, workspace, stream);
+}
+
+size_t spc_prompt_attn_workspace_size(int T, int B, int n_q, int n_kv, int d) {
+  if (T < 0 || T > kMaxRows || B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024)
+    return 0;
+  return prompt_attn_workspace(T, B, n_q, n_kv);
+}
+
+int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int T, int B, int n_q,
+                    int n_kv, int d, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, void* out,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024) return SPC_ERR_SHAPE;
+  if (B < 1 || B > SPC_MAX_BATCH || T < 0 || T > kMaxRows) return SPC_ERR_SHAPE;
+  if (!(scale > 0.f) || scale > 3e38f) return SPC_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < prompt_attn_workspace(T, B, n_q, n_kv)) return SPC_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
+  if (T == 0) return SPC_OK;
+  if (!q || !k || !v || !cu_seqlens || !out) return SPC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(cu_seqlens))
+    return SPC_ERR_INVALID_ARG;
+  const int64_t qr = (int64_t)n_q * d, kr = (int64_t)n_kv * d;
+  if (q_stride < qr || k_stride < kr || v_stride < kr || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+      q_stride > (1ll << 32) || k_stride > (1ll << 32) || v_stride > (1ll << 32))
+    return SPC_ERR_SHAPE;
+  PromptAttnCall c{};
+  c.q = static_cast<const uint16_t*>(q); c.k = static_cast<const uint16_t*>(k); c.v = static_cast<const uint16_t*>(v);
+  c.cu = cu_seqlens; c.out = static_cast<uint16_t*>(out);
+  c.q_stride = q_stride; c.k_stride = k_stride; c.v_stride = v_stride;
+  c.T = T; c.B = B; c.n_q = n_q; c.n_kv = n_kv; c.scale2 = scale * kLog2e;
+  return prompt_attn_launch(c, workspace, stream);
+}
+
 int spc_host_device_pointer(void* host_ptr, void** device_ptr) {
   if (!host_ptr || !device_ptr) return SPC_ERR_INVALID_ARG;
   void* p = nullptr;

@@ -1,0 +1,103 @@
+// Rows of K and V into and out of the paged 4-bit cache.
+//
+// One warp holds one (token, KV head): lanes 0-15 its K row, lanes 16-31 its V
+// row, 8 values a lane, so that a group of 16 values is a pair of lanes.
+// Rounding: the scale is e4m3(max|x| / 6) of the correctly rounded quotient;
+// the codes need e2m1(x / s) of the exact quotient, ties included. x has 8
+// significant bits and s has 4, so a quotient that is not a tie of e2m1 is at
+// least 2^-8 (relative) away from one; x * (1 / s) in fp32 is within 2^-23 of
+// it, and rounding that product to fp16 (11 bits) returns the tie exactly
+// where there is one and stays on its side where there is none. The
+// conversion of the fp16 value to e2m1 therefore rounds the exact quotient.
+// Bound: HBM (512 bytes read and 144 written a row, or the reverse).
+#include <cuda_runtime.h>
+
+#include "kv4.cuh"
+#include "spc_device.cuh"
+#include "spc_internal.h"
+
+namespace spc {
+
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ uint8_t* kv4_record(const Kv4RowsCall& a, int slot, int g) {
+  const int blk = slot >> a.block_shift, r = slot & ((1 << a.block_shift) - 1);
+  return a.cache + ((((size_t)blk * a.n_kv + g) << a.block_shift) + r) * kKv4Rec;
+}
+
+__global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(Kv4RowsCall a) {
+  const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
+  const long long n = (long long)a.T * a.n_kv;
+  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
+  for (long long i = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < n; i += warps) {
+    const int t = (int)(i / a.n_kv), g = (int)(i - (long long)t * a.n_kv);
+    const int slot = __ldg(a.slot_map + t);
+    if (slot < 0 || slot >= a.n_cache_slots) continue;
+    const uint16_t* src = (isv ? a.v + (size_t)t * a.v_stride : a.k + (size_t)t * a.k_stride) + g * kD + 8 * hl;
+    const uint4 w = ldg_stream(src);
+    // largest magnitude of the group: bit patterns without the sign order like
+    // the magnitudes, NaN above infinity
+    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m & 0xffffu, m >> 16);
+    const float amax = __uint_as_float(m << 16);
+    const uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
+    const float s = f16_lo(e4m3x2_to_f16(sb));
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    float x[8];
+    unpack8(w, x);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const __half2 h = __floats2half2_rn(x[j] * r, x[j + 1] * r);
+      x[j] = __low2float(h);
+      x[j + 1] = __high2float(h);
+    }
+    uint8_t* rec = kv4_record(a, slot, g);
+    *reinterpret_cast<uint32_t*>(rec + isv * kKv4V + 4 * hl) = f32_to_e2m1x8(x);
+    // the scales of four groups (eight lanes) as one word
+    uint32_t sw = sb | (__shfl_down_sync(0xffffffffu, sb, 2) << 8);
+    sw |= __shfl_down_sync(0xffffffffu, sw, 4) << 16;
+    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kKv4Scale + 4 * (lane >> 3)) = sw;
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4RowsCall a) {
+  const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
+  const long long n = (long long)a.T * a.n_kv;
+  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
+  for (long long i = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < n; i += warps) {
+    const int t = (int)(i / a.n_kv), g = (int)(i - (long long)t * a.n_kv);
+    const int slot = __ldg(a.slot_map + t);
+    if (slot < 0 || slot >= a.n_cache_slots) continue;
+    const uint8_t* rec = kv4_record(a, slot, g);
+    const uint32_t codes = *reinterpret_cast<const uint32_t*>(rec + isv * kKv4V + 4 * hl);
+    const uint32_t s = e4m3_dup_f16(rec[kKv4Scale + 8 * isv + (hl >> 1)]);
+    uint32_t h[4];
+    e2m1x8_to_f16(codes, h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = hmul2(h[j], s);
+      h[j] = pack_bf16(f16_lo(h[j]), f16_hi(h[j]));
+    }
+    uint16_t* dst = const_cast<uint16_t*>(isv ? a.v + (size_t)t * a.v_stride : a.k + (size_t)t * a.k_stride) + g * kD + 8 * hl;
+    stg_v4(dst, make_uint4(h[0], h[1], h[2], h[3]));
+  }
+}
+
+static int rows_grid(const Kv4RowsCall& c) {
+  const long long n = (long long)c.T * c.n_kv, per = kRowThreads / 32;
+  const long long g = (n + per - 1) / per;
+  return (int)(g < 152 * 8 ? g : 152 * 8);
+}
+
+int kv4_store_launch(const Kv4RowsCall& c, void* stream) {
+  kv4_store_kernel<<<rows_grid(c), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+}
+
+int kv4_load_launch(const Kv4RowsCall& c, void* stream) {
+  kv4_load_kernel<<<rows_grid(c), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+}
+
+}  // namespace spc

@@ -146,6 +146,59 @@ size_t batch_select_workspace(int B, int cap, int budget);
 int batch_select_launch(const float* scores, int32_t* len, int B, int n_kv, int cap, int budget, int n_sink,
                         int n_recent, int32_t* selected, void* workspace, void* stream);
 
+// Paged 4-bit cache (block_map.cu, kv4_rows.cu, kv4_attn.cu) and the prompt
+// attention that precedes it (prompt_attn.cu). block_shift is log2(block_size).
+struct BlockMapCall {
+  const int32_t* len;
+  const int32_t* len_next;
+  int32_t* table;
+  int32_t* free_list;
+  const int32_t* n_free;
+  int32_t* n_free_next;
+  int32_t* cu_new;
+  int32_t* slot_map;
+  int32_t* status;
+  int B, max_blocks, block_shift, num_blocks, n_slots;
+};
+int block_map_launch(const BlockMapCall& c, void* stream);
+
+struct Kv4RowsCall {
+  const uint16_t* k;      // load: written
+  const uint16_t* v;
+  int64_t k_stride, v_stride;
+  const int32_t* slot_map;
+  uint8_t* cache;
+  int T, n_kv, block_shift, n_cache_slots;
+};
+int kv4_store_launch(const Kv4RowsCall& c, void* stream);
+int kv4_load_launch(const Kv4RowsCall& c, void* stream);
+
+struct Kv4AttnCall {
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int32_t* table;
+  const int32_t* len;
+  const int32_t* selected;
+  uint16_t* out;
+  int B, n_q, n_kv, num_blocks, block_shift, max_blocks, budget;
+  float scale2;           // scale * log2(e)
+};
+size_t kv4_attn_workspace(int B, int n_q, int n_kv, int max_blocks, int block_size, int budget);
+int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream);
+
+struct PromptAttnCall {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const int32_t* cu;
+  uint16_t* out;
+  int64_t q_stride, k_stride, v_stride;
+  int T, B, n_q, n_kv;
+  float scale2;
+};
+size_t prompt_attn_workspace(int T, int B, int n_q, int n_kv);
+int prompt_attn_launch(const PromptAttnCall& c, void* workspace, void* stream);
+
 int stream_read_launch(const void* src, size_t bytes, uint32_t* sink, int n_blocks, void* stream);
 
 int device_sm_count();
