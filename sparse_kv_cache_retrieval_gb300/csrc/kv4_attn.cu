@@ -1,5 +1,41 @@
-// Decode attention over the paged 4-bit cache: one warp a (request, query
-// head), one position at a time, four values of K and V a lane.
+// Decode attention over the paged 4-bit cache, one query token per request.
+//
+// out = sum_p softmax_p(scale q.K_p) V_p over the context, or over selected
+// positions, of (request, KV head) segments. Both products run on mma.sync
+// (m16n8k16, fp16 operands, fp32 accumulators) with the cache rows as the
+// 16-row operand and up to 8 query heads of the group as the 8 columns:
+//   S^T [16 positions][8 heads] = K [16][128] Q^T [128][8]
+//   O^T [128 dims][8 heads]    += V^T [128][16 positions] P^T [16][8]
+// A 4-bit code times its e4m3 scale is exact in fp16, so dequantised operands
+// lose nothing. The queries are scaled per head by a power of two to below 2
+// and rounded to fp16 (11 bits; bf16 has 8, so only values 2^-14 below the
+// head's largest lose bits, at most 2^-25 of it). The weights P are rounded to
+// fp16 (2^-11); maxima, sums and outputs are fp32.
+//
+// Layout: a record is 36 words, so 8 consecutive rows start 4 banks apart.
+// The 32 positions of a step are dealt to the two 16-row tiles so that both
+// the 16-byte K loads (rows 4 apart, mod 8, in a quarter warp) and the 8-byte
+// V loads (rows 2 apart in a half warp) touch every bank once: tile t, row
+// m = 8h + 2i + o is position 16h + 8o + ((2i + 4o) mod 8) + t.
+//   K: lane (gid, tig) reads 16 bytes, values 32 tig .. 32 tig + 31 of a row;
+//      the contraction index is permuted the same way in Q's fragments.
+//   V: a weight's row pairs must share a register, so the nibbles of two rows
+//      are interleaved (two shifts, two selects per 8 values of each) before
+//      the conversion; lane (gid, tig) then holds dims 16 gid .. 16 gid + 15,
+//      one scale group.
+//
+// The running maximum of a head is raised only when a logit passes it by more
+// than 2^8 (weights stay below 2^8, exact in the sums' fp32 and no coarser in
+// fp16), which takes the shuffles out of the common case.
+//
+// Work: all segments' 64-position tiles in one line, cut into equal runs, one
+// per CTA (the lengths are read on the device). Tile t of a run belongs to
+// warp t mod 8; a warp copies its own tiles ahead of itself into its own ring
+// (cp.async.bulk, one instruction per cache block, or per record for selected
+// positions), so warps meet only at the end of a segment, where their partial
+// (m, l, O) are merged through shared memory. A segment cut by a run's end
+// leaves a partial per CTA in the workspace and the last CTA to finish merges
+// them in CTA order (deterministic).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
@@ -8,49 +44,559 @@
 
 namespace spc {
 
-__global__ void __launch_bounds__(32) kv4_attn_kernel(Kv4AttnCall a) {
-  const int lane = threadIdx.x, b = blockIdx.x / a.n_q, h = blockIdx.x % a.n_q, G = a.n_q / a.n_kv, g = h / G;
-  const uint2 qw = *reinterpret_cast<const uint2*>(a.q + (size_t)blockIdx.x * kD + 4 * lane);
-  const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
-  const int L = max(0, min(a.len[b], a.max_blocks << a.block_shift));
-  const int n = a.selected ? a.budget : L;
-  const int32_t* sel = a.selected ? a.selected + ((size_t)b * a.n_kv + g) * a.budget : nullptr;
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const int p = sel ? sel[i] : i;
-    if (p < 0 || p >= L) continue;
-    const int blk = a.table[(size_t)b * a.max_blocks + (p >> a.block_shift)];
-    if (blk < 0 || blk >= a.num_blocks) continue;
-    const uint8_t* rec = a.cache + ((((size_t)blk * a.n_kv + g) << a.block_shift) + (p & ((1 << a.block_shift) - 1))) * kKv4Rec;
-    uint32_t kh[4], vh[4];
-    const uint32_t kc = *reinterpret_cast<const uint16_t*>(rec + 2 * lane);
-    const uint32_t vc = *reinterpret_cast<const uint16_t*>(rec + kKv4V + 2 * lane);
-    e2m1x8_to_f16(kc | vc << 16, kh);
-    const uint32_t ks = e4m3_dup_f16(rec[kKv4Scale + (lane >> 2)]), vs = e4m3_dup_f16(rec[kKv4Scale + 8 + (lane >> 2)]);
-    vh[0] = hmul2(kh[2], vs);
-    vh[1] = hmul2(kh[3], vs);
-    kh[0] = hmul2(kh[0], ks);
-    kh[1] = hmul2(kh[1], ks);
-    const float x = a.scale2 * warp_sum(q0 * f16_lo(kh[0]) + q1 * f16_hi(kh[0]) + q2 * f16_lo(kh[1]) + q3 * f16_hi(kh[1]));
-    const float M = fmaxf(m, x);
-    const float c = exp2f(m - M), e = exp2f(x - M);
-    l = l * c + e;
-    o0 = o0 * c + e * f16_lo(vh[0]);
-    o1 = o1 * c + e * f16_hi(vh[0]);
-    o2 = o2 * c + e * f16_lo(vh[1]);
-    o3 = o3 * c + e * f16_hi(vh[1]);
-    m = M;
-  }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.out + (size_t)blockIdx.x * kD + 4 * lane) =
-      make_uint2(pack_bf16(o0 * r, o1 * r), pack_bf16(o2 * r, o3 * r));
+constexpr int kK4Warps = 8;
+constexpr int kK4Threads = 32 * kK4Warps;
+constexpr int kK4Tile = 64;                          // positions a tile
+constexpr int kK4Stages = 2;                         // tiles in a warp's ring
+constexpr int kK4MinRun = 8;                         // tiles a CTA takes at least
+constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
+constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
+constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
+constexpr float kK4Headroom = 8.f;
+constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
+
+// shared memory
+constexpr uint32_t kK4OffRing = 0;
+constexpr uint32_t kK4OffMerge = kK4OffRing + kK4Warps * kK4Stages * kK4StageBytes;   // [warps][8 heads][kK4Part]
+constexpr uint32_t kK4OffQ = kK4OffMerge + kK4Warps * 8 * kK4Part * 4;                // [4 head tiles][8 k-steps][32 lanes] x 8 bytes
+constexpr uint32_t kK4OffBar = kK4OffQ + 4 * 8 * 32 * 8;
+constexpr uint32_t kK4OffMask = kK4OffBar + kK4Warps * kK4Stages * 8;
+constexpr uint32_t kK4Smem = kK4OffMask + kK4Warps * kK4Stages * 8;
+
+struct Kv4Args {
+  Kv4AttnCall c;
+  int ht;            // head tiles (8 heads) a segment
+  int hsplit;        // segments a KV head's group is split into
+  int* status;
+  uint32_t* counters;
+  float* part;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^x by the MUFU approximation (relative error about 2^-22); -inf gives 0
+__device__ __forceinline__ float k4_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-size_t kv4_attn_workspace(int, int, int, int, int, int) { return 256; }
+// the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
+struct K4Line {
+  int pre[SPC_MAX_BATCH + 1];
+  int nt[SPC_MAX_BATCH];       // tiles a segment of request b
+  int len[SPC_MAX_BATCH];
+};
 
-int kv4_attn_launch(const Kv4AttnCall& c, void*, void* stream) {
-  kv4_attn_kernel<<<c.B * c.n_q, 32, 0, static_cast<cudaStream_t>(stream)>>>(c);
+// a tile of the line: segment (b, s) with s = g * hsplit + hh, tile i of it
+struct K4Cursor {
+  int t, b, s, i;
+};
+__device__ __forceinline__ K4Cursor k4_at(const K4Line& ln, int B, int t) {
+  int lo = 0, hi = B;          // pre[lo] <= t < pre[hi]; requests without tiles are passed over
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ln.pre[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int r = t - ln.pre[lo], nt = max(1, ln.nt[lo]);
+  K4Cursor x;
+  x.t = t;
+  x.b = lo;
+  x.s = r / nt;
+  x.i = r - x.s * nt;
+  return x;
+}
+__device__ __forceinline__ void k4_step(const K4Line& ln, int B, int segs, K4Cursor& x, int n) {
+  x.t += n;
+  x.i += n;
+  while (x.b < B && x.i >= ln.nt[x.b]) {
+    x.i -= ln.nt[x.b];
+    if (++x.s == segs) {
+      x.s = 0;
+      do ++x.b; while (x.b < B && ln.nt[x.b] == 0);
+    }
+  }
+}
+
+// Copies tile x into a stage: valid rows only, their bytes announced on the
+// stage's barrier, their positions noted in the stage's mask. One warp.
+__device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Line& ln, const K4Cursor& x, uint8_t* stage,
+                                         uint64_t* bar, uint2* mask) {
+  const Kv4AttnCall& c = a.c;
+  const int lane = threadIdx.x & 31, g = x.s / a.hsplit;
+  const int bs = 1 << c.block_shift;
+  const int32_t* table = c.table + (size_t)x.b * c.max_blocks;
+  uint32_t m[2] = {0u, 0u};
+  if (c.selected == nullptr) {
+    const int p0 = x.i * kK4Tile, n = min(kK4Tile, ln.len[x.b] - p0);      // rows of the tile
+    const int span = min(bs, kK4Tile), pages = kK4Tile / span;             // pages of `span` rows
+    // lane i < pages: page i of the tile
+    int rows = 0;
+    const uint8_t* src = nullptr;
+    if (lane < pages && lane * span < n) {
+      const int p = p0 + lane * span, blk = __ldg(table + (p >> c.block_shift));
+      if (blk >= 0 && blk < c.num_blocks) {
+        rows = min(span, n - lane * span);
+        src = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
+      }
+    }
+    if (rows > 0) {
+      const uint64_t bits = (rows == 64 ? ~0ull : (1ull << rows) - 1) << (lane * span);
+      m[0] = (uint32_t)bits;
+      m[1] = (uint32_t)(bits >> 32);
+    }
+    const uint32_t m0 = __reduce_or_sync(0xffffffffu, m[0]), m1 = __reduce_or_sync(0xffffffffu, m[1]);
+    if (lane == 0) {
+      *mask = make_uint2(m0, m1);
+      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(m0) + __popc(m1)) * kKv4Rec);
+    }
+    __syncwarp();
+    if (rows > 0) bulk_g2s(stage + (uint32_t)(lane * span) * kKv4Rec, src, (uint32_t)rows * kKv4Rec, bar);
+  } else {
+    const int32_t* sel = c.selected + ((size_t)x.b * c.n_kv + g) * c.budget + x.i * kK4Tile;
+    const uint8_t* src[2] = {nullptr, nullptr};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = 32 * e + lane;
+      const int p = x.i * kK4Tile + j < c.budget ? __ldg(sel + j) : -1;
+      if (p >= 0 && p < ln.len[x.b]) {
+        const int blk = __ldg(table + (p >> c.block_shift));
+        if (blk >= 0 && blk < c.num_blocks)
+          src[e] = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
+      }
+      m[e] = __ballot_sync(0xffffffffu, src[e] != nullptr);
+    }
+    if (lane == 0) {
+      *mask = make_uint2(m[0], m[1]);
+      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(m[0]) + __popc(m[1])) * kKv4Rec);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (src[e]) bulk_g2s(stage + (uint32_t)(32 * e + lane) * kKv4Rec, src[e], kKv4Rec, bar);
+  }
+}
+
+// The 32 positions [32 sb, +32) of a stage: logits, weights, sums.
+// FULL: every position of the step counts.
+template <int HT, bool FULL>
+__device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, const uint2* sq, const uint32_t (&qr)[16],
+                                          const float (&f)[HT][2], float (&m)[HT][2], float (&l)[HT][2],
+                                          float (&o)[HT][8][4]) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int od = gid & 1;
+  const int rk = 8 * od + ((2 * (gid >> 1) + 4 * od) & 7);       // this lane's K row (+ 16, + tile)
+  float s[HT][2][4];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint4 w[2];
+    uint32_t sc[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* r = rows + (rk + 16 * h + t) * kKv4Rec;
+      w[h] = *reinterpret_cast<const uint4*>(r + 16 * tig);
+      const uint32_t e = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(r + kKv4Scale + 2 * tig));
+      sc[h][0] = __byte_perm(e, e, 0x1010);
+      sc[h][1] = __byte_perm(e, e, 0x3232);
+    }
+#pragma unroll
+    for (int n = 0; n < HT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t h0[4], h1[4];
+      e2m1x8_to_f16(reinterpret_cast<const uint32_t*>(&w[0])[x], h0);
+      e2m1x8_to_f16(reinterpret_cast<const uint32_t*>(&w[1])[x], h1);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t av[4] = {hmul2(h0[2 * y], sc[0][x >> 1]), hmul2(h1[2 * y], sc[1][x >> 1]),
+                                hmul2(h0[2 * y + 1], sc[0][x >> 1]), hmul2(h1[2 * y + 1], sc[1][x >> 1])};
+        const int j = 2 * x + y;
+        if constexpr (HT == 1) {
+          mma_f16(s[0][t], av, qr[2 * j], qr[2 * j + 1]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < HT; ++n) {
+            const uint2 b = sq[(n * 8 + j) * 32 + lane];
+            mma_f16(s[n][t], av, b.x, b.y);
+          }
+        }
+      }
+    }
+  }
+  uint32_t p[HT][2][2];
+#pragma unroll
+  for (int n = 0; n < HT; ++n) {
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][t][e] *= f[n][e & 1];
+        if (!FULL && !((valid >> (rk + 16 * (e >> 1) + t)) & 1u)) s[n][t][e] = -INFINITY;
+        mx[e & 1] = fmaxf(mx[e & 1], s[n][t][e]);
+      }
+    const bool up = mx[0] > m[n][0] + kK4Headroom || mx[1] > m[n][1] + kK4Headroom;
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int k = 4; k <= 16; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], k));
+        const float M = fmaxf(m[n][e], mx[e]);
+        // a first finite maximum takes 0 of what was (nothing)
+        const float c = k4_ex2(m[n][e] - (M == -INFINITY ? 0.f : M));
+        m[n][e] = M;
+        l[n][e] *= c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[n][j][e] *= c;
+          o[n][j][e + 2] *= c;
+        }
+      }
+    }
+    const float ms[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][t][e] = k4_ex2(s[n][t][e] - ms[e & 1]);
+        l[n][e & 1] += s[n][t][e];
+      }
+      p[n][t][0] = movmatrix(pack_f16(s[n][t][0], s[n][t][1]));
+      p[n][t][1] = movmatrix(pack_f16(s[n][t][2], s[n][t][3]));
+    }
+  }
+  const int rv0 = 2 * tig, rv1 = 8 + ((2 * tig + 4) & 7);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint2 v[4];
+    uint32_t b[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int row = ((h & 1) ? rv1 : rv0) + 16 * (h >> 1) + t;
+      const uint8_t* r = rows + row * kKv4Rec;
+      v[h] = *reinterpret_cast<const uint2*>(r + kKv4V + 8 * gid);
+      b[h] = r[kKv4Scale + 8 + gid];
+      // what does not count must not reach the sums: codes are always finite, a scale may be NaN
+      if (!FULL && !((valid >> row) & 1u)) b[h] = 0;
+    }
+    const uint32_t sc0 = e4m3x2_to_f16(b[0] | b[1] << 8), sc1 = e4m3x2_to_f16(b[2] | b[3] << 8);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t ev0[4], od0[4], ev1[4], od1[4];
+      const uint32_t a0 = x ? v[0].y : v[0].x, a1 = x ? v[1].y : v[1].x, a2 = x ? v[2].y : v[2].x, a3 = x ? v[3].y : v[3].x;
+      constexpr uint32_t M = 0x0f0f0f0fu;
+      e2m1x8_to_f16((a0 & M) | ((a1 << 4) & ~M), ev0);
+      e2m1x8_to_f16(((a0 >> 4) & M) | (a1 & ~M), od0);
+      e2m1x8_to_f16((a2 & M) | ((a3 << 4) & ~M), ev1);
+      e2m1x8_to_f16(((a2 >> 4) & M) | (a3 & ~M), od1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t av[4] = {hmul2(ev0[i], sc0), hmul2(od0[i], sc0), hmul2(ev1[i], sc1), hmul2(od1[i], sc1)};
+#pragma unroll
+        for (int n = 0; n < HT; ++n) mma_f16(o[n][4 * x + i], av, p[n][t][0], p[n][t][1]);
+      }
+    }
+  }
+}
+
+template <int HT>
+__global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
+  extern __shared__ __align__(128) uint8_t k4_smem[];
+  __shared__ K4Line ln;
+  __shared__ int s_last;
+  const Kv4AttnCall& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int G = c.n_q / c.n_kv, segs = c.n_kv * a.hsplit, heads = min(8 * HT, G);
+  uint8_t* ring = k4_smem + kK4OffRing + (uint32_t)warp * kK4Stages * kK4StageBytes;
+  float* mrg = reinterpret_cast<float*>(k4_smem + kK4OffMerge);
+  uint2* sq = reinterpret_cast<uint2*>(k4_smem + kK4OffQ);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(k4_smem + kK4OffBar) + warp * kK4Stages;
+  uint2* masks = reinterpret_cast<uint2*>(k4_smem + kK4OffMask) + warp * kK4Stages;
+
+  if (lane == 0) {
+    for (int s = 0; s < kK4Stages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    // tiles a segment of each request, two requests a lane
+    int n[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * lane + e;
+      int L = b < c.B ? c.len[b] : 0;
+      L = max(0, min(L, c.max_blocks << c.block_shift));
+      const int nt = b < c.B ? ((c.selected ? c.budget : L) + kK4Tile - 1) / kK4Tile : 0;
+      ln.len[b] = L;
+      ln.nt[b] = nt;
+      n[e] = nt * segs;
+    }
+    const int incl = warp_incl_scan(n[0] + n[1]);
+    ln.pre[2 * lane] = incl - n[0] - n[1];
+    ln.pre[2 * lane + 1] = incl - n[1];
+    if (lane == 31) ln.pre[SPC_MAX_BATCH] = incl;
+  }
+  __syncthreads();
+  const int total = ln.pre[c.B];
+  const int run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kK4MinRun);
+  const int t0 = min(total, (int)blockIdx.x * run), t1 = min(total, t0 + run);
+
+  // segments without a tile: zeros
+  for (int b = 0; b < c.B; ++b) {
+    if (ln.nt[b] != 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
+    for (int i = blockIdx.x * kK4Threads + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * kK4Threads)
+      dst[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  bool dead = false;
+  int n_wait = 0;                                    // tiles this warp has waited for
+  K4Cursor nx = k4_at(ln, c.B, t0 + warp);           // next tile to copy
+  int n_issued = 0;
+  if (t0 + warp < t1) {
+#pragma unroll 1
+    for (; n_issued < kK4Stages && nx.t < t1; ++n_issued) {
+      k4_issue(a, ln, nx, ring + n_issued * kK4StageBytes, &bars[n_issued], &masks[n_issued]);
+      k4_step(ln, c.B, segs, nx, kK4Warps);
+    }
+  }
+
+  K4Cursor pc = k4_at(ln, c.B, min(t0, max(total - 1, 0)));   // the piece at hand
+  for (int pt = t0; pt < t1;) {
+    const int b = pc.b, sg = pc.s, nt = ln.nt[b];
+    const int pe = min(t1, pt + nt - pc.i);          // end of this CTA's piece of the segment
+    const int g = sg / a.hsplit, hh = sg - g * a.hsplit;
+    const int h0 = g * G + hh * 8 * HT;              // first query head
+    // ---- queries: per head a power of two that brings the largest value below 2
+    uint32_t qr[16];
+    float f[HT][2];
+#pragma unroll
+    for (int n = 0; n < HT; ++n) {
+      const int h = 8 * n + gid;
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = h < heads ? __ldg(reinterpret_cast<const uint4*>(c.q + ((size_t)b * c.n_q + h0 + h) * kD + 32 * tig) + i)
+                         : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                   __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // biased exponent of the largest value; 2^-e as two factors, each normal
+      const int e = max((int)(mx >> 7), 1) - 127;
+      const int e1 = e / 2, e2 = e - e1;
+      const float d1 = __uint_as_float((uint32_t)(127 - e1) << 23), d2 = __uint_as_float((uint32_t)(127 - e2) << 23);
+      const float u1 = __uint_as_float((uint32_t)(127 + e1) << 23), u2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+      const float fh = c.scale2 * u1 * u2;           // of head 8 n + gid
+      f[n][0] = __shfl_sync(0xffffffffu, fh, 8 * tig);
+      f[n][1] = __shfl_sync(0xffffffffu, fh, 8 * tig + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[8];
+        unpack8(w[i], x);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t b0 = pack_f16(x[4 * y] * d1 * d2, x[4 * y + 1] * d1 * d2);
+          const uint32_t b1 = pack_f16(x[4 * y + 2] * d1 * d2, x[4 * y + 3] * d1 * d2);
+          if constexpr (HT == 1) {
+            qr[4 * i + 2 * y] = b0;
+            qr[4 * i + 2 * y + 1] = b1;
+          } else if (warp == 0) {
+            sq[(n * 8 + 2 * i + y) * 32 + lane] = make_uint2(b0, b1);
+          }
+        }
+      }
+    }
+    if constexpr (HT > 1) __syncthreads();
+
+    float m[HT][2], l[HT][2], o[HT][8][4];
+#pragma unroll
+    for (int n = 0; n < HT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+    }
+    // this warp's tiles of the piece
+    const int k0 = (pt - t0 + kK4Warps - 1 - warp) / kK4Warps;
+#pragma unroll 1
+    for (int t = t0 + warp + k0 * kK4Warps; t < pe; t += kK4Warps) {
+      const int st = n_wait % kK4Stages;
+      if (!dead && !mbar_wait_bounded(&bars[st], (n_wait / kK4Stages) & 1, kK4WaitLimit)) {
+        set_status(a.status, SPC_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) continue;                            // its barriers are still reached; nothing more is copied
+      ++n_wait;
+      const uint8_t* rows = ring + st * kK4StageBytes;
+      const uint2 mk = masks[st];
+#pragma unroll 1
+      for (int sb = 0; sb < 2; ++sb) {
+        const uint32_t valid = sb ? mk.y : mk.x;
+        if (valid == 0xffffffffu)
+          k4_step32<HT, true>(rows + sb * 32 * kKv4Rec, valid, sq, qr, f, m, l, o);
+        else if (valid != 0)
+          k4_step32<HT, false>(rows + sb * 32 * kKv4Rec, valid, sq, qr, f, m, l, o);
+      }
+      __syncwarp();
+      if (nx.t < t1) {
+        k4_issue(a, ln, nx, ring + st * kK4StageBytes, &bars[st], &masks[st]);
+        ++n_issued;
+        k4_step(ln, c.B, segs, nx, kK4Warps);
+      }
+    }
+
+    // ---- merge of the warps' partials, 8 heads at a time
+    const int seg = b * segs + sg;
+    const int s0 = pt - pc.i, s1 = s0 + nt;          // the segment's tiles in the line
+    const int w0 = s0 / run, w1 = (s1 - 1) / run;    // CTAs that have a piece of it
+    const bool whole = w0 == w1;
+    float* res = a.part + ((size_t)blockIdx.x * 2 + (s0 > t0 ? 1 : 0)) * (size_t)(8 * HT) * kK4Part;
+#pragma unroll 1
+    for (int n = 0; n < HT; ++n) {
+      float mm[2], ll[2];
+      float* dst = mrg + (size_t)(warp * 8 + 2 * tig) * kK4Part;
+#pragma unroll
+      for (int k = 0; k < HT; ++k) {
+        if (k != n) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mm[e] = m[k][e];
+          ll[e] = l[k][e];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<float4*>(dst + e * kK4Part + 4 + 16 * gid + 4 * y) =
+                make_float4(o[k][2 * y][e], o[k][2 * y][e + 2], o[k][2 * y + 1][e], o[k][2 * y + 1][e + 2]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int k = 4; k <= 16; k <<= 1) ll[e] += __shfl_xor_sync(0xffffffffu, ll[e], k);
+        if (gid == 0) {
+          dst[e * kK4Part] = mm[e];
+          dst[e * kK4Part + 1] = ll[e];
+        }
+      }
+      __syncthreads();
+      const int h = 8 * n + warp;                    // warp w merges head w of the eight
+      if (h < heads) {
+        float M = -INFINITY;
+        for (int w = 0; w < kK4Warps; ++w) M = fmaxf(M, mrg[(w * 8 + warp) * kK4Part]);
+        const float Ms = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kK4Warps; ++w) {
+          const float* src = mrg + (size_t)(w * 8 + warp) * kK4Part;
+          const float wt = k4_ex2(src[0] - Ms);
+          const float4 x = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
+          L += wt * src[1];
+          v.x += wt * x.x; v.y += wt * x.y; v.z += wt * x.z; v.w += wt * x.w;
+        }
+        if (whole) {
+          const float r = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint2*>(c.out + ((size_t)b * c.n_q + h0 + h) * kD + 4 * lane) =
+              make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+        } else {
+          float* p = res + (size_t)h * kK4Part;
+          if (lane == 0) {
+            p[0] = M;
+            p[1] = L;
+          }
+          *reinterpret_cast<float4*>(p + 4 + 4 * lane) = v;
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s_last = atomicAdd(&a.counters[seg], 1u) == (uint32_t)(w1 - w0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int h = warp; h < heads; h += kK4Warps) {
+          float M = -INFINITY, L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int w = w0; w <= w1; ++w) {
+            const float* p = a.part + (((size_t)w * 2 + (s0 > w * run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+            const float M2 = fmaxf(M, ml.x), Ms = M2 == -INFINITY ? 0.f : M2;
+            const float wa = k4_ex2(M - Ms), wb = k4_ex2(ml.x - Ms);
+            L = L * wa + ml.y * wb;
+            v.x = v.x * wa + x.x * wb; v.y = v.y * wa + x.y * wb;
+            v.z = v.z * wa + x.z * wb; v.w = v.w * wa + x.w * wb;
+            M = M2;
+          }
+          const float r = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint2*>(c.out + ((size_t)b * c.n_q + h0 + h) * kD + 4 * lane) =
+              make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+        }
+        if (threadIdx.x == 0) a.counters[seg] = 0u;
+      }
+      __syncthreads();
+    }
+    k4_step(ln, c.B, segs, pc, pe - pt);
+    pt = pe;
+  }
+  // copies that nobody waited for (a wait gave up) land before the CTA ends
+  for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&bars[n_wait % kK4Stages], (n_wait / kK4Stages) & 1, kK4WaitLimit);
+}
+
+static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
+static int k4_head_tiles(int G) { return G <= 8 ? 1 : G == 16 ? 2 : 4; }
+
+size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int) {
+  const int G = n_q / n_kv, ht = k4_head_tiles(G), hsplit = G > 32 ? G / 32 : 1;
+  return 256 + k4_round((size_t)B * n_kv * hsplit * 4) + (size_t)kK4Ctas * 2 * 8 * ht * kK4Part * 4;
+}
+
+template <int HT>
+static int k4_run(const Kv4Args& a, void* stream) {
+  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kK4Smem);
+  if (e != cudaSuccess) return SPC_ERR_CUDA;
+  kv4_attn_kernel<HT><<<kK4Ctas, kK4Threads, kK4Smem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+}
+
+int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
+  const int G = c.n_q / c.n_kv;
+  Kv4Args a{};
+  a.c = c;
+  a.ht = k4_head_tiles(G);
+  a.hsplit = G > 32 ? G / 32 : 1;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<int*>(ws);
+  a.counters = reinterpret_cast<uint32_t*>(ws + 256);
+  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * c.n_kv * a.hsplit * 4));
+  switch (a.ht) {
+    case 1: return k4_run<1>(a, stream);
+    case 2: return k4_run<2>(a, stream);
+    default: return k4_run<4>(a, stream);
+  }
 }
 
 }  // namespace spc
