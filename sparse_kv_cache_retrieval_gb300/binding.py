@@ -286,87 +286,110 @@ def spc_mla_decode_attn(q, Wuk, Wuv, views, selected, slot_pos, n_layers, B, bud
 # ------------------------------------------------------------------ paged 4-bit cache
 SPC_KV4_RECORD, SPC_KV4_GROUP = 144, 16
 
-_BF16 = ("torch.bfloat16", "torch.int16", "torch.uint16")
-_I32 = ("torch.int32",)
-_BYTES = ("torch.uint8", "torch.int8")
+# accepted dtypes, filled in by _device() (torch is imported on first use)
+_BF16, _I32, _BYTES = set(), set(), set()
 
 
-def _dev(name, t, dtypes, numel):
-    """Pointer of a contiguous device tensor of at least `numel` elements (an
-    int is taken as a device address, None stays None)."""
+_torch = None
+
+
+def _device():
+    """Index of the current CUDA device (-2, no tensor's, before CUDA is up)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
+        _BYTES.update((torch.uint8, torch.int8))
+        _I32.add(torch.int32)
+        _torch = torch
+    return _torch.cuda.current_device() if _torch.cuda.is_initialized() else -2
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch.cuda.current_stream(dev).cuda_stream if dev >= 0 else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dev(name, t, dtypes, numel, dev):
+    """Pointer of a contiguous tensor of at least `numel` elements on device
+    `dev` (an int is taken as a device address, None stays None)."""
     if t is None or isinstance(t, int):
         return t
-    if str(t.dtype) not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(dtypes)}")
+    if t.dtype in dtypes and t.numel() >= numel and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(sorted(map(str, dtypes)))}")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
-    _on_current_device(name, t)
-    return t.data_ptr()
+    raise _wrong_device(name, t, dev)
 
 
-def _on_current_device(name, t):
-    if t.device.type != "cuda":
-        raise ValueError(f"{name}: tensor is on {t.device}, expected a CUDA device")
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _wrong_device(name, t, dev):
+    return ValueError(f"{name}: tensor is on {t.device}, expected " +
+                      (f"the current device cuda:{dev}" if dev >= 0 else "a CUDA device"))
 
 
-def _rows(name, t, T, n, d, stride):
+def _rows(name, t, T, n, d, stride, dev):
     """(pointer, row stride in elements) of bf16 rows [T][n][d] whose rows may
     lie `stride` elements apart."""
     if t is None or isinstance(t, int):
         return t, n * d if stride is None else int(stride)
-    if str(t.dtype) not in _BF16:
+    if t.dtype not in _BF16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected bf16 values or bit patterns")
-    if t.dim() != 3 or t.shape[0] < T or t.shape[1] != n or t.shape[2] != d:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{T}][{n}][{d}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < T or shape[1] != n or shape[2] != d:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{T}][{n}][{d}]")
     s0, s1, s2 = t.stride()
     # a dimension of one element may carry any stride
     if (s2 != 1 and d > 1) or (s1 != d and n > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if t.shape[0] <= 1:
-        s0 = max(s0, n * d) // 8 * 8
+    if shape[0] <= 1:
+        s0 = n * d
     if stride is not None and stride != s0:
         raise ValueError(f"{name}: stride {stride} given for a tensor of row stride {s0}")
-    _on_current_device(name, t)
+    if t.get_device() != dev:
+        raise _wrong_device(name, t, dev)
     return t.data_ptr(), s0
 
 
 def spc_block_map(len, len_next, block_table, free_list, n_free, n_free_next, cu_new, slot_map, status, B, max_blocks,
                   block_size, num_blocks, n_slots, stream=None) -> None:
     """Block tables, free stack and slot map of the requests' next lengths."""
+    dev = _device()
     _check("spc_block_map", lib().spc_block_map(
-        _dev("len", len, _I32, B), _dev("len_next", len_next, _I32, B),
-        _dev("block_table", block_table, _I32, B * max_blocks), _dev("free_list", free_list, _I32, num_blocks),
-        _dev("n_free", n_free, _I32, 1), _dev("n_free_next", n_free_next, _I32, 1),
-        _dev("cu_new", cu_new, _I32, B + 1), _dev("slot_map", slot_map, _I32, n_slots),
-        _dev("status", status, _I32, 1), B, max_blocks, block_size, num_blocks, n_slots, _stream(stream)))
+        _dev("len", len, _I32, B, dev), _dev("len_next", len_next, _I32, B, dev),
+        _dev("block_table", block_table, _I32, B * max_blocks, dev), _dev("free_list", free_list, _I32, num_blocks, dev),
+        _dev("n_free", n_free, _I32, 1, dev), _dev("n_free_next", n_free_next, _I32, 1, dev),
+        _dev("cu_new", cu_new, _I32, B + 1, dev), _dev("slot_map", slot_map, _I32, n_slots, dev),
+        _dev("status", status, _I32, 1, dev), B, max_blocks, block_size, num_blocks, n_slots, _raw_stream(stream, dev)))
 
 
 def spc_kv4_store(k, v, slot_map, cache, T, n_kv, d, num_blocks, block_size, k_stride=None, v_stride=None,
                   stream=None) -> None:
     """Rows of K and V into the slots of the 4-bit cache. The row strides are
     the tensors' own; they are given only with plain addresses."""
-    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
-    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    dev = _device()
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride, dev)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride, dev)
     _check("spc_kv4_store", lib().spc_kv4_store(
-        k, v, k_stride, v_stride, _dev("slot_map", slot_map, _I32, T),
-        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD), T, n_kv, d, num_blocks,
-        block_size, _stream(stream)))
+        k, v, k_stride, v_stride, _dev("slot_map", slot_map, _I32, T, dev),
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev), T, n_kv, d, num_blocks,
+        block_size, _raw_stream(stream, dev)))
 
 
 def spc_kv4_load(cache, slot_map, k, v, T, n_kv, d, num_blocks, block_size, k_stride=None, v_stride=None,
                  stream=None) -> None:
     """Rows of the 4-bit cache's slots as bf16 (exact)."""
-    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
-    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    dev = _device()
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride, dev)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride, dev)
     _check("spc_kv4_load", lib().spc_kv4_load(
-        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD),
-        _dev("slot_map", slot_map, _I32, T), k, v, k_stride, v_stride, T, n_kv, d, num_blocks, block_size,
-        _stream(stream)))
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev),
+        _dev("slot_map", slot_map, _I32, T, dev), k, v, k_stride, v_stride, T, n_kv, d, num_blocks, block_size,
+        _raw_stream(stream, dev)))
 
 
 def spc_kv4_decode_attn_workspace_size(B, n_q, n_kv, d, max_blocks, block_size, budget) -> int:
@@ -379,13 +402,14 @@ def spc_kv4_decode_attn(q, cache, block_table, len, selected, B, n_q, n_kv, d, n
     (selected, budget) the positions kept per KV head."""
     if workspace_bytes is None:
         workspace_bytes = _nbytes(workspace)
+    dev = _device()
     _check("spc_kv4_decode_attn", lib().spc_kv4_decode_attn(
-        _dev("q", q, _BF16, B * n_q * d),
-        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD),
-        _dev("block_table", block_table, _I32, B * max_blocks), _dev("len", len, _I32, B),
-        _dev("selected", selected, _I32, B * n_kv * budget), B, n_q, n_kv, d, num_blocks, block_size, max_blocks,
-        budget, float(scale), _dev("out", out, _BF16, B * n_q * d), _dev("workspace", workspace, _BYTES, 0),
-        workspace_bytes, _stream(stream)))
+        _dev("q", q, _BF16, B * n_q * d, dev),
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev),
+        _dev("block_table", block_table, _I32, B * max_blocks, dev), _dev("len", len, _I32, B, dev),
+        _dev("selected", selected, _I32, B * n_kv * budget, dev), B, n_q, n_kv, d, num_blocks, block_size, max_blocks,
+        budget, float(scale), _dev("out", out, _BF16, B * n_q * d, dev), _dev("workspace", workspace, _BYTES, workspace_bytes, dev),
+        workspace_bytes, _raw_stream(stream, dev)))
 
 
 def spc_prompt_attn_workspace_size(T, B, n_q, n_kv, d) -> int:
@@ -398,13 +422,14 @@ def spc_prompt_attn(q, k, v, cu_seqlens, T, B, n_q, n_kv, d, scale, out, workspa
     tensors' own; they are given only with plain addresses."""
     if workspace_bytes is None:
         workspace_bytes = _nbytes(workspace)
-    q, q_stride = _rows("q", q, T, n_q, d, q_stride)
-    k, k_stride = _rows("k", k, T, n_kv, d, k_stride)
-    v, v_stride = _rows("v", v, T, n_kv, d, v_stride)
+    dev = _device()
+    q, q_stride = _rows("q", q, T, n_q, d, q_stride, dev)
+    k, k_stride = _rows("k", k, T, n_kv, d, k_stride, dev)
+    v, v_stride = _rows("v", v, T, n_kv, d, v_stride, dev)
     _check("spc_prompt_attn", lib().spc_prompt_attn(
-        q, k, v, _dev("cu_seqlens", cu_seqlens, _I32, B + 1), T, B, n_q, n_kv, d, q_stride, k_stride, v_stride,
-        float(scale), _dev("out", out, _BF16, T * n_q * d), _dev("workspace", workspace, _BYTES, 0), workspace_bytes,
-        _stream(stream)))
+        q, k, v, _dev("cu_seqlens", cu_seqlens, _I32, B + 1, dev), T, B, n_q, n_kv, d, q_stride, k_stride, v_stride,
+        float(scale), _dev("out", out, _BF16, T * n_q * d, dev),
+        _dev("workspace", workspace, _BYTES, workspace_bytes, dev), workspace_bytes, _raw_stream(stream, dev)))
 
 
 def spc_device_sm_count() -> int:

@@ -142,14 +142,15 @@ def test_binding_refuses_wrong_tensors(lib):
                 dict(k=k.view(4, 1024)), dict(k=k[:, :, ::2]), dict(k_stride=2048), dict(k=k)):
         with pytest.raises(ValueError):
             store(**bad)                                    # (the last one: right shape, but host memory)
+    B._device()
     fused = torch.zeros(4, 20, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="CUDA device"):
+    with pytest.raises(ValueError, match="device"):
         store(k=fused[:, :8])                               # row stride and shape pass, host memory does not
     for name, t, dt, n in (("cache", cache.float(), B._BYTES, 1), ("cache", cache[:1], B._BYTES, cache.numel()),
                            ("slot_map", slots.long(), B._I32, 1), ("slot_map", slots[:3], B._I32, 4),
                            ("block_table", slots.view(2, 2).t(), B._I32, 4), ("slot_map", slots, B._I32, 4)):
         with pytest.raises(ValueError, match=name):
-            B._dev(name, t, dt, n)
+            B._dev(name, t, dt, n, -2)
     with pytest.raises(B.SpcError) as e:
         B.spc_prompt_attn(FAKE, FAKE, FAKE, FAKE, 4, 1, 8, 8, 64, 0.1, FAKE, FAKE, 1 << 20, stream=0)
     assert e.value.status == -2
@@ -162,23 +163,22 @@ def test_row_strides_come_from_the_tensor():
         def __init__(self, shape, strides):
             self.shape, self._s = shape, strides
 
-        def dim(self):
-            return len(self.shape)
-
         def stride(self):
             return self._s
+
+        def get_device(self):
+            return 0
 
         def data_ptr(self):
             return FAKE
 
-    real, B._on_current_device = B._on_current_device, lambda *a: None
-    try:
-        assert B._rows("k", OnDevice((4, 8, 128), (2048, 128, 1)), 4, 8, 128, None) == (FAKE, 2048)
-        assert B._rows("k", OnDevice((4, 1, 128), (512, 7, 1)), 4, 1, 128, None) == (FAKE, 512)
-        assert B._rows("k", OnDevice((1, 2, 128), (3, 128, 1)), 1, 2, 128, None) == (FAKE, 256)
+    B._device()
+    assert B._rows("k", OnDevice((4, 8, 128), (2048, 128, 1)), 4, 8, 128, None, 0) == (FAKE, 2048)
+    assert B._rows("k", OnDevice((4, 1, 128), (512, 7, 1)), 4, 1, 128, None, 0) == (FAKE, 512)
+    assert B._rows("k", OnDevice((1, 2, 128), (3, 128, 1)), 1, 2, 128, None, 0) == (FAKE, 256)
+    for shape, strides, dev in (((4, 8, 128), (128, 512, 1), 0), ((4, 8, 128), (2048, 128, 1), 1),
+                                ((4, 8, 128), (2048, 128, 1), -2)):
         with pytest.raises(ValueError):
-            B._rows("k", OnDevice((4, 8, 128), (128, 512, 1)), 4, 8, 128, None)
-    finally:
-        B._on_current_device = real
-    assert B._rows("k", FAKE, 4, 8, 128, None) == (FAKE, 1024)
-    assert B._rows("k", FAKE, 4, 8, 128, 4096) == (FAKE, 4096)
+            B._rows("k", OnDevice(shape, strides), 4, 8, 128, None, dev)
+    assert B._rows("k", FAKE, 4, 8, 128, None, -2) == (FAKE, 1024)
+    assert B._rows("k", FAKE, 4, 8, 128, 4096, -2) == (FAKE, 4096)
