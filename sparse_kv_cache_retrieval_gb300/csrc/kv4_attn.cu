@@ -44,24 +44,27 @@
 
 namespace spc {
 
-constexpr int kK4Warps = 8;
-constexpr int kK4Threads = 32 * kK4Warps;
-constexpr int kK4Tile = 64;                          // positions a tile
-constexpr int kK4Stages = 2;                         // tiles in a warp's ring
-constexpr int kK4MinRun = 8;                         // tiles a CTA takes at least
+constexpr int kK4Tile = 32;                          // positions a tile
+constexpr int kK4MinRun = 32;                        // tiles a CTA takes at least
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
 constexpr float kK4Headroom = 8.f;
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
-// shared memory
-constexpr uint32_t kK4OffRing = 0;
-constexpr uint32_t kK4OffMerge = kK4OffRing + kK4Warps * kK4Stages * kK4StageBytes;   // [warps][8 heads][kK4Part]
-constexpr uint32_t kK4OffQ = kK4OffMerge + kK4Warps * 8 * kK4Part * 4;                // [4 head tiles][8 k-steps][32 lanes] x 8 bytes
-constexpr uint32_t kK4OffBar = kK4OffQ + 4 * 8 * 32 * 8;
-constexpr uint32_t kK4OffMask = kK4OffBar + kK4Warps * kK4Stages * 8;
-constexpr uint32_t kK4Smem = kK4OffMask + kK4Warps * kK4Stages * 8;
+// The CTA of a kernel for HT head tiles: warps, and tiles in a warp's ring.
+template <int HT>
+struct K4Cfg {
+  static constexpr int kWarps = HT == 1 ? 16 : 8;
+  static constexpr int kStages = HT == 1 ? 2 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  // shared memory
+  static constexpr uint32_t kOffMerge = kWarps * kStages * kK4StageBytes;              // [warps][8 heads][kK4Part]
+  static constexpr uint32_t kOffQ = kOffMerge + kWarps * 8 * kK4Part * 4;              // HT > 1: [HT][8 k-steps][32 lanes] x 8 bytes
+  static constexpr uint32_t kOffBar = kOffQ + (HT > 1 ? HT * 8 * 32 * 8 : 0);
+  static constexpr uint32_t kOffMask = kOffBar + kWarps * kStages * 8;
+  static constexpr uint32_t kSmem = kOffMask + kWarps * kStages * 4;
+};
 
 struct Kv4Args {
   Kv4AttnCall c;
@@ -92,6 +95,19 @@ __device__ __forceinline__ float k4_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 k4_fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)),
+      "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 k4_add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
 // the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
@@ -131,66 +147,71 @@ __device__ __forceinline__ void k4_step(const K4Line& ln, int B, int segs, K4Cur
   }
 }
 
-// Copies tile x into a stage: valid rows only, their bytes announced on the
-// stage's barrier, their positions noted in the stage's mask. One warp.
+// Copies tile x into a stage: valid rows only, completion counted on the
+// stage's barrier (dense: one arrival and the bytes; selected: one arrival a
+// lane when its copies have landed), the valid rows noted in *mask. One warp.
 __device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Line& ln, const K4Cursor& x, uint8_t* stage,
-                                         uint64_t* bar, uint2* mask) {
+                                         uint64_t* bar, uint32_t* mask) {
   const Kv4AttnCall& c = a.c;
   const int lane = threadIdx.x & 31, g = x.s / a.hsplit;
-  const int bs = 1 << c.block_shift;
+  const int bs = 1 << c.block_shift, p0 = x.i * kK4Tile;
   const int32_t* table = c.table + (size_t)x.b * c.max_blocks;
-  uint32_t m[2] = {0u, 0u};
   if (c.selected == nullptr) {
-    const int p0 = x.i * kK4Tile, n = min(kK4Tile, ln.len[x.b] - p0);      // rows of the tile
-    const int span = min(bs, kK4Tile), pages = kK4Tile / span;             // pages of `span` rows
-    // lane i < pages: page i of the tile
-    int rows = 0;
-    const uint8_t* src = nullptr;
-    if (lane < pages && lane * span < n) {
-      const int p = p0 + lane * span, blk = __ldg(table + (p >> c.block_shift));
-      if (blk >= 0 && blk < c.num_blocks) {
-        rows = min(span, n - lane * span);
-        src = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
+    const int n = min(kK4Tile, ln.len[x.b] - p0);                          // rows of the tile
+    if (bs >= kK4Tile) {
+      // inside one block
+      const int blk = __ldg(table + (p0 >> c.block_shift));
+      const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
+      if (lane == 0) {
+        *mask = ok ? 0xffffffffu >> (32 - n) : 0u;
+        mbar_arrive_expect_tx(bar, ok ? (uint32_t)n * kKv4Rec : 0u);
+        if (ok)
+          bulk_g2s(stage, c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p0 & (bs - 1))) * kKv4Rec,
+                   (uint32_t)n * kKv4Rec, bar);
       }
+    } else {
+      // two blocks of 16, a lane each
+      int rows = 0;
+      const uint8_t* src = nullptr;
+      if (lane < 2 && lane * 16 < n) {
+        const int blk = __ldg(table + (p0 >> 4) + lane);
+        if ((unsigned)blk < (unsigned)c.num_blocks) {
+          rows = min(16, n - lane * 16);
+          src = c.cache + (((size_t)blk * c.n_kv + g) << 4) * kKv4Rec;
+        }
+      }
+      const uint32_t m = __reduce_or_sync(0xffffffffu, ((1u << rows) - 1) << (16 * (lane & 1)));
+      if (lane == 0) {
+        *mask = m;
+        mbar_arrive_expect_tx(bar, (uint32_t)__popc(m) * kKv4Rec);
+      }
+      __syncwarp();
+      if (rows > 0) bulk_g2s(stage + lane * 16 * kKv4Rec, src, (uint32_t)rows * kKv4Rec, bar);
     }
-    if (rows > 0) {
-      const uint64_t bits = (rows == 64 ? ~0ull : (1ull << rows) - 1) << (lane * span);
-      m[0] = (uint32_t)bits;
-      m[1] = (uint32_t)(bits >> 32);
-    }
-    const uint32_t m0 = __reduce_or_sync(0xffffffffu, m[0]), m1 = __reduce_or_sync(0xffffffffu, m[1]);
-    if (lane == 0) {
-      *mask = make_uint2(m0, m1);
-      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(m0) + __popc(m1)) * kKv4Rec);
-    }
-    __syncwarp();
-    if (rows > 0) bulk_g2s(stage + (uint32_t)(lane * span) * kKv4Rec, src, (uint32_t)rows * kKv4Rec, bar);
   } else {
-    const int32_t* sel = c.selected + ((size_t)x.b * c.n_kv + g) * c.budget + x.i * kK4Tile;
-    const uint8_t* src[2] = {nullptr, nullptr};
+    // one record a lane; its nine 16-byte words are dealt to the lanes in
+    // order, so that a warp's copies cover whole records
+    const int p = p0 + lane < c.budget ? __ldg(c.selected + ((size_t)x.b * c.n_kv + g) * c.budget + p0 + lane) : -1;
+    const uint8_t* src = nullptr;
+    if (p >= 0 && p < ln.len[x.b]) {
+      const int blk = __ldg(table + (p >> c.block_shift));
+      if ((unsigned)blk < (unsigned)c.num_blocks)
+        src = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
+    if (lane == 0) *mask = m;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = 32 * e + lane;
-      const int p = x.i * kK4Tile + j < c.budget ? __ldg(sel + j) : -1;
-      if (p >= 0 && p < ln.len[x.b]) {
-        const int blk = __ldg(table + (p >> c.block_shift));
-        if (blk >= 0 && blk < c.num_blocks)
-          src[e] = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
-      }
-      m[e] = __ballot_sync(0xffffffffu, src[e] != nullptr);
+    for (int k = 0; k < kKv4Rec / 16; ++k) {
+      const int w = 32 * k + lane, r = w / 9, part = w - 9 * r;
+      const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), r));
+      if (s) cp_async16(stage + 16 * w, s + 16 * part, 16);
     }
-    if (lane == 0) {
-      *mask = make_uint2(m[0], m[1]);
-      mbar_arrive_expect_tx(bar, (uint32_t)(__popc(m[0]) + __popc(m[1])) * kKv4Rec);
-    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
     __syncwarp();
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (src[e]) bulk_g2s(stage + (uint32_t)(32 * e + lane) * kKv4Rec, src[e], kKv4Rec, bar);
   }
 }
 
-// The 32 positions [32 sb, +32) of a stage: logits, weights, sums.
+// The 32 positions of a stage: logits, weights, sums.
 // FULL: every position of the step counts.
 template <int HT, bool FULL>
 __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, const uint2* sq, const uint32_t (&qr)[16],
@@ -246,10 +267,12 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[n][t][e] *= f[n][e & 1];
         if (!FULL && !((valid >> (rk + 16 * (e >> 1) + t)) & 1u)) s[n][t][e] = -INFINITY;
         mx[e & 1] = fmaxf(mx[e & 1], s[n][t][e]);
       }
+    // logits in base 2; f > 0, so the maximum may be scaled alone
+    mx[0] *= f[n][0];
+    mx[1] *= f[n][1];
     const bool up = mx[0] > m[n][0] + kK4Headroom || mx[1] > m[n][1] + kK4Headroom;
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -268,17 +291,22 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
         }
       }
     }
-    const float ms[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
+    const float2 nm = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0], m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+    const float2 ff = make_float2(f[n][0], f[n][1]);
+    float2 ls = make_float2(l[n][0], l[n][1]);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][t][e] = k4_ex2(s[n][t][e] - ms[e & 1]);
-        l[n][e & 1] += s[n][t][e];
+      for (int e = 0; e < 2; ++e) {
+        float2 x = k4_fma2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), ff, nm);
+        x.x = k4_ex2(x.x);
+        x.y = k4_ex2(x.y);
+        ls = k4_add2(ls, x);
+        p[n][t][e] = movmatrix(pack_f16(x.x, x.y));
       }
-      p[n][t][0] = movmatrix(pack_f16(s[n][t][0], s[n][t][1]));
-      p[n][t][1] = movmatrix(pack_f16(s[n][t][2], s[n][t][3]));
     }
+    l[n][0] = ls.x;
+    l[n][1] = ls.y;
   }
   const int rv0 = 2 * tig, rv1 = 8 + ((2 * tig + 4) & 7);
 #pragma unroll
@@ -315,21 +343,23 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
 }
 
 template <int HT>
-__global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
+__global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Args a) {
+  using Cfg = K4Cfg<HT>;
+  constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages;
   extern __shared__ __align__(128) uint8_t k4_smem[];
   __shared__ K4Line ln;
   __shared__ int s_last;
   const Kv4AttnCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int G = c.n_q / c.n_kv, segs = c.n_kv * a.hsplit, heads = min(8 * HT, G);
-  uint8_t* ring = k4_smem + kK4OffRing + (uint32_t)warp * kK4Stages * kK4StageBytes;
-  float* mrg = reinterpret_cast<float*>(k4_smem + kK4OffMerge);
-  uint2* sq = reinterpret_cast<uint2*>(k4_smem + kK4OffQ);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(k4_smem + kK4OffBar) + warp * kK4Stages;
-  uint2* masks = reinterpret_cast<uint2*>(k4_smem + kK4OffMask) + warp * kK4Stages;
+  uint8_t* ring = k4_smem + (uint32_t)warp * kStages * kK4StageBytes;
+  float* mrg = reinterpret_cast<float*>(k4_smem + Cfg::kOffMerge);
+  uint2* sq = reinterpret_cast<uint2*>(k4_smem + Cfg::kOffQ);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(k4_smem + Cfg::kOffBar) + warp * kStages;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(k4_smem + Cfg::kOffMask) + warp * kStages;
 
   if (lane == 0) {
-    for (int s = 0; s < kK4Stages; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], c.selected ? 32 : 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
   for (int b = 0; b < c.B; ++b) {
     if (ln.nt[b] != 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
-    for (int i = blockIdx.x * kK4Threads + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * kK4Threads)
+    for (int i = blockIdx.x * Cfg::kThreads + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * Cfg::kThreads)
       dst[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 
@@ -369,9 +399,9 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
   int n_issued = 0;
   if (t0 + warp < t1) {
 #pragma unroll 1
-    for (; n_issued < kK4Stages && nx.t < t1; ++n_issued) {
+    for (; n_issued < kStages && nx.t < t1; ++n_issued) {
       k4_issue(a, ln, nx, ring + n_issued * kK4StageBytes, &bars[n_issued], &masks[n_issued]);
-      k4_step(ln, c.B, segs, nx, kK4Warps);
+      k4_step(ln, c.B, segs, nx, kWarps);
     }
   }
 
@@ -438,11 +468,11 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
         for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
     }
     // this warp's tiles of the piece
-    const int k0 = (pt - t0 + kK4Warps - 1 - warp) / kK4Warps;
+    const int k0 = (pt - t0 + kWarps - 1 - warp) / kWarps;
 #pragma unroll 1
-    for (int t = t0 + warp + k0 * kK4Warps; t < pe; t += kK4Warps) {
-      const int st = n_wait % kK4Stages;
-      if (!dead && !mbar_wait_bounded(&bars[st], (n_wait / kK4Stages) & 1, kK4WaitLimit)) {
+    for (int t = t0 + warp + k0 * kWarps; t < pe; t += kWarps) {
+      const int st = n_wait % kStages;
+      if (!dead && !mbar_wait_bounded(&bars[st], (n_wait / kStages) & 1, kK4WaitLimit)) {
         set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
@@ -450,20 +480,16 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
       if (dead) continue;                            // its barriers are still reached; nothing more is copied
       ++n_wait;
       const uint8_t* rows = ring + st * kK4StageBytes;
-      const uint2 mk = masks[st];
-#pragma unroll 1
-      for (int sb = 0; sb < 2; ++sb) {
-        const uint32_t valid = sb ? mk.y : mk.x;
-        if (valid == 0xffffffffu)
-          k4_step32<HT, true>(rows + sb * 32 * kKv4Rec, valid, sq, qr, f, m, l, o);
-        else if (valid != 0)
-          k4_step32<HT, false>(rows + sb * 32 * kKv4Rec, valid, sq, qr, f, m, l, o);
-      }
+      const uint32_t valid = masks[st];
+      if (valid == 0xffffffffu)
+        k4_step32<HT, true>(rows, valid, sq, qr, f, m, l, o);
+      else if (valid != 0)
+        k4_step32<HT, false>(rows, valid, sq, qr, f, m, l, o);
       __syncwarp();
       if (nx.t < t1) {
         k4_issue(a, ln, nx, ring + st * kK4StageBytes, &bars[st], &masks[st]);
         ++n_issued;
-        k4_step(ln, c.B, segs, nx, kK4Warps);
+        k4_step(ln, c.B, segs, nx, kWarps);
       }
     }
 
@@ -500,15 +526,15 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
         }
       }
       __syncthreads();
-      const int h = 8 * n + warp;                    // warp w merges head w of the eight
-      if (h < heads) {
+      const int h = 8 * n + warp;                    // warp w < 8 merges head w of the eight
+      if (warp < 8 && h < heads) {
         float M = -INFINITY;
-        for (int w = 0; w < kK4Warps; ++w) M = fmaxf(M, mrg[(w * 8 + warp) * kK4Part]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * 8 + warp) * kK4Part]);
         const float Ms = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kK4Warps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           const float* src = mrg + (size_t)(w * 8 + warp) * kK4Part;
           const float wt = k4_ex2(src[0] - Ms);
           const float4 x = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
@@ -537,19 +563,34 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
       __syncthreads();
       if (s_last) {
         __threadfence();
-        for (int h = warp; h < heads; h += kK4Warps) {
-          float M = -INFINITY, L = 0.f;
+        // a lane reads one piece's (m, l); then the pieces' O, several in flight
+        const int np = w1 - w0 + 1;
+        for (int h = warp; h < heads; h += kWarps) {
+          auto piece = [&](int i) {
+            const int w = w0 + i;
+            return a.part + (((size_t)w * 2 + (s0 > w * run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
+          };
+          float M = -INFINITY;
+          for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(piece(i)));
+          M = warp_max(M);
+          const float Ms = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = w0; w <= w1; ++w) {
-            const float* p = a.part + (((size_t)w * 2 + (s0 > w * run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
-            const float M2 = fmaxf(M, ml.x), Ms = M2 == -INFINITY ? 0.f : M2;
-            const float wa = k4_ex2(M - Ms), wb = k4_ex2(ml.x - Ms);
-            L = L * wa + ml.y * wb;
-            v.x = v.x * wa + x.x * wb; v.y = v.y * wa + x.y * wb;
-            v.z = v.z * wa + x.z * wb; v.w = v.w * wa + x.w * wb;
-            M = M2;
+          for (int i0 = 0; i0 < np; i0 += 32) {
+            float wt = 0.f, lt = 0.f;
+            if (i0 + lane < np) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane)));
+              wt = k4_ex2(ml.x - Ms);
+              lt = wt * ml.y;
+            }
+            L += warp_sum(lt);
+            const int ne = min(32, np - i0);
+#pragma unroll 8
+            for (int i = 0; i < ne; ++i) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 4) + lane);
+              const float w = __shfl_sync(0xffffffffu, wt, i);
+              v.x += w * x.x; v.y += w * x.y; v.z += w * x.z; v.w += w * x.w;
+            }
           }
           const float r = L == 0.f ? 0.f : 1.f / L;
           *reinterpret_cast<uint2*>(c.out + ((size_t)b * c.n_q + h0 + h) * kD + 4 * lane) =
@@ -563,7 +604,7 @@ __global__ void __launch_bounds__(kK4Threads, 1) kv4_attn_kernel(Kv4Args a) {
     pt = pe;
   }
   // copies that nobody waited for (a wait gave up) land before the CTA ends
-  for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&bars[n_wait % kK4Stages], (n_wait / kK4Stages) & 1, kK4WaitLimit);
+  for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&bars[n_wait % kStages], (n_wait / kStages) & 1, kK4WaitLimit);
 }
 
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
@@ -576,9 +617,9 @@ size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int) {
 
 template <int HT>
 static int k4_run(const Kv4Args& a, void* stream) {
-  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kK4Smem);
+  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K4Cfg<HT>::kSmem);
   if (e != cudaSuccess) return SPC_ERR_CUDA;
-  kv4_attn_kernel<HT><<<kK4Ctas, kK4Threads, kK4Smem, static_cast<cudaStream_t>(stream)>>>(a);
+  kv4_attn_kernel<HT><<<kK4Ctas, K4Cfg<HT>::kThreads, K4Cfg<HT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
