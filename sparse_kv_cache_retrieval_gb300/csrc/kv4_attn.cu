@@ -69,7 +69,7 @@ struct K4Cfg {
 struct Kv4Args {
   Kv4AttnCall c;
   int ht;            // head tiles (8 heads) a segment
-  int hsplit;        // segments a KV head's group is split into
+  int hshift;        // log2 of the segments a KV head's group is split into
   int* status;
   uint32_t* counters;
   float* part;
@@ -117,50 +117,74 @@ struct K4Line {
   int len[SPC_MAX_BATCH];
 };
 
-// a tile of the line: segment (b, s) with s = g * hsplit + hh, tile i of it
+// a tile of the line: tile i of segment (b, s), s = (g << hshift) + hh, with what
+// its copy needs of the segment
 struct K4Cursor {
-  int t, b, s, i;
+  int t, i, b, s;
+  int nt, len;                 // the segment's tiles, the request's context
+  const int32_t* table;        // the request's table row
+  int e;                       // this lane's entry of tile i, fetched a tile ahead of its use
 };
-__device__ __forceinline__ K4Cursor k4_at(const K4Line& ln, int B, int t) {
-  int lo = 0, hi = B;          // pre[lo] <= t < pre[hi]; requests without tiles are passed over
+__device__ __forceinline__ void k4_seg(const Kv4AttnCall& c, const K4Line& ln, K4Cursor& x) {
+  const int b = min(x.b, c.B - 1);
+  x.nt = max(1, ln.nt[b]);
+  x.len = ln.len[b];
+  x.table = c.table + (size_t)b * c.max_blocks;
+}
+// dense: the table entry of the lane's block in the tile; selected: the lane's position
+__device__ __forceinline__ void k4_fetch(const Kv4Args& a, K4Cursor& x) {
+  const Kv4AttnCall& c = a.c;
+  const int lane = threadIdx.x & 31, p0 = x.i * kK4Tile;
+  if (c.selected) {
+    x.e = p0 + lane < c.budget
+              ? __ldg(c.selected + ((size_t)min(x.b, c.B - 1) * c.n_kv + (x.s >> a.hshift)) * c.budget + p0 + lane) : -1;
+  } else {
+    const int p = p0 + 16 * (lane & 1);
+    x.e = p < x.len ? __ldg(x.table + (p >> c.block_shift)) : -1;
+  }
+}
+__device__ __forceinline__ K4Cursor k4_at(const Kv4AttnCall& c, const K4Line& ln, int t) {
+  int lo = 0, hi = c.B;        // pre[lo] <= t < pre[hi]; requests without tiles are passed over
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (ln.pre[mid] <= t) lo = mid; else hi = mid;
   }
-  const int r = t - ln.pre[lo], nt = max(1, ln.nt[lo]);
   K4Cursor x;
   x.t = t;
   x.b = lo;
-  x.s = r / nt;
-  x.i = r - x.s * nt;
+  k4_seg(c, ln, x);
+  const int r = t - ln.pre[lo];
+  x.s = r / x.nt;
+  x.i = r - x.s * x.nt;
   return x;
 }
-__device__ __forceinline__ void k4_step(const K4Line& ln, int B, int segs, K4Cursor& x, int n) {
+__device__ __forceinline__ void k4_step(const Kv4AttnCall& c, const K4Line& ln, int segs, K4Cursor& x, int n) {
   x.t += n;
   x.i += n;
-  while (x.b < B && x.i >= ln.nt[x.b]) {
+  if (x.i < x.nt) return;
+  while (x.b < c.B && x.i >= ln.nt[x.b]) {
     x.i -= ln.nt[x.b];
     if (++x.s == segs) {
       x.s = 0;
-      do ++x.b; while (x.b < B && ln.nt[x.b] == 0);
+      do ++x.b; while (x.b < c.B && ln.nt[x.b] == 0);
     }
   }
+  k4_seg(c, ln, x);
 }
 
 // Copies tile x into a stage: valid rows only, completion counted on the
 // stage's barrier (dense: one arrival and the bytes; selected: one arrival a
 // lane when its copies have landed), the valid rows noted in *mask. One warp.
-__device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Line& ln, const K4Cursor& x, uint8_t* stage,
-                                         uint64_t* bar, uint32_t* mask) {
+__device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Cursor& x, uint8_t* stage, uint64_t* bar,
+                                         uint32_t* mask) {
   const Kv4AttnCall& c = a.c;
-  const int lane = threadIdx.x & 31, g = x.s / a.hsplit;
+  const int lane = threadIdx.x & 31, g = x.s >> a.hshift;
   const int bs = 1 << c.block_shift, p0 = x.i * kK4Tile;
-  const int32_t* table = c.table + (size_t)x.b * c.max_blocks;
   if (c.selected == nullptr) {
-    const int n = min(kK4Tile, ln.len[x.b] - p0);                          // rows of the tile
+    const int n = min(kK4Tile, x.len - p0);                          // rows of the tile
     if (bs >= kK4Tile) {
       // inside one block
-      const int blk = __ldg(table + (p0 >> c.block_shift));
+      const int blk = x.e;
       const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
       if (lane == 0) {
         *mask = ok ? 0xffffffffu >> (32 - n) : 0u;
@@ -174,7 +198,7 @@ __device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Line& ln, con
       int rows = 0;
       const uint8_t* src = nullptr;
       if (lane < 2 && lane * 16 < n) {
-        const int blk = __ldg(table + (p0 >> 4) + lane);
+        const int blk = x.e;
         if ((unsigned)blk < (unsigned)c.num_blocks) {
           rows = min(16, n - lane * 16);
           src = c.cache + (((size_t)blk * c.n_kv + g) << 4) * kKv4Rec;
@@ -191,10 +215,10 @@ __device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Line& ln, con
   } else {
     // one record a lane; its nine 16-byte words are dealt to the lanes in
     // order, so that a warp's copies cover whole records
-    const int p = p0 + lane < c.budget ? __ldg(c.selected + ((size_t)x.b * c.n_kv + g) * c.budget + p0 + lane) : -1;
+    const int p = x.e;
     const uint8_t* src = nullptr;
-    if (p >= 0 && p < ln.len[x.b]) {
-      const int blk = __ldg(table + (p >> c.block_shift));
+    if (p >= 0 && p < x.len) {
+      const int blk = __ldg(x.table + (p >> c.block_shift));
       if ((unsigned)blk < (unsigned)c.num_blocks)
         src = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
     }
@@ -351,7 +375,7 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
   __shared__ int s_last;
   const Kv4AttnCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const int G = c.n_q / c.n_kv, segs = c.n_kv * a.hsplit, heads = min(8 * HT, G);
+  const int G = c.n_q / c.n_kv, segs = c.n_kv << a.hshift, heads = min(8 * HT, G);
   uint8_t* ring = k4_smem + (uint32_t)warp * kStages * kK4StageBytes;
   float* mrg = reinterpret_cast<float*>(k4_smem + Cfg::kOffMerge);
   uint2* sq = reinterpret_cast<uint2*>(k4_smem + Cfg::kOffQ);
@@ -395,21 +419,23 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
 
   bool dead = false;
   int n_wait = 0;                                    // tiles this warp has waited for
-  K4Cursor nx = k4_at(ln, c.B, t0 + warp);           // next tile to copy
+  K4Cursor nx = k4_at(c, ln, t0 + warp);           // next tile to copy
+  if (nx.t < t1) k4_fetch(a, nx);
   int n_issued = 0;
   if (t0 + warp < t1) {
 #pragma unroll 1
     for (; n_issued < kStages && nx.t < t1; ++n_issued) {
-      k4_issue(a, ln, nx, ring + n_issued * kK4StageBytes, &bars[n_issued], &masks[n_issued]);
-      k4_step(ln, c.B, segs, nx, kWarps);
+      k4_issue(a, nx, ring + n_issued * kK4StageBytes, &bars[n_issued], &masks[n_issued]);
+      k4_step(c, ln, segs, nx, kWarps);
+      if (nx.t < t1) k4_fetch(a, nx);
     }
   }
 
-  K4Cursor pc = k4_at(ln, c.B, min(t0, max(total - 1, 0)));   // the piece at hand
+  K4Cursor pc = k4_at(c, ln, min(t0, max(total - 1, 0)));   // the piece at hand
   for (int pt = t0; pt < t1;) {
-    const int b = pc.b, sg = pc.s, nt = ln.nt[b];
+    const int b = pc.b, sg = pc.s, nt = pc.nt;
     const int pe = min(t1, pt + nt - pc.i);          // end of this CTA's piece of the segment
-    const int g = sg / a.hsplit, hh = sg - g * a.hsplit;
+    const int g = sg >> a.hshift, hh = sg - (g << a.hshift);
     const int h0 = g * G + hh * 8 * HT;              // first query head
     // ---- queries: per head a power of two that brings the largest value below 2
     uint32_t qr[16];
@@ -487,9 +513,10 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
         k4_step32<HT, false>(rows, valid, sq, qr, f, m, l, o);
       __syncwarp();
       if (nx.t < t1) {
-        k4_issue(a, ln, nx, ring + st * kK4StageBytes, &bars[st], &masks[st]);
+        k4_issue(a, nx, ring + st * kK4StageBytes, &bars[st], &masks[st]);
         ++n_issued;
-        k4_step(ln, c.B, segs, nx, kWarps);
+        k4_step(c, ln, segs, nx, kWarps);
+        if (nx.t < t1) k4_fetch(a, nx);
       }
     }
 
@@ -600,7 +627,7 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
       }
       __syncthreads();
     }
-    k4_step(ln, c.B, segs, pc, pe - pt);
+    k4_step(c, ln, segs, pc, pe - pt);
     pt = pe;
   }
   // copies that nobody waited for (a wait gave up) land before the CTA ends
@@ -628,11 +655,11 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   Kv4Args a{};
   a.c = c;
   a.ht = k4_head_tiles(G);
-  a.hsplit = G > 32 ? G / 32 : 1;
+  a.hshift = G > 32 ? 1 : 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
-  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * c.n_kv * a.hsplit * 4));
+  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * 4));
   switch (a.ht) {
     case 1: return k4_run<1>(a, stream);
     case 2: return k4_run<2>(a, stream);
