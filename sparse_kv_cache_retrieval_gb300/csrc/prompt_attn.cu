@@ -1,50 +1,524 @@
-// Causal attention over packed prompts: one warp a (row, query head), one key
-// at a time, four values of a row a lane.
+// Causal attention over whole packed prompts on the 5th-generation tensor
+// cores: out_i = sum_{j <= i} softmax_j(scale q_i.k_j) v_j within a sequence.
+//
+// Rows are (token, query head of the group) pairs: a 128-row tile holds 128/G
+// tokens x G heads of one KV head, so that every group size fills the tile,
+// its causal edge is only 128/G tokens wide and K and V are read once for the
+// whole group. A work item is two such tiles (A and B, consecutive tokens) of
+// one (sequence, KV head) against that head's keys in blocks of 128:
+//   S[128][128] = Q K^T     Q, K in shared memory (TMA, 128-byte swizzle)
+//   O[128][128] += P V      P in tensor memory over S's columns, V MN-major
+// The tensor cores work on one tile while the other one's softmax runs: the
+// issue order is S_A S_B, then PV_A(j) S_A(j+1) PV_B(j) S_B(j+1), ...; the
+// tensor pipe executes one thread's MMAs in order, so S(j+1) does not
+// overwrite P(j) before PV(j) has read it.
+// Softmax: one thread a row (no exchange between threads), in base 2. The
+// running maximum is raised only when a logit passes it by more than 8 (P stays
+// below 2^8), and only then is the row of O rescaled. P is rounded to bf16
+// (2^-9 on average less: its errors are independent), its sum is that of the
+// fp32 values; S, O, maximum and sum are fp32.
+//
+// What a row does not see must not reach it, NaN and infinities included. In S
+// masked columns are replaced. In P V they meet P = 0, which a non-finite V
+// defeats: V rows behind the sequence's end are zeroed in shared memory before
+// they are used, and a row whose sum is finite but whose result is not (a
+// non-finite V in its own sequence, seen or not) is computed again by a warp
+// from global memory over exactly the keys it sees.
+//
+// One CTA per SM, persistent over items ordered by the number of key blocks,
+// longest first, and dealt to the CTAs in a snake:
+//   warps 0-3, 4-7  softmax and epilogue of tile A, B
+//   warp 8          tensor memory, MMA issue (one lane)
+//   warp 9          item schedule, TMA loads (Q per tile, K and V ring)
+// Every wait is bounded: one that gives up records SPC_ERR_TIMEOUT and the
+// roles run to their ends without waiting.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "spc_device.cuh"
 #include "spc_internal.h"
+#include "spc_tc.cuh"
 
 namespace spc {
 
-__global__ void __launch_bounds__(128) prompt_attn_kernel(PromptAttnCall a) {
-  const int lane = threadIdx.x & 31;
-  const long long n = (long long)a.T * a.n_q, warps = (long long)gridDim.x * 4;
-  for (long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); w < n; w += warps) {
-    const int t = (int)(w / a.n_q), h = (int)(w % a.n_q), g = h / (a.n_q / a.n_kv);
-    int first = -1;
-    for (int b = 0; b < a.B; ++b) {
-      const int s = max(0, min(a.cu[b], a.T)), e = max(s, min(a.cu[b + 1], a.T));
-      if (t >= s && t < e) first = s;
+constexpr int kPaKeys = 128;                          // keys a block
+constexpr uint32_t kPaTile = 128 * kRowBytes;         // 32 KiB: a Q, K or V tile
+constexpr uint32_t kPaBlock = kPaTile / 2;            // its 64-value half
+constexpr int kPaSlots = 4;                           // K/V ring
+constexpr int kPaItems = 2;                           // item ring
+constexpr int kPaSoftWarps = 8;
+constexpr int kPaWarpMma = 8, kPaWarpTma = 9;
+constexpr int kPaThreads = 384;                       // warps 10, 11 fill the third warpgroup
+// registers a thread: 168 at launch (384 threads); the softmax warpgroups take
+// 208, the third keeps 88 (2 * 208 + 88 = 3 * 168)
+constexpr int kPaRegSoft = 208, kPaRegRest = 88;
+constexpr int kPaCtas = 152;
+constexpr float kPaHeadroom = 8.f;
+constexpr long long kPaWait = 4000000000ll;           // clock cycles
+constexpr int kPaTmemCols = 512;                      // S_A, S_B, O_A, O_B
+constexpr uint32_t kPaColO = 256;
+constexpr uint32_t kPaIdescS = umma_idesc_bf16(128, kPaKeys, false);
+constexpr uint32_t kPaIdescO = umma_idesc_bf16(128, kD, true);
+
+// shared memory, from a 1024-byte aligned base
+constexpr uint32_t kPaOffQ = 0;                                       // [2] tiles
+constexpr uint32_t kPaOffKv = kPaOffQ + 2 * kPaTile;
+constexpr uint32_t kPaOffItem = kPaOffKv + kPaSlots * kPaTile;        // [kPaItems] PaItem
+constexpr uint32_t kPaOffBar = kPaOffItem + kPaItems * 32;
+constexpr int kPaBars = 2 * kPaSlots + 2 * kPaItems + 2 * 6;
+constexpr size_t kPaSmem = 1024 + kPaOffBar + kPaBars * 8 + 16;
+
+struct PaArgs {
+  PromptAttnCall c;
+  int G, gshift, tpm;      // heads a group, its log2, tokens a tile
+  int* status;
+};
+
+struct PaItem {
+  int start, len;          // the sequence's first row and length; len < 0: no more items
+  int g, t0;               // KV head, first token (in the sequence) of tile A
+  int nA, nB;              // key blocks of the tiles
+};
+
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kPaWait));
+}
+__device__ __forceinline__ float pa_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void pa_tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+
+// One row by one warp, from global memory, over the keys it sees: the result
+// of lane l is dims 4l .. 4l + 3.
+__device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g) {
+  const PromptAttnCall& c = a.c;
+  const int lane = threadIdx.x & 31, t = start + qpos;
+  const uint2 qw = *reinterpret_cast<const uint2*>(c.q + t * c.q_stride + (size_t)h * kD + 4 * lane);
+  const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
+  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+  for (int j = start; j <= t; ++j) {
+    const uint2 k = *reinterpret_cast<const uint2*>(c.k + j * c.k_stride + (size_t)g * kD + 4 * lane);
+    const uint2 v = *reinterpret_cast<const uint2*>(c.v + j * c.v_stride + (size_t)g * kD + 4 * lane);
+    const float x = c.scale2 * warp_sum(q0 * bf_lo(k.x) + q1 * bf_hi(k.x) + q2 * bf_lo(k.y) + q3 * bf_hi(k.y));
+    const float M = fmaxf(m, x);
+    const float e0 = m == -INFINITY ? 0.f : exp2f(m - M), e = exp2f(x - M);
+    l = l * e0 + e;
+    o0 = o0 * e0 + e * bf_lo(v.x);
+    o1 = o1 * e0 + e * bf_hi(v.x);
+    o2 = o2 * e0 + e * bf_lo(v.y);
+    o3 = o3 * e0 + e * bf_hi(v.y);
+    m = M;
+  }
+  const float r = 1.f / l;
+  *reinterpret_cast<uint2*>(c.out + ((size_t)t * c.n_q + h) * kD + 4 * lane) =
+      make_uint2(pack_bf16(o0 * r, o1 * r), pack_bf16(o2 * r, o3 * r));
+}
+
+__global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                    const __grid_constant__ CUtensorMap kmap,
+                                                                    const __grid_constant__ CUtensorMap vmap,
+                                                                    const PaArgs a) {
+  extern __shared__ uint8_t pa_raw[];
+  const uint32_t raw_addr = smem_u32(pa_raw);
+  uint8_t* base = pa_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  volatile PaItem* items = reinterpret_cast<volatile PaItem*>(base + kPaOffItem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kPaOffBar);
+  uint64_t* kvfull = bars;                    // [kPaSlots] TMA bytes
+  uint64_t* kvfree = kvfull + kPaSlots;       // [kPaSlots] commit after the last MMA that reads the slot
+  uint64_t* ifull = kvfree + kPaSlots;        // [kPaItems] item written
+  uint64_t* ifree = ifull + kPaItems;         // [kPaItems] MMA warp and 8 softmax warps have read it
+  uint64_t* qfull = ifree + kPaItems;         // [2] TMA bytes
+  uint64_t* qfree = qfull + 2;                // [2] commit after the tile's last S
+  uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
+  uint64_t* pfull = sfull + 2;                // [2] 4 warp arrivals: P written, O rescaled
+  uint64_t* pvdone = pfull + 2;               // [2] commit: PV of a block done
+  uint64_t* ofull = pvdone + 2;               // [2] commit: the item's last PV done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofull + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPaSlots; ++s) {
+      mbar_init(&kvfull[s], 1);
+      mbar_init(&kvfree[s], 1);
     }
-    if (first < 0) continue;
-    const uint2 qw = *reinterpret_cast<const uint2*>(a.q + t * a.q_stride + (size_t)h * kD + 4 * lane);
-    const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
-    float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-    for (int j = first; j <= t; ++j) {
-      const uint2 k = *reinterpret_cast<const uint2*>(a.k + j * a.k_stride + (size_t)g * kD + 4 * lane);
-      const uint2 v = *reinterpret_cast<const uint2*>(a.v + j * a.v_stride + (size_t)g * kD + 4 * lane);
-      const float x = a.scale2 * warp_sum(q0 * bf_lo(k.x) + q1 * bf_hi(k.x) + q2 * bf_lo(k.y) + q3 * bf_hi(k.y));
-      const float M = fmaxf(m, x);
-      const float c = m == -INFINITY ? 0.f : exp2f(m - M), e = exp2f(x - M);
-      l = l * c + e;
-      o0 = o0 * c + e * bf_lo(v.x);
-      o1 = o1 * c + e * bf_hi(v.x);
-      o2 = o2 * c + e * bf_lo(v.y);
-      o3 = o3 * c + e * bf_hi(v.y);
-      m = M;
+    for (int s = 0; s < kPaItems; ++s) {
+      mbar_init(&ifull[s], 1);
+      mbar_init(&ifree[s], kPaSoftWarps + 1);
     }
-    const float r = 1.f / l;
-    *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.n_q + h) * kD + 4 * lane) =
-        make_uint2(pack_bf16(o0 * r, o1 * r), pack_bf16(o2 * r, o3 * r));
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qfree[s], 1);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pfull[s], kPaSoftWarps / 2);
+      mbar_init(&pvdone[s], 1);
+      mbar_init(&ofull[s], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kPaWarpMma) tmem_alloc<kPaTmemCols>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t qs = smem_u32(base + kPaOffQ), kvs = smem_u32(base + kPaOffKv);
+  bool dead = false;
+
+  if (warp >= kPaSoftWarps)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPaRegSoft));
+
+  if (warp == kPaWarpTma) {
+    // ================= schedule and loads
+    const PromptAttnCall& c = a.c;
+    int start[2], len[2], nb[2];
+    const int per = 2 * a.tpm;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 32 * e + lane;
+      start[e] = len[e] = 0;
+      if (b < c.B) {
+        start[e] = max(0, min(c.cu[b], c.T));
+        len[e] = max(start[e], min(c.cu[b + 1], c.T)) - start[e];
+      }
+      nb[e] = (len[e] + per - 1) / per;
+    }
+    // items with block index >= q, over n_kv
+    auto at_least = [&](int q) {
+      return (int)__reduce_add_sync(0xffffffffu, (unsigned)(max(0, nb[0] - q) + max(0, nb[1] - q)));
+    };
+    const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(nb[0], nb[1]));
+    const long long n_items = (long long)at_least(0) * c.n_kv;
+    int slot = 0, ns = 0, it = 0, nq[2] = {0, 0};
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !pa_wait(bar, parity)) {
+        if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+        dead = true;
+      }
+    };
+    for (int round = 0;; ++round, ++it) {
+      // snake: even rounds in CTA order, odd ones in reverse
+      const int cta = (round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+      const long long k = (long long)round * gridDim.x + cta;
+      PaItem x;
+      x.len = -1;
+      if (k < n_items && !dead) {
+        const int r0 = (int)(k / c.n_kv), g = (int)(k - (long long)r0 * c.n_kv);
+        int lo = 0, hi = most;                        // at_least(lo) > r0 >= at_least(hi)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at_least(mid) > r0) lo = mid; else hi = mid;
+        }
+        // the (r0 - at_least(lo + 1))-th sequence that has a block lo
+        int r = r0 - at_least(lo + 1);
+        const uint32_t m0 = __ballot_sync(0xffffffffu, nb[0] > lo), m1 = __ballot_sync(0xffffffffu, nb[1] > lo);
+        const int n0 = __popc(m0), e = r >= n0 ? 1 : 0;
+        if (e) r -= n0;
+        const int src = __fns(e ? m1 : m0, 0, r + 1);
+        x.start = __shfl_sync(0xffffffffu, e ? start[1] : start[0], src);
+        x.len = __shfl_sync(0xffffffffu, e ? len[1] : len[0], src);
+        x.g = g;
+        x.t0 = lo * per;
+        x.nA = (min(x.t0 + a.tpm, x.len) + kPaKeys - 1) / kPaKeys;
+        x.nB = x.t0 + a.tpm < x.len ? (min(x.t0 + per, x.len) + kPaKeys - 1) / kPaKeys : 0;
+      }
+      const int is = it % kPaItems;
+      acquire(&ifree[is], ((it / kPaItems) & 1) ^ 1);
+      if (lane == 0) {
+        items[is].start = x.start; items[is].len = x.len; items[is].g = x.g; items[is].t0 = x.t0;
+        items[is].nA = x.nA; items[is].nB = x.nB;
+        mbar_arrive(&ifull[is]);
+      }
+      __syncwarp();
+      if (x.len < 0) break;
+      const int n = max(x.nA, x.nB);
+      auto load_q = [&](int i) {
+        acquire(&qfree[i], (nq[i] & 1) ^ 1);
+        ++nq[i];
+        if (lane == 0 && !dead) {
+          mbar_arrive_expect_tx(&qfull[i], kPaTile);
+          const int row = x.start + x.t0 + i * a.tpm;
+          pa_tma_3d(qs + i * kPaTile, &qmap, 0, x.g << a.gshift, row, &qfull[i]);
+          pa_tma_3d(qs + i * kPaTile + kPaBlock, &qmap, 64, x.g << a.gshift, row, &qfull[i]);
+        }
+      };
+      auto load_kv = [&](const CUtensorMap* map, int j) {
+        acquire(&kvfree[slot], (ns & 1) ^ 1);
+        if (lane == 0 && !dead) {
+          mbar_arrive_expect_tx(&kvfull[slot], kPaTile);
+          pa_tma_3d(kvs + slot * kPaTile, map, 0, x.g, x.start + j * kPaKeys, &kvfull[slot]);
+          pa_tma_3d(kvs + slot * kPaTile + kPaBlock, map, 64, x.g, x.start + j * kPaKeys, &kvfull[slot]);
+        }
+        if (++slot == kPaSlots) { slot = 0; ++ns; }
+      };
+      load_q(0);
+      load_kv(&kmap, 0);
+      if (x.nB) load_q(1);
+      load_kv(&vmap, 0);
+      for (int j = 1; j < n; ++j) {
+        load_kv(&kmap, j);
+        load_kv(&vmap, j);
+      }
+    }
+    // every copy lands before the CTA ends: each slot's last fill has been
+    // waited for by the MMA warp, unless that gave up
+    if (lane == 0 && dead)
+      for (int s = 0; s < kPaSlots; ++s) mbar_wait_bounded(&kvfull[s], 0, kPaWait / 64);
+    __syncwarp();
+  } else if (warp == kPaWarpMma) {
+    // ================= MMA issue
+    if (lane == 0) {
+      auto acquire = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait_bounded(bar, parity, kPaWait)) {
+          set_status(a.status, SPC_ERR_TIMEOUT);
+          dead = true;
+        }
+      };
+      int slot = 0, ns = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      for (int it = 0;; ++it) {
+        const int is = it % kPaItems;
+        acquire(&ifull[is], (it / kPaItems) & 1);
+        if (dead) break;
+        const int nA = items[is].nA, nB = items[is].nB, len = items[is].len;
+        mbar_arrive(&ifree[is]);
+        if (len < 0) break;
+        const int nt[2] = {nA, nB}, n = max(nA, nB);
+        auto next_slot = [&]() { const int s = slot; acquire(&kvfull[s], ns & 1); if (++slot == kPaSlots) { slot = 0; ++ns; } return s; };
+        auto issue_s = [&](int i, int ks, bool last) {
+          if (dead) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * kPaBlock + (uint32_t)(kk & 3) * 32;
+            umma_f16(tmem + i * kPaKeys, umma_desc_sw128(qs + i * kPaTile + off), umma_desc_sw128(kvs + ks * kPaTile + off),
+                     kPaIdescS, kk ? 1u : 0u);
+          }
+          umma_commit(&sfull[i]);
+          if (last) umma_commit(&qfree[i]);
+        };
+        auto issue_pv = [&](int i, int vs, bool first) {
+          acquire(&pfull[i], np[i] & 1);
+          ++np[i];
+          if (dead) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kPaKeys / 16; ++kk)
+            umma_f16_tmem_a(tmem + kPaColO + i * kD, tmem + i * kPaKeys + kk * 8,
+                            umma_desc_sw128_mn(kvs + vs * kPaTile + (uint32_t)kk * 16 * 128, kPaBlock), kPaIdescO,
+                            (first && kk == 0) ? 0u : 1u);
+          umma_commit(&pvdone[i]);
+        };
+        int ks = next_slot();
+        for (int i = 0; i < 2; ++i) {
+          if (nt[i] == 0) continue;
+          acquire(&qfull[i], nq[i] & 1);
+          ++nq[i];
+          issue_s(i, ks, nt[i] == 1);
+        }
+        if (!dead) umma_commit(&kvfree[ks]);
+        for (int j = 0; j < n; ++j) {
+          const int vs = next_slot();
+          if (j + 1 < n) ks = next_slot();
+          for (int i = 0; i < 2; ++i) {
+            if (j >= nt[i]) continue;
+            issue_pv(i, vs, j == 0);
+            if (j + 1 < nt[i]) issue_s(i, ks, j + 2 == nt[i]);
+            else if (!dead) umma_commit(&ofull[i]);
+          }
+          if (!dead) {
+            umma_commit(&kvfree[vs]);
+            if (j + 1 < n) umma_commit(&kvfree[ks]);
+          }
+        }
+      }
+      // tensor memory is released below: wait for the MMAs in flight (the
+      // softmax warps waited for every item's last one, unless something gave up)
+      if (dead) mbar_wait_bounded(&ofull[0], 0, kPaWait / 64);
+    }
+    __syncwarp();
+  } else if (warp < kPaSoftWarps) {
+    // ================= softmax and epilogue of tile i, one row a thread
+    const PromptAttnCall& c = a.c;
+    const int i = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * kPaKeys, to = tmem + lanes + kPaColO + i * kD;
+    int n_s = 0, n_o = 0, slot = 0, ns = 0;
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !pa_wait(bar, parity)) {
+        if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+        dead = true;
+      }
+    };
+    for (int it = 0;; ++it) {
+      const int is = it % kPaItems;
+      acquire(&ifull[is], (it / kPaItems) & 1);
+      if (dead) break;
+      const int start = items[is].start, len = items[is].len, g = items[is].g, nA = items[is].nA, nB = items[is].nB;
+      const int t0 = items[is].t0 + i * a.tpm;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (len < 0) break;
+      const int n = i ? nB : nA, nmax = max(nA, nB);
+      const int qpos = t0 + (row >> a.gshift);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        acquire(&sfull[i], n_s & 1);
+        tc_fence_after();
+        float s[128];
+        if (!dead) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
+          tmem_ld_wait();
+        }
+        const int seen = qpos - j * kPaKeys;          // columns 0 .. seen are visible
+        if ((j + 1) * kPaKeys > t0 + 1) {             // the block reaches behind the tile's first token
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e > seen) s[e] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
+        const float M = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c.scale2;
+        float alpha = 1.f;
+        const bool up = M > m + kPaHeadroom;
+        if (up) {
+          alpha = m == -INFINITY ? 0.f : pa_ex2(m - M);
+          l *= alpha;
+          m = M;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, up)) {
+          // O holds earlier blocks: their PV must be done
+          acquire(&pvdone[i], (n_s - 1) & 1);
+          tc_fence_after();
+          if (!dead) {
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+              float o[16];
+              tmem_ld16(to + 16 * q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha;
+              tmem_st16(to + 16 * q, o);
+            }
+          }
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x0 = pa_ex2(fmaf(s[64 * q + 2 * e], c.scale2, -mm));
+            const float x1 = pa_ex2(fmaf(s[64 * q + 2 * e + 1], c.scale2, -mm));
+            sum[e & 1] += x0;
+            sum[2 + (e & 1)] += x1;
+            p[e] = pack_bf16(x0, x1);
+          }
+          if (!dead) tmem_st32(ts + 32 * q, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if ((j + 1) * kPaKeys > len) {
+          // V rows behind the sequence's end: zeros. K(0), V(0), K(1), ... follow
+          // one another in the ring from this item's first slot on
+          const int v = slot + 2 * j + 1, vs = v % kPaSlots;
+          acquire(&kvfull[vs], (ns + v / kPaSlots) & 1);
+          if (row >= len - j * kPaKeys && !dead) {
+            uint4* r0 = reinterpret_cast<uint4*>(base + kPaOffKv + vs * kPaTile + row * 128);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              r0[e] = make_uint4(0u, 0u, 0u, 0u);
+              r0[e + kPaBlock / 16] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (!dead) tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[i]);
+        ++n_s;
+      }
+      slot += 2 * nmax;
+      ns += slot / kPaSlots;
+      slot %= kPaSlots;
+      if (n == 0) continue;
+      // ---- epilogue
+      acquire(&ofull[i], n_o & 1);
+      ++n_o;
+      tc_fence_after();
+      if (dead) continue;
+      const bool live = qpos < len;
+      const int h = (g << a.gshift) + (row & (a.G - 1));
+      uint16_t* dst = c.out + ((size_t)(start + qpos) * c.n_q + h) * kD;
+      const float r = 1.f / l;
+      bool odd = false;                                // a value that is not finite
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float o[32];
+        tmem_ld32(to + 32 * q, o);
+        tmem_ld_wait();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const float x0 = o[8 * e + 2 * f] * r, x1 = o[8 * e + 2 * f + 1] * r;
+              odd = odd || !(fabsf(x0) < INFINITY) || !(fabsf(x1) < INFINITY);
+              w[f] = pack_bf16(x0, x1);
+            }
+            stg_v4(dst + 32 * q + 8 * e, make_uint4(w[0], w[1], w[2], w[3]));
+          }
+        }
+      }
+      tc_fence_before();
+      uint32_t again = __ballot_sync(0xffffffffu, live && odd && l < INFINITY);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        pa_row_again(a, start, __shfl_sync(0xffffffffu, qpos, src), __shfl_sync(0xffffffffu, h, src), g);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPaWarpMma) {
+    tc_fence_after();
+    tmem_dealloc<kPaTmemCols>(tmem);
   }
 }
 
 size_t prompt_attn_workspace(int, int, int, int) { return 256; }
 
-int prompt_attn_launch(const PromptAttnCall& c, void*, void* stream) {
-  const long long n = ((long long)c.T * c.n_q + 3) / 4;
-  prompt_attn_kernel<<<(int)(n < 152 * 64 ? n : 152 * 64), 128, 0, static_cast<cudaStream_t>(stream)>>>(c);
+int prompt_attn_launch(const PromptAttnCall& c, void* workspace, void* stream) {
+  PaArgs a{};
+  a.c = c;
+  a.G = c.n_q / c.n_kv;
+  while ((1 << a.gshift) < a.G) ++a.gshift;
+  a.tpm = 128 >> a.gshift;
+  a.status = static_cast<int*>(workspace);
+  CUtensorMap qmap, kmap, vmap;
+  auto map = [&](CUtensorMap* m, const void* p, int heads, int64_t stride, uint32_t bh, uint32_t bt) {
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)heads, (uint64_t)c.T};
+    const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, bh, bt};
+    return tensor_map_bf16_sw128(m, p, 3, dims, strides, box);
+  };
+  if (!map(&qmap, c.q, c.n_q, c.q_stride, a.G, a.tpm) || !map(&kmap, c.k, c.n_kv, c.k_stride, 1, kPaKeys) ||
+      !map(&vmap, c.v, c.n_kv, c.v_stride, 1, kPaKeys))
+    return SPC_ERR_CUDA;
+  if (set_func_attr((const void*)prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPaSmem) != cudaSuccess)
+    return SPC_ERR_CUDA;
+  const long long most = ((long long)c.T / (2 * a.tpm) + c.B) * c.n_kv;      // items at most
+  const int grid = (int)(most < kPaCtas ? most : kPaCtas);
+  prompt_attn_kernel<<<grid, kPaThreads, kPaSmem, static_cast<cudaStream_t>(stream)>>>(qmap, kmap, vmap, a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
