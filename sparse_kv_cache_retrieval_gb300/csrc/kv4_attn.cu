@@ -97,19 +97,6 @@ __device__ __forceinline__ float k4_ex2(float x) {
   return y;
 }
 
-// two fp32 operations an instruction
-__device__ __forceinline__ float2 k4_fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-      "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 k4_add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-
 // the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
 struct K4Line {
   int pre[SPC_MAX_BATCH + 1];
@@ -322,10 +309,10 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float2 x = k4_fma2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), ff, nm);
+        float2 x = fma2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), ff, nm);
         x.x = k4_ex2(x.x);
         x.y = k4_ex2(x.y);
-        ls = k4_add2(ls, x);
+        ls = add2(ls, x);
         p[n][t][e] = movmatrix(pack_f16(x.x, x.y));
       }
     }

@@ -168,13 +168,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
   const uint32_t qs = smem_u32(base + kPaOffQ), kvs = smem_u32(base + kPaOffKv);
   bool dead = false;
 
-  if (warp >= kPaSoftWarps)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPaRegSoft));
-
   if (warp == kPaWarpTma) {
     // ================= schedule and loads
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
     const PromptAttnCall& c = a.c;
     int start[2], len[2], nb[2];
     const int per = 2 * a.tpm;
@@ -272,6 +268,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     __syncwarp();
   } else if (warp == kPaWarpMma) {
     // ================= MMA issue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
     if (lane == 0) {
       auto acquire = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait_bounded(bar, parity, kPaWait)) {
@@ -343,6 +340,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     __syncwarp();
   } else if (warp < kPaSoftWarps) {
     // ================= softmax and epilogue of tile i, one row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPaRegSoft));
     const PromptAttnCall& c = a.c;
     const int i = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -409,21 +407,22 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           }
         }
         const float mm = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc = make_float2(c.scale2, c.scale2), nm = make_float2(-mm, -mm);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[32];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x0 = pa_ex2(fmaf(s[64 * q + 2 * e], c.scale2, -mm));
-            const float x1 = pa_ex2(fmaf(s[64 * q + 2 * e + 1], c.scale2, -mm));
-            sum[e & 1] += x0;
-            sum[2 + (e & 1)] += x1;
-            p[e] = pack_bf16(x0, x1);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(make_float2(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), sc, nm);
+            x.x = pa_ex2(x.x);
+            x.y = pa_ex2(x.y);
+            sum[e & 1] = add2(sum[e & 1], x);
+            p[e] = pack_bf16(x.x, x.y);
           }
-          if (!dead) tmem_st32(ts + 32 * q, p);
+          if (!dead) tmem_st16(ts + 16 * q, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         if ((j + 1) * kPaKeys > len) {
           // V rows behind the sequence's end: zeros. K(0), V(0), K(1), ... follow
           // one another in the ring from this item's first slot on
@@ -486,6 +485,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         pa_row_again(a, start, __shfl_sync(0xffffffffu, qpos, src), __shfl_sync(0xffffffffu, h, src), g);
       }
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
   }
   tc_fence_before();
   __syncthreads();
