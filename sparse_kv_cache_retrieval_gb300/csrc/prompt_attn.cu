@@ -30,10 +30,13 @@
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
 //   warp 8          tensor memory, MMA issue (one lane)
 //   warp 9          item schedule, TMA loads (Q per tile, K and V ring)
-// Every wait is bounded: one that gives up records SPC_ERR_TIMEOUT and the
-// roles run to their ends without waiting.
+// Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
+// and leaves, the others' waits then give up in turn; copies land and MMAs
+// complete before the CTA releases its tensor memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "spc_device.cuh"
 #include "spc_internal.h"
@@ -44,7 +47,7 @@ namespace spc {
 constexpr int kPaKeys = 128;                          // keys a block
 constexpr uint32_t kPaTile = 128 * kRowBytes;         // 32 KiB: a Q, K or V tile
 constexpr uint32_t kPaBlock = kPaTile / 2;            // its 64-value half
-constexpr int kPaSlots = 4;                           // K/V ring
+constexpr int kPaStages = 2;                          // ring of (V of a block, K of the next one)
 constexpr int kPaItems = 2;                           // item ring
 constexpr int kPaSoftWarps = 8;
 constexpr int kPaWarpMma = 8, kPaWarpTma = 9;
@@ -63,9 +66,10 @@ constexpr uint32_t kPaIdescO = umma_idesc_bf16(128, kD, true);
 // shared memory, from a 1024-byte aligned base
 constexpr uint32_t kPaOffQ = 0;                                       // [2] tiles
 constexpr uint32_t kPaOffKv = kPaOffQ + 2 * kPaTile;
-constexpr uint32_t kPaOffItem = kPaOffKv + kPaSlots * kPaTile;        // [kPaItems] PaItem
+constexpr uint32_t kPaOffK0 = kPaOffKv + kPaStages * 2 * kPaTile;     // an item's first K
+constexpr uint32_t kPaOffItem = kPaOffK0 + kPaTile;                   // [kPaItems] PaItem
 constexpr uint32_t kPaOffBar = kPaOffItem + kPaItems * 32;
-constexpr int kPaBars = 2 * kPaSlots + 2 * kPaItems + 2 * 6;
+constexpr int kPaBars = 2 * kPaStages + 2 + 2 * kPaItems + 2 * 5 + 1;
 constexpr size_t kPaSmem = 1024 + kPaOffBar + kPaBars * 8 + 16;
 
 struct PaArgs {
@@ -87,6 +91,56 @@ __device__ __forceinline__ float pa_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// A shared-memory matrix descriptor (spc_tc.cuh) in two words: the low one
+// holds the address (in 16-byte units) and the leading byte offset, the high
+// one is the same for every operand here (1024 bytes between 8-row groups,
+// 128-byte swizzle). K-major operands have leading offset 16, V's 64-value
+// blocks lie kPaBlock apart.
+constexpr uint32_t kPaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kPaDescVLo = ((kPaBlock >> 4) - 1u) << 16;      // on top of a K-major low word
+__device__ __forceinline__ uint32_t pa_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t pa_desc(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float pa_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// tcgen05.wait::ld, with the values it makes valid passed through it
+__device__ __forceinline__ void pa_ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+               :: "memory");
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
+}
+// 32 logits of a row: weights 2^(s scale - m) to 16 packed columns, their sum, their largest logit
+__device__ __forceinline__ void pa_weights(const float* s, float scale2, float m, float2 (&sum)[2], uint32_t tp) {
+  const float2 sc = make_float2(scale2, scale2), nm = make_float2(-m, -m);
+  uint32_t p[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sc, nm);
+    x.x = pa_ex2(x.x);
+    x.y = pa_ex2(x.y);
+    sum[e & 1] = add2(sum[e & 1], x);
+    p[e] = pack_bf16(x.x, x.y);
+  }
+  tmem_st16(tp, p);
+}
+__device__ __forceinline__ void pa_max32(const float* s, float (&mx)[4]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) mx[f] = pa_max3(mx[f], s[e + f], s[e + 4 + f]);
 }
 __device__ __forceinline__ void pa_tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -128,24 +182,28 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
   uint8_t* base = pa_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   volatile PaItem* items = reinterpret_cast<volatile PaItem*>(base + kPaOffItem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kPaOffBar);
-  uint64_t* kvfull = bars;                    // [kPaSlots] TMA bytes
-  uint64_t* kvfree = kvfull + kPaSlots;       // [kPaSlots] commit after the last MMA that reads the slot
-  uint64_t* ifull = kvfree + kPaSlots;        // [kPaItems] item written
+  uint64_t* kvfull = bars;                    // [kPaStages] TMA bytes
+  uint64_t* kvfree = kvfull + kPaStages;      // [kPaStages] commit after the last MMA that reads the stage
+  uint64_t* k0full = kvfree + kPaStages;      // TMA bytes
+  uint64_t* k0free = k0full + 1;              // commit after the item's first S
+  uint64_t* ifull = k0free + 1;               // [kPaItems] item written
   uint64_t* ifree = ifull + kPaItems;         // [kPaItems] MMA warp and 8 softmax warps have read it
   uint64_t* qfull = ifree + kPaItems;         // [2] TMA bytes
   uint64_t* qfree = qfull + 2;                // [2] commit after the tile's last S
   uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
   uint64_t* pfull = sfull + 2;                // [2] 4 warp arrivals: P written, O rescaled
-  uint64_t* pvdone = pfull + 2;               // [2] commit: PV of a block done
-  uint64_t* ofull = pvdone + 2;               // [2] commit: the item's last PV done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofull + 2);
+  uint64_t* ofull = pfull + 2;                // [2] commit: the item's last PV done
+  uint64_t* drain = ofull + 2;                // commit after the last MMA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPaSlots; ++s) {
+    for (int s = 0; s < kPaStages; ++s) {
       mbar_init(&kvfull[s], 1);
       mbar_init(&kvfree[s], 1);
     }
+    mbar_init(k0full, 1);
+    mbar_init(k0free, 1);
     for (int s = 0; s < kPaItems; ++s) {
       mbar_init(&ifull[s], 1);
       mbar_init(&ifree[s], kPaSoftWarps + 1);
@@ -155,9 +213,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       mbar_init(&qfree[s], 1);
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], kPaSoftWarps / 2);
-      mbar_init(&pvdone[s], 1);
       mbar_init(&ofull[s], 1);
     }
+    mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == kPaWarpMma) tmem_alloc<kPaTmemCols>(tmem_slot);
@@ -190,7 +248,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     };
     const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(nb[0], nb[1]));
     const long long n_items = (long long)at_least(0) * c.n_kv;
-    int slot = 0, ns = 0, it = 0, nq[2] = {0, 0};
+    int it = 0, nkv = 0, nk0 = 0, nq[2] = {0, 0};
     auto acquire = [&](uint64_t* bar, uint32_t parity) {
       if (!dead && !pa_wait(bar, parity)) {
         if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -235,109 +293,150 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       const int n = max(x.nA, x.nB);
       auto load_q = [&](int i) {
         acquire(&qfree[i], (nq[i] & 1) ^ 1);
+        if (dead) return;
         ++nq[i];
-        if (lane == 0 && !dead) {
+        if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[i], kPaTile);
           const int row = x.start + x.t0 + i * a.tpm;
           pa_tma_3d(qs + i * kPaTile, &qmap, 0, x.g << a.gshift, row, &qfull[i]);
           pa_tma_3d(qs + i * kPaTile + kPaBlock, &qmap, 64, x.g << a.gshift, row, &qfull[i]);
         }
       };
-      auto load_kv = [&](const CUtensorMap* map, int j) {
-        acquire(&kvfree[slot], (ns & 1) ^ 1);
-        if (lane == 0 && !dead) {
-          mbar_arrive_expect_tx(&kvfull[slot], kPaTile);
-          pa_tma_3d(kvs + slot * kPaTile, map, 0, x.g, x.start + j * kPaKeys, &kvfull[slot]);
-          pa_tma_3d(kvs + slot * kPaTile + kPaBlock, map, 64, x.g, x.start + j * kPaKeys, &kvfull[slot]);
-        }
-        if (++slot == kPaSlots) { slot = 0; ++ns; }
+      auto load = [&](const CUtensorMap* map, uint32_t dst, int j, uint64_t* bar) {
+        pa_tma_3d(dst, map, 0, x.g, x.start + j * kPaKeys, bar);
+        pa_tma_3d(dst + kPaBlock, map, 64, x.g, x.start + j * kPaKeys, bar);
       };
       load_q(0);
-      load_kv(&kmap, 0);
+      acquire(k0free, (nk0 & 1) ^ 1);
+      if (!dead) {
+        ++nk0;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(k0full, kPaTile);
+          load(&kmap, qs + (kPaOffK0 - kPaOffQ), 0, k0full);
+        }
+      }
       if (x.nB) load_q(1);
-      load_kv(&vmap, 0);
-      for (int j = 1; j < n; ++j) {
-        load_kv(&kmap, j);
-        load_kv(&vmap, j);
+      for (int j = 0; j < n; ++j) {
+        const int st = nkv % kPaStages;
+        acquire(&kvfree[st], ((nkv / kPaStages) & 1) ^ 1);
+        if (dead) break;
+        ++nkv;
+        if (lane == 0) {
+          const uint32_t dst = kvs + (uint32_t)st * 2 * kPaTile;
+          mbar_arrive_expect_tx(&kvfull[st], j + 1 < n ? 2 * kPaTile : kPaTile);
+          load(&vmap, dst, j, &kvfull[st]);
+          if (j + 1 < n) load(&kmap, dst + kPaTile, j + 1, &kvfull[st]);
+        }
       }
     }
-    // every copy lands before the CTA ends: each slot's last fill has been
-    // waited for by the MMA warp, unless that gave up
-    if (lane == 0 && dead)
-      for (int s = 0; s < kPaSlots; ++s) mbar_wait_bounded(&kvfull[s], 0, kPaWait / 64);
+    // every copy lands before the CTA ends (they have, unless a role gave up)
+    if (lane == 0) {
+      for (int k = max(0, nkv - kPaStages); k < nkv; ++k)
+        mbar_wait_bounded(&kvfull[k % kPaStages], (k / kPaStages) & 1, kPaWait);
+      if (nk0 > 0) mbar_wait_bounded(k0full, (nk0 - 1) & 1, kPaWait);
+      for (int i = 0; i < 2; ++i)
+        if (nq[i] > 0) mbar_wait_bounded(&qfull[i], (nq[i] - 1) & 1, kPaWait);
+    }
     __syncwarp();
   } else if (warp == kPaWarpMma) {
-    // ================= MMA issue
+    // ================= MMA issue. The whole warp runs the loop, so that its
+    // values stay warp-uniform (operands of tcgen05.mma are uniform registers;
+    // built by a single lane they cost about 90 cycles an instruction and held
+    // the tensor pipe at 60%); one elected lane issues.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
-    if (lane == 0) {
-      auto acquire = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait_bounded(bar, parity, kPaWait)) {
-          set_status(a.status, SPC_ERR_TIMEOUT);
-          dead = true;
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !pa_wait(bar, parity)) {
+        if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+        dead = true;
+      }
+    };
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int nkv = 0, nk0 = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+    // S of tile i against the K tile whose descriptor is kd; last: of the item
+    auto issue_s = [&](auto tile, uint32_t kd, bool last) {
+      constexpr int i = decltype(tile)::value;
+      if (elect_one()) {
+        const uint32_t qd = pa_desc_lo(qs + i * kPaTile);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * (kPaBlock >> 4) + (uint32_t)(kk & 3) * 2;
+          umma_f16(tm + i * kPaKeys, pa_desc(qd + off, kPaDescHi), pa_desc(kd + off, kPaDescHi), kPaIdescS, kk ? 1u : 0u);
         }
-      };
-      int slot = 0, ns = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      for (int it = 0;; ++it) {
-        const int is = it % kPaItems;
-        acquire(&ifull[is], (it / kPaItems) & 1);
-        if (dead) break;
-        const int nA = items[is].nA, nB = items[is].nB, len = items[is].len;
-        mbar_arrive(&ifree[is]);
-        if (len < 0) break;
-        const int nt[2] = {nA, nB}, n = max(nA, nB);
-        auto next_slot = [&]() { const int s = slot; acquire(&kvfull[s], ns & 1); if (++slot == kPaSlots) { slot = 0; ++ns; } return s; };
-        auto issue_s = [&](int i, int ks, bool last) {
-          if (dead) return;
-          tc_fence_after();
+        umma_commit(&sfull[i]);
+        if (last) umma_commit(&qfree[i]);
+      }
+      __syncwarp();
+    };
+    // PV of block j of tile i, then S of block j + 1. The tensor pipe queues
+    // only a few MMAs, so nothing waits between the two
+    auto issue = [&](auto tile, uint32_t st, int j, int n) {
+      constexpr int i = decltype(tile)::value;
+      acquire(&pfull[i], np[i] & 1);
+      ++np[i];
+      if (dead) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t vd = st + kPaDescVLo, kd = st + (kPaTile >> 4), qd = pa_desc_lo(qs + i * kPaTile);
+#pragma unroll
+        for (int kk = 0; kk < kPaKeys / 16; ++kk)
+          umma_f16_tmem_a(tm + kPaColO + i * kD, tm + i * kPaKeys + kk * 8, pa_desc(vd + (uint32_t)kk * 128, kPaDescHi),
+                          kPaIdescO, kk ? 1u : (j ? 1u : 0u));
+        if (j + 1 < n) {
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * kPaBlock + (uint32_t)(kk & 3) * 32;
-            umma_f16(tmem + i * kPaKeys, umma_desc_sw128(qs + i * kPaTile + off), umma_desc_sw128(kvs + ks * kPaTile + off),
-                     kPaIdescS, kk ? 1u : 0u);
+            const uint32_t off = (uint32_t)(kk >> 2) * (kPaBlock >> 4) + (uint32_t)(kk & 3) * 2;
+            umma_f16(tm + i * kPaKeys, pa_desc(qd + off, kPaDescHi), pa_desc(kd + off, kPaDescHi), kPaIdescS, kk ? 1u : 0u);
           }
           umma_commit(&sfull[i]);
-          if (last) umma_commit(&qfree[i]);
-        };
-        auto issue_pv = [&](int i, int vs, bool first) {
-          acquire(&pfull[i], np[i] & 1);
-          ++np[i];
-          if (dead) return;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kPaKeys / 16; ++kk)
-            umma_f16_tmem_a(tmem + kPaColO + i * kD, tmem + i * kPaKeys + kk * 8,
-                            umma_desc_sw128_mn(kvs + vs * kPaTile + (uint32_t)kk * 16 * 128, kPaBlock), kPaIdescO,
-                            (first && kk == 0) ? 0u : 1u);
-          umma_commit(&pvdone[i]);
-        };
-        int ks = next_slot();
-        for (int i = 0; i < 2; ++i) {
-          if (nt[i] == 0) continue;
-          acquire(&qfull[i], nq[i] & 1);
-          ++nq[i];
-          issue_s(i, ks, nt[i] == 1);
-        }
-        if (!dead) umma_commit(&kvfree[ks]);
-        for (int j = 0; j < n; ++j) {
-          const int vs = next_slot();
-          if (j + 1 < n) ks = next_slot();
-          for (int i = 0; i < 2; ++i) {
-            if (j >= nt[i]) continue;
-            issue_pv(i, vs, j == 0);
-            if (j + 1 < nt[i]) issue_s(i, ks, j + 2 == nt[i]);
-            else if (!dead) umma_commit(&ofull[i]);
-          }
-          if (!dead) {
-            umma_commit(&kvfree[vs]);
-            if (j + 1 < n) umma_commit(&kvfree[ks]);
-          }
+          if (j + 2 == n) umma_commit(&qfree[i]);
+        } else {
+          umma_commit(&ofull[i]);
         }
       }
-      // tensor memory is released below: wait for the MMAs in flight (the
-      // softmax warps waited for every item's last one, unless something gave up)
-      if (dead) mbar_wait_bounded(&ofull[0], 0, kPaWait / 64);
+      __syncwarp();
+    };
+    constexpr std::integral_constant<int, 0> tA{};
+    constexpr std::integral_constant<int, 1> tB{};
+    for (int it = 0;; ++it) {
+      const int is = it % kPaItems;
+      acquire(&ifull[is], (it / kPaItems) & 1);
+      if (dead) break;
+      const int nA = items[is].nA, nB = items[is].nB, len = items[is].len;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (len < 0) break;
+      const int n = max(nA, nB);
+      const uint32_t k0 = pa_desc_lo(qs + (kPaOffK0 - kPaOffQ));
+      acquire(k0full, nk0++ & 1);
+      acquire(&qfull[0], nq[0]++ & 1);
+      if (dead) break;
+      tc_fence_after();
+      issue_s(tA, k0, nA == 1);
+      if (nB) {
+        acquire(&qfull[1], nq[1]++ & 1);
+        if (dead) break;
+        issue_s(tB, k0, nB == 1);
+      }
+      if (elect_one()) umma_commit(k0free);
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int st = nkv % kPaStages;
+        acquire(&kvfull[st], (nkv / kPaStages) & 1);
+        ++nkv;
+        const uint32_t sd = pa_desc_lo(kvs) + (uint32_t)st * (2 * kPaTile >> 4);
+        if (j < nA) issue(tA, sd, j, nA);
+        if (j < nB) issue(tB, sd, j, nB);
+        if (!dead && elect_one()) umma_commit(&kvfree[st]);
+        __syncwarp();
+      }
+      if (dead) break;
     }
+    // tensor memory is released below: every MMA has completed (the softmax
+    // warps wait for each item's last one, unless something gave up)
+    if (elect_one()) umma_commit(drain);
     __syncwarp();
+    pa_wait(drain, 0);
   } else if (warp < kPaSoftWarps) {
     // ================= softmax and epilogue of tile i, one row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPaRegSoft));
@@ -345,7 +444,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     const int i = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + i * kPaKeys, to = tmem + lanes + kPaColO + i * kD;
-    int n_s = 0, n_o = 0, slot = 0, ns = 0;
+    int n_s = 0, n_o = 0, nkv = 0;
     auto acquire = [&](uint64_t* bar, uint32_t parity) {
       if (!dead && !pa_wait(bar, parity)) {
         if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -366,35 +465,50 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         acquire(&sfull[i], n_s & 1);
+        if (dead) break;
         tc_fence_after();
-        float s[128];
-        if (!dead) {
+        float s[128], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        bool redo = true;
+        float M;
+        if ((j + 1) * kPaKeys <= t0 + 1 && !__any_sync(0xffffffffu, m == -INFINITY)) {
+          // every row sees the whole block and has a maximum: weights against
+          // it at once, while the block's own maximum is being found
+          tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            pa_ld_wait(s + 32 * q);
+            if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
+            pa_max32(s + 32 * q, mx);
+            pa_weights(s + 32 * q, c.scale2, m, sum, ts + 16 * q);
+          }
+          M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
+          redo = __any_sync(0xffffffffu, M > m + kPaHeadroom);
+        } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
-          tmem_ld_wait();
-        }
-        const int seen = qpos - j * kPaKeys;          // columns 0 .. seen are visible
-        if ((j + 1) * kPaKeys > t0 + 1) {             // the block reaches behind the tile's first token
+          const int seen = qpos - j * kPaKeys;        // columns 0 .. seen are visible
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > seen) s[e] = -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int q = 0; q < 4; ++q) {
+            pa_ld_wait(s + 32 * q);
 #pragma unroll
-        for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
-        const float M = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c.scale2;
-        float alpha = 1.f;
-        const bool up = M > m + kPaHeadroom;
-        if (up) {
-          alpha = m == -INFINITY ? 0.f : pa_ex2(m - M);
-          l *= alpha;
-          m = M;
+            for (int e = 32 * q; e < 32 * q + 32; ++e)
+              if (e > seen) s[e] = -INFINITY;
+            pa_max32(s + 32 * q, mx);
+          }
+          M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
         }
-        if (j > 0 && __any_sync(0xffffffffu, up)) {
-          // O holds earlier blocks: their PV must be done
-          acquire(&pvdone[i], (n_s - 1) & 1);
-          tc_fence_after();
-          if (!dead) {
+        if (redo) {
+          float alpha = 1.f;
+          const bool up = M > m + kPaHeadroom;
+          if (up) {
+            alpha = m == -INFINITY ? 0.f : pa_ex2(m - M);
+            l *= alpha;
+            m = M;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, up)) {
+            // O holds earlier blocks; their PV is done, for this block's S was
+            // issued behind it and the commit it came with covers both
 #pragma unroll 1
             for (int q = 0; q < 8; ++q) {
               float o[16];
@@ -405,31 +519,19 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
               tmem_st16(to + 16 * q, o);
             }
           }
-        }
-        const float mm = m == -INFINITY ? 0.f : m;
-        const float2 sc = make_float2(c.scale2, c.scale2), nm = make_float2(-mm, -mm);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float mm = m == -INFINITY ? 0.f : m;
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = fma2(make_float2(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), sc, nm);
-            x.x = pa_ex2(x.x);
-            x.y = pa_ex2(x.y);
-            sum[e & 1] = add2(sum[e & 1], x);
-            p[e] = pack_bf16(x.x, x.y);
-          }
-          if (!dead) tmem_st16(ts + 16 * q, p);
+          for (int q = 0; q < 4; ++q) pa_weights(s + 32 * q, c.scale2, mm, sum, ts + 16 * q);
         }
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         if ((j + 1) * kPaKeys > len) {
-          // V rows behind the sequence's end: zeros. K(0), V(0), K(1), ... follow
-          // one another in the ring from this item's first slot on
-          const int v = slot + 2 * j + 1, vs = v % kPaSlots;
-          acquire(&kvfull[vs], (ns + v / kPaSlots) & 1);
-          if (row >= len - j * kPaKeys && !dead) {
-            uint4* r0 = reinterpret_cast<uint4*>(base + kPaOffKv + vs * kPaTile + row * 128);
+          // V rows behind the sequence's end: zeros
+          const int v = nkv + j, vs = v % kPaStages;
+          acquire(&kvfull[vs], (v / kPaStages) & 1);
+          if (dead) break;
+          if (row >= len - j * kPaKeys) {
+            uint4* r0 = reinterpret_cast<uint4*>(base + kPaOffKv + vs * 2 * kPaTile + row * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               r0[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -438,21 +540,20 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           }
           fence_proxy_async_smem();
         }
-        if (!dead) tmem_st_wait();
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[i]);
         ++n_s;
       }
-      slot += 2 * nmax;
-      ns += slot / kPaSlots;
-      slot %= kPaSlots;
+      if (dead) break;
+      nkv += nmax;
       if (n == 0) continue;
       // ---- epilogue
       acquire(&ofull[i], n_o & 1);
+      if (dead) break;
       ++n_o;
       tc_fence_after();
-      if (dead) continue;
       const bool live = qpos < len;
       const int h = (g << a.gshift) + (row & (a.G - 1));
       uint16_t* dst = c.out + ((size_t)(start + qpos) * c.n_q + h) * kD;
