@@ -25,67 +25,107 @@ __device__ __forceinline__ uint8_t* kv4_record(const Kv4RowsCall& a, int slot, i
   return a.cache + ((((size_t)blk * a.n_kv + g) << a.block_shift) + r) * kKv4Rec;
 }
 
+// A warp takes kRowBatch consecutive (token, head) pairs at a time and loads
+// all of their rows before it works on the first.
+constexpr int kRowBatch = 4;
+
+// slot and head of pair i, -1 where there is none
+__device__ __forceinline__ int row_slot(const Kv4RowsCall& a, long long i, long long n, int& t, int& g) {
+  t = 0;
+  g = 0;
+  if (i >= n) return -1;
+  t = a.n_kv == 1 ? (int)i : (int)(i / a.n_kv);
+  g = (int)(i - (long long)t * a.n_kv);
+  const int slot = __ldg(a.slot_map + t);
+  return slot < a.n_cache_slots ? slot : -1;
+}
+
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(Kv4RowsCall a) {
   const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
   const long long n = (long long)a.T * a.n_kv;
-  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
-  for (long long i = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < n; i += warps) {
-    const int t = (int)(i / a.n_kv), g = (int)(i - (long long)t * a.n_kv);
-    const int slot = __ldg(a.slot_map + t);
-    if (slot < 0 || slot >= a.n_cache_slots) continue;
-    const uint16_t* src = (isv ? a.v + (size_t)t * a.v_stride : a.k + (size_t)t * a.k_stride) + g * kD + 8 * hl;
-    const uint4 w = ldg_stream(src);
-    // largest magnitude of the group: bit patterns without the sign order like
-    // the magnitudes, NaN above infinity
-    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m & 0xffffu, m >> 16);
-    const float amax = __uint_as_float(m << 16);
-    const uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
-    const float s = f16_lo(e4m3x2_to_f16(sb));
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    float x[8];
-    unpack8(w, x);
+  const long long step = (long long)gridDim.x * (kRowThreads / 32) * kRowBatch;
+  const uint16_t* base = (isv ? a.v : a.k) + 8 * hl;
+  const int64_t stride = isv ? a.v_stride : a.k_stride;
+  for (long long i = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kRowBatch; i < n; i += step) {
+    uint4 w[kRowBatch];
+    int slot[kRowBatch], g[kRowBatch];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const __half2 h = __floats2half2_rn(x[j] * r, x[j + 1] * r);
-      x[j] = __low2float(h);
-      x[j + 1] = __high2float(h);
+    for (int b = 0; b < kRowBatch; ++b) {
+      int t;
+      slot[b] = row_slot(a, i + b, n, t, g[b]);
+      w[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (i + b < n) w[b] = ldg_stream(base + t * stride + g[b] * kD);
     }
-    uint8_t* rec = kv4_record(a, slot, g);
-    *reinterpret_cast<uint32_t*>(rec + isv * kKv4V + 4 * hl) = f32_to_e2m1x8(x);
-    // the scales of four groups (eight lanes) as one word
-    uint32_t sw = sb | (__shfl_down_sync(0xffffffffu, sb, 2) << 8);
-    sw |= __shfl_down_sync(0xffffffffu, sw, 4) << 16;
-    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kKv4Scale + 4 * (lane >> 3)) = sw;
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b) {
+      // largest magnitude of the group: bit patterns without the sign order
+      // like the magnitudes, NaN above infinity
+      constexpr uint32_t A = 0x7fff7fffu;
+      uint32_t m = __vmaxu2(__vmaxu2(w[b].x & A, w[b].y & A), __vmaxu2(w[b].z & A, w[b].w & A));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m & 0xffffu, m >> 16);
+      const uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(m << 16), 6.f), __NV_SATFINITE, __NV_E4M3);
+      const float s = f16_lo(e4m3x2_to_f16(sb));
+      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+      float x[8];
+      unpack8(w[b], x);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const __half2 h = __floats2half2_rn(x[j] * r, x[j + 1] * r);
+        x[j] = __low2float(h);
+        x[j + 1] = __high2float(h);
+      }
+      const uint32_t codes = f32_to_e2m1x8(x);
+      // the scales of four groups (eight lanes) as one word
+      uint32_t sw = sb | (__shfl_down_sync(0xffffffffu, sb, 2) << 8);
+      sw |= __shfl_down_sync(0xffffffffu, sw, 4) << 16;
+      if (slot[b] < 0) continue;
+      uint8_t* rec = kv4_record(a, slot[b], g[b]);
+      *reinterpret_cast<uint32_t*>(rec + isv * kKv4V + 4 * hl) = codes;
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kKv4Scale + 4 * (lane >> 3)) = sw;
+    }
   }
 }
 
 __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4RowsCall a) {
   const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
   const long long n = (long long)a.T * a.n_kv;
-  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
-  for (long long i = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < n; i += warps) {
-    const int t = (int)(i / a.n_kv), g = (int)(i - (long long)t * a.n_kv);
-    const int slot = __ldg(a.slot_map + t);
-    if (slot < 0 || slot >= a.n_cache_slots) continue;
-    const uint8_t* rec = kv4_record(a, slot, g);
-    const uint32_t codes = *reinterpret_cast<const uint32_t*>(rec + isv * kKv4V + 4 * hl);
-    const uint32_t s = e4m3_dup_f16(rec[kKv4Scale + 8 * isv + (hl >> 1)]);
-    uint32_t h[4];
-    e2m1x8_to_f16(codes, h);
+  const long long step = (long long)gridDim.x * (kRowThreads / 32) * kRowBatch;
+  uint16_t* base = const_cast<uint16_t*>(isv ? a.v : a.k) + 8 * hl;
+  const int64_t stride = isv ? a.v_stride : a.k_stride;
+  for (long long i = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kRowBatch; i < n; i += step) {
+    uint32_t codes[kRowBatch], sb[kRowBatch];
+    uint16_t* dst[kRowBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = hmul2(h[j], s);
-      h[j] = pack_bf16(f16_lo(h[j]), f16_hi(h[j]));
+    for (int b = 0; b < kRowBatch; ++b) {
+      int t, g;
+      const int slot = row_slot(a, i + b, n, t, g);
+      dst[b] = nullptr;
+      codes[b] = sb[b] = 0;
+      if (slot >= 0) {
+        const uint8_t* rec = kv4_record(a, slot, g);
+        codes[b] = __ldg(reinterpret_cast<const uint32_t*>(rec + isv * kKv4V + 4 * hl));
+        sb[b] = __ldg(rec + kKv4Scale + 8 * isv + (hl >> 1));
+        dst[b] = base + t * stride + g * kD;
+      }
     }
-    uint16_t* dst = const_cast<uint16_t*>(isv ? a.v + (size_t)t * a.v_stride : a.k + (size_t)t * a.k_stride) + g * kD + 8 * hl;
-    stg_v4(dst, make_uint4(h[0], h[1], h[2], h[3]));
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b) {
+      const uint32_t s = e4m3_dup_f16(sb[b]);
+      uint32_t h[4];
+      e2m1x8_to_f16(codes[b], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = hmul2(h[j], s);
+        h[j] = pack_bf16(f16_lo(h[j]), f16_hi(h[j]));
+      }
+      if (dst[b]) stg_v4(dst[b], make_uint4(h[0], h[1], h[2], h[3]));
+    }
   }
 }
 
 static int rows_grid(const Kv4RowsCall& c) {
-  const long long n = (long long)c.T * c.n_kv, per = kRowThreads / 32;
+  const long long n = (long long)c.T * c.n_kv, per = kRowThreads / 32 * kRowBatch;
   const long long g = (n + per - 1) / per;
   return (int)(g < 152 * 8 ? g : 152 * 8);
 }

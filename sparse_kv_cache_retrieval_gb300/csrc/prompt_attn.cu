@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       const int h = (g << a.gshift) + (row & (a.G - 1));
       uint16_t* dst = c.out + ((size_t)(start + qpos) * c.n_q + h) * kD;
       const float r = 1.f / l;
+      const bool wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;   // whole sectors a store
       bool odd = false;                                // a value that is not finite
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -566,15 +567,22 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         tmem_ld_wait();
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[8];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float x0 = o[8 * e + 2 * f] * r, x1 = o[8 * e + 2 * f + 1] * r;
+            for (int f = 0; f < 8; ++f) {
+              const float x0 = o[16 * e + 2 * f] * r, x1 = o[16 * e + 2 * f + 1] * r;
               odd = odd || !(fabsf(x0) < INFINITY) || !(fabsf(x1) < INFINITY);
               w[f] = pack_bf16(x0, x1);
             }
-            stg_v4(dst + 32 * q + 8 * e, make_uint4(w[0], w[1], w[2], w[3]));
+            uint16_t* d = dst + 32 * q + 16 * e;
+            if (wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                           "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+            } else {
+              stg_v4(d, make_uint4(w[0], w[1], w[2], w[3]));
+              stg_v4(d + 8, make_uint4(w[4], w[5], w[6], w[7]));
+            }
           }
         }
       }
