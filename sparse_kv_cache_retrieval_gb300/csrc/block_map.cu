@@ -55,6 +55,10 @@ __device__ __forceinline__ int bm_popped(const BlockMapCall& a, const BmShared& 
   return a.table[(size_t)b * a.max_blocks + s.want[b] + (r - s.push[b])];
 }
 
+// V consecutive slots a thread: one search, one block entry in most cases.
+// V = 4 once there are more slots than threads (1.7 M slots: 5.9 us, with V =
+// 1 10.0), else V = 1 (64 slots of 64 requests: 2.6 us, with V = 4 3.5).
+template <int V>
 __global__ void __launch_bounds__(kBmThreads) block_map_kernel(BlockMapCall a) {
   __shared__ BmShared s;
   const int bs = 1 << a.block_shift;
@@ -114,21 +118,46 @@ __global__ void __launch_bounds__(kBmThreads) block_map_kernel(BlockMapCall a) {
     a.free_list[s.n_free + i] = a.table[(size_t)b * a.max_blocks + s.want[b] + (i - s.push[b])];
   }
   const int n_new = bad ? 0 : s.cu[kBmBatch];
-  for (int t = tid; t < a.n_slots; t += stride) {
-    int slot = -1;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slot_map) & 15u) == 0;
+  for (int t = V * tid; t < a.n_slots; t += V * stride) {
+    int out[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = -1;
     if (t < n_new) {
-      const int b = bm_find(s.cu, kBmBatch, t);
-      const int p = s.old[b] + (t - s.cu[b]), k = p >> a.block_shift;
-      const int blk = k < s.have[b] ? a.table[(size_t)b * a.max_blocks + k] : bm_popped(a, s, s.pop[b] + k - s.have[b]);
-      if (blk >= 0 && blk < a.num_blocks) slot = (blk << a.block_shift) + (p & (bs - 1));
+      int b = bm_find(s.cu, kBmBatch, t), seen = -1, blk = -1;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (t + e >= n_new) break;
+        if (t + e >= s.cu[b + 1]) {
+          do ++b; while (t + e >= s.cu[b + 1]);
+          seen = -1;
+        }
+        const int p = s.old[b] + (t + e - s.cu[b]), k = p >> a.block_shift;
+        if (k != seen) {
+          seen = k;
+          blk = k < s.have[b] ? a.table[(size_t)b * a.max_blocks + k] : bm_popped(a, s, s.pop[b] + k - s.have[b]);
+        }
+        if (blk >= 0 && blk < a.num_blocks) out[e] = (blk << a.block_shift) + (p & (bs - 1));
+      }
     }
-    a.slot_map[t] = slot;
+    if (V == 4 && wide && t + 4 <= a.n_slots) {
+      *reinterpret_cast<int4*>(a.slot_map + t) = make_int4(out[0], out[V > 1 ? 1 : 0], out[V > 2 ? 2 : 0], out[V > 3 ? 3 : 0]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (t + e < a.n_slots) a.slot_map[t + e] = out[e];
+    }
   }
 }
 
 int block_map_launch(const BlockMapCall& c, void* stream) {
-  const int grid = max(1, min((c.n_slots + kBmThreads - 1) / kBmThreads, 152 * 4));
-  block_map_kernel<<<grid, kBmThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  constexpr int most = 152 * 4;
+  const int v = c.n_slots > most * kBmThreads ? 4 : 1;
+  const int grid = min((c.n_slots + v * kBmThreads - 1) / (v * kBmThreads), most);
+  if (v == 4)
+    block_map_kernel<4><<<grid, kBmThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  else
+    block_map_kernel<1><<<grid, kBmThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 

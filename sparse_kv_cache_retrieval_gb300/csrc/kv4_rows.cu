@@ -1,15 +1,23 @@
 // Rows of K and V into and out of the paged 4-bit cache.
 //
-// One warp holds one (token, KV head): lanes 0-15 its K row, lanes 16-31 its V
-// row, 8 values a lane, so that a group of 16 values is a pair of lanes.
-// Rounding: the scale is e4m3(max|x| / 6) of the correctly rounded quotient;
-// the codes need e2m1(x / s) of the exact quotient, ties included. x has 8
-// significant bits and s has 4, so a quotient that is not a tie of e2m1 is at
-// least 2^-8 (relative) away from one; x * (1 / s) in fp32 is within 2^-23 of
-// it, and rounding that product to fp16 (11 bits) returns the tie exactly
-// where there is one and stays on its side where there is none. The
-// conversion of the fp16 value to e2m1 therefore rounds the exact quotient.
-// Bound: HBM (512 bytes read and 144 written a row, or the reverse).
+// A group of 16 values, its scale and its 16 codes are one lane's: 8 lanes a K
+// or V row, two (token, KV head) pairs a warp, and kRowBatch such steps loaded
+// before the first is worked on: 2 where there are more steps than warps
+// (65536 tokens of 8 heads, store and load: 122 us, with 1 step 147), else 1
+// (8 tokens: 3.3 us, with 2 steps 4.1).
+//
+// Rounding. The scale is e4m3 of the exact quotient max / 6, the codes are
+// e2m1 of the exact quotients x / s, ties to even. Neither division is done:
+// x (bf16) has 8 significant bits, s has 4, ties of e4m3 have 5 and ties of
+// e2m1 at most 3, so a quotient that is not a tie is at least 2^-8 (relative)
+// away from one. max * (1/6) in fp32 is within 2^-22 of the quotient; rounded
+// to fp16 (11 bits) it is the tie where there is one and stays on its side
+// where there is none, and e4m3 of that is e4m3 of the quotient. In the same
+// way x * r, r within 2^-22 of 1/s, is rounded to multiples of 2^-11 (ties of
+// e2m1 are multiples of 1/4, and a quotient beside one of at least 1/4 is at
+// least 2^-10 away) by adding and subtracting 6144 in fp32.
+//
+// Bound: HBM (512 bytes read and 144 written a pair, or the reverse).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
@@ -19,125 +27,184 @@
 namespace spc {
 
 constexpr int kRowThreads = 256;
+constexpr int kRowCtas = 152 * 8;         // 8 CTAs of 8 warps fill an SM
 
 __device__ __forceinline__ uint8_t* kv4_record(const Kv4RowsCall& a, int slot, int g) {
   const int blk = slot >> a.block_shift, r = slot & ((1 << a.block_shift) - 1);
   return a.cache + ((((size_t)blk * a.n_kv + g) << a.block_shift) + r) * kKv4Rec;
 }
-
-// A warp takes kRowBatch consecutive (token, head) pairs at a time and loads
-// all of their rows before it works on the first.
-constexpr int kRowBatch = 4;
-
-// slot and head of pair i, -1 where there is none
-__device__ __forceinline__ int row_slot(const Kv4RowsCall& a, long long i, long long n, int& t, int& g) {
-  t = 0;
-  g = 0;
-  if (i >= n) return -1;
-  t = a.n_kv == 1 ? (int)i : (int)(i / a.n_kv);
-  g = (int)(i - (long long)t * a.n_kv);
-  const int slot = __ldg(a.slot_map + t);
-  return slot < a.n_cache_slots ? slot : -1;
+// 32 bytes a lane; one instruction where the rows are 32-byte aligned
+__device__ __forceinline__ void row_load(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+  } else {
+    const uint4 x = ldg_stream(p), y = ldg_stream(p + 8);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+  }
+}
+__device__ __forceinline__ void row_store(uint16_t* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  } else {
+    stg_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+    stg_v4(p + 8, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+__device__ __forceinline__ bool rows_wide(const uint16_t* p, int64_t stride) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride * 2) & 31u) == 0;
 }
 
+// Steps of two pairs: pair 2 step + (lane / 16), in (token, head) order. The
+// division is made once and carried on.
+struct RowCursor {
+  long long i;
+  int t, g;
+};
+__device__ __forceinline__ RowCursor row_at(const Kv4RowsCall& a, long long i) {
+  RowCursor c;
+  c.i = i;
+  c.t = (int)(i / a.n_kv);
+  c.g = (int)(i - (long long)c.t * a.n_kv);
+  return c;
+}
+__device__ __forceinline__ void row_next(const Kv4RowsCall& a, RowCursor& c, int n) {
+  c.i += n;
+  c.g += n;
+  while (c.g >= a.n_kv) {
+    c.g -= a.n_kv;
+    ++c.t;
+  }
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int kRowBatch>
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(Kv4RowsCall a) {
-  const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
+  const int lane = threadIdx.x & 31, q = lane & 7, isv = (lane >> 3) & 1, half = lane >> 4;
   const long long n = (long long)a.T * a.n_kv;
-  const long long step = (long long)gridDim.x * (kRowThreads / 32) * kRowBatch;
-  const uint16_t* base = (isv ? a.v : a.k) + 8 * hl;
+  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
+  const uint16_t* base = (isv ? a.v : a.k) + 16 * q;
   const int64_t stride = isv ? a.v_stride : a.k_stride;
-  for (long long i = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kRowBatch; i < n; i += step) {
-    uint4 w[kRowBatch];
-    int slot[kRowBatch], g[kRowBatch];
+  const bool wide = rows_wide(base, stride);
+  for (long long s0 = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); s0 * 2 * kRowBatch < n; s0 += warps) {
+    uint32_t w[kRowBatch][8];
+    uint8_t* rec[kRowBatch];
+    RowCursor c = row_at(a, s0 * 2 * kRowBatch + half);
 #pragma unroll
     for (int b = 0; b < kRowBatch; ++b) {
-      int t;
-      slot[b] = row_slot(a, i + b, n, t, g[b]);
-      w[b] = make_uint4(0u, 0u, 0u, 0u);
-      if (i + b < n) w[b] = ldg_stream(base + t * stride + g[b] * kD);
+      rec[b] = nullptr;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[b][j] = 0u;
+      if (c.i < n) {
+        const int slot = __ldg(a.slot_map + c.t);
+        row_load(base + c.t * stride + c.g * kD, wide, w[b]);
+        if (slot >= 0 && slot < a.n_cache_slots) rec[b] = kv4_record(a, slot, c.g);
+      }
+      row_next(a, c, 2);
     }
 #pragma unroll
     for (int b = 0; b < kRowBatch; ++b) {
-      // largest magnitude of the group: bit patterns without the sign order
-      // like the magnitudes, NaN above infinity
-      constexpr uint32_t A = 0x7fff7fffu;
-      uint32_t m = __vmaxu2(__vmaxu2(w[b].x & A, w[b].y & A), __vmaxu2(w[b].z & A, w[b].w & A));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m & 0xffffu, m >> 16);
-      const uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(m << 16), 6.f), __NV_SATFINITE, __NV_E4M3);
-      const float s = f16_lo(e4m3x2_to_f16(sb));
-      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-      float x[8];
-      unpack8(w[b], x);
+      // largest magnitude: bit patterns without the sign order like the
+      // magnitudes, NaN above infinity
+      uint32_t m = w[b][0] & 0x7fff7fffu;
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const __half2 h = __floats2half2_rn(x[j] * r, x[j + 1] * r);
-        x[j] = __low2float(h);
-        x[j + 1] = __high2float(h);
+      for (int j = 1; j < 8; ++j) m = __vmaxu2(m, w[b][j] & 0x7fff7fffu);
+      m = max(m & 0xffffu, m >> 16);
+      const __half2 a6 = __floats2half2_rn(__uint_as_float(m << 16) * (1.f / 6.f), 0.f);
+      const uint32_t sb = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(a6), __NV_SATFINITE, __NV_E4M3) & 0xffu;
+      const float s = f16_lo(e4m3x2_to_f16(sb));
+      const float r = s > 0.f ? rcp_fast(s) : 0.f;
+      const float2 rr = make_float2(r, r), up = make_float2(6144.f, 6144.f), dn = make_float2(-6144.f, -6144.f);
+      uint32_t codes[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t v = w[b][4 * e + j];
+          const float2 z = make_float2(bf_lo(v), bf_hi(v)), y = add2(fma2(z, rr, up), dn);
+          x[2 * j] = copysignf(y.x, z.x);            // what rounds to zero keeps its sign
+          x[2 * j + 1] = copysignf(y.y, z.y);
+        }
+        codes[e] = f32_to_e2m1x8(x);
       }
-      const uint32_t codes = f32_to_e2m1x8(x);
-      // the scales of four groups (eight lanes) as one word
-      uint32_t sw = sb | (__shfl_down_sync(0xffffffffu, sb, 2) << 8);
-      sw |= __shfl_down_sync(0xffffffffu, sw, 4) << 16;
-      if (slot[b] < 0) continue;
-      uint8_t* rec = kv4_record(a, slot[b], g[b]);
-      *reinterpret_cast<uint32_t*>(rec + isv * kKv4V + 4 * hl) = codes;
-      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kKv4Scale + 4 * (lane >> 3)) = sw;
+      if (rec[b]) {
+        *reinterpret_cast<uint2*>(rec[b] + isv * kKv4V + 8 * q) = make_uint2(codes[0], codes[1]);
+        rec[b][kKv4Scale + 8 * isv + q] = (uint8_t)sb;
+      }
     }
   }
 }
 
+template <int kRowBatch>
 __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4RowsCall a) {
-  const int lane = threadIdx.x & 31, hl = lane & 15, isv = lane >> 4;
+  const int lane = threadIdx.x & 31, q = lane & 7, isv = (lane >> 3) & 1, half = lane >> 4;
   const long long n = (long long)a.T * a.n_kv;
-  const long long step = (long long)gridDim.x * (kRowThreads / 32) * kRowBatch;
-  uint16_t* base = const_cast<uint16_t*>(isv ? a.v : a.k) + 8 * hl;
+  const long long warps = (long long)gridDim.x * (kRowThreads / 32);
+  uint16_t* base = const_cast<uint16_t*>(isv ? a.v : a.k) + 16 * q;
   const int64_t stride = isv ? a.v_stride : a.k_stride;
-  for (long long i = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kRowBatch; i < n; i += step) {
-    uint32_t codes[kRowBatch], sb[kRowBatch];
+  const bool wide = rows_wide(base, stride);
+  for (long long s0 = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); s0 * 2 * kRowBatch < n; s0 += warps) {
+    uint2 codes[kRowBatch];
+    uint32_t sb[kRowBatch];
     uint16_t* dst[kRowBatch];
+    RowCursor c = row_at(a, s0 * 2 * kRowBatch + half);
 #pragma unroll
     for (int b = 0; b < kRowBatch; ++b) {
-      int t, g;
-      const int slot = row_slot(a, i + b, n, t, g);
       dst[b] = nullptr;
-      codes[b] = sb[b] = 0;
-      if (slot >= 0) {
-        const uint8_t* rec = kv4_record(a, slot, g);
-        codes[b] = __ldg(reinterpret_cast<const uint32_t*>(rec + isv * kKv4V + 4 * hl));
-        sb[b] = __ldg(rec + kKv4Scale + 8 * isv + (hl >> 1));
-        dst[b] = base + t * stride + g * kD;
+      codes[b] = make_uint2(0u, 0u);
+      sb[b] = 0;
+      if (c.i < n) {
+        const int slot = __ldg(a.slot_map + c.t);
+        if (slot >= 0 && slot < a.n_cache_slots) {
+          const uint8_t* rec = kv4_record(a, slot, c.g);
+          codes[b] = __ldg(reinterpret_cast<const uint2*>(rec + isv * kKv4V + 8 * q));
+          sb[b] = __ldg(rec + kKv4Scale + 8 * isv + q);
+          dst[b] = base + c.t * stride + c.g * kD;
+        }
       }
+      row_next(a, c, 2);
     }
 #pragma unroll
     for (int b = 0; b < kRowBatch; ++b) {
       const uint32_t s = e4m3_dup_f16(sb[b]);
-      uint32_t h[4];
-      e2m1x8_to_f16(codes[b], h);
+      uint32_t h[8];
+      e2m1x8_to_f16(codes[b].x, *reinterpret_cast<uint32_t (*)[4]>(h));
+      e2m1x8_to_f16(codes[b].y, *reinterpret_cast<uint32_t (*)[4]>(h + 4));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         h[j] = hmul2(h[j], s);
         h[j] = pack_bf16(f16_lo(h[j]), f16_hi(h[j]));
       }
-      if (dst[b]) stg_v4(dst[b], make_uint4(h[0], h[1], h[2], h[3]));
+      if (dst[b]) row_store(dst[b], wide, h);
     }
   }
 }
 
-static int rows_grid(const Kv4RowsCall& c) {
-  const long long n = (long long)c.T * c.n_kv, per = kRowThreads / 32 * kRowBatch;
-  const long long g = (n + per - 1) / per;
-  return (int)(g < 152 * 8 ? g : 152 * 8);
+static int rows_launch(void (*one)(Kv4RowsCall), void (*two)(Kv4RowsCall), const Kv4RowsCall& c, void* stream) {
+  const long long n = (long long)c.T * c.n_kv, per = kRowThreads / 32 * 2;     // pairs a CTA, a step
+  const long long ctas = (n + per - 1) / per;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ctas <= kRowCtas)
+    one<<<(int)ctas, kRowThreads, 0, st>>>(c);
+  else
+    two<<<(int)((ctas + 1) / 2 < kRowCtas ? (ctas + 1) / 2 : kRowCtas), kRowThreads, 0, st>>>(c);
+  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
 int kv4_store_launch(const Kv4RowsCall& c, void* stream) {
-  kv4_store_kernel<<<rows_grid(c), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
-  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+  return rows_launch(kv4_store_kernel<1>, kv4_store_kernel<2>, c, stream);
 }
 
 int kv4_load_launch(const Kv4RowsCall& c, void* stream) {
-  kv4_load_kernel<<<rows_grid(c), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(c);
-  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+  return rows_launch(kv4_load_kernel<1>, kv4_load_kernel<2>, c, stream);
 }
 
 }  // namespace spc
