@@ -52,17 +52,19 @@ constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 
 constexpr float kK4Headroom = 8.f;
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
-// The CTA of a kernel for HT head tiles: warps, and tiles in a warp's ring.
-template <int HT>
+// The CTA of a kernel for HT head tiles. Whole context: the last warp copies
+// for the others; selected positions: each warp gathers for itself.
+template <int HT, bool SEL>
 struct K4Cfg {
-  static constexpr int kWarps = HT == 1 ? 16 : 8;
-  static constexpr int kStages = HT == 1 ? 2 : 4;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kAll = HT == 1 ? 16 : 8;        // warps
+  static constexpr int kWarps = SEL ? kAll : kAll - 1; // warps that compute
+  static constexpr int kStages = HT == 1 ? 2 : 4;      // tiles in a warp's ring
+  static constexpr int kThreads = 32 * kAll;
   // shared memory
   static constexpr uint32_t kOffMerge = kWarps * kStages * kK4StageBytes;              // [warps][8 heads][kK4Part]
   static constexpr uint32_t kOffQ = kOffMerge + kWarps * 8 * kK4Part * 4;              // HT > 1: [HT][8 k-steps][32 lanes] x 8 bytes
-  static constexpr uint32_t kOffBar = kOffQ + (HT > 1 ? HT * 8 * 32 * 8 : 0);
-  static constexpr uint32_t kOffMask = kOffBar + kWarps * kStages * 8;
+  static constexpr uint32_t kOffBar = kOffQ + (HT > 1 ? HT * 8 * 32 * 8 : 0);          // [warps][stages] full, then free
+  static constexpr uint32_t kOffMask = kOffBar + 2 * kWarps * kStages * 8;
   static constexpr uint32_t kSmem = kOffMask + kWarps * kStages * 4;
 };
 
@@ -97,6 +99,13 @@ __device__ __forceinline__ float k4_ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
 struct K4Line {
   int pre[SPC_MAX_BATCH + 1];
@@ -110,25 +119,12 @@ struct K4Cursor {
   int t, i, b, s;
   int nt, len;                 // the segment's tiles, the request's context
   const int32_t* table;        // the request's table row
-  int e;                       // this lane's entry of tile i, fetched a tile ahead of its use
 };
 __device__ __forceinline__ void k4_seg(const Kv4AttnCall& c, const K4Line& ln, K4Cursor& x) {
   const int b = min(x.b, c.B - 1);
   x.nt = max(1, ln.nt[b]);
   x.len = ln.len[b];
   x.table = c.table + (size_t)b * c.max_blocks;
-}
-// dense: the table entry of the lane's block in the tile; selected: the lane's position
-__device__ __forceinline__ void k4_fetch(const Kv4Args& a, K4Cursor& x) {
-  const Kv4AttnCall& c = a.c;
-  const int lane = threadIdx.x & 31, p0 = x.i * kK4Tile;
-  if (c.selected) {
-    x.e = p0 + lane < c.budget
-              ? __ldg(c.selected + ((size_t)min(x.b, c.B - 1) * c.n_kv + (x.s >> a.hshift)) * c.budget + p0 + lane) : -1;
-  } else {
-    const int p = p0 + 16 * (lane & 1);
-    x.e = p < x.len ? __ldg(x.table + (p >> c.block_shift)) : -1;
-  }
 }
 __device__ __forceinline__ K4Cursor k4_at(const Kv4AttnCall& c, const K4Line& ln, int t) {
   int lo = 0, hi = c.B;        // pre[lo] <= t < pre[hi]; requests without tiles are passed over
@@ -159,67 +155,105 @@ __device__ __forceinline__ void k4_step(const Kv4AttnCall& c, const K4Line& ln, 
   k4_seg(c, ln, x);
 }
 
-// Copies tile x into a stage: valid rows only, completion counted on the
-// stage's barrier (dense: one arrival and the bytes; selected: one arrival a
-// lane when its copies have landed), the valid rows noted in *mask. One warp.
-__device__ __forceinline__ void k4_issue(const Kv4Args& a, const K4Cursor& x, uint8_t* stage, uint64_t* bar,
-                                         uint32_t* mask) {
+// Whole context: the copying warp. Lane w serves warp w: tiles t0 + w, t0 + w
+// + W, ... go into its ring as its stages fall free, so that one instruction
+// stream computes the addresses of W tiles. A lane's table entries are fetched
+// one tile ahead.
+template <int W, int S>
+__device__ __forceinline__ void k4_copy(const Kv4Args& a, const K4Line& ln, int segs, int t0, int t1, uint8_t* ring,
+                                        uint64_t* full, uint64_t* empty, uint32_t* masks) {
   const Kv4AttnCall& c = a.c;
-  const int lane = threadIdx.x & 31, g = x.s >> a.hshift;
-  const int bs = 1 << c.block_shift, p0 = x.i * kK4Tile;
-  if (c.selected == nullptr) {
-    const int n = min(kK4Tile, x.len - p0);                          // rows of the tile
-    if (bs >= kK4Tile) {
-      // inside one block
-      const int blk = x.e;
-      const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
-      if (lane == 0) {
-        *mask = ok ? 0xffffffffu >> (32 - n) : 0u;
-        mbar_arrive_expect_tx(bar, ok ? (uint32_t)n * kKv4Rec : 0u);
-        if (ok)
-          bulk_g2s(stage, c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p0 & (bs - 1))) * kKv4Rec,
-                   (uint32_t)n * kKv4Rec, bar);
+  const int lane = threadIdx.x & 31, bs = 1 << c.block_shift, sh = c.block_shift;
+  const bool mine = lane < W;
+  K4Cursor x = k4_at(c, ln, t0 + (mine ? lane : 0));
+  if (!mine) x.t = t1;
+  ring += lane * S * kK4StageBytes;
+  full += lane * S;
+  empty += lane * S;
+  masks += lane * S;
+  int k = 0, e0 = -1, e1 = -1;
+  auto fetch = [&]() {
+    if (x.t >= t1) return;
+    const int p = x.i * kK4Tile;
+    e0 = __ldg(x.table + (p >> sh));
+    e1 = (bs < kK4Tile && p + 16 < x.len) ? __ldg(x.table + (p >> sh) + 1) : -1;
+  };
+  fetch();
+  long long idle = clock64();
+  while (__any_sync(0xffffffffu, x.t < t1)) {
+    const int st = k % S;
+    const bool ready = x.t < t1 && (k < S || mbar_test(&empty[st], ((k / S) & 1) ^ 1));
+    if (ready) {
+      const int p = x.i * kK4Tile, n = min(kK4Tile, x.len - p), g = x.s >> a.hshift;
+      const bool ok0 = (unsigned)e0 < (unsigned)c.num_blocks;
+      uint8_t* dst = ring + st * kK4StageBytes;
+      if (bs >= kK4Tile) {
+        masks[st] = ok0 ? 0xffffffffu >> (32 - n) : 0u;
+        mbar_arrive_expect_tx(&full[st], ok0 ? (uint32_t)n * kKv4Rec : 0u);
+        if (ok0)
+          bulk_g2s(dst, c.cache + ((((size_t)e0 * c.n_kv + g) << sh) + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec,
+                   &full[st]);
+      } else {
+        // two blocks of 16
+        const bool ok1 = (unsigned)e1 < (unsigned)c.num_blocks;
+        const int n0 = ok0 ? min(16, n) : 0, n1 = ok1 ? max(0, n - 16) : 0;
+        masks[st] = ((1u << n0) - 1) | ((1u << n1) - 1) << 16;
+        mbar_arrive_expect_tx(&full[st], (uint32_t)(n0 + n1) * kKv4Rec);
+        if (n0 > 0)
+          bulk_g2s(dst, c.cache + (((size_t)e0 * c.n_kv + g) << sh) * kKv4Rec, (uint32_t)n0 * kKv4Rec, &full[st]);
+        if (n1 > 0)
+          bulk_g2s(dst + 16 * kKv4Rec, c.cache + (((size_t)e1 * c.n_kv + g) << sh) * kKv4Rec, (uint32_t)n1 * kKv4Rec,
+                   &full[st]);
       }
+      ++k;
+      k4_step(c, ln, segs, x, W);
+      fetch();
+    }
+    if (__any_sync(0xffffffffu, ready)) {
+      idle = clock64();
     } else {
-      // two blocks of 16, a lane each
-      int rows = 0;
-      const uint8_t* src = nullptr;
-      if (lane < 2 && lane * 16 < n) {
-        const int blk = x.e;
-        if ((unsigned)blk < (unsigned)c.num_blocks) {
-          rows = min(16, n - lane * 16);
-          src = c.cache + (((size_t)blk * c.n_kv + g) << 4) * kKv4Rec;
-        }
+      if (__any_sync(0xffffffffu, clock64() - idle > kK4WaitLimit)) {   // a warp gave up: stop copying
+        set_status(a.status, SPC_ERR_TIMEOUT);
+        break;
       }
-      const uint32_t m = __reduce_or_sync(0xffffffffu, ((1u << rows) - 1) << (16 * (lane & 1)));
-      if (lane == 0) {
-        *mask = m;
-        mbar_arrive_expect_tx(bar, (uint32_t)__popc(m) * kKv4Rec);
-      }
-      __syncwarp();
-      if (rows > 0) bulk_g2s(stage + lane * 16 * kKv4Rec, src, (uint32_t)rows * kKv4Rec, bar);
+      __nanosleep(40);
     }
-  } else {
-    // one record a lane; its nine 16-byte words are dealt to the lanes in
-    // order, so that a warp's copies cover whole records
-    const int p = x.e;
-    const uint8_t* src = nullptr;
-    if (p >= 0 && p < x.len) {
-      const int blk = __ldg(x.table + (p >> c.block_shift));
-      if ((unsigned)blk < (unsigned)c.num_blocks)
-        src = c.cache + ((((size_t)blk * c.n_kv + g) << c.block_shift) + (p & (bs - 1))) * kKv4Rec;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
-    if (lane == 0) *mask = m;
-#pragma unroll
-    for (int k = 0; k < kKv4Rec / 16; ++k) {
-      const int w = 32 * k + lane, r = w / 9, part = w - 9 * r;
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), r));
-      if (s) cp_async16(stage + 16 * w, s + 16 * part, 16);
-    }
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
-    __syncwarp();
   }
+  // every copy lands before the CTA ends
+  for (int j = max(0, k - S); j < k; ++j) mbar_wait_bounded(&full[j % S], (j / S) & 1, kK4WaitLimit);
+  __syncwarp();
+}
+
+// Selected positions: a warp gathers tile x into a stage of its own ring, one
+// record a lane; the records' nine 16-byte words are dealt to the lanes in
+// order, so that a warp's copies cover whole records. sel: this lane's
+// position of the tile, fetched a tile ahead. Each lane arrives on the stage's
+// barrier when its copies have landed.
+__device__ __forceinline__ int k4_position(const Kv4Args& a, const K4Cursor& x) {
+  const Kv4AttnCall& c = a.c;
+  const int i = x.i * kK4Tile + (threadIdx.x & 31);
+  return i < c.budget ? __ldg(c.selected + ((size_t)min(x.b, c.B - 1) * c.n_kv + (x.s >> a.hshift)) * c.budget + i) : -1;
+}
+__device__ __forceinline__ void k4_gather(const Kv4Args& a, const K4Cursor& x, int p, uint8_t* stage, uint64_t* bar,
+                                          uint32_t* mask) {
+  const Kv4AttnCall& c = a.c;
+  const int lane = threadIdx.x & 31, g = x.s >> a.hshift, sh = c.block_shift;
+  const uint8_t* src = nullptr;
+  if (p >= 0 && p < x.len) {
+    const int blk = __ldg(x.table + (p >> sh));
+    if ((unsigned)blk < (unsigned)c.num_blocks)
+      src = c.cache + ((((size_t)blk * c.n_kv + g) << sh) + (p & ((1 << sh) - 1))) * kKv4Rec;
+  }
+  const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
+  if (lane == 0) *mask = m;
+#pragma unroll
+  for (int k = 0; k < kKv4Rec / 16; ++k) {
+    const int w = 32 * k + lane, r = w / 9, part = w - 9 * r;
+    const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), r));
+    if (s) cp_async16(stage + 16 * w, s + 16 * part, 16);
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+  __syncwarp();
 }
 
 // The 32 positions of a stage: logits, weights, sums.
@@ -353,9 +387,9 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
   }
 }
 
-template <int HT>
-__global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Args a) {
-  using Cfg = K4Cfg<HT>;
+template <int HT, bool SEL>
+__global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(Kv4Args a) {
+  using Cfg = K4Cfg<HT, SEL>;
   constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages;
   extern __shared__ __align__(128) uint8_t k4_smem[];
   __shared__ K4Line ln;
@@ -363,14 +397,17 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
   const Kv4AttnCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int G = c.n_q / c.n_kv, segs = c.n_kv << a.hshift, heads = min(8 * HT, G);
-  uint8_t* ring = k4_smem + (uint32_t)warp * kStages * kK4StageBytes;
   float* mrg = reinterpret_cast<float*>(k4_smem + Cfg::kOffMerge);
   uint2* sq = reinterpret_cast<uint2*>(k4_smem + Cfg::kOffQ);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(k4_smem + Cfg::kOffBar) + warp * kStages;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(k4_smem + Cfg::kOffMask) + warp * kStages;
+  uint64_t* all_full = reinterpret_cast<uint64_t*>(k4_smem + Cfg::kOffBar);
+  uint64_t* all_free = all_full + kWarps * kStages;
+  uint32_t* all_masks = reinterpret_cast<uint32_t*>(k4_smem + Cfg::kOffMask);
 
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], c.selected ? 32 : 1);
+  if (warp == 1) {
+    for (int s = lane; s < kWarps * kStages; s += 32) {
+      mbar_init(&all_full[s], SEL ? 32 : 1);
+      mbar_init(&all_free[s], 1);
+    }
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -381,7 +418,7 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
       const int b = 2 * lane + e;
       int L = b < c.B ? c.len[b] : 0;
       L = max(0, min(L, c.max_blocks << c.block_shift));
-      const int nt = b < c.B ? ((c.selected ? c.budget : L) + kK4Tile - 1) / kK4Tile : 0;
+      const int nt = b < c.B ? ((SEL ? c.budget : L) + kK4Tile - 1) / kK4Tile : 0;
       ln.len[b] = L;
       ln.nt[b] = nt;
       n[e] = nt * segs;
@@ -396,26 +433,40 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
   const int run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kK4MinRun);
   const int t0 = min(total, (int)blockIdx.x * run), t1 = min(total, t0 + run);
 
-  // segments without a tile: zeros
-  for (int b = 0; b < c.B; ++b) {
-    if (ln.nt[b] != 0) continue;
-    uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
-    for (int i = blockIdx.x * Cfg::kThreads + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * Cfg::kThreads)
-      dst[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (!SEL && warp == kWarps) {
+    k4_copy<kWarps, kStages>(a, ln, segs, t0, t1, k4_smem, all_full, all_free, all_masks);
+    return;
   }
+  // the warps that compute
+  auto sync = [&]() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory"); };
+  uint8_t* ring = k4_smem + (uint32_t)warp * kStages * kK4StageBytes;
+  uint64_t* full = all_full + warp * kStages;
+  uint64_t* empty = all_free + warp * kStages;
+  uint32_t* masks = all_masks + warp * kStages;
 
   bool dead = false;
   int n_wait = 0;                                    // tiles this warp has waited for
-  K4Cursor nx = k4_at(c, ln, t0 + warp);           // next tile to copy
-  if (nx.t < t1) k4_fetch(a, nx);
-  int n_issued = 0;
-  if (t0 + warp < t1) {
+  K4Cursor nx;                                       // SEL: next tile to gather
+  int n_issued = 0, next_p = -1;
+  if constexpr (SEL) {
+    nx = k4_at(c, ln, t0 + warp);
+    if (nx.t < t1) next_p = k4_position(a, nx);
 #pragma unroll 1
     for (; n_issued < kStages && nx.t < t1; ++n_issued) {
-      k4_issue(a, nx, ring + n_issued * kK4StageBytes, &bars[n_issued], &masks[n_issued]);
+      const K4Cursor x = nx;
+      const int p = next_p;
       k4_step(c, ln, segs, nx, kWarps);
-      if (nx.t < t1) k4_fetch(a, nx);
+      if (nx.t < t1) next_p = k4_position(a, nx);
+      k4_gather(a, x, p, ring + n_issued * kK4StageBytes, &full[n_issued], &masks[n_issued]);
     }
+  }
+
+  // requests without a tile: zeros
+  for (int b = 0; b < c.B; ++b) {
+    if (ln.nt[b] != 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
+    for (int i = blockIdx.x * 32 * kWarps + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * 32 * kWarps)
+      dst[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 
   K4Cursor pc = k4_at(c, ln, min(t0, max(total - 1, 0)));   // the piece at hand
@@ -468,7 +519,7 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
         }
       }
     }
-    if constexpr (HT > 1) __syncthreads();
+    if constexpr (HT > 1) sync();
 
     float m[HT][2], l[HT][2], o[HT][8][4];
 #pragma unroll
@@ -485,12 +536,12 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
 #pragma unroll 1
     for (int t = t0 + warp + k0 * kWarps; t < pe; t += kWarps) {
       const int st = n_wait % kStages;
-      if (!dead && !mbar_wait_bounded(&bars[st], (n_wait / kStages) & 1, kK4WaitLimit)) {
+      if (!dead && !mbar_wait_bounded(&full[st], (n_wait / kStages) & 1, kK4WaitLimit)) {
         set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
       dead = __any_sync(0xffffffffu, dead);
-      if (dead) continue;                            // its barriers are still reached; nothing more is copied
+      if (dead) continue;                            // the other warps' barriers are still reached
       ++n_wait;
       const uint8_t* rows = ring + st * kK4StageBytes;
       const uint32_t valid = masks[st];
@@ -499,11 +550,17 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
       else if (valid != 0)
         k4_step32<HT, false>(rows, valid, sq, qr, f, m, l, o);
       __syncwarp();
-      if (nx.t < t1) {
-        k4_issue(a, nx, ring + st * kK4StageBytes, &bars[st], &masks[st]);
-        ++n_issued;
-        k4_step(c, ln, segs, nx, kWarps);
-        if (nx.t < t1) k4_fetch(a, nx);
+      if constexpr (SEL) {
+        if (nx.t < t1) {
+          const K4Cursor x = nx;
+          const int p = next_p;
+          k4_step(c, ln, segs, nx, kWarps);
+          if (nx.t < t1) next_p = k4_position(a, nx);
+          k4_gather(a, x, p, ring + st * kK4StageBytes, &full[st], &masks[st]);
+          ++n_issued;
+        }
+      } else if (lane == 0) {
+        mbar_arrive(&empty[st]);
       }
     }
 
@@ -539,17 +596,20 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
           dst[e * kK4Part + 1] = ll[e];
         }
       }
-      __syncthreads();
-      const int h = 8 * n + warp;                    // warp w < 8 merges head w of the eight
-      if (warp < 8 && h < heads) {
+      sync();
+#pragma unroll 1
+      for (int e = warp; e < 8; e += kWarps) {       // head e of the eight
+        const int h = 8 * n + e;
+        if (h >= heads) break;
         float M = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * 8 + warp) * kK4Part]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * 8 + e) * kK4Part]);
         const float Ms = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float* src = mrg + (size_t)(w * 8 + warp) * kK4Part;
+          const float* src = mrg + (size_t)(w * 8 + e) * kK4Part;
           const float wt = k4_ex2(src[0] - Ms);
           const float4 x = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
           L += wt * src[1];
@@ -568,13 +628,13 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
           *reinterpret_cast<float4*>(p + 4 + 4 * lane) = v;
         }
       }
-      __syncthreads();
+      sync();
     }
     if (!whole) {
       __threadfence();
-      __syncthreads();
+      sync();
       if (threadIdx.x == 0) s_last = atomicAdd(&a.counters[seg], 1u) == (uint32_t)(w1 - w0);
-      __syncthreads();
+      sync();
       if (s_last) {
         __threadfence();
         // a lane reads one piece's (m, l); then the pieces' O, several in flight
@@ -612,13 +672,14 @@ __global__ void __launch_bounds__(K4Cfg<HT>::kThreads, 1) kv4_attn_kernel(Kv4Arg
         }
         if (threadIdx.x == 0) a.counters[seg] = 0u;
       }
-      __syncthreads();
+      sync();
     }
     k4_step(c, ln, segs, pc, pe - pt);
     pt = pe;
   }
   // copies that nobody waited for (a wait gave up) land before the CTA ends
-  for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&bars[n_wait % kStages], (n_wait / kStages) & 1, kK4WaitLimit);
+  if constexpr (SEL)
+    for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&full[n_wait % kStages], (n_wait / kStages) & 1, kK4WaitLimit);
 }
 
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
@@ -629,11 +690,11 @@ size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int) {
   return 256 + k4_round((size_t)B * n_kv * hsplit * 4) + (size_t)kK4Ctas * 2 * 8 * ht * kK4Part * 4;
 }
 
-template <int HT>
+template <int HT, bool SEL>
 static int k4_run(const Kv4Args& a, void* stream) {
-  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K4Cfg<HT>::kSmem);
+  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K4Cfg<HT, SEL>::kSmem);
   if (e != cudaSuccess) return SPC_ERR_CUDA;
-  kv4_attn_kernel<HT><<<kK4Ctas, K4Cfg<HT>::kThreads, K4Cfg<HT>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
+  kv4_attn_kernel<HT, SEL><<<kK4Ctas, K4Cfg<HT, SEL>::kThreads, K4Cfg<HT, SEL>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
@@ -648,9 +709,9 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
   a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * 4));
   switch (a.ht) {
-    case 1: return k4_run<1>(a, stream);
-    case 2: return k4_run<2>(a, stream);
-    default: return k4_run<4>(a, stream);
+    case 1: return c.selected ? k4_run<1, true>(a, stream) : k4_run<1, false>(a, stream);
+    case 2: return c.selected ? k4_run<2, true>(a, stream) : k4_run<2, false>(a, stream);
+    default: return c.selected ? k4_run<4, true>(a, stream) : k4_run<4, false>(a, stream);
   }
 }
 
