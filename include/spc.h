@@ -470,7 +470,7 @@ int spc_mla_decode_attn(const void* q, const void* Wuk, const void* Wuv, const s
  *   bytes 136 .. 143  V scales
  * Value = code * scale of its group; every such product is exact in bf16.
  * Cache: uint8 [num_blocks][n_kv][block_size][144], 16-byte aligned,
- * block_size in {16, 32, 64, 128}, num_blocks * block_size < 2^31. Slot s is
+ * block_size in {16, 32, 64, 128}, num_blocks * n_kv * block_size < 2^31. Slot s is
  * position s % block_size of block s / block_size. A block table row
  * int32 [max_blocks] names the block of each block_size positions of one
  * request; max_blocks * block_size <= SPC_MAX_CAP.

@@ -401,8 +401,11 @@ int spc_mla_decode_attn(const void* q, const void* Wuk, const void* Wuv, const s
 static int block_shift_of(int block_size) {
   return block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : block_size == 128 ? 7 : -1;
 }
-static bool pool_ok(int num_blocks, int block_size) {
-  return num_blocks >= 1 && block_shift_of(block_size) > 0 && (long long)num_blocks * block_size < (1ll << 31);
+// a pool whose records of all heads are counted in 31 bits: 2^31 of them are
+// 309 GB, more than the device has
+static bool pool_ok(int num_blocks, int block_size, int n_heads) {
+  return num_blocks >= 1 && block_shift_of(block_size) > 0 && n_heads >= 1 && n_heads <= 1024 &&
+         (long long)num_blocks * block_size * n_heads < (1ll << 31);
 }
 static bool table_ok(int max_blocks, int block_size) {
   return max_blocks >= 1 && (long long)max_blocks * block_size <= SPC_MAX_CAP;
@@ -419,7 +422,7 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
   if (!aligned4(len) || !aligned4(len_next) || !aligned4(block_table) || !aligned4(free_list) || !aligned4(n_free) ||
       !aligned4(n_free_next) || !aligned4(cu_new) || !aligned4(slot_map) || !aligned4(status))
     return SPC_ERR_INVALID_ARG;
-  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size) || !table_ok(max_blocks, block_size))
+  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, 1) || !table_ok(max_blocks, block_size))
     return SPC_ERR_SHAPE;
   if (n_slots < 1 || n_slots > kMaxRows) return SPC_ERR_SHAPE;
   BlockMapCall c{};
@@ -432,7 +435,7 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
 
 static int kv4_rows_check(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
                           const void* cache, int T, int n_kv, int d, int num_blocks, int block_size) {
-  if (d != SPC_HEAD_DIM || n_kv < 1 || n_kv > 1024 || T < 0 || T > kMaxRows || !pool_ok(num_blocks, block_size))
+  if (d != SPC_HEAD_DIM || n_kv < 1 || n_kv > 1024 || T < 0 || T > kMaxRows || !pool_ok(num_blocks, block_size, n_kv))
     return SPC_ERR_SHAPE;
   if (T == 0) return SPC_OK;
   if (!k || !v || !slot_map || !cache) return SPC_ERR_INVALID_ARG;
@@ -489,7 +492,7 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
       !aligned4(selected))
     return SPC_ERR_INVALID_ARG;
   if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > 1024) return SPC_ERR_SHAPE;
-  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size) || !table_ok(max_blocks, block_size))
+  if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, n_kv) || !table_ok(max_blocks, block_size))
     return SPC_ERR_SHAPE;
   if (budget < 0 || budget > SPC_MAX_BUDGET) return SPC_ERR_SHAPE;
   if (!(scale > 0.f) || scale > 3e38f) return SPC_ERR_INVALID_ARG;

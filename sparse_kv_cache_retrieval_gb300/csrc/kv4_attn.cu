@@ -49,15 +49,18 @@ constexpr int kK4MinRun = 32;                        // tiles a CTA takes at lea
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
+
 constexpr float kK4Headroom = 8.f;
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
-// The CTA of a kernel for HT head tiles. Whole context: the last warp copies
-// for the others; selected positions: each warp gathers for itself.
+// The CTA of a kernel for HT head tiles; the last warps copy for the others:
+// one where the whole context is read, 5 (or 2 of 8) where positions are
+// gathered (64 segments of 4096: 2 warps 30 us, 3 25, 4 23, 5 22, 6 22).
 template <int HT, bool SEL>
 struct K4Cfg {
   static constexpr int kAll = HT == 1 ? 16 : 8;        // warps
-  static constexpr int kWarps = SEL ? kAll : kAll - 1; // warps that compute
+  static constexpr int kCopy = !SEL ? 1 : HT == 1 ? 5 : 2;
+  static constexpr int kWarps = kAll - kCopy;          // warps that compute
   static constexpr int kStages = HT == 1 ? 2 : 4;      // tiles in a warp's ring
   static constexpr int kThreads = 32 * kAll;
   // shared memory
@@ -224,36 +227,92 @@ __device__ __forceinline__ void k4_copy(const Kv4Args& a, const K4Line& ln, int 
   __syncwarp();
 }
 
-// Selected positions: a warp gathers tile x into a stage of its own ring, one
-// record a lane; the records' nine 16-byte words are dealt to the lanes in
-// order, so that a warp's copies cover whole records. sel: this lane's
-// position of the tile, fetched a tile ahead. Each lane arrives on the stage's
-// barrier when its copies have landed.
-__device__ __forceinline__ int k4_position(const Kv4Args& a, const K4Cursor& x) {
+// Selected positions: copying warp w of N takes the run's tiles w, w + N, ...,
+// one position a lane. A position is fetched four tiles ahead of its copy and
+// its table entry two; the 32 records' nine 16-byte words each are dealt to
+// the lanes in order, so that an instruction's copies cover whole records.
+// (One cp.async.bulk of 144 bytes a record measured 70 cycles each: 74 us
+// against 22 at 64 segments of 4096 positions.) Each lane arrives on the stage's
+// barrier when its copies have landed, and lane 0 once the mask is written.
+template <int W, int S, int N>
+__device__ __forceinline__ void k4_gather(const Kv4Args& a, const K4Line& ln, int segs, int t0, int t1, int w, uint8_t* ring,
+                                          uint64_t* full, uint64_t* empty, uint32_t* masks) {
   const Kv4AttnCall& c = a.c;
-  const int i = x.i * kK4Tile + (threadIdx.x & 31);
-  return i < c.budget ? __ldg(c.selected + ((size_t)min(x.b, c.B - 1) * c.n_kv + (x.s >> a.hshift)) * c.budget + i) : -1;
-}
-__device__ __forceinline__ void k4_gather(const Kv4Args& a, const K4Cursor& x, int p, uint8_t* stage, uint64_t* bar,
-                                          uint32_t* mask) {
-  const Kv4AttnCall& c = a.c;
-  const int lane = threadIdx.x & 31, g = x.s >> a.hshift, sh = c.block_shift;
-  const uint8_t* src = nullptr;
-  if (p >= 0 && p < x.len) {
-    const int blk = __ldg(x.table + (p >> sh));
-    if ((unsigned)blk < (unsigned)c.num_blocks)
-      src = c.cache + ((((size_t)blk * c.n_kv + g) << sh) + (p & ((1 << sh) - 1))) * kKv4Rec;
-  }
-  const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
-  if (lane == 0) *mask = m;
+  const int lane = threadIdx.x & 31, sh = c.block_shift;
+  constexpr int kWords = kKv4Rec / 16;
+  struct Tile {
+    int p, blk, len, g;
+    const int32_t* table;
+  };
+  K4Cursor x = k4_at(c, ln, min(t0 + w, max(ln.pre[c.B] - 1, 0)));
+  auto position = [&](Tile& y, int t) {             // x is at tile t
+    y.p = -1;
+    y.blk = -1;
+    if (t >= t1) return;
+    const int i = x.i * kK4Tile + lane;
+    y.len = x.len;
+    y.table = x.table;
+    y.g = x.s >> a.hshift;
+    if (i < c.budget) y.p = __ldg(c.selected + ((size_t)x.b * c.n_kv + y.g) * c.budget + i);
+    k4_step(c, ln, segs, x, N);
+  };
+  auto lookup = [&](Tile& y) {
+    if (y.p >= 0 && y.p < y.len) y.blk = __ldg(y.table + (y.p >> sh));
+  };
+  // word 32 k + lane of a tile: its record and its address in the cache but for the record
+  int row[kWords];
+  const uint8_t* word[kWords];
 #pragma unroll
-  for (int k = 0; k < kKv4Rec / 16; ++k) {
-    const int w = 32 * k + lane, r = w / 9, part = w - 9 * r;
-    const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), r));
-    if (s) cp_async16(stage + 16 * w, s + 16 * part, 16);
+  for (int k = 0; k < kWords; ++k) {
+    row[k] = (32 * k + lane) / kWords;
+    word[k] = c.cache + 16 * (32 * k + lane - kWords * row[k]);
   }
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
-  __syncwarp();
+  // tiles in flight, by turns without moves (a move would wait for its load)
+  Tile q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) position(q[j], t0 + w + j * N);
+  lookup(q[0]);
+  lookup(q[1]);
+  bool dead = false;
+  int wp = w, use = 0;                              // the tile is the use-th of warp wp
+#pragma unroll 1
+  for (int t = t0 + w; t < t1 && !dead;) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (t >= t1 || dead) break;
+      lookup(q[(j + 2) & 3]);
+      const int slot = wp * S + use % S;
+      if (use >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], ((use / S) & 1) ^ 1, kK4WaitLimit))) {
+        dead = true;
+        break;
+      }
+      const bool ok = (unsigned)q[j].blk < (unsigned)c.num_blocks;
+      const uint32_t m = __ballot_sync(0xffffffffu, ok);
+      const uint32_t rec = (((uint32_t)q[j].blk * c.n_kv + q[j].g) << sh) + (q[j].p & ((1 << sh) - 1));
+      uint8_t* dst = ring + (uint32_t)slot * kK4StageBytes + 16 * lane;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t r = __shfl_sync(0xffffffffu, rec, row[k]);
+        if ((m >> row[k]) & 1u) cp_async16(dst + 512 * k, word[k] + (size_t)r * kKv4Rec, 16);
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full[slot])) : "memory");
+      if (lane == 0) {
+        masks[slot] = m;
+        mbar_arrive(&full[slot]);
+      }
+      position(q[j], t + 4 * N);
+      t += N;
+      wp += N;
+      if (wp >= W) {
+        wp -= W;
+        ++use;
+      }
+    }
+  }
+  if (dead && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+  // every copy lands before the CTA ends
+  cp_async_commit();
+  cp_async_wait<0>();
 }
 
 // The 32 positions of a stage: logits, weights, sums.
@@ -405,7 +464,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
 
   if (warp == 1) {
     for (int s = lane; s < kWarps * kStages; s += 32) {
-      mbar_init(&all_full[s], SEL ? 32 : 1);
+      mbar_init(&all_full[s], SEL ? 33 : 1);
       mbar_init(&all_free[s], 1);
     }
     fence_mbar_init();
@@ -433,8 +492,11 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
   const int run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kK4MinRun);
   const int t0 = min(total, (int)blockIdx.x * run), t1 = min(total, t0 + run);
 
-  if (!SEL && warp == kWarps) {
-    k4_copy<kWarps, kStages>(a, ln, segs, t0, t1, k4_smem, all_full, all_free, all_masks);
+  if (warp >= kWarps) {
+    if constexpr (SEL)
+      k4_gather<kWarps, kStages, Cfg::kCopy>(a, ln, segs, t0, t1, warp - kWarps, k4_smem, all_full, all_free, all_masks);
+    else
+      k4_copy<kWarps, kStages>(a, ln, segs, t0, t1, k4_smem, all_full, all_free, all_masks);
     return;
   }
   // the warps that compute
@@ -446,20 +508,6 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
 
   bool dead = false;
   int n_wait = 0;                                    // tiles this warp has waited for
-  K4Cursor nx;                                       // SEL: next tile to gather
-  int n_issued = 0, next_p = -1;
-  if constexpr (SEL) {
-    nx = k4_at(c, ln, t0 + warp);
-    if (nx.t < t1) next_p = k4_position(a, nx);
-#pragma unroll 1
-    for (; n_issued < kStages && nx.t < t1; ++n_issued) {
-      const K4Cursor x = nx;
-      const int p = next_p;
-      k4_step(c, ln, segs, nx, kWarps);
-      if (nx.t < t1) next_p = k4_position(a, nx);
-      k4_gather(a, x, p, ring + n_issued * kK4StageBytes, &full[n_issued], &masks[n_issued]);
-    }
-  }
 
   // requests without a tile: zeros
   for (int b = 0; b < c.B; ++b) {
@@ -550,18 +598,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
       else if (valid != 0)
         k4_step32<HT, false>(rows, valid, sq, qr, f, m, l, o);
       __syncwarp();
-      if constexpr (SEL) {
-        if (nx.t < t1) {
-          const K4Cursor x = nx;
-          const int p = next_p;
-          k4_step(c, ln, segs, nx, kWarps);
-          if (nx.t < t1) next_p = k4_position(a, nx);
-          k4_gather(a, x, p, ring + st * kK4StageBytes, &full[st], &masks[st]);
-          ++n_issued;
-        }
-      } else if (lane == 0) {
-        mbar_arrive(&empty[st]);
-      }
+      if (lane == 0) mbar_arrive(&empty[st]);
     }
 
     // ---- merge of the warps' partials, 8 heads at a time
@@ -677,9 +714,6 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     k4_step(c, ln, segs, pc, pe - pt);
     pt = pe;
   }
-  // copies that nobody waited for (a wait gave up) land before the CTA ends
-  if constexpr (SEL)
-    for (; n_wait < n_issued; ++n_wait) mbar_wait_bounded(&full[n_wait % kStages], (n_wait / kStages) & 1, kK4WaitLimit);
 }
 
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
@@ -692,7 +726,8 @@ size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int) {
 
 template <int HT, bool SEL>
 static int k4_run(const Kv4Args& a, void* stream) {
-  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K4Cfg<HT, SEL>::kSmem);
+  cudaError_t e = set_func_attr((const void*)kv4_attn_kernel<HT, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)K4Cfg<HT, SEL>::kSmem);
   if (e != cudaSuccess) return SPC_ERR_CUDA;
   kv4_attn_kernel<HT, SEL><<<kK4Ctas, K4Cfg<HT, SEL>::kThreads, K4Cfg<HT, SEL>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
