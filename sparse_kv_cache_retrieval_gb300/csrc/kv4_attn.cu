@@ -50,6 +50,7 @@ constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
 
+constexpr int kK4Slack = 32;
 constexpr float kK4Headroom = 8.f;
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
@@ -113,7 +114,16 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 struct K4Line {
   int pre[SPC_MAX_BATCH + 1];
   int nt[SPC_MAX_BATCH];       // tiles a segment of request b
+  int run;                     // tiles a CTA takes; 2^30: runs end with their segments
+  int t0, t1;                  // this CTA's run
+  int first, last;             // whole runs: the CTAs of its segment
   int len[SPC_MAX_BATCH];
+};
+
+// a segment whose tiles several CTAs share: its index, request, first head,
+// first tile, first and last CTA, tiles a run
+struct K4Open {
+  int seg, b, h0, s0, w0, w1, run;
 };
 
 // a tile of the line: tile i of segment (b, s), s = (g << hshift) + hh, with what
@@ -446,6 +456,78 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
   }
 }
 
+// The last CTA to arrive at a segment merges its CTAs' partials, in CTA order.
+// kMg heads at a time: the pieces' (m, l) to shared memory, a weight per (head,
+// piece), then O by (head, float4) items, kFly loads in flight, the first of
+// them ahead of the weights.
+
+template <int HT, int W>
+__device__ __forceinline__ void k4_merge(const Kv4Args& a, const K4Open& u, int heads, float* mrg) {
+  const Kv4AttnCall& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto sync = [&]() { asm volatile("bar.sync 1, %0;" :: "n"(32 * W) : "memory"); };
+  constexpr int kMg = HT == 1 ? 8 : 16, kFly = 8;
+  const int np = u.w1 - u.w0 + 1;
+  float2* wl = reinterpret_cast<float2*>(mrg);                  // [kMg][kK4Ctas]
+  float* lsum = mrg + 2 * kMg * kK4Ctas;                        // [kMg]
+  static_assert((2 * kMg * kK4Ctas + kMg) * 4 <= W * 8 * kK4Part * 4, "merge scratch");
+  auto piece = [&](int i, int h) {
+    const int w = u.w0 + i;
+    return a.part + (((size_t)w * 2 + (u.run < (1 << 30) && u.s0 > w * u.run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
+  };
+#pragma unroll 1
+  for (int hb = 0; hb < heads; hb += kMg) {
+    const int nh = min(kMg, heads - hb);
+    float4 x[kFly];
+    auto load = [&](int i, int q0) {
+#pragma unroll
+      for (int q = 0; q < kFly; ++q)
+        if (q0 + q < np) x[q] = __ldcg(reinterpret_cast<const float4*>(piece(q0 + q, hb + (i >> 5)) + 4) + (i & 31));
+    };
+    if (threadIdx.x < nh * 32) load(threadIdx.x, 0);
+    for (int i = threadIdx.x; i < nh * np; i += 32 * W) {
+      const int h = i / np, q = i - h * np;
+      wl[h * kK4Ctas + q] = __ldcg(reinterpret_cast<const float2*>(piece(q, hb + h)));
+    }
+    sync();
+    for (int h = warp; h < nh; h += W) {
+      float M = -INFINITY;
+      for (int q = lane; q < np; q += 32) M = fmaxf(M, wl[h * kK4Ctas + q].x);
+      M = warp_max(M);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      for (int q = lane; q < np; q += 32) {
+        const float2 ml = wl[h * kK4Ctas + q];
+        const float wt = k4_ex2(ml.x - Ms);
+        L += wt * ml.y;
+        wl[h * kK4Ctas + q].x = wt;
+      }
+      L = warp_sum(L);
+      if (lane == 0) lsum[h] = L == 0.f ? 0.f : 1.f / L;
+    }
+    sync();
+    for (int i = threadIdx.x; i < nh * 32; i += 32 * W) {
+      const int h = i >> 5, f4 = i & 31;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int q0 = 0; q0 < np; q0 += kFly) {
+        if (q0 > 0 || i != threadIdx.x) load(i, q0);
+#pragma unroll
+        for (int q = 0; q < kFly; ++q) {
+          if (q0 + q >= np) break;
+          const float w = wl[h * kK4Ctas + q0 + q].x;
+          v.x += w * x[q].x; v.y += w * x[q].y; v.z += w * x[q].z; v.w += w * x[q].w;
+        }
+      }
+      const float r = lsum[h];
+      *reinterpret_cast<uint2*>(c.out + ((size_t)u.b * c.n_q + u.h0 + hb + h) * kD + 4 * f4) =
+          make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+    }
+    sync();
+  }
+  if (threadIdx.x == 0) a.counters[u.seg] = 0u;
+}
+
 template <int HT, bool SEL>
 __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(Kv4Args a) {
   using Cfg = K4Cfg<HT, SEL>;
@@ -486,11 +568,51 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     ln.pre[2 * lane] = incl - n[0] - n[1];
     ln.pre[2 * lane + 1] = incl - n[1];
     if (lane == 31) ln.pre[SPC_MAX_BATCH] = incl;
+    // Equal runs of the line, or runs that end with their segment where a run
+    // of at most kK4Slack more tiles allows that: a second piece costs a CTA
+    // as much (queries, merge, fence) and the segments' last merges wait for it
+    const int total = __shfl_sync(0xffffffffu, incl, 31), grid = gridDim.x;
+    const int even = max((total + grid - 1) / grid, kK4MinRun);
+    const int nt0 = ln.nt[2 * lane], nt1 = ln.nt[2 * lane + 1], blk = blockIdx.x;
+    int run = even, np0 = 0, np1 = 0;                // pieces a segment
+    bool whole = false;
+#pragma unroll 1
+    for (int k = 0; k <= 2 && !whole; ++k) {
+      run = even + k * (kK4Slack / 2);
+      np0 = (nt0 + run - 1) / run;
+      np1 = (nt1 + run - 1) / run;
+      whole = (int)__reduce_add_sync(0xffffffffu, (unsigned)((np0 + np1) * segs)) <= grid;
+    }
+    int t0, t1, first = 0, last = 0;
+    if (whole) {
+      const int end = warp_incl_scan((np0 + np1) * segs), c0 = end - (np0 + np1) * segs, c1 = end - np1 * segs;
+      // the last request whose segments start at or before this CTA
+      const int e = __popc(__ballot_sync(0xffffffffu, c0 <= blk)) + __popc(__ballot_sync(0xffffffffu, c1 <= blk)) - 1;
+      const int np = __shfl_sync(0xffffffffu, e & 1 ? np1 : np0, e >> 1), nt = __shfl_sync(0xffffffffu, e & 1 ? nt1 : nt0, e >> 1);
+      const int c0e = __shfl_sync(0xffffffffu, e & 1 ? c1 : c0, e >> 1);
+      t0 = t1 = total;
+      if (blk < __shfl_sync(0xffffffffu, end, 31)) {
+        const int r = blk - c0e, sg = r / np, q = r - sg * np, s0 = ln.pre[e] + sg * nt;
+        first = blk - q;
+        last = first + np - 1;
+        t0 = s0 + nt * q / np;
+        t1 = s0 + nt * (q + 1) / np;
+      }
+    } else {
+      run = even;
+      t0 = min(total, blk * run);
+      t1 = min(total, t0 + run);
+    }
+    if (lane == 0) {
+      ln.run = whole ? 1 << 30 : run;
+      ln.t0 = t0;
+      ln.t1 = t1;
+      ln.first = first;
+      ln.last = last;
+    }
   }
   __syncthreads();
-  const int total = ln.pre[c.B];
-  const int run = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kK4MinRun);
-  const int t0 = min(total, (int)blockIdx.x * run), t1 = min(total, t0 + run);
+  const int total = ln.pre[c.B], t0 = ln.t0, t1 = ln.t1;
 
   if (warp >= kWarps) {
     if constexpr (SEL)
@@ -604,9 +726,11 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     // ---- merge of the warps' partials, 8 heads at a time
     const int seg = b * segs + sg;
     const int s0 = pt - pc.i, s1 = s0 + nt;          // the segment's tiles in the line
-    const int w0 = s0 / run, w1 = (s1 - 1) / run;    // CTAs that have a piece of it
+    // CTAs that have a piece of it
+    const int run = ln.run, ends = run == 1 << 30;
+    const int w0 = ends ? ln.first : s0 / run, w1 = ends ? ln.last : (s1 - 1) / run;
     const bool whole = w0 == w1;
-    float* res = a.part + ((size_t)blockIdx.x * 2 + (s0 > t0 ? 1 : 0)) * (size_t)(8 * HT) * kK4Part;
+    float* res = a.part + ((size_t)blockIdx.x * 2 + (!ends && s0 > t0 ? 1 : 0)) * (size_t)(8 * HT) * kK4Part;
 #pragma unroll 1
     for (int n = 0; n < HT; ++n) {
       float mm[2], ll[2];
@@ -674,42 +798,8 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
       sync();
       if (s_last) {
         __threadfence();
-        // a lane reads one piece's (m, l); then the pieces' O, several in flight
-        const int np = w1 - w0 + 1;
-        for (int h = warp; h < heads; h += kWarps) {
-          auto piece = [&](int i) {
-            const int w = w0 + i;
-            return a.part + (((size_t)w * 2 + (s0 > w * run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
-          };
-          float M = -INFINITY;
-          for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(piece(i)));
-          M = warp_max(M);
-          const float Ms = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i0 = 0; i0 < np; i0 += 32) {
-            float wt = 0.f, lt = 0.f;
-            if (i0 + lane < np) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane)));
-              wt = k4_ex2(ml.x - Ms);
-              lt = wt * ml.y;
-            }
-            L += warp_sum(lt);
-            const int ne = min(32, np - i0);
-#pragma unroll 8
-            for (int i = 0; i < ne; ++i) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 4) + lane);
-              const float w = __shfl_sync(0xffffffffu, wt, i);
-              v.x += w * x.x; v.y += w * x.y; v.z += w * x.z; v.w += w * x.w;
-            }
-          }
-          const float r = L == 0.f ? 0.f : 1.f / L;
-          *reinterpret_cast<uint2*>(c.out + ((size_t)b * c.n_q + h0 + h) * kD + 4 * lane) =
-              make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
-        }
-        if (threadIdx.x == 0) a.counters[seg] = 0u;
+        k4_merge<HT, kWarps>(a, K4Open{seg, b, h0, s0, w0, w1, run}, heads, mrg);
       }
-      sync();
     }
     k4_step(c, ln, segs, pc, pe - pt);
     pt = pe;
