@@ -487,13 +487,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
-          const int seen = qpos - j * kPaKeys;        // columns 0 .. seen are visible
+          // columns 0 .. seen are visible, 0 .. seen0 to every row of the warp
+          const int seen = qpos - j * kPaKeys, seen0 = t0 + (((warp & 3) * 32) >> a.gshift) - j * kPaKeys;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             pa_ld_wait(s + 32 * q);
+            if (seen0 < 32 * q + 31) {
 #pragma unroll
-            for (int e = 32 * q; e < 32 * q + 32; ++e)
-              if (e > seen) s[e] = -INFINITY;
+              for (int e = 32 * q; e < 32 * q + 32; ++e)
+                if (e > seen) s[e] = -INFINITY;
+            }
             pa_max32(s + 32 * q, mx);
           }
           M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
