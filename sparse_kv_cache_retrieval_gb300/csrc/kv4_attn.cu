@@ -45,12 +45,10 @@
 namespace spc {
 
 constexpr int kK4Tile = 32;                          // positions a tile
-constexpr int kK4MinRun = 32;                        // tiles a CTA takes at least
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
 
-constexpr int kK4Slack = 32;
 constexpr float kK4Headroom = 8.f;
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
@@ -63,6 +61,8 @@ struct K4Cfg {
   static constexpr int kCopy = !SEL ? 1 : HT == 1 ? 5 : 2;
   static constexpr int kWarps = kAll - kCopy;          // warps that compute
   static constexpr int kStages = HT == 1 ? 2 : 4;      // tiles in a warp's ring
+  static constexpr int kMinRun = 2 * kAll;             // tiles a CTA takes before a segment is split
+  static constexpr int kSlack = 2 * kAll;              // tiles that a second piece costs a CTA, about
   static constexpr int kThreads = 32 * kAll;
   // shared memory
   static constexpr uint32_t kOffMerge = kWarps * kStages * kK4StageBytes;              // [warps][8 heads][kK4Part]
@@ -302,6 +302,7 @@ __device__ __forceinline__ void k4_gather(const Kv4Args& a, const K4Line& ln, in
       uint8_t* dst = ring + (uint32_t)slot * kK4StageBytes + 16 * lane;
 #pragma unroll
       for (int k = 0; k < kWords; ++k) {
+        if (m == 0) break;
         const uint32_t r = __shfl_sync(0xffffffffu, rec, row[k]);
         if ((m >> row[k]) & 1u) cp_async16(dst + 512 * k, word[k] + (size_t)r * kKv4Rec, 16);
       }
@@ -568,26 +569,42 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     ln.pre[2 * lane] = incl - n[0] - n[1];
     ln.pre[2 * lane + 1] = incl - n[1];
     if (lane == 31) ln.pre[SPC_MAX_BATCH] = incl;
-    // Equal runs of the line, or runs that end with their segment where a run
-    // of at most kK4Slack more tiles allows that: a second piece costs a CTA
-    // as much (queries, merge, fence) and the segments' last merges wait for it
-    const int total = __shfl_sync(0xffffffffu, incl, 31), grid = gridDim.x;
-    const int even = max((total + grid - 1) / grid, kK4MinRun);
-    const int nt0 = ln.nt[2 * lane], nt1 = ln.nt[2 * lane + 1], blk = blockIdx.x;
-    int run = even, np0 = 0, np1 = 0;                // pieces a segment
-    bool whole = false;
-#pragma unroll 1
+    // Which tiles of the line this CTA takes. A second piece costs a CTA about
+    // kSlack tiles (queries, merge, fence), and a split segment waits for its
+    // last piece, so runs end with their segments where they can:
+    //  - segments of at most kMinRun tiles are never split: each CTA takes those
+    //    that start in its share of the line;
+    //  - with fewer segments than CTAs, each gets a number of CTAs of its own,
+    //    if that makes no run longer than kSlack tiles above an equal share;
+    //  - else equal runs of the line.
+    const int total = __shfl_sync(0xffffffffu, incl, 31), grid = gridDim.x, blk = blockIdx.x;
+    const int nt0 = ln.nt[2 * lane], nt1 = ln.nt[2 * lane + 1];
+    int run = max((total + grid - 1) / grid, Cfg::kMinRun), np0 = 0, np1 = 0;      // np: pieces a segment
+    const bool small = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(nt0, nt1)) <= Cfg::kMinRun;
+    bool whole = small;
     for (int k = 0; k <= 2 && !whole; ++k) {
-      run = even + k * (kK4Slack / 2);
-      np0 = (nt0 + run - 1) / run;
-      np1 = (nt1 + run - 1) / run;
+      const int r = run + k * (Cfg::kSlack / 2);
+      np0 = (nt0 + r - 1) / r;
+      np1 = (nt1 + r - 1) / r;
       whole = (int)__reduce_add_sync(0xffffffffu, (unsigned)((np0 + np1) * segs)) <= grid;
     }
-    int t0, t1, first = 0, last = 0;
-    if (whole) {
+    int t0, t1, first = blk, last = blk;
+    // the last request that starts at or before x (the starts s0, s1 of this lane's two)
+    auto find = [&](int s0, int s1, int x) {
+      return __popc(__ballot_sync(0xffffffffu, s0 <= x)) + __popc(__ballot_sync(0xffffffffu, s1 <= x)) - 1;
+    };
+    if (small) {
+      const int s0 = incl - n[0] - n[1], s1 = incl - n[1];
+      auto start = [&](int x) {                      // of the first segment that starts at or behind tile x
+        const int e = find(s0, s1, x), nt = max(1, __shfl_sync(0xffffffffu, e & 1 ? nt1 : nt0, e >> 1));
+        const int p = __shfl_sync(0xffffffffu, e & 1 ? s1 : s0, e >> 1);
+        return min(total, p + (x - p + nt - 1) / nt * nt);
+      };
+      t0 = start(total * blk / grid);          // total is at most 2^22 here
+      t1 = start(total * (blk + 1) / grid);
+    } else if (whole) {
       const int end = warp_incl_scan((np0 + np1) * segs), c0 = end - (np0 + np1) * segs, c1 = end - np1 * segs;
-      // the last request whose segments start at or before this CTA
-      const int e = __popc(__ballot_sync(0xffffffffu, c0 <= blk)) + __popc(__ballot_sync(0xffffffffu, c1 <= blk)) - 1;
+      const int e = find(c0, c1, blk);
       const int np = __shfl_sync(0xffffffffu, e & 1 ? np1 : np0, e >> 1), nt = __shfl_sync(0xffffffffu, e & 1 ? nt1 : nt0, e >> 1);
       const int c0e = __shfl_sync(0xffffffffu, e & 1 ? c1 : c0, e >> 1);
       t0 = t1 = total;
@@ -599,7 +616,6 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
         t1 = s0 + nt * (q + 1) / np;
       }
     } else {
-      run = even;
       t0 = min(total, blk * run);
       t1 = min(total, t0 + run);
     }
