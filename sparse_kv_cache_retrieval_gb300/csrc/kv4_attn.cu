@@ -38,6 +38,8 @@
 // them in CTA order (deterministic).
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kv4.cuh"
 #include "spc_device.cuh"
 #include "spc_internal.h"
@@ -79,6 +81,8 @@ struct Kv4Args {
   int* status;
   uint32_t* counters;
   float* part;
+  long long wait_limit;
+  int starve;        // test builds: no copy is issued, so that every wait runs out
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -225,7 +229,7 @@ __device__ __forceinline__ void k4_copy(const Kv4Args& a, const K4Line& ln, int 
     if (__any_sync(0xffffffffu, ready)) {
       idle = clock64();
     } else {
-      if (__any_sync(0xffffffffu, clock64() - idle > kK4WaitLimit)) {   // a warp gave up: stop copying
+      if (__any_sync(0xffffffffu, clock64() - idle > a.wait_limit)) {   // a warp gave up: stop copying
         set_status(a.status, SPC_ERR_TIMEOUT);
         break;
       }
@@ -233,7 +237,7 @@ __device__ __forceinline__ void k4_copy(const Kv4Args& a, const K4Line& ln, int 
     }
   }
   // every copy lands before the CTA ends
-  for (int j = max(0, k - S); j < k; ++j) mbar_wait_bounded(&full[j % S], (j / S) & 1, kK4WaitLimit);
+  for (int j = max(0, k - S); j < k; ++j) mbar_wait_bounded(&full[j % S], (j / S) & 1, a.wait_limit);
   __syncwarp();
 }
 
@@ -292,7 +296,7 @@ __device__ __forceinline__ void k4_gather(const Kv4Args& a, const K4Line& ln, in
       if (t >= t1 || dead) break;
       lookup(q[(j + 2) & 3]);
       const int slot = wp * S + use % S;
-      if (use >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], ((use / S) & 1) ^ 1, kK4WaitLimit))) {
+      if (use >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], ((use / S) & 1) ^ 1, a.wait_limit))) {
         dead = true;
         break;
       }
@@ -631,6 +635,9 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
   const int total = ln.pre[c.B], t0 = ln.t0, t1 = ln.t1;
 
   if (warp >= kWarps) {
+#ifdef SPC_TEST_HOOKS
+    if (a.starve) return;
+#endif
     if constexpr (SEL)
       k4_gather<kWarps, kStages, Cfg::kCopy>(a, ln, segs, t0, t1, warp - kWarps, k4_smem, all_full, all_free, all_masks);
     else
@@ -722,7 +729,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
 #pragma unroll 1
     for (int t = t0 + warp + k0 * kWarps; t < pe; t += kWarps) {
       const int st = n_wait % kStages;
-      if (!dead && !mbar_wait_bounded(&full[st], (n_wait / kStages) & 1, kK4WaitLimit)) {
+      if (!dead && !mbar_wait_bounded(&full[st], (n_wait / kStages) & 1, a.wait_limit)) {
         set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
@@ -822,6 +829,18 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
   }
 }
 
+#ifdef SPC_TEST_HOOKS
+static std::atomic<int> g_starve_calls{0};
+static std::atomic<long long> g_starve_wait{0};
+bool paged_starve(long long* wait_limit) {
+  int n = g_starve_calls.load();
+  while (n > 0 && !g_starve_calls.compare_exchange_weak(n, n - 1)) {
+  }
+  if (n > 0) *wait_limit = g_starve_wait.load();
+  return n > 0;
+}
+#endif
+
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
 static int k4_head_tiles(int G) { return G <= 8 ? 1 : G == 16 ? 2 : 4; }
 
@@ -845,6 +864,10 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   a.c = c;
   a.ht = k4_head_tiles(G);
   a.hshift = G > 32 ? 1 : 0;
+  a.wait_limit = kK4WaitLimit;
+#ifdef SPC_TEST_HOOKS
+  a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
+#endif
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
@@ -857,3 +880,15 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
 }
 
 }  // namespace spc
+
+#ifdef SPC_TEST_HOOKS
+// Test builds only: the next `calls` launches of the 4-bit decode attention or
+// the prompt attention issue no copies and give up waiting after `wait_cycles`
+// clock cycles.
+extern "C" int spc_test_starve_paged(int calls, long long wait_cycles) {
+  if (calls < 0 || wait_cycles < 1) return SPC_ERR_INVALID_ARG;
+  spc::g_starve_wait.store(wait_cycles);
+  spc::g_starve_calls.store(calls);
+  return SPC_OK;
+}
+#endif

@@ -76,6 +76,8 @@ struct PaArgs {
   PromptAttnCall c;
   int G, gshift, tpm;      // heads a group, its log2, tokens a tile
   int* status;
+  long long wait_limit;
+  int starve;              // test builds: no copy is issued, so that every wait runs out
 };
 
 struct PaItem {
@@ -84,8 +86,8 @@ struct PaItem {
   int nA, nB;              // key blocks of the tiles
 };
 
-__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kPaWait));
+__device__ __forceinline__ bool pa_wait(const PaArgs& a, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
 }
 __device__ __forceinline__ float pa_ex2(float x) {
   float y;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     const long long n_items = (long long)at_least(0) * c.n_kv;
     int it = 0, nkv = 0, nk0 = 0, nq[2] = {0, 0};
     auto acquire = [&](uint64_t* bar, uint32_t parity) {
-      if (!dead && !pa_wait(bar, parity)) {
+      if (!dead && !pa_wait(a, bar, parity)) {
         if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
@@ -290,6 +292,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       }
       __syncwarp();
       if (x.len < 0) break;
+#ifdef SPC_TEST_HOOKS
+      if (a.starve) break;
+#endif
       const int n = max(x.nA, x.nB);
       auto load_q = [&](int i) {
         acquire(&qfree[i], (nq[i] & 1) ^ 1);
@@ -332,10 +337,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     // every copy lands before the CTA ends (they have, unless a role gave up)
     if (lane == 0) {
       for (int k = max(0, nkv - kPaStages); k < nkv; ++k)
-        mbar_wait_bounded(&kvfull[k % kPaStages], (k / kPaStages) & 1, kPaWait);
-      if (nk0 > 0) mbar_wait_bounded(k0full, (nk0 - 1) & 1, kPaWait);
+        mbar_wait_bounded(&kvfull[k % kPaStages], (k / kPaStages) & 1, a.wait_limit);
+      if (nk0 > 0) mbar_wait_bounded(k0full, (nk0 - 1) & 1, a.wait_limit);
       for (int i = 0; i < 2; ++i)
-        if (nq[i] > 0) mbar_wait_bounded(&qfull[i], (nq[i] - 1) & 1, kPaWait);
+        if (nq[i] > 0) mbar_wait_bounded(&qfull[i], (nq[i] - 1) & 1, a.wait_limit);
     }
     __syncwarp();
   } else if (warp == kPaWarpMma) {
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     // the tensor pipe at 60%); one elected lane issues.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
     auto acquire = [&](uint64_t* bar, uint32_t parity) {
-      if (!dead && !pa_wait(bar, parity)) {
+      if (!dead && !pa_wait(a, bar, parity)) {
         if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     // warps wait for each item's last one, unless something gave up)
     if (elect_one()) umma_commit(drain);
     __syncwarp();
-    pa_wait(drain, 0);
+    pa_wait(a, drain, 0);
   } else if (warp < kPaSoftWarps) {
     // ================= softmax and epilogue of tile i, one row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPaRegSoft));
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     const uint32_t ts = tmem + lanes + i * kPaKeys, to = tmem + lanes + kPaColO + i * kD;
     int n_s = 0, n_o = 0, nkv = 0;
     auto acquire = [&](uint64_t* bar, uint32_t parity) {
-      if (!dead && !pa_wait(bar, parity)) {
+      if (!dead && !pa_wait(a, bar, parity)) {
         if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
         dead = true;
       }
@@ -617,6 +622,10 @@ int prompt_attn_launch(const PromptAttnCall& c, void* workspace, void* stream) {
   while ((1 << a.gshift) < a.G) ++a.gshift;
   a.tpm = 128 >> a.gshift;
   a.status = static_cast<int*>(workspace);
+  a.wait_limit = kPaWait;
+#ifdef SPC_TEST_HOOKS
+  a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
+#endif
   CUtensorMap qmap, kmap, vmap;
   auto map = [&](CUtensorMap* m, const void* p, int heads, int64_t stride, uint32_t bh, uint32_t bt) {
     const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)heads, (uint64_t)c.T};

@@ -199,6 +199,12 @@ struct PromptAttnCall {
 size_t prompt_attn_workspace(int T, int B, int n_q, int n_kv);
 int prompt_attn_launch(const PromptAttnCall& c, void* workspace, void* stream);
 
+#ifdef SPC_TEST_HOOKS
+// Test builds only: whether the next launch of the two kernels above runs
+// starved (its copies are not issued), and the wait limit it then has.
+bool paged_starve(long long* wait_limit);
+#endif
+
 int stream_read_launch(const void* src, size_t bytes, uint32_t* sink, int n_blocks, void* stream);
 
 int device_sm_count();

@@ -227,3 +227,24 @@ def test_a_pool_beyond_32_bit_offsets():
     c.num_blocks = num
     got, _ = decode(c, q.to(DEV), cache=cache, table=i32(where[None]))
     check(got, want, decode_tol(want, mag))
+
+
+# ------------------------------------------------------------------ how the work is cut
+@pytest.mark.parametrize("n_q,budget", [(8, 0), (8, 1500), (128, 0), (256, 0)])
+def test_more_long_segments_than_ctas(n_q, budget):
+    # 160 segments, too long to go whole: runs that end inside segments and hold pieces of two
+    rng = np.random.default_rng(50 + n_q)
+    lens = [int(x) for x in rng.integers(1100, 1900, 20)]
+    c = Cache(rng, lens, 8, 64)
+    run(c, bf16(rng, 20, n_q, 128), selection(rng, lens, 8, budget) if budget else None)
+
+
+def test_one_long_segment_over_all_ctas_and_heads_in_two_halves():
+    rng = np.random.default_rng(51)
+    run(Cache(rng, [30001], 1, 128), bf16(rng, 1, 64, 128))
+
+
+def test_a_long_request_among_empty_and_short_ones():
+    rng = np.random.default_rng(52)
+    lens = [0, 3, 9000, 0, 0, 64, 1] + [5] * 20 + [0]
+    run(Cache(rng, lens, 4, 16), bf16(rng, len(lens), 16, 128))
