@@ -41,6 +41,7 @@
 #include <atomic>
 
 #include "kv4.cuh"
+#include "kv4_attn.cuh"
 #include "spc_device.cuh"
 #include "spc_internal.h"
 
@@ -48,11 +49,6 @@ namespace spc {
 
 constexpr int kK4Tile = 32;                          // positions a tile
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
-constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
-constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
-
-constexpr float kK4Headroom = 8.f;
-constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
 // The CTA of a kernel for HT head tiles; the last warps copy for the others:
 // one where the whole context is read, 5 (or 2 of 8) where positions are
@@ -74,17 +70,6 @@ struct K4Cfg {
   static constexpr uint32_t kSmem = kOffMask + kWarps * kStages * 4;
 };
 
-struct Kv4Args {
-  Kv4AttnCall c;
-  int ht;            // head tiles (8 heads) a segment
-  int hshift;        // log2 of the segments a KV head's group is split into
-  int* status;
-  uint32_t* counters;
-  float* part;
-  long long wait_limit;
-  int starve;        // test builds: no copy is issued, so that every wait runs out
-};
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                "{%0,%1,%2,%3};"
@@ -96,82 +81,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// 2^x by the MUFU approximation (relative error about 2^-22); -inf gives 0
-__device__ __forceinline__ float k4_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-
-// the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
-struct K4Line {
-  int pre[SPC_MAX_BATCH + 1];
-  int nt[SPC_MAX_BATCH];       // tiles a segment of request b
-  int run;                     // tiles a CTA takes; 2^30: runs end with their segments
-  int t0, t1;                  // this CTA's run
-  int first, last;             // whole runs: the CTAs of its segment
-  int len[SPC_MAX_BATCH];
-};
-
-// a segment whose tiles several CTAs share: its index, request, first head,
-// first tile, first and last CTA, tiles a run
-struct K4Open {
-  int seg, b, h0, s0, w0, w1, run;
-};
-
-// a tile of the line: tile i of segment (b, s), s = (g << hshift) + hh, with what
-// its copy needs of the segment
-struct K4Cursor {
-  int t, i, b, s;
-  int nt, len;                 // the segment's tiles, the request's context
-  const int32_t* table;        // the request's table row
-};
-__device__ __forceinline__ void k4_seg(const Kv4AttnCall& c, const K4Line& ln, K4Cursor& x) {
-  const int b = min(x.b, c.B - 1);
-  x.nt = max(1, ln.nt[b]);
-  x.len = ln.len[b];
-  x.table = c.table + (size_t)b * c.max_blocks;
-}
-__device__ __forceinline__ K4Cursor k4_at(const Kv4AttnCall& c, const K4Line& ln, int t) {
-  int lo = 0, hi = c.B;        // pre[lo] <= t < pre[hi]; requests without tiles are passed over
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ln.pre[mid] <= t) lo = mid; else hi = mid;
-  }
-  K4Cursor x;
-  x.t = t;
-  x.b = lo;
-  k4_seg(c, ln, x);
-  const int r = t - ln.pre[lo];
-  x.s = r / x.nt;
-  x.i = r - x.s * x.nt;
-  return x;
-}
-__device__ __forceinline__ void k4_step(const Kv4AttnCall& c, const K4Line& ln, int segs, K4Cursor& x, int n) {
-  x.t += n;
-  x.i += n;
-  if (x.i < x.nt) return;
-  while (x.b < c.B && x.i >= ln.nt[x.b]) {
-    x.i -= ln.nt[x.b];
-    if (++x.s == segs) {
-      x.s = 0;
-      do ++x.b; while (x.b < c.B && ln.nt[x.b] == 0);
-    }
-  }
-  k4_seg(c, ln, x);
-}
-
 // Whole context: the copying warp. Lane w serves warp w: tiles t0 + w, t0 + w
 // + W, ... go into its ring as its stages fall free, so that one instruction
 // stream computes the addresses of W tiles. A lane's table entries are fetched
@@ -461,78 +370,6 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
   }
 }
 
-// The last CTA to arrive at a segment merges its CTAs' partials, in CTA order.
-// kMg heads at a time: the pieces' (m, l) to shared memory, a weight per (head,
-// piece), then O by (head, float4) items, kFly loads in flight, the first of
-// them ahead of the weights.
-
-template <int HT, int W>
-__device__ __forceinline__ void k4_merge(const Kv4Args& a, const K4Open& u, int heads, float* mrg) {
-  const Kv4AttnCall& c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto sync = [&]() { asm volatile("bar.sync 1, %0;" :: "n"(32 * W) : "memory"); };
-  constexpr int kMg = HT == 1 ? 8 : 16, kFly = 8;
-  const int np = u.w1 - u.w0 + 1;
-  float2* wl = reinterpret_cast<float2*>(mrg);                  // [kMg][kK4Ctas]
-  float* lsum = mrg + 2 * kMg * kK4Ctas;                        // [kMg]
-  static_assert((2 * kMg * kK4Ctas + kMg) * 4 <= W * 8 * kK4Part * 4, "merge scratch");
-  auto piece = [&](int i, int h) {
-    const int w = u.w0 + i;
-    return a.part + (((size_t)w * 2 + (u.run < (1 << 30) && u.s0 > w * u.run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
-  };
-#pragma unroll 1
-  for (int hb = 0; hb < heads; hb += kMg) {
-    const int nh = min(kMg, heads - hb);
-    float4 x[kFly];
-    auto load = [&](int i, int q0) {
-#pragma unroll
-      for (int q = 0; q < kFly; ++q)
-        if (q0 + q < np) x[q] = __ldcg(reinterpret_cast<const float4*>(piece(q0 + q, hb + (i >> 5)) + 4) + (i & 31));
-    };
-    if (threadIdx.x < nh * 32) load(threadIdx.x, 0);
-    for (int i = threadIdx.x; i < nh * np; i += 32 * W) {
-      const int h = i / np, q = i - h * np;
-      wl[h * kK4Ctas + q] = __ldcg(reinterpret_cast<const float2*>(piece(q, hb + h)));
-    }
-    sync();
-    for (int h = warp; h < nh; h += W) {
-      float M = -INFINITY;
-      for (int q = lane; q < np; q += 32) M = fmaxf(M, wl[h * kK4Ctas + q].x);
-      M = warp_max(M);
-      const float Ms = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      for (int q = lane; q < np; q += 32) {
-        const float2 ml = wl[h * kK4Ctas + q];
-        const float wt = k4_ex2(ml.x - Ms);
-        L += wt * ml.y;
-        wl[h * kK4Ctas + q].x = wt;
-      }
-      L = warp_sum(L);
-      if (lane == 0) lsum[h] = L == 0.f ? 0.f : 1.f / L;
-    }
-    sync();
-    for (int i = threadIdx.x; i < nh * 32; i += 32 * W) {
-      const int h = i >> 5, f4 = i & 31;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int q0 = 0; q0 < np; q0 += kFly) {
-        if (q0 > 0 || i != threadIdx.x) load(i, q0);
-#pragma unroll
-        for (int q = 0; q < kFly; ++q) {
-          if (q0 + q >= np) break;
-          const float w = wl[h * kK4Ctas + q0 + q].x;
-          v.x += w * x[q].x; v.y += w * x[q].y; v.z += w * x[q].z; v.w += w * x[q].w;
-        }
-      }
-      const float r = lsum[h];
-      *reinterpret_cast<uint2*>(c.out + ((size_t)u.b * c.n_q + u.h0 + hb + h) * kD + 4 * f4) =
-          make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
-    }
-    sync();
-  }
-  if (threadIdx.x == 0) a.counters[u.seg] = 0u;
-}
-
 template <int HT, bool SEL>
 __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(Kv4Args a) {
   using Cfg = K4Cfg<HT, SEL>;
@@ -556,81 +393,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     }
     fence_mbar_init();
   }
-  if (warp == 0) {
-    // tiles a segment of each request, two requests a lane
-    int n[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int b = 2 * lane + e;
-      int L = b < c.B ? c.len[b] : 0;
-      L = max(0, min(L, c.max_blocks << c.block_shift));
-      const int nt = b < c.B ? ((SEL ? c.budget : L) + kK4Tile - 1) / kK4Tile : 0;
-      ln.len[b] = L;
-      ln.nt[b] = nt;
-      n[e] = nt * segs;
-    }
-    const int incl = warp_incl_scan(n[0] + n[1]);
-    ln.pre[2 * lane] = incl - n[0] - n[1];
-    ln.pre[2 * lane + 1] = incl - n[1];
-    if (lane == 31) ln.pre[SPC_MAX_BATCH] = incl;
-    // Which tiles of the line this CTA takes. A second piece costs a CTA about
-    // kSlack tiles (queries, merge, fence), and a split segment waits for its
-    // last piece, so runs end with their segments where they can:
-    //  - segments of at most kMinRun tiles are never split: each CTA takes those
-    //    that start in its share of the line;
-    //  - with fewer segments than CTAs, each gets a number of CTAs of its own,
-    //    if that makes no run longer than kSlack tiles above an equal share;
-    //  - else equal runs of the line.
-    const int total = __shfl_sync(0xffffffffu, incl, 31), grid = gridDim.x, blk = blockIdx.x;
-    const int nt0 = ln.nt[2 * lane], nt1 = ln.nt[2 * lane + 1];
-    int run = max((total + grid - 1) / grid, Cfg::kMinRun), np0 = 0, np1 = 0;      // np: pieces a segment
-    const bool small = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(nt0, nt1)) <= Cfg::kMinRun;
-    bool whole = small;
-    for (int k = 0; k <= 2 && !whole; ++k) {
-      const int r = run + k * (Cfg::kSlack / 2);
-      np0 = (nt0 + r - 1) / r;
-      np1 = (nt1 + r - 1) / r;
-      whole = (int)__reduce_add_sync(0xffffffffu, (unsigned)((np0 + np1) * segs)) <= grid;
-    }
-    int t0, t1, first = blk, last = blk;
-    // the last request that starts at or before x (the starts s0, s1 of this lane's two)
-    auto find = [&](int s0, int s1, int x) {
-      return __popc(__ballot_sync(0xffffffffu, s0 <= x)) + __popc(__ballot_sync(0xffffffffu, s1 <= x)) - 1;
-    };
-    if (small) {
-      const int s0 = incl - n[0] - n[1], s1 = incl - n[1];
-      auto start = [&](int x) {                      // of the first segment that starts at or behind tile x
-        const int e = find(s0, s1, x), nt = max(1, __shfl_sync(0xffffffffu, e & 1 ? nt1 : nt0, e >> 1));
-        const int p = __shfl_sync(0xffffffffu, e & 1 ? s1 : s0, e >> 1);
-        return min(total, p + (x - p + nt - 1) / nt * nt);
-      };
-      t0 = start(total * blk / grid);          // total is at most 2^22 here
-      t1 = start(total * (blk + 1) / grid);
-    } else if (whole) {
-      const int end = warp_incl_scan((np0 + np1) * segs), c0 = end - (np0 + np1) * segs, c1 = end - np1 * segs;
-      const int e = find(c0, c1, blk);
-      const int np = __shfl_sync(0xffffffffu, e & 1 ? np1 : np0, e >> 1), nt = __shfl_sync(0xffffffffu, e & 1 ? nt1 : nt0, e >> 1);
-      const int c0e = __shfl_sync(0xffffffffu, e & 1 ? c1 : c0, e >> 1);
-      t0 = t1 = total;
-      if (blk < __shfl_sync(0xffffffffu, end, 31)) {
-        const int r = blk - c0e, sg = r / np, q = r - sg * np, s0 = ln.pre[e] + sg * nt;
-        first = blk - q;
-        last = first + np - 1;
-        t0 = s0 + nt * q / np;
-        t1 = s0 + nt * (q + 1) / np;
-      }
-    } else {
-      t0 = min(total, blk * run);
-      t1 = min(total, t0 + run);
-    }
-    if (lane == 0) {
-      ln.run = whole ? 1 << 30 : run;
-      ln.t0 = t0;
-      ln.t1 = t1;
-      ln.first = first;
-      ln.last = last;
-    }
-  }
+  if (warp == 0) k4_plan<kK4Tile, Cfg::kMinRun, Cfg::kSlack>(a, ln, segs, SEL);
   __syncthreads();
   const int total = ln.pre[c.B], t0 = ln.t0, t1 = ln.t1;
 
@@ -821,7 +584,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
       sync();
       if (s_last) {
         __threadfence();
-        k4_merge<HT, kWarps>(a, K4Open{seg, b, h0, s0, w0, w1, run}, heads, mrg);
+        k4_merge<HT, kWarps, kWarps * 8 * kK4Part * 4>(a, K4Open{seg, b, h0, s0, w0, w1, run}, heads, mrg);
       }
     }
     k4_step(c, ln, segs, pc, pe - pt);
@@ -842,11 +605,18 @@ bool paged_starve(long long* wait_limit) {
 #endif
 
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
-static int k4_head_tiles(int G) { return G <= 8 ? 1 : G == 16 ? 2 : 4; }
+// The whole context of groups of 16 heads and more goes to the tcgen05 kernel
+// (8 requests of 65536 positions on one KV head, us there and here: 16 heads
+// TC16 and 35, 32 TC32 and 62, 64 TC64 and 89); selected positions stay here.
+static bool k4_on_tc(int G, int budget) { return G >= 16 && budget == 0; }
+// head tiles a segment, and log2 of the segments a group is split into
+static int k4_head_tiles(int G, int budget) { return k4_on_tc(G, budget) ? G / 8 : G <= 8 ? 1 : G == 16 ? 2 : 4; }
+static int k4_split(int G, int budget) { return !k4_on_tc(G, budget) && G > 32 ? 1 : 0; }
 
-size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int) {
-  const int G = n_q / n_kv, ht = k4_head_tiles(G), hsplit = G > 32 ? G / 32 : 1;
-  return 256 + k4_round((size_t)B * n_kv * hsplit * 4) + (size_t)kK4Ctas * 2 * 8 * ht * kK4Part * 4;
+size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int budget) {
+  const int G = n_q / n_kv;
+  return 256 + k4_round((size_t)B * (n_kv << k4_split(G, budget)) * kK4SegBytes) +
+         (size_t)kK4Ctas * 2 * 8 * k4_head_tiles(G, budget) * kK4Part * 4;
 }
 
 template <int HT, bool SEL>
@@ -862,8 +632,8 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   const int G = c.n_q / c.n_kv;
   Kv4Args a{};
   a.c = c;
-  a.ht = k4_head_tiles(G);
-  a.hshift = G > 32 ? 1 : 0;
+  a.ht = k4_head_tiles(G, c.budget);
+  a.hshift = k4_split(G, c.budget);
   a.wait_limit = kK4WaitLimit;
 #ifdef SPC_TEST_HOOKS
   a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
@@ -871,11 +641,13 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
-  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * 4));
+  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * kK4SegBytes));
+  if (k4_on_tc(G, c.budget)) return kv4_attn_tc_launch(a, G, stream);
+  if (!c.selected) return k4_run<1, false>(a, stream);
   switch (a.ht) {
-    case 1: return c.selected ? k4_run<1, true>(a, stream) : k4_run<1, false>(a, stream);
-    case 2: return c.selected ? k4_run<2, true>(a, stream) : k4_run<2, false>(a, stream);
-    default: return c.selected ? k4_run<4, true>(a, stream) : k4_run<4, false>(a, stream);
+    case 1: return k4_run<1, true>(a, stream);
+    case 2: return k4_run<2, true>(a, stream);
+    default: return k4_run<4, true>(a, stream);
   }
 }
 
