@@ -605,10 +605,11 @@ bool paged_starve(long long* wait_limit) {
 #endif
 
 static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
-// The whole context of groups of 16 heads and more goes to the tcgen05 kernel
-// (8 requests of 65536 positions on one KV head, us there and here: 16 heads
-// TC16 and 35, 32 TC32 and 62, 64 TC64 and 89); selected positions stay here.
-static bool k4_on_tc(int G, int budget) { return G >= 16 && budget == 0; }
+// The whole context of groups of 32 and 64 heads goes to the tcgen05 kernel (8
+// requests of 65536 positions on one KV head, us there and here: 64 heads 48
+// and 89, 32 heads 39 and 62, but 16 heads 35 and 35, and on four KV heads 108
+// and 88). Selected positions stay here.
+static bool k4_on_tc(int G, int budget) { return G >= 32 && budget == 0; }
 // head tiles a segment, and log2 of the segments a group is split into
 static int k4_head_tiles(int G, int budget) { return k4_on_tc(G, budget) ? G / 8 : G <= 8 ? 1 : G == 16 ? 2 : 4; }
 static int k4_split(int G, int budget) { return !k4_on_tc(G, budget) && G > 32 ? 1 : 0; }
@@ -643,7 +644,7 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
   a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * kK4SegBytes));
   if (k4_on_tc(G, c.budget)) return kv4_attn_tc_launch(a, G, stream);
-  if (!c.selected) return k4_run<1, false>(a, stream);
+  if (!c.selected) return a.ht == 1 ? k4_run<1, false>(a, stream) : k4_run<2, false>(a, stream);
   switch (a.ht) {
     case 1: return k4_run<1, true>(a, stream);
     case 2: return k4_run<2, true>(a, stream);

@@ -27,7 +27,7 @@ struct Kv4Args {
   int starve;        // test builds: no copy is issued, so that every wait runs out
 };
 
-// groups of 16, 32 or 64 heads over the whole context (kv4_attn_tc.cu); G = ht * 8
+// groups of 32 or 64 heads over the whole context (kv4_attn_tc.cu)
 int kv4_attn_tc_launch(const Kv4Args& a, int G, void* stream);
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -1,9 +1,9 @@
-// Decode attention over the paged 4-bit cache for groups of 16, 32 or 64 query
+// Decode attention over the paged 4-bit cache for groups of 32 or 64 query
 // heads, whole context, on the 5th-generation tensor cores.
 //
-// With N heads a record feeds 512 N flops; from 16 heads on the mma.sync
-// kernel is bound by its dequantised operands' reuse (8 heads an instruction)
-// and by few, register-heavy warps. Here a tile of 128 positions is
+// With N heads a record feeds 512 N flops; from 32 heads on the mma.sync
+// kernel is bound by the reuse of its dequantised operands (8 heads an
+// instruction) and by few, register-heavy warps. Here a tile of 128 positions is
 // dequantised once, for all heads, and both products are transposed, with the
 // positions in the tensor memory lanes:
 //   S^T [128 positions][N heads] = K [128][128] Q^T     K in tensor memory
@@ -21,9 +21,13 @@
 //   0-3    softmax and epilogue (one position, in the epilogue one dim, a thread)
 //   4-11   dequantisation, two groups of four that take the tiles by turns
 //   12     tensor memory, MMA issue: S(t + 1) ahead of PV(t)
-//   13     copies (cp.async.bulk, one a cache block), four tiles ahead
-// Bound: HBM (18 KB a tile, 800 cycles of an SM's share) up to N = 64, where
-// the two products take about as long.
+//   13     copies (cp.async.bulk, one a cache block), six tiles ahead
+// Bound: a tile's 18 KB are 800 cycles of an SM's share of HBM, its two products
+// about 720; the softmax warps' own path through a tile is longer (1800 cycles
+// at N = 64, 1000 at N = 32: logits 150, exponentials 64 N / 16, the stores of P
+// and their proxy fence, the barrier), and it is what bounds the kernel.
+// Measured (8 requests of 65536 positions on one KV head, 75 MB, floor 11 us):
+// N = 64 48 us, N = 32 39 us; the mma.sync kernel 89 and 62.
 // Every wait is bounded; a warp whose wait gives up records SPC_ERR_TIMEOUT and
 // runs on without waiting, so that the softmax warps' barriers are reached.
 #include <cuda_runtime.h>
@@ -35,7 +39,8 @@ namespace spc {
 
 constexpr int kKtTile = 128;                          // positions
 constexpr uint32_t kKtRaw = kKtTile * kKv4Rec;        // 18 KB: a tile's records
-constexpr int kKtStages = 4;
+constexpr int kKtStages = 6;
+constexpr int kKtMasks = 16;                          // tiles whose masks are kept
 constexpr int kKtMinRun = 8, kKtSlack = 8;            // see k4_plan
 constexpr uint32_t kKtV = kKtTile * kRowBytes;        // 32 KB: V of a tile, fp16
 constexpr uint32_t kKtP = kKtTile * 128;              // 16 KB: P, 64 heads a row
@@ -55,8 +60,8 @@ constexpr uint32_t kKtOffMf = kKtOffRaw + kKtStages * kKtRaw;        // [64] flo
 constexpr uint32_t kKtOffM = kKtOffMf + 64 * 8;                      // [64] running maxima
 constexpr uint32_t kKtOffAl = kKtOffM + 64 * 4;                      // [64] rescale factors; 1 / sums
 constexpr uint32_t kKtOffRed = kKtOffAl + 64 * 4;                    // [4 warps][64]
-constexpr uint32_t kKtOffMask = kKtOffRed + 4 * 64 * 4;              // [8 tiles][4 words]
-constexpr uint32_t kKtOffBar = kKtOffMask + 8 * 16;
+constexpr uint32_t kKtOffMask = kKtOffRed + 4 * 64 * 4;              // [kKtMasks][4 words]
+constexpr uint32_t kKtOffBar = kKtOffMask + kKtMasks * 16;
 constexpr int kKtBars = 2 * kKtStages + 2 * 5 + 4;
 constexpr size_t kKtSmem = 1024 + kKtOffBar + kKtBars * 8 + 16;
 
@@ -85,19 +90,16 @@ __device__ __forceinline__ bool kt_any(bool x) {
                : "=r"(r) : "r"((uint32_t)x) : "memory");
   return r != 0;
 }
-// N (16, 32 or 64) consecutive fp32 columns of this thread's lane
+// N (32 or 64) consecutive fp32 columns of this thread's lane
 template <int N>
 __device__ __forceinline__ void kt_ld(uint32_t t, float (&v)[N]) {
-  if constexpr (N == 16) {
-    tmem_ld16(t, v);
-  } else {
 #pragma unroll
-    for (int q = 0; q < N; q += 32) tmem_ld32(t + q, *reinterpret_cast<float (*)[32]>(v + q));
-  }
+  for (int q = 0; q < N; q += 32) tmem_ld32(t + q, *reinterpret_cast<float (*)[32]>(v + q));
   tmem_ld_wait();
 }
-// v[h] over the warp's lanes reduced for every h at once, halving the number of
-// heads a lane keeps at each step; the result of head h goes to red[h]
+
+// v[h] over the warp's lanes reduced for all N (32 or 64) heads at once, halving
+// the heads a lane keeps at each step; the result of head h goes to red[h]
 template <int N, class F>
 __device__ __forceinline__ void kt_reduce(float (&v)[N], float* red, F f) {
   const int lane = threadIdx.x & 31;
@@ -105,21 +107,16 @@ __device__ __forceinline__ void kt_reduce(float (&v)[N], float* red, F f) {
 #pragma unroll
   for (int s = 0; s < 5; ++s) {
     const int x = 16 >> s, keep = N >> (s + 1);       // lanes apart, heads kept
-    if (keep >= 1) {
-      const bool up = (lane & x) != 0;
+    const bool up = (lane & x) != 0;
 #pragma unroll
-      for (int j = 0; j < keep; ++j) {
-        const float send = up ? v[j] : v[j + keep], mine = up ? v[j + keep] : v[j];
-        v[j] = f(mine, __shfl_xor_sync(0xffffffffu, send, x));
-      }
-      h += up ? keep : 0;
-    } else {
-      v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], x));
+    for (int j = 0; j < keep; ++j) {
+      const float send = up ? v[j] : v[j + keep], mine = up ? v[j + keep] : v[j];
+      v[j] = f(mine, __shfl_xor_sync(0xffffffffu, send, x));
     }
+    h += up ? keep : 0;
   }
-  constexpr int last = N >= 32 ? N / 32 : 1;
 #pragma unroll
-  for (int j = 0; j < last; ++j) red[h + j] = v[j];
+  for (int j = 0; j < N / 32; ++j) red[h + j] = v[j];
 }
 
 // 64 codes (four words of 8, twice) and their scales as fp16 pairs
@@ -211,7 +208,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       acquire(&raw_free[st], ((i / kKtStages) & 1) ^ 1);
       if (dead) break;
       const uint32_t bits = (1u << rows) - 1, hi = __shfl_down_sync(0xffffffffu, bits, 1);
-      if (lane < 8 && !(lane & 1)) masks[(i & 7) * 4 + (lane >> 1)] = bits | hi << 16;
+      if (lane < 8 && !(lane & 1)) masks[i % kKtMasks * 4 + (lane >> 1)] = bits | hi << 16;
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, (unsigned)rows) * kKv4Rec;
       if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], bytes);
       __syncwarp();
@@ -230,12 +227,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm = smem_u32(base);
     constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);             // descriptors' high word (spc_tc.cuh)
     auto desc = [&](uint32_t addr, uint32_t lead) { return (uint64_t)hi << 32 | (addr >> 4) | (lead >> 4) << 16; };
-    int nq = 0;
-    auto issue_s = [&](int i, bool first) {
-      acquire(&kv_full[i & 1], (i >> 1) & 1);
-      acquire(&s_free[i & 1], ((i >> 1) & 1) ^ 1);
-      if (first) acquire(q_full, nq++ & 1);
-      if (dead) return;
+    auto issue_s = [&](int i) {
       tc_fence_after();
       if (kt_elect()) {
 #pragma unroll
@@ -248,8 +240,6 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       __syncwarp();
     };
     auto issue_pv = [&](int i, bool first) {
-      acquire(&p_full[i & 1], (i >> 1) & 1);
-      if (dead) return;
       tc_fence_after();
       if (kt_elect()) {
 #pragma unroll
@@ -261,18 +251,43 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       }
       __syncwarp();
     };
+    // S up to two tiles ahead of PV, whichever has its operands; the first S
+    // of a segment waits for its queries, which are written when the segment
+    // before is done
     if (nt_run > 0) {
-      K4Cursor x = k4_at(c, ln, t0);                  // tile i
-      bool first = true;                              // of its piece
-      issue_s(0, true);
-#pragma unroll 1
-      for (int i = 0; i < nt_run; ++i) {
-        const bool last = x.i + 1 == x.nt;            // the next tile is another segment's: its queries come after this PV
-        if (i + 1 < nt_run && !last) issue_s(i + 1, false);
-        issue_pv(i, first);
-        if (i + 1 < nt_run && last) issue_s(i + 1, true);
-        first = last;
-        k4_step(c, ln, segs, x, 1);
+      K4Cursor x = k4_at(c, ln, t0);
+      int is = 0, ip = 0, nq = 0;                     // next S, next PV
+      int end = min(nt_run, x.nt - x.i);              // of the segment that S is at
+      int begin = 0, pv_end = end, pv_begin = 0;      // and the one that PV is at
+      long long idle = clock64();
+      while (ip < nt_run) {
+        bool s_ok = is < nt_run && is < ip + 2 && mbar_test(&kv_full[is & 1], (is >> 1) & 1) &&
+                    mbar_test(&s_free[is & 1], ((is >> 1) & 1) ^ 1) && (is != begin || mbar_test(q_full, nq & 1));
+        s_ok = __all_sync(0xffffffffu, s_ok);
+        if (s_ok) {
+          if (is == begin) ++nq;
+          issue_s(is);
+          if (++is == end && is < nt_run) {
+            k4_step(c, ln, segs, x, end - begin);
+            begin = end;
+            end = min(nt_run, begin + x.nt);
+          }
+          idle = clock64();
+          continue;
+        }
+        if (__all_sync(0xffffffffu, ip < is && mbar_test(&p_full[ip & 1], (ip >> 1) & 1))) {
+          issue_pv(ip, ip == pv_begin);
+          if (++ip == pv_end) {
+            pv_begin = pv_end;
+            pv_end = end;                             // S is in the next segment by now, or at its start
+          }
+          idle = clock64();
+          continue;
+        }
+        if (__any_sync(0xffffffffu, clock64() - idle > a.wait_limit)) {
+          if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+          break;
+        }
       }
     }
     // every MMA has completed before tensor memory is released
@@ -290,7 +305,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       const int st = i % kKtStages, u = i >> 1;
       acquire(&raw_full[st], (i / kKtStages) & 1);
       const uint8_t* rec = base + kKtOffRaw + (uint32_t)st * kKtRaw + (uint32_t)row * kKv4Rec;
-      const bool valid = !dead && ((masks[(i & 7) * 4 + (warp & 3)] >> lane) & 1u);
+      const bool valid = !dead && ((masks[i % kKtMasks * 4 + (warp & 3)] >> lane) & 1u);
       uint4 w[4];
       uint2 sc;
       auto load = [&](int off, int soff) {
@@ -361,8 +376,14 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       const int b = pc.b, g = pc.s, nt = pc.nt, pt = t0 + i, i1 = min(nt_run, i + nt - pc.i), h0 = g * N;
       // ---- queries: per head a power of two that brings the largest value
       // below 2; four dims a lane, one head a warp at a time
-      for (int h = warp; h < N; h += 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(c.q + ((size_t)b * c.n_q + h0 + h) * kD) + lane);
+      uint2 qw[N / 4];
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k)
+        qw[k] = __ldg(reinterpret_cast<const uint2*>(c.q + ((size_t)b * c.n_q + h0 + warp + 4 * k) * kD) + lane);
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const int h = warp + 4 * k;
+        const uint2 w = qw[k];
         uint32_t mx = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
         const int e = max((int)(mx >> 7), 1) - 127, e1 = e / 2, e2 = e - e1;
@@ -384,42 +405,68 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       float l[N];
 #pragma unroll
       for (int h = 0; h < N; ++h) l[h] = 0.f;
-      bool first = true;
+      bool first = true, none = true;                 // of the piece; no position counted yet
 #pragma unroll 1
       for (; i < i1; ++i) {
         const int u = i >> 1, bf = i & 1;
         float s[N];
         acquire(&s_full[bf], u & 1);
         tc_fence_after();
-        if (!dead) kt_ld<N>(tl + kKtColS + bf * 64, s);
-        const bool valid = !dead && ((masks[(i & 7) * 4 + warp] >> lane) & 1u);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[bf]);
-        float mx = -INFINITY;
+        const uint4 mk = *reinterpret_cast<const uint4*>(masks + i % kKtMasks * 4);
+        const uint32_t word = warp == 0 ? mk.x : warp == 1 ? mk.y : warp == 2 ? mk.z : mk.w;
+        const bool some = (mk.x | mk.y | mk.z | mk.w) != 0;
+        auto load = [&]() {
+          if (!dead) kt_ld<N>(tl + kKtColS + bf * 64, s);
+          if (dead || word != 0xffffffffu) {
 #pragma unroll
-        for (int h = 0; h < N; h += 2) {
-          const float4 k = *reinterpret_cast<const float4*>(mf + h);
-          const float2 x = fma2(make_float2(s[h], s[h + 1]), make_float2(k.x, k.z), make_float2(k.y, k.w));
-          mx = fmaxf(mx, fmaxf(x.x, x.y));
-        }
-        if (kt_any(first || (valid && mx > kK4Headroom))) {
-          // a maximum to raise: every head's over the tile, HB heads at a time
-          constexpr int HB = N < 32 ? N : 32;
+            for (int h = 0; h < N; ++h) s[h] = !dead && ((word >> lane) & 1u) ? s[h] : -INFINITY;
+          }
+        };
+        load();
+        // P of tile i - 2 has been read
+        if (u > 0) acquire(&pv_done[bf], (u - 1) & 1);
+        // s becomes the weights against the maxima at hand, and P; returns the
+        // largest logit above its head's maximum
+        const uint32_t pb = smem_u32(base) + kKtOffP + (uint32_t)bf * kKtP + (uint32_t)row * 128;
+        auto weights = [&]() {
+          float mx = -INFINITY;
 #pragma unroll
-          for (int hb = 0; hb < N; hb += HB) {
-            float v[HB];
+          for (int n = 0; n < N / 8; ++n) {
+            uint32_t p[4];
 #pragma unroll
-            for (int h = 0; h < HB; ++h) v[h] = valid ? s[hb + h] * mf[hb + h].x : -INFINITY;
-            kt_reduce<HB>(v, red + warp * 64 + hb, [](float x, float y) { return fmaxf(x, y); });
+            for (int j = 0; j < 4; ++j) {
+              const int h = 8 * n + 2 * j;
+              const float4 k = *reinterpret_cast<const float4*>(mf + h);
+              const float2 x = fma2(make_float2(s[h], s[h + 1]), make_float2(k.x, k.z), make_float2(k.y, k.w));
+              mx = fmaxf(mx, fmaxf(x.x, x.y));
+              s[h] = k4_ex2(x.x);
+              s[h + 1] = k4_ex2(x.y);
+              p[j] = pack_f16(s[h], s[h + 1]);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(pb + (uint32_t)((n ^ (row & 7)) << 4)), "r"(p[0]),
+                         "r"(p[1]), "r"(p[2]), "r"(p[3]) : "memory");
+          }
+          return mx;
+        };
+        const bool start = none && some;              // the first that counts: no maximum to try
+        if (start || kt_any(weights() > kK4Headroom)) {
+          // a maximum to raise: every head's over the tile, 32 heads at a time
+          if (!start) load();
+#pragma unroll
+          for (int hb = 0; hb < N; hb += 32) {
+            float v[32];
+#pragma unroll
+            for (int h = 0; h < 32; ++h) v[h] = s[hb + h] * mf[hb + h].x;
+            kt_reduce<32>(v, red + warp * 64 + hb, [](float x, float y) { return fmaxf(x, y); });
           }
           kt_sync();
           if (row < N) {
-            const float tmx = fmaxf(fmaxf(red[row], red[64 + row]), fmaxf(red[128 + row], red[192 + row]));
+            // (finite from the first position that counts on)
+            const float tmx = fmaxf(fmaxf(fmaxf(red[row], red[64 + row]), fmaxf(red[128 + row], red[192 + row])), -3e38f);
             const float m = mrun[row], M = tmx > m + kK4Headroom ? tmx : m;
             al[row] = M == m ? 1.f : k4_ex2(m - M);
             mrun[row] = M;
-            mf[row].y = -M;                          // +inf while nothing counted: the first that does raises it
+            mf[row].y = -M;
           }
           kt_sync();
 #pragma unroll
@@ -441,32 +488,23 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
               tmem_st_wait();
             }
           }
+          weights();
         }
         first = false;
-        // P of tile i - 2 has been read
-        if (u > 0) acquire(&pv_done[bf], (u - 1) & 1);
-        const uint32_t pb = smem_u32(base) + kKtOffP + (uint32_t)bf * kKtP + (uint32_t)row * 128;
+        none = none && !some;
 #pragma unroll
-        for (int n = 0; n < N / 8; ++n) {
-          uint32_t p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int h = 8 * n + 2 * j;
-            const float4 k = *reinterpret_cast<const float4*>(mf + h);
-            float2 x = fma2(make_float2(s[h], s[h + 1]), make_float2(k.x, k.z), make_float2(k.y, k.w));
-            x.x = valid ? k4_ex2(x.x) : 0.f;
-            x.y = valid ? k4_ex2(x.y) : 0.f;
-            l[h] += x.x;
-            l[h + 1] += x.y;
-            p[j] = pack_f16(x.x, x.y);
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(pb + (uint32_t)((n ^ (row & 7)) << 4)), "r"(p[0]), "r"(p[1]),
-                       "r"(p[2]), "r"(p[3]) : "memory");
+        for (int h = 0; h < N; h += 2) {
+          const float2 x = add2(make_float2(l[h], l[h + 1]), make_float2(s[h], s[h + 1]));
+          l[h] = x.x;
+          l[h + 1] = x.y;
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[bf]);
+        if (lane == 0) {
+          mbar_arrive(&s_free[bf]);
+          mbar_arrive(&p_full[bf]);
+        }
       }
 
       // ---- the piece's end: sums over the positions, O
@@ -594,7 +632,6 @@ static int kt_run(const Kv4Args& a, void* stream) {
 
 int kv4_attn_tc_launch(const Kv4Args& a, int G, void* stream) {
   switch (G) {
-    case 16: return kt_run<16>(a, stream);
     case 32: return kt_run<32>(a, stream);
     default: return kt_run<64>(a, stream);
   }
