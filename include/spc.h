@@ -540,8 +540,9 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
  * workspace  spc_kv4_decode_attn_workspace_size() bytes, 256-byte aligned,
  *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
  *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
- *            that may overlap must use distinct workspaces.
- * Limits: d = 128, G in {1,2,4,8,16,32,64}, 1 <= B <= 64, n_kv <= 1024,
+ *            that may overlap must use distinct workspaces; calls of any
+ *            shapes may take turns on one that is large enough for each.
+ * Limits: d = 128, G in {1,2,4,8,16,32,64}, 1 <= B <= 64, n_kv <= 128,
  *         budget <= 4096, scale > 0. */
 size_t spc_kv4_decode_attn_workspace_size(int B, int n_q, int n_kv, int d, int max_blocks, int block_size,
                                           int budget);

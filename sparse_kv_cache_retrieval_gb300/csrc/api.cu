@@ -476,7 +476,7 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
 
 size_t spc_kv4_decode_attn_workspace_size(int B, int n_q, int n_kv, int d, int max_blocks, int block_size,
                                           int budget) {
-  if (B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > 1024 ||
+  if (B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > kv4_attn_max_kv() ||
       block_shift_of(block_size) < 0 || !table_ok(max_blocks, block_size) || budget < 0 || budget > SPC_MAX_BUDGET)
     return 0;
   return kv4_attn_workspace(B, n_q, n_kv, max_blocks, block_size, budget);
@@ -491,7 +491,7 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned4(block_table) || !aligned4(len) ||
       !aligned4(selected))
     return SPC_ERR_INVALID_ARG;
-  if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > 1024) return SPC_ERR_SHAPE;
+  if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_kv > kv4_attn_max_kv()) return SPC_ERR_SHAPE;
   if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, n_kv) || !table_ok(max_blocks, block_size))
     return SPC_ERR_SHAPE;
   if (budget < 0 || budget > SPC_MAX_BUDGET) return SPC_ERR_SHAPE;

@@ -604,7 +604,6 @@ bool paged_starve(long long* wait_limit) {
 }
 #endif
 
-static size_t k4_round(size_t x) { return (x + 255) & ~size_t(255); }
 // The whole context of groups of 32 and 64 heads goes to the tcgen05 kernel (8
 // requests of 65536 positions on one KV head, us there and here: 64 heads 48
 // and 89, 32 heads 39 and 62, but 16 heads 35 and 35, and on four KV heads 108
@@ -614,10 +613,8 @@ static bool k4_on_tc(int G, int budget) { return G >= 32 && budget == 0; }
 static int k4_head_tiles(int G, int budget) { return k4_on_tc(G, budget) ? G / 8 : G <= 8 ? 1 : G == 16 ? 2 : 4; }
 static int k4_split(int G, int budget) { return !k4_on_tc(G, budget) && G > 32 ? 1 : 0; }
 
-size_t kv4_attn_workspace(int B, int n_q, int n_kv, int, int, int budget) {
-  const int G = n_q / n_kv;
-  return 256 + k4_round((size_t)B * (n_kv << k4_split(G, budget)) * kK4SegBytes) +
-         (size_t)kK4Ctas * 2 * 8 * k4_head_tiles(G, budget) * kK4Part * 4;
+size_t kv4_attn_workspace(int, int n_q, int n_kv, int, int, int budget) {
+  return kK4OffPart + (size_t)kK4Ctas * 2 * 8 * k4_head_tiles(n_q / n_kv, budget) * kK4Part * 4;
 }
 
 template <int HT, bool SEL>
@@ -628,6 +625,8 @@ static int k4_run(const Kv4Args& a, void* stream) {
   kv4_attn_kernel<HT, SEL><<<kK4Ctas, K4Cfg<HT, SEL>::kThreads, K4Cfg<HT, SEL>::kSmem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
+
+int kv4_attn_max_kv() { return kK4MaxKv; }
 
 int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
   const int G = c.n_q / c.n_kv;
@@ -641,8 +640,9 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
 #endif
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
-  a.counters = reinterpret_cast<uint32_t*>(ws + 256);
-  a.part = reinterpret_cast<float*>(ws + 256 + k4_round((size_t)c.B * (c.n_kv << a.hshift) * kK4SegBytes));
+  a.counters = reinterpret_cast<uint32_t*>(ws + kK4OffCount);
+  a.segments = ws + kK4OffSeg;
+  a.part = reinterpret_cast<float*>(ws + kK4OffPart);
   if (k4_on_tc(G, c.budget)) return kv4_attn_tc_launch(a, G, stream);
   if (!c.selected) return a.ht == 1 ? k4_run<1, false>(a, stream) : k4_run<2, false>(a, stream);
   switch (a.ht) {

@@ -12,7 +12,13 @@ namespace spc {
 
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
-constexpr int kK4SegBytes = 16;                      // workspace a segment: a counter, or where its partials are
+constexpr int kK4MaxKv = 128;                        // KV heads
+// workspace: status, arrival counters (zero between calls), where a segment's
+// partials are (tcgen05 kernel), partials. The offsets do not depend on the
+// shapes, so that calls of different shapes may take turns on one workspace.
+constexpr size_t kK4OffCount = 256;
+constexpr size_t kK4OffSeg = kK4OffCount + (size_t)SPC_MAX_BATCH * kK4MaxKv * 2 * 4;
+constexpr size_t kK4OffPart = kK4OffSeg + (size_t)SPC_MAX_BATCH * kK4MaxKv * 16;
 constexpr float kK4Headroom = 8.f;                   // log2 growth allowed before the maximum is raised
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
@@ -21,7 +27,8 @@ struct Kv4Args {
   int ht;            // head tiles (8 heads) a segment
   int hshift;        // log2 of the segments a KV head's group is split into
   int* status;
-  uint32_t* counters; // kK4SegBytes a segment
+  uint32_t* counters; // one a segment
+  void* segments;     // KtSegment, one a segment
   float* part;
   long long wait_limit;
   int starve;        // test builds: no copy is issued, so that every wait runs out

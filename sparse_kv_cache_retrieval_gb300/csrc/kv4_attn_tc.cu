@@ -70,7 +70,7 @@ constexpr size_t kKtSmem = 1024 + kKtOffBar + kKtBars * 8 + 16;
 struct KtSegment {
   int w0, np, s0, run;
 };
-static_assert(sizeof(KtSegment) == kK4SegBytes, "one entry a segment in the workspace");
+static_assert(sizeof(KtSegment) * SPC_MAX_BATCH * kK4MaxKv <= kK4OffPart - kK4OffSeg, "one entry a segment in the workspace");
 
 template <int N>
 constexpr uint32_t kKtIdescS = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kKtTile >> 4) << 24);
@@ -621,7 +621,7 @@ static int kt_run(const Kv4Args& a, void* stream) {
   if (set_func_attr((const void*)kv4_attn_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKtSmem) != cudaSuccess)
     return SPC_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  KtSegment* segments = reinterpret_cast<KtSegment*>(a.counters);
+  KtSegment* segments = static_cast<KtSegment*>(a.segments);
   kv4_attn_tc_kernel<N><<<kK4Ctas, kKtThreads, kKtSmem, st>>>(a, segments);
   if (cudaGetLastError() != cudaSuccess) return SPC_ERR_CUDA;
   // no segment is split where the table has room for kKtMinRun tiles at most

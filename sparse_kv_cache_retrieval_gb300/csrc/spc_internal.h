@@ -184,6 +184,7 @@ struct Kv4AttnCall {
   float scale2;           // scale * log2(e)
 };
 size_t kv4_attn_workspace(int B, int n_q, int n_kv, int max_blocks, int block_size, int budget);
+int kv4_attn_max_kv();
 int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream);
 
 struct PromptAttnCall {

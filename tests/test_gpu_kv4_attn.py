@@ -248,3 +248,18 @@ def test_a_long_request_among_empty_and_short_ones():
     rng = np.random.default_rng(52)
     lens = [0, 3, 9000, 0, 0, 64, 1] + [5] * 20 + [0]
     run(Cache(rng, lens, 4, 16), bf16(rng, len(lens), 16, 128))
+
+
+def test_calls_of_different_shapes_take_turns_on_one_workspace():
+    rng = np.random.default_rng(53)
+    calls, size = [], 0
+    for lens, n_q, n_kv, budget in (([3000, 40], 64, 1, 0), ([3000, 40], 64, 1, 500), ([2500] * 40, 16, 2, 0),
+                                    ([9000], 8, 1, 0), ([1500] * 12, 128, 4, 0), ([100, 7000], 32, 2, 3000)):
+        c = Cache(rng, lens, n_kv, 64)
+        sel = selection(rng, lens, n_kv, budget) if budget else None
+        calls.append((c, bf16(rng, len(lens), n_q, 128), sel))
+        size = max(size, spc.spc_kv4_decode_attn_workspace_size(len(lens), n_q, n_kv, 128, c.max_blocks, 64, budget))
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for c, q, sel in calls:
+            run(c, q, sel, ws=ws)

@@ -99,7 +99,7 @@ def test_kv4_decode_attn_refusals(lib):
     assert ws > 0
     for bad in ((0, 32, 8, 128, 16, 64, 0), (65, 32, 8, 128, 16, 64, 0), (2, 30, 8, 128, 16, 64, 0),
                 (2, 32, 8, 64, 16, 64, 0), (2, 32, 8, 128, 0, 64, 0), (2, 32, 8, 128, 5000, 64, 0),
-                (2, 32, 8, 128, 16, 63, 0), (2, 32, 8, 128, 16, 64, 5000), (2, 32, 8, 128, 16, 64, -1)):
+                (2, 32, 8, 128, 16, 63, 0), (2, 129, 129, 128, 16, 64, 0), (2, 32, 8, 128, 16, 64, 5000), (2, 32, 8, 128, 16, 64, -1)):
         assert B.spc_kv4_decode_attn_workspace_size(*bad) == 0, bad
     ok = [FAKE, FAKE, FAKE, FAKE, None, 2, 32, 8, 128, 100, 64, 16, 0, 0.1, FAKE, FAKE, ws, None]
     nan, inf = float("nan"), float("inf")
