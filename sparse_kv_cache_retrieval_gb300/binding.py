@@ -307,7 +307,8 @@ def _device():
 
 def _raw_stream(stream, dev):
     if stream is None:
-        return _torch.cuda.current_stream(dev).cuda_stream if dev >= 0 else 0
+        # the handle alone: torch.cuda.current_stream builds a Stream object, 1-2 us a call
+        return _torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

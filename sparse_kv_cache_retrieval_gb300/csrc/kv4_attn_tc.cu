@@ -119,7 +119,7 @@ __device__ __forceinline__ void kt_reduce(float (&v)[N], float* red, F f) {
   for (int j = 0; j < N / 32; ++j) red[h + j] = v[j];
 }
 
-// 64 codes (four words of 8, twice) and their scales as fp16 pairs
+// 32 codes (four words of 8) times their two scales, as fp16 pairs (exact)
 __device__ __forceinline__ void kt_dequant32(const uint4& w, uint32_t scales, uint32_t (&h)[16]) {
   const uint32_t s = e4m3x2_to_f16(scales);
   const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
