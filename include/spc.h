@@ -536,7 +536,7 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
  * block_table int32 [B][max_blocks]; len int32 [B] (at most max_blocks *
  *            block_size positions count).
  * selected   int32 [B][n_kv][budget], or NULL with budget 0.
- * out        bf16 [B][n_q][d], 16-byte aligned.
+ * out        bf16 [B][n_q][d], 16-byte aligned; must not overlap q.
  * workspace  spc_kv4_decode_attn_workspace_size() bytes, 256-byte aligned,
  *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
  *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
@@ -563,7 +563,8 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
  *            row's size (the three may lie in one fused projection's output).
  * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are an
  *            empty sequence.
- * out        bf16 [T][n_q][d], 16-byte aligned; must not overlap q, k or v.
+ * out        bf16 [T][n_q][d], 16-byte aligned; must not overlap the memory from
+ *            the first to the last element of q, k or v.
  * workspace  spc_prompt_attn_workspace_size() bytes, 256-byte aligned,
  *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
  *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls

@@ -411,6 +411,12 @@ static bool table_ok(int max_blocks, int block_size) {
   return max_blocks >= 1 && (long long)max_blocks * block_size <= SPC_MAX_CAP;
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+// the kernels take the scale times log2(e), which has to be finite as well
+static bool scale_ok(float scale) { return scale > 0.f && scale * kLog2e <= 3.4e38f; }
 constexpr int kMaxRows = 1 << 24;
 
 int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_table, int32_t* free_list,
@@ -495,10 +501,12 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
   if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, n_kv) || !table_ok(max_blocks, block_size))
     return SPC_ERR_SHAPE;
   if (budget < 0 || budget > SPC_MAX_BUDGET) return SPC_ERR_SHAPE;
-  if (!(scale > 0.f) || scale > 3e38f) return SPC_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return SPC_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < kv4_attn_workspace(B, n_q, n_kv, max_blocks, block_size, budget))
     return SPC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
+  const int64_t io = (int64_t)B * n_q * d * 2;
+  if (overlap(out, io, q, io)) return SPC_ERR_INVALID_ARG;
   Kv4AttnCall c{};
   c.q = static_cast<const uint16_t*>(q); c.cache = static_cast<const uint8_t*>(cache); c.table = block_table;
   c.len = len; c.selected = selected; c.out = static_cast<uint16_t*>(out);
@@ -518,7 +526,7 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
                     void* workspace, size_t workspace_bytes, void* stream) {
   if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024) return SPC_ERR_SHAPE;
   if (B < 1 || B > SPC_MAX_BATCH || T < 0 || T > kMaxRows) return SPC_ERR_SHAPE;
-  if (!(scale > 0.f) || scale > 3e38f) return SPC_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return SPC_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < prompt_attn_workspace(T, B, n_q, n_kv)) return SPC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
   if (T == 0) return SPC_OK;
@@ -529,6 +537,10 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
   if (q_stride < qr || k_stride < kr || v_stride < kr || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
       q_stride > (1ll << 32) || k_stride > (1ll << 32) || v_stride > (1ll << 32))
     return SPC_ERR_SHAPE;
+  const int64_t ob = T * qr * 2;
+  if (overlap(out, ob, q, ((T - 1) * q_stride + qr) * 2) || overlap(out, ob, k, ((T - 1) * k_stride + kr) * 2) ||
+      overlap(out, ob, v, ((T - 1) * v_stride + kr) * 2))
+    return SPC_ERR_INVALID_ARG;
   PromptAttnCall c{};
   c.q = static_cast<const uint16_t*>(q); c.k = static_cast<const uint16_t*>(k); c.v = static_cast<const uint16_t*>(v);
   c.cu = cu_seqlens; c.out = static_cast<uint16_t*>(out);

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
       const int e1 = e / 2, e2 = e - e1;
       const float d1 = __uint_as_float((uint32_t)(127 - e1) << 23), d2 = __uint_as_float((uint32_t)(127 - e2) << 23);
       const float u1 = __uint_as_float((uint32_t)(127 + e1) << 23), u2 = __uint_as_float((uint32_t)(127 + e2) << 23);
-      const float fh = c.scale2 * u1 * u2;           // of head 8 n + gid
+      const float fh = k4_factor(c.scale2 * u1 * u2);           // of head 8 n + gid
       f[n][0] = __shfl_sync(0xffffffffu, fh, 8 * tig);
       f[n][1] = __shfl_sync(0xffffffffu, fh, 8 * tig + 4);
 #pragma unroll

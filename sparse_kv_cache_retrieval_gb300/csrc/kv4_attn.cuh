@@ -41,6 +41,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// A head's logit factor, kept from vanishing (queries of zeros, a small scale):
+// masked logits are -inf, and -inf times zero would not be. At this factor every
+// logit is zero but for 2^-100.
+__device__ __forceinline__ float k4_factor(float f) { return fmaxf(f, 1.17549435e-38f); }
 // 2^x by the MUFU approximation (relative error about 2^-22); -inf gives 0
 __device__ __forceinline__ float k4_ex2(float x) {
   float y;

@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
                      :: "r"(dst), "r"(pack_f16(bf_lo(w.x) * d1 * d2, bf_hi(w.x) * d1 * d2)),
                         "r"(pack_f16(bf_lo(w.y) * d1 * d2, bf_hi(w.y) * d1 * d2)) : "memory");
         if (lane == 0) {
-          mf[h] = make_float2(c.scale2 * __uint_as_float((uint32_t)(127 + e1) << 23) * __uint_as_float((uint32_t)(127 + e2) << 23), 0.f);
+          const float u1 = __uint_as_float((uint32_t)(127 + e1) << 23), u2 = __uint_as_float((uint32_t)(127 + e2) << 23);
+          mf[h] = make_float2(k4_factor(c.scale2 * u1 * u2), 0.f);
           mrun[h] = -INFINITY;
         }
       }

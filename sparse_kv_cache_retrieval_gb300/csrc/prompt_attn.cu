@@ -21,9 +21,10 @@
 // What a row does not see must not reach it, NaN and infinities included. In S
 // masked columns are replaced. In P V they meet P = 0, which a non-finite V
 // defeats: V rows behind the sequence's end are zeroed in shared memory before
-// they are used, and a row whose sum is finite but whose result is not (a
-// non-finite V in its own sequence, seen or not) is computed again by a warp
-// from global memory over exactly the keys it sees.
+// they are used, and a row whose sum is finite but whose result is not, though
+// no V that it sees explains that (a non-finite V behind it, or weights above 1
+// on values near the type's largest), is computed again by a warp from global
+// memory over exactly the keys it sees.
 //
 // One CTA per SM, persistent over items ordered by the number of key blocks,
 // longest first, and dealt to the CTAs in a snake:
@@ -46,6 +47,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "spc_device.cuh"
@@ -159,30 +161,96 @@ __device__ __forceinline__ void pa_tma_3d(uint32_t dst, const CUtensorMap* map, 
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
 }
 
-// One row by one warp, from global memory, over the keys it sees: the result
-// of lane l is dims 4l .. 4l + 3.
+__device__ __forceinline__ bool pa_not_finite(uint32_t bf) { return (bf & 0x7f80u) == 0x7f80u; }
+
+// One row by one warp, from global memory, over the keys it sees (h is the
+// query head, g its KV head): the result of lane l is dims 4l .. 4l + 3, held
+// as a running mean, so that it does not overflow where the mean does not.
 __device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g) {
+  constexpr int U = 8;                                 // keys a step, their loads in flight together
   const PromptAttnCall& c = a.c;
   const int lane = threadIdx.x & 31, t = start + qpos;
   const uint2 qw = *reinterpret_cast<const uint2*>(c.q + t * c.q_stride + (size_t)h * kD + 4 * lane);
   const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  for (int j = start; j <= t; ++j) {
-    const uint2 k = *reinterpret_cast<const uint2*>(c.k + j * c.k_stride + (size_t)g * kD + 4 * lane);
-    const uint2 v = *reinterpret_cast<const uint2*>(c.v + j * c.v_stride + (size_t)g * kD + 4 * lane);
-    const float x = c.scale2 * warp_sum(q0 * bf_lo(k.x) + q1 * bf_hi(k.x) + q2 * bf_lo(k.y) + q3 * bf_hi(k.y));
-    const float M = fmaxf(m, x);
-    const float e0 = m == -INFINITY ? 0.f : exp2f(m - M), e = exp2f(x - M);
-    l = l * e0 + e;
-    o0 = o0 * e0 + e * bf_lo(v.x);
-    o1 = o1 * e0 + e * bf_hi(v.x);
-    o2 = o2 * e0 + e * bf_lo(v.y);
-    o3 = o3 * e0 + e * bf_hi(v.y);
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j = start; j <= t; j += U) {
+    uint2 k[U], v[U];
+    float x[U], M = m;
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      k[e] = v[e] = make_uint2(0u, 0u);
+      if (j + e <= t) {
+        k[e] = *reinterpret_cast<const uint2*>(c.k + (j + e) * c.k_stride + (size_t)g * kD + 4 * lane);
+        v[e] = *reinterpret_cast<const uint2*>(c.v + (j + e) * c.v_stride + (size_t)g * kD + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      x[e] = c.scale2 * warp_sum(q0 * bf_lo(k[e].x) + q1 * bf_hi(k[e].x) + q2 * bf_lo(k[e].y) + q3 * bf_hi(k[e].y));
+      if (j + e > t) x[e] = -INFINITY;
+      M = fmaxf(M, x[e]);
+    }
+    const float Ms = M == -INFINITY ? 0.f : M, old = l * exp2f(m - Ms);
+    l = old;
+#pragma unroll
+    for (int e = 0; e < U; ++e) l += x[e] = exp2f(x[e] - Ms);
     m = M;
+    if (l == 0.f) continue;                            // nothing but -inf so far
+    const float r = 1.f / l;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] *= old * r;
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const float w = x[e] * r;
+      if (j + e > t) break;
+      o[0] += w * bf_lo(v[e].x);
+      o[1] += w * bf_hi(v[e].x);
+      o[2] += w * bf_lo(v[e].y);
+      o[3] += w * bf_hi(v[e].y);
+    }
   }
-  const float r = 1.f / l;
+  if (l == 0.f) o[0] = o[1] = o[2] = o[3] = NAN;
   *reinterpret_cast<uint2*>(c.out + ((size_t)t * c.n_q + h) * kD + 4 * lane) =
-      make_uint2(pack_bf16(o0 * r, o1 * r), pack_bf16(o2 * r, o3 * r));
+      make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+}
+
+// The rows of a warp's lanes in `again` have results that are not finite. In
+// the dims where a V that the row sees is not finite they stay; a row with
+// another such dim is computed again. One pass over V tells each dim's first
+// non-finite key, for all rows.
+__device__ void pa_rows_again(const PaArgs& a, uint32_t again, int start, int qpos, int h, int g) {
+  constexpr int U = 8;
+  const PromptAttnCall& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const int top = __reduce_max_sync(0xffffffffu, again >> lane & 1 ? qpos : 0);
+  int first[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
+  for (int j = 0; j <= top; j += U) {
+    uint2 v[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      v[e] = make_uint2(0u, 0u);
+      if (j + e <= top)
+        v[e] = *reinterpret_cast<const uint2*>(c.v + (start + j + e) * c.v_stride + (size_t)g * kD + 4 * lane);
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (pa_not_finite(v[e].x)) first[0] = min(first[0], j + e);
+      if (pa_not_finite(v[e].x >> 16)) first[1] = min(first[1], j + e);
+      if (pa_not_finite(v[e].y)) first[2] = min(first[2], j + e);
+      if (pa_not_finite(v[e].y >> 16)) first[3] = min(first[3], j + e);
+    }
+    if (__all_sync(0xffffffffu, max(max(first[0], first[1]), max(first[2], first[3])) < INT_MAX)) break;
+  }
+  __syncwarp();                                        // the rows' results are read by other lanes
+  while (again) {
+    const int src = __ffs(again) - 1;
+    again &= again - 1;
+    const int qp = __shfl_sync(0xffffffffu, qpos, src), hh = __shfl_sync(0xffffffffu, h, src);
+    const uint2 o = __ldcg(reinterpret_cast<const uint2*>(c.out + ((size_t)(start + qp) * c.n_q + hh) * kD) + lane);
+    if (__any_sync(0xffffffffu, (pa_not_finite(o.x) && first[0] > qp) || (pa_not_finite(o.x >> 16) && first[1] > qp) ||
+                                    (pa_not_finite(o.y) && first[2] > qp) || (pa_not_finite(o.y >> 16) && first[3] > qp)))
+      pa_row_again(a, start, qp, hh, g);
+  }
 }
 
 __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -605,12 +673,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         }
       }
       tc_fence_before();
-      uint32_t again = __ballot_sync(0xffffffffu, live && odd && l < INFINITY);
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        pa_row_again(a, start, __shfl_sync(0xffffffffu, qpos, src), __shfl_sync(0xffffffffu, h, src), g);
-      }
+      const uint32_t again = __ballot_sync(0xffffffffu, live && odd && l < INFINITY);
+      if (again) pa_rows_again(a, again, start, qpos, h, g);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));

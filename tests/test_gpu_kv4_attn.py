@@ -94,6 +94,18 @@ def test_zero_queries_average_the_values():
     run(c, torch.zeros(1, 4, 128, dtype=torch.bfloat16))
 
 
+@pytest.mark.parametrize("n_q", [8, 32])
+@pytest.mark.parametrize("scale", [1e-9, 1e-37])
+def test_zero_and_tiny_queries_at_a_small_scale(n_q, scale):
+    # every logit vanishes, the masked ones must not: 100 of 128 positions, and 37 selected ones of a tile
+    rng = np.random.default_rng(22)
+    c = Cache(rng, [100], 1, 16)
+    q = torch.zeros(1, n_q, 128, dtype=torch.bfloat16)
+    q[0, 1:] = (bf16(rng, n_q - 1, 128).float() * 1e-36).to(torch.bfloat16)
+    run(c, q, scale=scale)
+    run(c, q, selection(rng, [100], 1, 37), scale=scale)
+
+
 def test_what_lies_behind_the_context_does_not_count():
     # every byte behind the lengths is 0xff: codes -6 under NaN scales (Cache fills it so); longer tables too
     rng = np.random.default_rng(13)

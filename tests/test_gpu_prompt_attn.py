@@ -130,6 +130,34 @@ def test_later_rows_and_other_sequences_do_not_reach_a_row(bad):
     assert np.all(g[sum(lens):] == 7)
 
 
+def test_values_that_are_not_finite_stay_in_their_dims():
+    # dim 3 of the first row reaches every row, dim 9 of row 700 those from 700 on: the other dims, and dim 9
+    # of the rows before (70 of them in its block of keys), are as if both were finite
+    rng = np.random.default_rng(18)
+    n = 900
+    q, k, v = (bf16(rng, n, m, 128).to(DEV) for m in (4, 1, 1))
+    want, mag = P.prompt_attention(f64(q), f64(k), f64(v), [0, n], SCALE)
+    v[0, 0, 3], v[700, 0, 9] = float("nan"), float("inf")
+    got, _ = call(q, k, v, [0, n])
+    g = f64(got)
+    bad = np.zeros(g.shape, bool)
+    bad[:, :, 3] = True
+    bad[700:, :, 9] = True
+    assert not np.any(np.isfinite(g[bad]))
+    assert np.all(np.abs(g - want)[~bad] <= prompt_tol(want, mag)[~bad])
+
+
+def test_values_near_the_largest():
+    # weights are summed before they are divided by their sum: a few hundred values of 3e38 pass fp32's range there
+    rng = np.random.default_rng(19)
+    n = 300
+    q, k = bf16(rng, n, 2, 128).to(DEV), bf16(rng, n, 1, 128).to(DEV)
+    v = (torch.from_numpy(rng.uniform(2.5, 3.3, (n, 1, 128)) * 1e38)).to(torch.bfloat16).to(DEV)
+    v[:, :, 1::2] *= -1
+    got, _ = call(q, k, v, [0, n])
+    compare(got, q, k, v, [0, n])
+
+
 def test_rows_far_apart():
     # row strides that put the rows beyond 32-bit offsets
     rng = np.random.default_rng(15)

@@ -129,6 +129,20 @@ def test_prompt_attn_refusals(lib):
     assert lib.spc_prompt_attn(*empty) == 0
 
 
+def test_attention_refuses_overlapping_output_and_overflowing_scale(lib):
+    # addresses that no call reads: every one of these is refused before a launch
+    far = FAKE + (1 << 30)
+    dec = [FAKE, far, far, far, None, 2, 32, 8, 128, 100, 64, 16, 0, 0.1, FAKE + (1 << 28), FAKE, 1 << 40, None]
+    for out in (FAKE, FAKE + 2 * 32 * 256 - 16, FAKE - 2 * 32 * 256 + 16):
+        assert lib.spc_kv4_decode_attn(*dec[:14], out, *dec[15:]) == -1, out
+    assert lib.spc_kv4_decode_attn(*dec[:13], 2.5e38, *dec[14:]) == -1
+    pro = [FAKE, far, 2 * far, FAKE, 100, 2, 32, 8, 128, 8192, 1024, 1024, 0.1, 4 * far, FAKE, 1 << 40, None]
+    q_end = FAKE + (99 * 8192 + 4096) * 2
+    for out in (FAKE, q_end - 16, far, far + (99 * 1024 + 1024) * 2 - 16, 2 * far - 100 * 8192 + 16):
+        assert lib.spc_prompt_attn(*pro[:13], out, *pro[14:]) == -1, out
+    assert lib.spc_prompt_attn(*pro[:12], 2.5e38, *pro[13:]) == -1
+
+
 # ------------------------------------------------------------------ binding refusals
 def test_binding_refuses_wrong_tensors(lib):
     k = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
