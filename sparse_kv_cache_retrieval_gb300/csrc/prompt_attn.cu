@@ -31,16 +31,16 @@
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
 //   warp 8          tensor memory, MMA issue (one lane)
 //   warp 9          item schedule, TMA loads (Q per tile, K and V ring)
+//   warp 10         gate: passes the loads' arrival on to the MMA warp's barriers
 // Bound: the tensor pipe. A block of keys against both tiles is four products
-// of 512 cycles each; its exponentials are another 512 cycles of the same SM.
-// Measured, 32 heads on 8 KV heads: one sequence of 16384 tokens (2199 GFLOP)
-// 1.28-1.34 ms, and 1.39 ms in a long run, where the power limit lowers the
-// clock (0.86 and 0.83 of the measured matrix rate; tensor pipe 73% busy, the
-// rest is the diagonal blocks, of which half is masked, and the items' ends);
-// 4096 tokens (137 GFLOP) 96 us, 0.75; 16 sequences of 1 to 700 tokens 43 us,
-// where an item has one to six blocks and its first Q, K and S and its last PV
-// and store, which no other work of the CTA covers, weigh as much as the blocks
-// (the bytes alone are 17 us).
+// of 512 cycles; a period was 2650 cycles in a clock trace, of which the chain
+// of one tile (its S, 1130 cycles from S to P, the MMA warp's wait, its PV) is
+// what is left. Measured, 32 heads on 8 KV heads: one sequence of 16384 tokens
+// (2199 GFLOP) 1.18-1.22 ms, 0.94-0.98 of the measured matrix rate; 4096 tokens
+// (137 GFLOP) 91 us, 0.79; 16 sequences of 1 to 700 tokens 44 us, where an item
+// has one to six blocks and its first Q, K and S and its last PV and store,
+// which no other work of the CTA covers, weigh as much as the blocks (the bytes
+// alone are 17 us).
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
 // and leaves, the others' waits then give up in turn; copies land and MMAs
 // complete before the CTA releases its tensor memory.
@@ -62,8 +62,8 @@ constexpr uint32_t kPaBlock = kPaTile / 2;            // its 64-value half
 constexpr int kPaStages = 2;                          // ring of (V of a block, K of the next one)
 constexpr int kPaItems = 2;                           // item ring
 constexpr int kPaSoftWarps = 8;
-constexpr int kPaWarpMma = 8, kPaWarpTma = 9;
-constexpr int kPaThreads = 384;                       // warps 10, 11 fill the third warpgroup
+constexpr int kPaWarpMma = 8, kPaWarpTma = 9, kPaWarpGate = 10;
+constexpr int kPaThreads = 384;                       // warp 11 fills the third warpgroup
 // registers a thread: 168 at launch (384 threads); the softmax warpgroups take
 // 208, the third keeps 88 (2 * 208 + 88 = 3 * 168)
 constexpr int kPaRegSoft = 208, kPaRegRest = 88;
@@ -267,11 +267,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
   uint64_t* k0full = kvfree + kPaStages;      // TMA bytes
   uint64_t* k0free = k0full + 1;              // commit after the item's first S
   uint64_t* ifull = k0free + 1;               // [kPaItems] item written
-  uint64_t* ifree = ifull + kPaItems;         // [kPaItems] MMA warp and 8 softmax warps have read it
+  uint64_t* ifree = ifull + kPaItems;         // [kPaItems] MMA, gate and softmax warps have read it
   uint64_t* qfull = ifree + kPaItems;         // [2] TMA bytes
   uint64_t* qfree = qfull + 2;                // [2] commit after the tile's last S
   uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
-  uint64_t* pfull = sfull + 2;                // [2] 4 warp arrivals: P written, O rescaled
+  uint64_t* pfull = sfull + 2;                // [2] 4 softmax warps: P written, O rescaled; gate: V and the next K are there
   uint64_t* ofull = pfull + 2;                // [2] commit: the item's last PV done
   uint64_t* drain = ofull + 2;                // commit after the last MMA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -286,13 +286,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     mbar_init(k0free, 1);
     for (int s = 0; s < kPaItems; ++s) {
       mbar_init(&ifull[s], 1);
-      mbar_init(&ifree[s], kPaSoftWarps + 1);
+      mbar_init(&ifree[s], kPaSoftWarps + 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&qfull[s], 1);
       mbar_init(&qfree[s], 1);
       mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], kPaSoftWarps / 2);
+      mbar_init(&pfull[s], kPaSoftWarps / 2 + 1);
       mbar_init(&ofull[s], 1);
     }
     mbar_init(drain, 1);
@@ -452,9 +452,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     };
     // PV of block j of tile i, then S of block j + 1. The tensor pipe queues
     // only a few MMAs, so nothing waits between the two
-    auto issue = [&](auto tile, uint32_t st, int j, int n) {
+    auto issue = [&](auto tile, uint32_t st, int j, int n, uint64_t* stage_free) {
       constexpr int i = decltype(tile)::value;
-      acquire(&pfull[i], np[i] & 1);
+      // mostly there: tested before it is waited for (90 against 190 cycles)
+      if (!__all_sync(0xffffffffu, mbar_test(&pfull[i], np[i] & 1))) acquire(&pfull[i], np[i] & 1);
       ++np[i];
       if (dead) return;
       tc_fence_after();
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         } else {
           umma_commit(&ofull[i]);
         }
+        if (stage_free) umma_commit(stage_free);
       }
       __syncwarp();
     };
@@ -505,13 +507,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const int st = nkv % kPaStages;
-        acquire(&kvfull[st], (nkv / kPaStages) & 1);
         ++nkv;
         const uint32_t sd = pa_desc_lo(kvs) + (uint32_t)st * (2 * kPaTile >> 4);
-        if (j < nA) issue(tA, sd, j, nA);
-        if (j < nB) issue(tB, sd, j, nB);
-        if (!dead && elect_one()) umma_commit(&kvfree[st]);
-        __syncwarp();
+        if (j < nA) issue(tA, sd, j, nA, j < nB ? nullptr : &kvfree[st]);
+        if (j < nB) issue(tB, sd, j, nB, &kvfree[st]);
       }
       if (dead) break;
     }
@@ -675,6 +674,40 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       tc_fence_before();
       const uint32_t again = __ballot_sync(0xffffffffu, live && odd && l < INFINITY);
       if (again) pa_rows_again(a, again, start, qpos, h, g);
+    }
+  } else if (warp == kPaWarpGate) {
+    // ================= gate: passes the arrival of V_j and K_(j+1) on to the
+    // tiles' P barriers, so that the MMA warp waits once a batch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !pa_wait(a, bar, parity)) {
+        if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+        dead = true;
+      }
+    };
+    int nkv = 0, np[2] = {0, 0};
+    for (int it = 0; !dead; ++it) {
+      const int is = it % kPaItems;
+      acquire(&ifull[is], (it / kPaItems) & 1);
+      if (dead) break;
+      const int nA = items[is].nA, nB = items[is].nB, len = items[is].len;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (len < 0) break;
+      for (int j = 0; j < max(nA, nB); ++j, ++nkv) {
+        acquire(&kvfull[nkv % kPaStages], (nkv / kPaStages) & 1);
+        if (dead) break;
+        // one arrival a phase: the block before's P has been written
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (j >= (i ? nB : nA)) continue;
+          if (np[i] > 0) acquire(&pfull[i], (np[i] - 1) & 1);
+          if (dead) break;
+          ++np[i];
+          if (lane == 0) mbar_arrive(&pfull[i]);
+        }
+        if (dead) break;
+      }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPaRegRest));
