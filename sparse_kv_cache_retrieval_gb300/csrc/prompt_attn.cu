@@ -36,11 +36,11 @@
 // of 512 cycles; a period was 2650 cycles in a clock trace, of which the chain
 // of one tile (its S, 1130 cycles from S to P, the MMA warp's wait, its PV) is
 // what is left. Measured, 32 heads on 8 KV heads: one sequence of 16384 tokens
-// (2199 GFLOP) 1.18-1.22 ms, 0.94-0.98 of the measured matrix rate; 4096 tokens
-// (137 GFLOP) 91 us, 0.79; 16 sequences of 1 to 700 tokens 44 us, where an item
-// has one to six blocks and its first Q, K and S and its last PV and store,
-// which no other work of the CTA covers, weigh as much as the blocks (the bytes
-// alone are 17 us).
+// (2199 GFLOP) 1.21-1.26 ms, 0.91-0.95 of the measured matrix rate, and 1.32 ms
+// in a long run, where the power limit lowers the clock; 4096 tokens (137 GFLOP)
+// 91 us, 0.79; 16 sequences of 1 to 700 tokens 44 us (their bytes alone are 17):
+// an item has one to six blocks, and its first S, its epilogue (about 3000
+// cycles) and the sixth item of a few CTAs weigh as much as the blocks.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
 // and leaves, the others' waits then give up in turn; copies land and MMAs
 // complete before the CTA releases its tensor memory.
