@@ -88,6 +88,18 @@ def test_queries_of_any_size(qscale):
     run(Cache(rng, [400, 90], 2, 64), q, scale=SCALE / qscale)
 
 
+@pytest.mark.parametrize("n_q", [8, 64])
+def test_addresses_on_16_byte_boundaries(n_q):
+    rng = np.random.default_rng(23)
+    c = Cache(rng, [333, 0], 1, 16)
+    q = bf16(rng, 2 * n_q * 128 + 8).to(DEV)[8:].view(2, n_q, 128)
+    cache = torch.zeros(c.rec.size + 16, dtype=torch.uint8, device=DEV)[16:]
+    cache.copy_(torch.from_numpy(c.rec.reshape(-1)))
+    out = torch.full((2 * n_q * 128 + 8,), 7.0, dtype=torch.bfloat16, device=DEV)[8:].view(2, n_q, 128)
+    run(c, q, out=out, cache=cache)
+    run(c, q, selection(rng, c.lens, 1, 50), out=out, cache=cache)
+
+
 def test_zero_queries_average_the_values():
     rng = np.random.default_rng(12)
     c = Cache(rng, [100], 1, 16)

@@ -8,7 +8,7 @@ import torch
 
 import oracle.paged_oracle as P
 from sparse_kv_cache_retrieval_gb300 import binding as spc
-from tests.paged_cases import DEV, SCALE, bf16, check, decode_tol, f64, i32, prompt_tol
+from tests.paged_cases import DEV, SCALE, Cache, bf16, check, decode, decode_tol, f64, i32, prompt_tol
 
 pytestmark = pytest.mark.gpu
 B, N_Q, N_KV, BS, MB, NUM = 3, 16, 2, 16, 12, 30
@@ -85,3 +85,40 @@ def test_prompts_decode_steps_and_a_new_request():
     spc.spc_kv4_load(r.d["cache"], i32(slots), k, v, n, N_KV, 128, NUM, BS)
     wk, wv = P.values(r.rec[slots // BS, :, slots % BS])
     assert np.array_equal(f64(k), wk) and np.array_equal(f64(v), wv)
+
+
+def test_calls_on_three_streams_at_once():
+    # each with a workspace of its own; every result the same as alone
+    rng = np.random.default_rng(41)
+    c = Cache(rng, [3000, 900, 5000], 1, 64)
+    lens = [700, 1300]
+    q, k, v = (bf16(rng, sum(lens), n, 128).to(DEV) for n in (16, 2, 2))
+    cu = i32([0, 700, 2000])
+    cache, table, ln = torch.from_numpy(c.rec).to(DEV), i32(c.table), i32(c.lens)
+
+    def prompt(stream, out, ws):
+        spc.spc_prompt_attn(q, k, v, cu, 2000, 2, 16, 2, 128, SCALE, out, ws, stream=stream)
+
+    def attend(n_q):
+        qd = bf16(rng, 3, n_q, 128).to(DEV)
+        return lambda stream, out, ws: decode(c, qd, out=out, ws=ws, cache=cache, table=table, lens=ln, stream=stream)
+
+    calls = [(prompt, (2000, 16, 128), spc.spc_prompt_attn_workspace_size(2000, 2, 16, 2, 128))]
+    for n_q in (8, 64):
+        calls.append((attend(n_q), (3, n_q, 128), spc.spc_kv4_decode_attn_workspace_size(3, n_q, 1, 128, c.max_blocks, 64, 0)))
+    runs = []
+    for f, shape, size in calls:
+        s, ws = torch.cuda.Stream(), torch.zeros(size, dtype=torch.uint8, device=DEV)
+        alone = torch.zeros(shape, dtype=torch.bfloat16, device=DEV)
+        s.wait_stream(torch.cuda.current_stream())
+        f(s, alone, ws)
+        s.synchronize()
+        runs.append((f, s, ws, alone, [torch.zeros_like(alone) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for f, s, ws, _, outs in runs:
+            f(s, outs[i], ws)
+    torch.cuda.synchronize()
+    for _, _, ws, alone, outs in runs:
+        assert int(ws[:4].view(torch.int32).item()) == 0
+        assert all(torch.equal(alone, o) for o in outs)

@@ -158,6 +158,15 @@ def test_values_near_the_largest():
     compare(got, q, k, v, [0, n])
 
 
+def test_addresses_on_16_byte_boundaries():
+    rng = np.random.default_rng(20)
+    lens = [70, 333]
+    q, k, v = (bf16(rng, 403 * n * 128 + 8).to(DEV)[8:].view(403, n, 128) for n in (8, 2, 2))
+    out = torch.full((403 * 8 * 128 + 8,), 7.0, dtype=torch.bfloat16, device=DEV)[8:].view(403, 8, 128)
+    got, _ = call(q, k, v, offsets(lens), out=out)
+    compare(got, q, k, v, offsets(lens))
+
+
 def test_rows_far_apart():
     # row strides that put the rows beyond 32-bit offsets
     rng = np.random.default_rng(15)
