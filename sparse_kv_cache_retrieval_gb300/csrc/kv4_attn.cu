@@ -70,7 +70,15 @@ struct K4Cfg {
   static constexpr int kCopy = !SEL ? 1 : HT == 1 ? 5 : 2;
   static constexpr int kWarps = kAll - kCopy;          // warps that compute
   static constexpr int kStages = HT == 1 ? 2 : 4;      // tiles in a warp's ring
-  static constexpr int kMinRun = 2 * kAll;             // tiles a CTA takes before a segment is split
+  // Tiles up to which a segment is never split, and that a CTA takes at least
+  // of one that is. A split costs about 2.5 us (8 segments of 10 tiles: 5.6 us
+  // whole, 8.1 split); where one is made, small runs spread the work (8
+  // segments of 63 tiles: 8.4 us at 8, 11.0 at 32) until the merge, which grows
+  // with the heads, outweighs it (16 heads, 125 tiles: 13.5 us at 12, 17.6 at 4
+  // and 13.1 at 16, but 32 tiles 11.6 at 12 and 13.1 at 16; 64 heads, 128
+  // selected tiles: 22 us at 16, 31 at 4).
+  static constexpr int kWhole = HT == 1 ? 24 : 16;
+  static constexpr int kMinRun = HT == 1 ? 8 : HT == 2 ? 12 : 16;
   static constexpr int kSlack = 2 * kAll;              // tiles that a second piece costs a CTA, about
   static constexpr int kThreads = 32 * kAll;
   // shared memory
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     }
     fence_mbar_init();
   }
-  if (warp == 0) k4_plan<kK4Tile, Cfg::kMinRun, Cfg::kSlack>(a, ln, segs, SEL);
+  if (warp == 0) k4_plan<kK4Tile, Cfg::kWhole, Cfg::kMinRun, Cfg::kSlack>(a, ln, segs, SEL);
   __syncthreads();
   const int total = ln.pre[c.B], t0 = ln.t0, t1 = ln.t1;
 

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 0) k4_plan<kKtTile, kKtMinRun, kKtSlack>(a, ln, segs, false);
+  if (warp == 0) k4_plan<kKtTile, kKtMinRun, kKtMinRun, kKtSlack>(a, ln, segs, false);
   if (warp == kKtWarpMma) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
