@@ -52,6 +52,14 @@ __device__ __forceinline__ float k4_ex2(float x) {
   return y;
 }
 
+// x / d for 0 <= x <= 2^21 (a request's tiles, or a segment's times the CTAs), d
+// >= 1. The approximate quotient is off by less than one there; an integer
+// division costs some 150 cycles each in a plan that every CTA waits for.
+__device__ __forceinline__ int k4_div(int x, int d) {
+  const int q = (int)__fdividef((float)x, (float)d), r = x - q * d;
+  return q + (r >= d ? 1 : 0) - (r < 0 ? 1 : 0);
+}
+
 // the line of tiles: request b's tiles (of every KV head and head split) start at pre[b]
 struct K4Line {
   int pre[SPC_MAX_BATCH + 1];
@@ -92,7 +100,7 @@ __device__ __forceinline__ K4Cursor k4_at(const Kv4AttnCall& c, const K4Line& ln
   x.b = lo;
   k4_seg(c, ln, x);
   const int r = t - ln.pre[lo];
-  x.s = r / x.nt;
+  x.s = k4_div(r, x.nt);
   x.i = r - x.s * x.nt;
   return x;
 }
@@ -141,15 +149,16 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
   //  - with fewer segments than CTAs, each gets a number of CTAs of its own,
   //    if that makes no run longer than SLACK tiles above an equal share;
   //  - else equal runs of the line.
-  const int total = __shfl_sync(0xffffffffu, incl, 31), grid = gridDim.x, blk = blockIdx.x;
+  constexpr int grid = kK4Ctas;
+  const int total = __shfl_sync(0xffffffffu, incl, 31), blk = blockIdx.x;
   const int nt0 = ln.nt[2 * lane], nt1 = ln.nt[2 * lane + 1];
   int run = max((total + grid - 1) / grid, MIN_RUN), np0 = 0, np1 = 0;      // np: pieces a segment
   const bool small = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(nt0, nt1)) <= WHOLE;
   bool whole = small;
   for (int k = 0; k <= 2 && !whole; ++k) {
     const int r = run + k * (SLACK / 2);
-    np0 = (nt0 + r - 1) / r;
-    np1 = (nt1 + r - 1) / r;
+    np0 = k4_div(nt0 + r - 1, r);
+    np1 = k4_div(nt1 + r - 1, r);
     whole = (int)__reduce_add_sync(0xffffffffu, (unsigned)((np0 + np1) * segs)) <= grid;
   }
   int t0, t1, first = blk, last = blk;
@@ -165,7 +174,7 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
     auto start = [&](int x) {                      // of the first segment that starts at or behind x of that line
       const int e = find(s0, s1, x), len = max(1, __shfl_sync(0xffffffffu, e & 1 ? w1 : w0, e >> 1));
       const int p = __shfl_sync(0xffffffffu, e & 1 ? s1 : s0, e >> 1);
-      return min(total, ln.pre[e] + (x - p + len - 1) / len * ln.nt[e]);
+      return min(total, ln.pre[e] + k4_div(x - p + len - 1, len) * ln.nt[e]);
     };
     t0 = start((int)((long long)wt * blk / grid));
     t1 = start((int)((long long)wt * (blk + 1) / grid));
@@ -176,11 +185,11 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
     const int c0e = __shfl_sync(0xffffffffu, e & 1 ? c1 : c0, e >> 1);
     t0 = t1 = total;
     if (blk < __shfl_sync(0xffffffffu, end, 31)) {
-      const int r = blk - c0e, sg = r / np, q = r - sg * np, s0 = ln.pre[e] + sg * nt;
+      const int r = blk - c0e, sg = k4_div(r, np), q = r - sg * np, s0 = ln.pre[e] + sg * nt;
       first = blk - q;
       last = first + np - 1;
-      t0 = s0 + nt * q / np;
-      t1 = s0 + nt * (q + 1) / np;
+      t0 = s0 + k4_div(nt * q, np);
+      t1 = s0 + k4_div(nt * (q + 1), np);
     }
   } else {
     t0 = min(total, blk * run);
