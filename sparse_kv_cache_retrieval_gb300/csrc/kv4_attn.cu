@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
   int n_wait = 0;                                    // tiles this warp has waited for
 
   // requests without a tile: zeros
-  for (int b = 0; b < c.B; ++b) {
+  for (int b = ln.empty ? 0 : c.B; b < c.B; ++b) {
     if (ln.nt[b] != 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
     for (int i = blockIdx.x * 32 * kWarps + threadIdx.x; i < c.n_q * kD / 8; i += gridDim.x * 32 * kWarps)
@@ -469,10 +469,10 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // biased exponent of the largest value; 2^-e as two factors, each normal
+      // exponent of the largest value; 2^e as two factors, each normal (2^-e may be subnormal, and is exact)
       const int e = max((int)(mx >> 7), 1) - 127;
       const int e1 = e / 2, e2 = e - e1;
-      const float d1 = __uint_as_float((uint32_t)(127 - e1) << 23), d2 = __uint_as_float((uint32_t)(127 - e2) << 23);
+      const float down = __uint_as_float((uint32_t)(127 - e1) << 23) * __uint_as_float((uint32_t)(127 - e2) << 23);
       const float u1 = __uint_as_float((uint32_t)(127 + e1) << 23), u2 = __uint_as_float((uint32_t)(127 + e2) << 23);
       const float fh = k4_factor(c.scale2 * u1 * u2);           // of head 8 n + gid
       f[n][0] = __shfl_sync(0xffffffffu, fh, 8 * tig);
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
         unpack8(w[i], x);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint32_t b0 = pack_f16(x[4 * y] * d1 * d2, x[4 * y + 1] * d1 * d2);
-          const uint32_t b1 = pack_f16(x[4 * y + 2] * d1 * d2, x[4 * y + 3] * d1 * d2);
+          const uint32_t b0 = pack_f16(x[4 * y] * down, x[4 * y + 1] * down);
+          const uint32_t b1 = pack_f16(x[4 * y + 2] * down, x[4 * y + 3] * down);
           if constexpr (HT == 1) {
             qr[4 * i + 2 * y] = b0;
             qr[4 * i + 2 * y + 1] = b1;

@@ -66,6 +66,7 @@ struct K4Line {
   int nt[SPC_MAX_BATCH];       // tiles a segment of request b
   int run;                     // tiles a CTA takes; 2^30: runs end with their segments
   int t0, t1;                  // this CTA's run
+  int empty;                   // some request has no tile
   int first, last;             // whole runs: the CTAs of its segment
   int len[SPC_MAX_BATCH];
 };
@@ -144,7 +145,7 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
   // last piece, so runs end with their segments where they can:
   //  - segments of at most WHOLE tiles are never split: each CTA takes those
   //    that start in its share of a line in which every segment is SLACK longer
-  //    (32 requests of 16 to 200 positions, 8 heads: 10.7 us, without 22.8);
+  //    (32 requests of 16 to 200 positions, 8 heads: 8.8 us, without about 20);
   //  - runs have MIN_RUN tiles at least;
   //  - with fewer segments than CTAs, each gets a number of CTAs of its own,
   //    if that makes no run longer than SLACK tiles above an equal share;
@@ -161,6 +162,7 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
     np1 = k4_div(nt1 + r - 1, r);
     whole = (int)__reduce_add_sync(0xffffffffu, (unsigned)((np0 + np1) * segs)) <= grid;
   }
+  const bool empty = __any_sync(0xffffffffu, (2 * lane < c.B && nt0 == 0) || (2 * lane + 1 < c.B && nt1 == 0));
   int t0, t1, first = blk, last = blk;
   __syncwarp();                              // all lanes' ln.pre and ln.nt are read below
   // the last request that starts at or before x (the starts s0, s1 of this lane's two)
@@ -197,6 +199,7 @@ __device__ __forceinline__ void k4_plan(const Kv4Args& a, K4Line& ln, int segs, 
   }
   if (lane == 0) {
     ln.run = whole ? 1 << 30 : run;
+    ln.empty = empty ? 1 : 0;
     ln.t0 = t0;
     ln.t1 = t1;
     ln.first = first;

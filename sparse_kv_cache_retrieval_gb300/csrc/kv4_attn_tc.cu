@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     float* al = reinterpret_cast<float*>(base + kKtOffAl);
     float* red = reinterpret_cast<float*>(base + kKtOffRed);
     // requests without a tile: zeros
-    for (int b = 0; b < c.B; ++b) {
+    for (int b = ln.empty ? 0 : c.B; b < c.B; ++b) {
       if (ln.nt[b] != 0) continue;
       uint4* dst = reinterpret_cast<uint4*>(c.out + (size_t)b * c.n_q * kD);
       for (int i = blockIdx.x * 128 + row; i < c.n_q * kD / 8; i += gridDim.x * 128) dst[i] = make_uint4(0u, 0u, 0u, 0u);
