@@ -41,7 +41,10 @@ constexpr int kKtTile = 128;                          // positions
 constexpr uint32_t kKtRaw = kKtTile * kKv4Rec;        // 18 KB: a tile's records
 constexpr int kKtStages = 6;
 constexpr int kKtMasks = 16;                          // tiles whose masks are kept
-constexpr int kKtMinRun = 8, kKtSlack = 8;            // see k4_plan
+// See k4_plan. A tile is 0.7 us of the CTA that has it, the merge some 3 us and
+// a little a piece: 64 heads on one, 1 x 2000: 10.6 us with these, 17.9 with 8
+// and 8; 1 x 65536 26.4 and 24.8.
+constexpr int kKtWhole = 4, kKtMinRun = 2, kKtSlack = 8;
 constexpr uint32_t kKtV = kKtTile * kRowBytes;        // 32 KB: V of a tile, fp16
 constexpr uint32_t kKtP = kKtTile * 128;              // 16 KB: P, 64 heads a row
 constexpr int kKtWarpMma = 12, kKtWarpCopy = 13;
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 0) k4_plan<kKtTile, kKtMinRun, kKtMinRun, kKtSlack>(a, ln, segs, false);
+  if (warp == 0) k4_plan<kKtTile, kKtWhole, kKtMinRun, kKtSlack>(a, ln, segs, false);
   if (warp == kKtWarpMma) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
@@ -625,8 +628,8 @@ static int kt_run(const Kv4Args& a, void* stream) {
   KtSegment* segments = static_cast<KtSegment*>(a.segments);
   kv4_attn_tc_kernel<N><<<kK4Ctas, kKtThreads, kKtSmem, st>>>(a, segments);
   if (cudaGetLastError() != cudaSuccess) return SPC_ERR_CUDA;
-  // no segment is split where the table has room for kKtMinRun tiles at most
-  if ((a.c.max_blocks << a.c.block_shift) <= kKtMinRun * kKtTile) return SPC_OK;
+  // no segment is split where the table has room for kKtWhole tiles at most
+  if ((a.c.max_blocks << a.c.block_shift) <= kKtWhole * kKtTile) return SPC_OK;
   kt_merge_kernel<N><<<dim3((unsigned)(a.c.B * a.c.n_kv), N / kKmWarps), 32 * kKmWarps, 0, st>>>(a, segments);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
