@@ -27,7 +27,7 @@
 // at N = 64, 1000 at N = 32: logits 150, exponentials 64 N / 16, the stores of P
 // and their proxy fence, the barrier), and it is what bounds the kernel.
 // Measured (8 requests of 65536 positions on one KV head, 75 MB, floor 11 us):
-// N = 64 48 us, N = 32 39 us; the mma.sync kernel 89 and 62.
+// N = 64 47 us, N = 32 38 us; the mma.sync kernel 89 and 62.
 // Every wait is bounded; a warp whose wait gives up records SPC_ERR_TIMEOUT and
 // runs on without waiting, so that the softmax warps' barriers are reached.
 #include <cuda_runtime.h>
