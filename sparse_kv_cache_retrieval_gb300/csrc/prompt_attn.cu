@@ -36,9 +36,9 @@
 // of 512 cycles; a period was 2650 cycles in a clock trace, of which the chain
 // of one tile (its S, 1130 cycles from S to P, the MMA warp's wait, its PV) is
 // what is left. Measured, 32 heads on 8 KV heads: one sequence of 16384 tokens
-// (2199 GFLOP) 1.21-1.26 ms, 0.91-0.95 of the measured matrix rate, and 1.32 ms
+// (2199 GFLOP) 1.19-1.24 ms, 0.93-0.97 of the measured matrix rate, and 1.32 ms
 // in a long run, where the power limit lowers the clock; 4096 tokens (137 GFLOP)
-// 91 us, 0.79; 16 sequences of 1 to 700 tokens 44 us (their bytes alone are 17):
+// 90 us, 0.80; 16 sequences of 1 to 700 tokens 41 us (their bytes alone are 17):
 // an item has one to six blocks, and its first S, its epilogue (about 3000
 // cycles) and the sixth item of a few CTAs weigh as much as the blocks.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
@@ -549,41 +549,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         acquire(&sfull[i], n_s & 1);
         if (dead) break;
         tc_fence_after();
-        float s[128], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        bool redo = true;
-        float M;
-        if ((j + 1) * kPaKeys <= t0 + 1 && !__any_sync(0xffffffffu, m == -INFINITY)) {
-          // every row sees the whole block and has a maximum: weights against
-          // it at once, while the block's own maximum is being found
-          tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            pa_ld_wait(s + 32 * q);
-            if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
-            pa_max32(s + 32 * q, mx);
-            pa_weights(s + 32 * q, c.scale2, m, sum, ts + 16 * q);
-          }
-          M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
-          redo = __any_sync(0xffffffffu, M > m + kPaHeadroom);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
-          // columns 0 .. seen are visible, 0 .. seen0 to every row of the warp
-          const int seen = qpos - j * kPaKeys, seen0 = t0 + (((warp & 3) * 32) >> a.gshift) - j * kPaKeys;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            pa_ld_wait(s + 32 * q);
-            if (seen0 < 32 * q + 31) {
-#pragma unroll
-              for (int e = 32 * q; e < 32 * q + 32; ++e)
-                if (e > seen) s[e] = -INFINITY;
-            }
-            pa_max32(s + 32 * q, mx);
-          }
-          M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
-        }
-        if (redo) {
+        // raises the row's maximum to M where that is needed
+        auto raise = [&](float M) {
           float alpha = 1.f;
           const bool up = M > m + kPaHeadroom;
           if (up) {
@@ -604,10 +573,62 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
               tmem_st16(to + 16 * q, o);
             }
           }
-          const float mm = m == -INFINITY ? 0.f : m;
-          sum[0] = sum[1] = make_float2(0.f, 0.f);
+        };
+        if ((j + 1) * kPaKeys <= t0 + 1 && !__any_sync(0xffffffffu, m == -INFINITY)) {
+          // every row sees the whole block and has a maximum: weights against
+          // it at once, while the block's own maximum is being found
+          float s[128];
+          tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) pa_weights(s + 32 * q, c.scale2, mm, sum, ts + 16 * q);
+          for (int q = 0; q < 4; ++q) {
+            pa_ld_wait(s + 32 * q);
+            if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
+            pa_max32(s + 32 * q, mx);
+            pa_weights(s + 32 * q, c.scale2, m, sum, ts + 16 * q);
+          }
+          const float M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
+          if (__any_sync(0xffffffffu, M > m + kPaHeadroom)) {
+            raise(M);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) pa_weights(s + 32 * q, c.scale2, m, sum, ts + 16 * q);
+          }
+        } else {
+          // An item's first block and its last one: S is read twice, in chunks
+          // of 32 columns, without the chunks that no row of the warp sees (64
+          // sequences of 100 tokens: 39.5 -> 35.1 us; all four chunks from
+          // registers, 39.5, and in loops, 42.9). Columns 0 .. seen are visible,
+          // 0 .. seen0 to every row of the warp, none behind seen1 to any; the
+          // tile's tokens lie in one block of keys, so that seen1 >= 0.
+          const int w0 = (warp & 3) * 32, at = t0 - j * kPaKeys;
+          const int seen = qpos - j * kPaKeys, seen0 = at + (w0 >> a.gshift), seen1 = at + ((w0 + 31) >> a.gshift);
+          auto load = [&](int q, float (&v)[32]) {
+            tmem_ld32(ts + 32 * q, v);
+            pa_ld_wait(v);
+            if (seen0 < 32 * q + 31) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * q + e > seen) v[e] = -INFINITY;
+            }
+          };
+          const int nq = min(4, seen1 / 32 + 1);
+#pragma unroll 1
+          for (int q = 0; q < nq; ++q) {
+            float v[32];
+            load(q, v);
+            pa_max32(v, mx);
+          }
+          raise(pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2);
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int q = 0; q < nq; ++q) {
+            float v[32];
+            load(q, v);
+            pa_weights(v, c.scale2, mm, sum, ts + 16 * q);
+          }
+          const uint32_t none[16] = {};
+#pragma unroll 1
+          for (int q = nq; q < 4; ++q) tmem_st16(ts + 16 * q, none);
         }
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         if ((j + 1) * kPaKeys > len) {
