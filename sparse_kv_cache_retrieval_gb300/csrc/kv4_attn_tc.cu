@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       if (dead) break;
       const uint32_t bits = (1u << rows) - 1, hi = __shfl_down_sync(0xffffffffu, bits, 1);
       if (lane < 8 && !(lane & 1)) masks[i % kKtMasks * 4 + (lane >> 1)] = bits | hi << 16;
+      __syncwarp();                                   // lane 0's arrival releases the four lanes' masks
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, (unsigned)rows) * kKv4Rec;
       if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], bytes);
       __syncwarp();
