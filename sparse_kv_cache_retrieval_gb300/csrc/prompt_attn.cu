@@ -588,6 +588,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           }
           const float M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
           if (__any_sync(0xffffffffu, M > m + kPaHeadroom)) {
+            // the weights go to the same columns again, and stores to tensor
+            // memory are asynchronous: the first ones have to be there
+            tmem_st_wait();
             raise(M);
             sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
