@@ -9,8 +9,13 @@
 // A 4-bit code times its e4m3 scale is exact in fp16, so dequantised operands
 // lose nothing. The queries are scaled per head by a power of two to below 2
 // and rounded to fp16 (11 bits; bf16 has 8, so only values 2^-14 below the
-// head's largest lose bits, at most 2^-25 of it). The weights P are rounded to
-// fp16 (2^-11); maxima, sums and outputs are fp32.
+// head's largest lose bits, at most 2^-25 of it); maxima, sums and outputs are
+// fp32. The weights P are rounded to fp16, whose range is used from its top:
+// they are kept 2^14 times those against the running maximum, in the sums as
+// well, so that they have 11 bits down to 2^-28 of the largest and are off by at
+// most 2^-39 of it below. (Without the factor, 2^-14 and 2^-25: where a position
+// with a V near zero takes nearly all the weight, 65536 small weights that the
+// sum counts and the products lose are the whole result.)
 //
 // Layout: a record is 36 words, so 8 consecutive rows start 4 banks apart.
 // The 32 positions of a step are dealt to the two 16-row tiles so that both
@@ -25,8 +30,8 @@
 //      one scale group.
 //
 // The running maximum of a head is raised only when a logit passes it by more
-// than 8 in base 2 (weights stay below 2^8, exact in the sums' fp32 and no
-// coarser in fp16), which takes the shuffles out of the common case.
+// than 1.75 in base 2 (weights stay below 2^15.75, under fp16's largest), which
+// takes the shuffles out of the common case.
 //
 // Work: all segments' 32-position tiles in one line, cut into runs, one per CTA
 // (k4_plan; the lengths are read on the device). Tile t of a run belongs to
@@ -60,6 +65,9 @@ namespace spc {
 
 constexpr int kK4Tile = 32;                          // positions a tile
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
+constexpr float kK4Bias = 14.f;                      // log2 of the factor of the weights
+constexpr float kK4Limit = kK4Bias + 1.75f;          // log2 of the largest weight before the maximum is raised
+static_assert(kK4Limit <= 15.9f, "weights within fp16's range");
 
 // The CTA of a kernel for HT head tiles; the last warps copy for the others:
 // one where the whole context is read, 5 (or 2 of 8) where positions are
@@ -320,13 +328,14 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
     // logits in base 2; f > 0, so the maximum may be scaled alone
     mx[0] *= f[n][0];
     mx[1] *= f[n][1];
-    const bool up = mx[0] > m[n][0] + kK4Headroom || mx[1] > m[n][1] + kK4Headroom;
+    // m is the running maximum less kK4Bias
+    const bool up = mx[0] > m[n][0] + kK4Limit || mx[1] > m[n][1] + kK4Limit;
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int k = 4; k <= 16; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], k));
-        const float M = fmaxf(m[n][e], mx[e]);
+        const float M = fmaxf(m[n][e], mx[e] - kK4Bias);
         // a first finite maximum takes 0 of what was (nothing)
         const float c = k4_ex2(m[n][e] - (M == -INFINITY ? 0.f : M));
         m[n][e] = M;

@@ -19,7 +19,6 @@ constexpr int kK4MaxKv = 128;                        // KV heads
 constexpr size_t kK4OffCount = 256;
 constexpr size_t kK4OffSeg = kK4OffCount + (size_t)SPC_MAX_BATCH * kK4MaxKv * 2 * 4;
 constexpr size_t kK4OffPart = kK4OffSeg + (size_t)SPC_MAX_BATCH * kK4MaxKv * 16;
-constexpr float kK4Headroom = 8.f;                   // log2 growth allowed before the maximum is raised
 constexpr long long kK4WaitLimit = 4000000000ll;     // clock cycles
 
 struct Kv4Args {

@@ -13,9 +13,14 @@
 // an MN-major operand; the softmax thread of the position has its logits of
 // all heads and writes one row of P. So nothing is exchanged between positions
 // but the heads' maxima, and those only when a logit passes the running one by
-// more than 8 (a barrier's OR tells), and the sums, once a segment.
+// more than 4.75 (a barrier's OR tells), and the sums, once a segment.
 // Operands are fp16: K and V exact, Q scaled per head by a power of two and P
-// rounded (2^-11); logits, maxima, sums and O are fp32.
+// rounded; logits, maxima, sums and O are fp32. P and the sums are kept 2^11
+// times the weights against the running maximum, the top of fp16's range (see
+// kv4_attn.cu): 11 bits down to 2^-25 of the largest, off by at most 2^-36 of it
+// below. A raise costs about a tile here, which is why more of the range is left
+// to growth than there (8 x 65536, 64 heads on one: 47.5 us with a factor of 2^10,
+// 47.9 with 2^11, 49.7 with 2^12).
 //
 // One CTA per SM, 16 warps:
 //   0-3    softmax and epilogue (one position, in the epilogue one dim, a thread)
@@ -41,6 +46,9 @@ constexpr int kKtTile = 128;                          // positions
 constexpr uint32_t kKtRaw = kKtTile * kKv4Rec;        // 18 KB: a tile's records
 constexpr int kKtStages = 6;
 constexpr int kKtMasks = 16;                          // tiles whose masks are kept
+constexpr float kKtBias = 11.f;                       // log2 of the factor of the weights
+constexpr float kKtHeadroom = 4.75f;                  // log2 growth allowed before a maximum is raised
+static_assert(kKtBias + kKtHeadroom <= 15.9f, "weights within fp16's range");
 // See k4_plan. A tile is 0.7 us of the CTA that has it, the merge some 3 us and
 // a little a piece: 64 heads on one, 1 x 2000: 10.6 us with these, 17.9 with 8
 // and 8; 1 x 65536 26.4 and 24.8.
@@ -59,7 +67,7 @@ constexpr uint32_t kKtOffV = 0;                                      // [2]
 constexpr uint32_t kKtOffP = kKtOffV + 2 * kKtV;                     // [2]
 constexpr uint32_t kKtOffQ = kKtOffP + 2 * kKtP;                     // [2 halves of 64 dims][N][128 bytes]
 constexpr uint32_t kKtOffRaw = kKtOffQ + 64 * kRowBytes;             // [kKtStages]
-constexpr uint32_t kKtOffMf = kKtOffRaw + kKtStages * kKtRaw;        // [64] float2: logit factor, -maximum
+constexpr uint32_t kKtOffMf = kKtOffRaw + kKtStages * kKtRaw;        // [64] float2: logit factor, bias - maximum
 constexpr uint32_t kKtOffM = kKtOffMf + 64 * 8;                      // [64] running maxima
 constexpr uint32_t kKtOffAl = kKtOffM + 64 * 4;                      // [64] rescale factors; 1 / sums
 constexpr uint32_t kKtOffRed = kKtOffAl + 64 * 4;                    // [4 warps][64]
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
         // P of tile i - 2 has been read
         if (u > 0) acquire(&pv_done[bf], (u - 1) & 1);
         // s becomes the weights against the maxima at hand, and P; returns the
-        // largest logit above its head's maximum
+        // largest exponent of a weight
         const uint32_t pb = smem_u32(base) + kKtOffP + (uint32_t)bf * kKtP + (uint32_t)row * 128;
         auto weights = [&]() {
           float mx = -INFINITY;
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
           return mx;
         };
         const bool start = none && some;              // the first that counts: no maximum to try
-        if (start || kt_any(weights() > kK4Headroom)) {
+        if (start || kt_any(weights() > kKtBias + kKtHeadroom)) {
           // a maximum to raise: every head's over the tile, 32 heads at a time
           if (!start) load();
 #pragma unroll
@@ -468,10 +476,10 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
           if (row < N) {
             // (finite from the first position that counts on)
             const float tmx = fmaxf(fmaxf(fmaxf(red[row], red[64 + row]), fmaxf(red[128 + row], red[192 + row])), -3e38f);
-            const float m = mrun[row], M = tmx > m + kK4Headroom ? tmx : m;
+            const float m = mrun[row], M = tmx > m + kKtHeadroom ? tmx : m;
             al[row] = M == m ? 1.f : k4_ex2(m - M);
             mrun[row] = M;
-            mf[row].y = -M;
+            mf[row].y = kKtBias - M;
           }
           kt_sync();
 #pragma unroll
