@@ -31,7 +31,9 @@
 //
 // The running maximum of a head is raised only when a logit passes it by more
 // than 1.75 in base 2 (weights stay below 2^15.75, under fp16's largest), which
-// takes the shuffles out of the common case.
+// takes the shuffles out of the common case. It is kept as a product q.K, without
+// the factor to base 2: a weight is 2^((q.K - maximum) factor). The rounding of a
+// large logit alone (beyond 2^25) would pass the range otherwise.
 //
 // Work: all segments' 32-position tiles in one line, cut into runs, one per CTA
 // (k4_plan; the lengths are read on the device). Tile t of a run belongs to
@@ -66,8 +68,8 @@ namespace spc {
 constexpr int kK4Tile = 32;                          // positions a tile
 constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr float kK4Bias = 14.f;                      // log2 of the factor of the weights
-constexpr float kK4Limit = kK4Bias + 1.75f;          // log2 of the largest weight before the maximum is raised
-static_assert(kK4Limit <= 15.9f, "weights within fp16's range");
+constexpr float kK4Headroom = 1.75f;                 // log2 growth allowed before the maximum is raised
+static_assert(kK4Bias + kK4Headroom <= 15.9f, "weights within fp16's range");
 
 // The CTA of a kernel for HT head tiles; the last warps copy for the others:
 // one where the whole context is read, 5 (or 2 of 8) where positions are
@@ -325,19 +327,15 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
         if (!FULL && !((valid >> (rk + 16 * (e >> 1) + t)) & 1u)) s[n][t][e] = -INFINITY;
         mx[e & 1] = fmaxf(mx[e & 1], s[n][t][e]);
       }
-    // logits in base 2; f > 0, so the maximum may be scaled alone
-    mx[0] *= f[n][0];
-    mx[1] *= f[n][1];
-    // m is the running maximum less kK4Bias
-    const bool up = mx[0] > m[n][0] + kK4Limit || mx[1] > m[n][1] + kK4Limit;
+    const bool up = (mx[0] - m[n][0]) * f[n][0] > kK4Headroom || (mx[1] - m[n][1]) * f[n][1] > kK4Headroom;
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int k = 4; k <= 16; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], k));
-        const float M = fmaxf(m[n][e], mx[e] - kK4Bias);
+        const float M = fmaxf(m[n][e], mx[e]);
         // a first finite maximum takes 0 of what was (nothing)
-        const float c = k4_ex2(m[n][e] - (M == -INFINITY ? 0.f : M));
+        const float c = k4_ex2((m[n][e] - (M == -INFINITY ? 0.f : M)) * f[n][e]);
         m[n][e] = M;
         l[n][e] *= c;
 #pragma unroll
@@ -348,13 +346,13 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
       }
     }
     const float2 nm = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0], m[n][1] == -INFINITY ? 0.f : -m[n][1]);
-    const float2 ff = make_float2(f[n][0], f[n][1]);
+    const float2 ff = make_float2(f[n][0], f[n][1]), bias = make_float2(kK4Bias, kK4Bias);
     float2 ls = make_float2(l[n][0], l[n][1]);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float2 x = fma2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), ff, nm);
+        float2 x = fma2(add2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), nm), ff, bias);
         x.x = k4_ex2(x.x);
         x.y = k4_ex2(x.y);
         ls = add2(ls, x);
@@ -547,7 +545,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
     float* res = a.part + ((size_t)blockIdx.x * 2 + (!ends && s0 > t0 ? 1 : 0)) * (size_t)(8 * HT) * kK4Part;
 #pragma unroll 1
     for (int n = 0; n < HT; ++n) {
-      float mm[2], ll[2];
+      float mm[2], ll[2], ff[2];
       float* dst = mrg + (size_t)(warp * 8 + 2 * tig) * kK4Part;
 #pragma unroll
       for (int k = 0; k < HT; ++k) {
@@ -556,6 +554,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
         for (int e = 0; e < 2; ++e) {
           mm[e] = m[k][e];
           ll[e] = l[k][e];
+          ff[e] = f[k][e];
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             *reinterpret_cast<float4*>(dst + e * kK4Part + 4 + 16 * gid + 4 * y) =
@@ -569,6 +568,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
         if (gid == 0) {
           dst[e * kK4Part] = mm[e];
           dst[e * kK4Part + 1] = ll[e];
+          dst[e * kK4Part + 2] = ff[e];
         }
       }
       sync();
@@ -579,13 +579,13 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * 8 + e) * kK4Part]);
-        const float Ms = M == -INFINITY ? 0.f : M;
+        const float Ms = M == -INFINITY ? 0.f : M, fh = mrg[e * kK4Part + 2];
         float L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float* src = mrg + (size_t)(w * 8 + e) * kK4Part;
-          const float wt = k4_ex2(src[0] - Ms);
+          const float wt = k4_ex2((src[0] - Ms) * fh);
           const float4 x = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
           L += wt * src[1];
           v.x += wt * x.x; v.y += wt * x.y; v.z += wt * x.z; v.w += wt * x.w;
@@ -596,10 +596,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
               make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
         } else {
           float* p = res + (size_t)h * kK4Part;
-          if (lane == 0) {
-            p[0] = M;
-            p[1] = L;
-          }
+          if (lane == 0) *reinterpret_cast<float4*>(p) = make_float4(M, L, fh, 0.f);
           *reinterpret_cast<float4*>(p + 4 + 4 * lane) = v;
         }
       }

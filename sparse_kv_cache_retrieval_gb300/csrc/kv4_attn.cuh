@@ -11,7 +11,7 @@
 namespace spc {
 
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
-constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, 2 unused, O[128]
+constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, factor of m to base 2, unused, O[128]
 constexpr int kK4MaxKv = 128;                        // KV heads
 // workspace: status, arrival counters (zero between calls), where a segment's
 // partials are (tcgen05 kernel), partials. The offsets do not depend on the
@@ -219,7 +219,8 @@ __device__ __forceinline__ void k4_merge(const Kv4Args& a, const K4Open& u, int 
   const int np = u.w1 - u.w0 + 1;
   float2* wl = reinterpret_cast<float2*>(mrg);                  // [kMg][kK4Ctas]
   float* lsum = mrg + 2 * kMg * kK4Ctas;                        // [kMg]
-  static_assert((2 * kMg * kK4Ctas + kMg) * 4 <= SCRATCH, "merge scratch");
+  float* fac = lsum + kMg;                                      // [kMg]
+  static_assert((2 * kMg * kK4Ctas + 2 * kMg) * 4 <= SCRATCH, "merge scratch");
   auto piece = [&](int i, int h) {
     const int w = u.w0 + i;
     return a.part + (((size_t)w * 2 + (u.run < (1 << 30) && u.s0 > w * u.run ? 1 : 0)) * (8 * HT) + h) * (size_t)kK4Part;
@@ -236,18 +237,20 @@ __device__ __forceinline__ void k4_merge(const Kv4Args& a, const K4Open& u, int 
     if (threadIdx.x < nh * 32) load(threadIdx.x, 0);
     for (int i = threadIdx.x; i < nh * np; i += 32 * W) {
       const int h = i / np, q = i - h * np;
-      wl[h * kK4Ctas + q] = __ldcg(reinterpret_cast<const float2*>(piece(q, hb + h)));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(q, hb + h)));
+      wl[h * kK4Ctas + q] = make_float2(x.x, x.y);
+      if (q == 0) fac[h] = x.z;
     }
     sync();
     for (int h = warp; h < nh; h += W) {
       float M = -INFINITY;
       for (int q = lane; q < np; q += 32) M = fmaxf(M, wl[h * kK4Ctas + q].x);
       M = warp_max(M);
-      const float Ms = M == -INFINITY ? 0.f : M;
+      const float Ms = M == -INFINITY ? 0.f : M, f = fac[h];
       float L = 0.f;
       for (int q = lane; q < np; q += 32) {
         const float2 ml = wl[h * kK4Ctas + q];
-        const float wt = k4_ex2(ml.x - Ms);
+        const float wt = k4_ex2((ml.x - Ms) * f);
         L += wt * ml.y;
         wl[h * kK4Ctas + q].x = wt;
       }

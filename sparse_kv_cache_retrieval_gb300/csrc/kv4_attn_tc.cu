@@ -12,8 +12,9 @@
 // tensor memory lane (no transpose, no swizzle) and the V row into one row of
 // an MN-major operand; the softmax thread of the position has its logits of
 // all heads and writes one row of P. So nothing is exchanged between positions
-// but the heads' maxima, and those only when a logit passes the running one by
-// more than 4.75 (a barrier's OR tells), and the sums, once a segment.
+// but the heads' maxima (as products q.K, see kv4_attn.cu), and those only when a
+// logit passes the running one by more than 4.75 (a barrier's OR tells), and the
+// sums, once a segment.
 // Operands are fp16: K and V exact, Q scaled per head by a power of two and P
 // rounded; logits, maxima, sums and O are fp32. P and the sums are kept 2^11
 // times the weights against the running maximum, the top of fp16's range (see
@@ -67,7 +68,7 @@ constexpr uint32_t kKtOffV = 0;                                      // [2]
 constexpr uint32_t kKtOffP = kKtOffV + 2 * kKtV;                     // [2]
 constexpr uint32_t kKtOffQ = kKtOffP + 2 * kKtP;                     // [2 halves of 64 dims][N][128 bytes]
 constexpr uint32_t kKtOffRaw = kKtOffQ + 64 * kRowBytes;             // [kKtStages]
-constexpr uint32_t kKtOffMf = kKtOffRaw + kKtStages * kKtRaw;        // [64] float2: logit factor, bias - maximum
+constexpr uint32_t kKtOffMf = kKtOffRaw + kKtStages * kKtRaw;        // [32 pairs of heads] float4: logit factors, -maxima
 constexpr uint32_t kKtOffM = kKtOffMf + 64 * 8;                      // [64] running maxima
 constexpr uint32_t kKtOffAl = kKtOffM + 64 * 4;                      // [64] rescale factors; 1 / sums
 constexpr uint32_t kKtOffRed = kKtOffAl + 64 * 4;                    // [4 warps][64]
@@ -371,7 +372,8 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kKtRegSoft));
     const int row = threadIdx.x;                      // position of a tile; dim in the epilogue
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-    float2* mf = reinterpret_cast<float2*>(base + kKtOffMf);
+    float* mf = reinterpret_cast<float*>(base + kKtOffMf);
+    auto mf_at = [](int h) { return (h >> 1) * 4 + (h & 1); };      // of head h's factor; its -maximum is 2 behind
     float* mrun = reinterpret_cast<float*>(base + kKtOffM);
     float* al = reinterpret_cast<float*>(base + kKtOffAl);
     float* red = reinterpret_cast<float*>(base + kKtOffRed);
@@ -407,7 +409,8 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
                         "r"(pack_f16(bf_lo(w.y) * d1 * d2, bf_hi(w.y) * d1 * d2)) : "memory");
         if (lane == 0) {
           const float u1 = __uint_as_float((uint32_t)(127 + e1) << 23), u2 = __uint_as_float((uint32_t)(127 + e2) << 23);
-          mf[h] = make_float2(k4_factor(c.scale2 * u1 * u2), 0.f);
+          mf[mf_at(h)] = k4_factor(c.scale2 * u1 * u2);
+          mf[mf_at(h) + 2] = 0.f;
           mrun[h] = -INFINITY;
         }
       }
@@ -449,8 +452,9 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int h = 8 * n + 2 * j;
-              const float4 k = *reinterpret_cast<const float4*>(mf + h);
-              const float2 x = fma2(make_float2(s[h], s[h + 1]), make_float2(k.x, k.z), make_float2(k.y, k.w));
+              const float4 k = *reinterpret_cast<const float4*>(mf + 2 * h);
+              const float2 x = fma2(add2(make_float2(s[h], s[h + 1]), make_float2(k.z, k.w)), make_float2(k.x, k.y),
+                                    make_float2(kKtBias, kKtBias));
               mx = fmaxf(mx, fmaxf(x.x, x.y));
               s[h] = k4_ex2(x.x);
               s[h + 1] = k4_ex2(x.y);
@@ -469,17 +473,17 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
           for (int hb = 0; hb < N; hb += 32) {
             float v[32];
 #pragma unroll
-            for (int h = 0; h < 32; ++h) v[h] = s[hb + h] * mf[hb + h].x;
+            for (int h = 0; h < 32; ++h) v[h] = s[hb + h];
             kt_reduce<32>(v, red + warp * 64 + hb, [](float x, float y) { return fmaxf(x, y); });
           }
           kt_sync();
           if (row < N) {
             // (finite from the first position that counts on)
             const float tmx = fmaxf(fmaxf(fmaxf(red[row], red[64 + row]), fmaxf(red[128 + row], red[192 + row])), -3e38f);
-            const float m = mrun[row], M = tmx > m + kKtHeadroom ? tmx : m;
-            al[row] = M == m ? 1.f : k4_ex2(m - M);
+            const float m = mrun[row], f = mf[mf_at(row)], M = (tmx - m) * f > kKtHeadroom ? tmx : m;
+            al[row] = M == m ? 1.f : k4_ex2((m - M) * f);
             mrun[row] = M;
-            mf[row].y = kKtBias - M;
+            mf[mf_at(row) + 2] = -M;
           }
           kt_sync();
 #pragma unroll
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       if (row < N) {
         const float L = (red[row] + red[64 + row]) + (red[128 + row] + red[192 + row]);
         al[row] = L == 0.f ? 0.f : 1.f / L;
-        if (!whole) *reinterpret_cast<float2*>(res + (size_t)row * kK4Part) = make_float2(mrun[row], L);
+        if (!whole) *reinterpret_cast<float4*>(res + (size_t)row * kK4Part) = make_float4(mrun[row], L, mf[mf_at(row)], 0.f);
       }
       acquire(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
       tc_fence_after();
@@ -595,18 +599,18 @@ __global__ void __launch_bounds__(32 * kKmWarps) kt_merge_kernel(Kv4Args a, cons
   };
   load(0);
   constexpr int kMl = (kK4Ctas + 31) / 32;
-  float2 ml[kMl];
+  float4 ml[kMl];
   float M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int k = 0; k < kMl; ++k) {
-    ml[k] = lane + 32 * k < u.np ? __ldcg(reinterpret_cast<const float2*>(piece(lane + 32 * k))) : make_float2(-INFINITY, 0.f);
+    ml[k] = lane + 32 * k < u.np ? __ldcg(reinterpret_cast<const float4*>(piece(lane + 32 * k))) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
     M = fmaxf(M, ml[k].x);
   }
   M = warp_max(M);
-  const float Ms = M == -INFINITY ? 0.f : M;
+  const float Ms = M == -INFINITY ? 0.f : M, f = __shfl_sync(0xffffffffu, ml[0].z, 0);
 #pragma unroll
   for (int k = 0; k < kMl; ++k) {
-    const float wt = k4_ex2(ml[k].x - Ms);
+    const float wt = k4_ex2((ml[k].x - Ms) * f);
     L += wt * ml[k].y;
     if (lane + 32 * k < u.np) wl[warp][lane + 32 * k] = wt;
   }

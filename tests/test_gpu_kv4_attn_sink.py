@@ -34,20 +34,23 @@ def sink_case(seed, lens, n_q, n_kv, gap, spread, at=0, bs=64):
     return c, q, scale
 
 
+def small_weights_tol(c, n_q):
+    """decode_tol counts on weights with 11 bits. Fp16 has them down to 2^-14 and steps of 2^-24 below; the weights
+    are kept at least 2^11 times those against the running maximum, so that a step is at most 2^-35 of the largest,
+    and the n positions' half steps come to at most 2^-36 sum |v|."""
+    tol = np.zeros((len(c.lens), n_q, 128))
+    for b, n in enumerate(c.lens):
+        pos = np.arange(n)
+        _, v = P.values(c.rec[c.table[b, pos // c.bs], :, pos % c.bs])          # [n][n_kv][128]
+        tol[b] = 2.0 ** -36 * np.repeat(np.abs(v).sum(0), n_q // c.n_kv, 0)
+    return tol
+
+
 def compare(c, q, scale, selected=None):
     got, ws = decode(c, q.to(DEV), None if selected is None else i32(selected), scale=scale)
     want, mag = P.decode_attention(f64(q), c.rec, c.table, c.lens, selected, scale)
     assert int(ws[:4].view(torch.int32).item()) == 0
-    # decode_tol counts on weights with 11 bits. Fp16 has them down to 2^-14 and steps of 2^-24 below; the weights
-    # are kept at least 2^11 times those against the running maximum, so that a step is at most 2^-35 of the largest,
-    # and the n positions' half steps come to at most 2^-36 sum |v|.
-    G = q.shape[1] // c.n_kv
-    tol = decode_tol(want, mag)
-    for b, n in enumerate(c.lens):
-        pos = np.arange(n)
-        _, v = P.values(c.rec[c.table[b, pos // c.bs], :, pos % c.bs])          # [n][n_kv][128]
-        tol[b] += 2.0 ** -36 * np.repeat(np.abs(v).sum(0), G, 0)
-    check(got, want, tol)
+    check(got, want, decode_tol(want, mag) + small_weights_tol(c, q.shape[1]))
 
 
 @pytest.mark.parametrize("n_q", [4, 16, 32, 64])
