@@ -42,8 +42,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // A head's logit factor, kept from vanishing (queries of zeros, a small scale):
 // masked logits are -inf, and -inf times zero would not be. At this factor every
-// logit is zero but for 2^-100.
-__device__ __forceinline__ float k4_factor(float f) { return fmaxf(f, 1.17549435e-38f); }
+// logit is zero but for 2^-100. And kept from passing fp32's range (a large scale
+// times large queries), where equal logits times infinity would be NaN: products
+// q.K are multiples of 2^-34 below 2^20, so that at 2^100 the largest takes all
+// and nothing overflows.
+__device__ __forceinline__ float k4_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 1.26765060e30f); }
 // 2^x by the MUFU approximation (relative error about 2^-22); -inf gives 0
 __device__ __forceinline__ float k4_ex2(float x) {
   float y;
