@@ -24,7 +24,9 @@
 // they are used, and a row whose sum is finite but whose result is not, though
 // no V that it sees explains that (a non-finite V behind it, or weights above 1
 // on values near the type's largest), is computed again by a warp from global
-// memory over exactly the keys it sees.
+// memory over exactly the keys it sees. So is a row whose maximum passes 2^26 in
+// base 2: a weight is 2^(s scale - m) with m rounded to fp32, and beyond 2^31 that
+// rounding alone passes the range of the weights.
 //
 // One CTA per SM, persistent over items ordered by the number of key blocks,
 // longest first, and dealt to the CTAs in a snake:
@@ -69,6 +71,7 @@ constexpr int kPaThreads = 384;                       // warp 11 fills the third
 constexpr int kPaRegSoft = 208, kPaRegRest = 88;
 constexpr int kPaCtas = 152;
 constexpr float kPaHeadroom = 8.f;
+constexpr float kPaLarge = 67108864.f;                // 2^26
 constexpr long long kPaWait = 4000000000ll;           // clock cycles
 constexpr int kPaTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kPaColO = 256;
@@ -165,7 +168,8 @@ __device__ __forceinline__ bool pa_not_finite(uint32_t bf) { return (bf & 0x7f80
 
 // One row by one warp, from global memory, over the keys it sees (h is the
 // query head, g its KV head): the result of lane l is dims 4l .. 4l + 3, held
-// as a running mean, so that it does not overflow where the mean does not.
+// as a running mean, so that it does not overflow where the mean does not. The
+// maximum is that of the products q.k, without the scale.
 __device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g) {
   constexpr int U = 8;                                 // keys a step, their loads in flight together
   const PromptAttnCall& c = a.c;
@@ -186,14 +190,14 @@ __device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g)
     }
 #pragma unroll
     for (int e = 0; e < U; ++e) {
-      x[e] = c.scale2 * warp_sum(q0 * bf_lo(k[e].x) + q1 * bf_hi(k[e].x) + q2 * bf_lo(k[e].y) + q3 * bf_hi(k[e].y));
+      x[e] = warp_sum(q0 * bf_lo(k[e].x) + q1 * bf_hi(k[e].x) + q2 * bf_lo(k[e].y) + q3 * bf_hi(k[e].y));
       if (j + e > t) x[e] = -INFINITY;
       M = fmaxf(M, x[e]);
     }
-    const float Ms = M == -INFINITY ? 0.f : M, old = l * exp2f(m - Ms);
+    const float Ms = M == -INFINITY ? 0.f : M, old = l * exp2f((m - Ms) * c.scale2);
     l = old;
 #pragma unroll
-    for (int e = 0; e < U; ++e) l += x[e] = exp2f(x[e] - Ms);
+    for (int e = 0; e < U; ++e) l += x[e] = exp2f((x[e] - Ms) * c.scale2);
     m = M;
     if (l == 0.f) continue;                            // nothing but -inf so far
     const float r = 1.f / l;
@@ -214,15 +218,16 @@ __device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g)
       make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
 }
 
-// The rows of a warp's lanes in `again` have results that are not finite. In
-// the dims where a V that the row sees is not finite they stay; a row with
-// another such dim is computed again. One pass over V tells each dim's first
-// non-finite key, for all rows.
-__device__ void pa_rows_again(const PaArgs& a, uint32_t again, int start, int qpos, int h, int g) {
+// The rows of a warp's lanes in `large` are computed again. Those in `again`
+// have results that are not finite: in the dims where a V that the row sees is
+// not finite they stay; a row with another such dim is computed again. One pass
+// over V tells each dim's first non-finite key, for all rows.
+__device__ void pa_rows_again(const PaArgs& a, uint32_t again, uint32_t large, int start, int qpos, int h, int g) {
   constexpr int U = 8;
   const PromptAttnCall& c = a.c;
   const int lane = threadIdx.x & 31;
-  const int top = __reduce_max_sync(0xffffffffu, again >> lane & 1 ? qpos : 0);
+  again &= ~large;
+  const int top = again ? __reduce_max_sync(0xffffffffu, again >> lane & 1 ? qpos : 0) : -1;
   int first[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
   for (int j = 0; j <= top; j += U) {
     uint2 v[U];
@@ -241,11 +246,14 @@ __device__ void pa_rows_again(const PaArgs& a, uint32_t again, int start, int qp
     }
     if (__all_sync(0xffffffffu, max(max(first[0], first[1]), max(first[2], first[3])) < INT_MAX)) break;
   }
-  __syncwarp();                                        // the rows' results are read by other lanes
-  while (again) {
-    const int src = __ffs(again) - 1;
-    again &= again - 1;
+  __syncwarp();                                        // the rows' results are read and written by other lanes
+  for (uint32_t rows = again | large; rows; rows &= rows - 1) {
+    const int src = __ffs(rows) - 1;
     const int qp = __shfl_sync(0xffffffffu, qpos, src), hh = __shfl_sync(0xffffffffu, h, src);
+    if (large >> src & 1) {
+      pa_row_again(a, start, qp, hh, g);
+      continue;
+    }
     const uint2 o = __ldcg(reinterpret_cast<const uint2*>(c.out + ((size_t)(start + qp) * c.n_q + hh) * kD) + lane);
     if (__any_sync(0xffffffffu, (pa_not_finite(o.x) && first[0] > qp) || (pa_not_finite(o.x >> 16) && first[1] > qp) ||
                                     (pa_not_finite(o.y) && first[2] > qp) || (pa_not_finite(o.y >> 16) && first[3] > qp)))
@@ -668,7 +676,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       uint16_t* dst = c.out + ((size_t)(start + qpos) * c.n_q + h) * kD;
       const float r = 1.f / l;
       const bool wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;   // whole sectors a store
-      bool odd = false;                                // a value that is not finite
+      // (an infinite maximum is the products' own, unless the scale can have made it so)
+      const bool large = live && fabsf(m) > kPaLarge && (fabsf(m) < INFINITY || c.scale2 > 1.f);
+      bool odd = large;                                // or a value that is not finite
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         float o[32];
@@ -696,8 +706,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         }
       }
       tc_fence_before();
-      const uint32_t again = __ballot_sync(0xffffffffu, live && odd && l < INFINITY);
-      if (again) pa_rows_again(a, again, start, qpos, h, g);
+      const uint32_t again = __ballot_sync(0xffffffffu, live && odd && (l < INFINITY || large));
+      if (again) pa_rows_again(a, again, __ballot_sync(0xffffffffu, large), start, qpos, h, g);
     }
   } else if (warp == kPaWarpGate) {
     // ================= gate: passes the arrival of V_j and K_(j+1) on to the
