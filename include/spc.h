@@ -512,7 +512,8 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
  * both rounded to nearest, ties to even, of the exact quotients. Values beyond
  * 6 * 448 saturate (infinities too); a NaN makes its group's scale NaN.
  * k, v      bf16, row t at k + t * k_stride elements: [n_kv][d], 16-byte
- *           aligned; strides are multiples of 8 elements, at least n_kv * d.
+ *           aligned; strides are multiples of 8 elements, at least n_kv * d and
+ *           at most 2^37. Neither span, first to last row, may overlap the cache.
  * slot_map  int32 [T]; a slot that occurs twice ends up with bytes of either row.
  * Limits: d = 128, 0 <= T <= 2^24, 1 <= n_kv <= 1024. */
 int spc_kv4_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
@@ -520,7 +521,8 @@ int spc_kv4_store(const void* k, const void* v, int64_t k_stride, int64_t v_stri
 
 /* Rows out of the cache: k[t], v[t] = the values of slot slot_map[t], exact in
  * bf16; rows whose slot is outside the cache are left as they were. Arguments
- * and limits as spc_kv4_store. */
+ * and limits as spc_kv4_store; no row of k may overlap one of v (they may lie
+ * beside one another in fused rows of one stride). */
 int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, int64_t k_stride,
                  int64_t v_stride, int T, int n_kv, int d, int num_blocks, int block_size, void* stream);
 

@@ -439,6 +439,24 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
   return block_map_launch(c, stream);
 }
 
+// whether rows of `row` bf16 values, T of them at k and at v with the strides
+// given, have an element in common. Rows that interleave (halves of one fused
+// row) do not; where the strides differ and the spans overlap, rows that could
+// meet beyond T count as meeting.
+static bool rows_meet(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int64_t row, int T) {
+  if (!overlap(k, ((T - 1) * k_stride + row) * 2, v, ((T - 1) * v_stride + row) * 2)) return false;
+  if (T == 1) return true;
+  int64_t a = k_stride, g = v_stride;
+  while (a) {
+    const int64_t r = g % a;
+    g = a;
+    a = r;
+  }
+  // distances between rows are v - k modulo the strides' common divisor
+  const int64_t step = 2 * g, d = (static_cast<const char*>(v) - static_cast<const char*>(k)) % step, m = d < 0 ? d + step : d;
+  return m < 2 * row || m > step - 2 * row;
+}
+
 static int kv4_rows_check(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
                           const void* cache, int T, int n_kv, int d, int num_blocks, int block_size) {
   if (d != SPC_HEAD_DIM || n_kv < 1 || n_kv > 1024 || T < 0 || T > kMaxRows || !pool_ok(num_blocks, block_size, n_kv))
@@ -447,9 +465,12 @@ static int kv4_rows_check(const void* k, const void* v, int64_t k_stride, int64_
   if (!k || !v || !slot_map || !cache) return SPC_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slot_map)) return SPC_ERR_INVALID_ARG;
   const int64_t row = (int64_t)n_kv * d;
-  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (1ll << 40) ||
-      v_stride > (1ll << 40))
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (1ll << 37) ||
+      v_stride > (1ll << 37))
     return SPC_ERR_SHAPE;
+  const int64_t pool = (int64_t)num_blocks * block_size * n_kv * SPC_KV4_RECORD;
+  if (overlap(cache, pool, k, ((T - 1) * k_stride + row) * 2) || overlap(cache, pool, v, ((T - 1) * v_stride + row) * 2))
+    return SPC_ERR_INVALID_ARG;
   return SPC_OK;
 }
 
@@ -476,6 +497,7 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
                  int T, int n_kv, int d, int num_blocks, int block_size, void* stream) {
   const int bad = kv4_rows_check(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, d, num_blocks, block_size);
   if (bad != SPC_OK || T == 0) return bad;
+  if (rows_meet(k, v, k_stride, v_stride, (int64_t)n_kv * d, T)) return SPC_ERR_INVALID_ARG;
   return kv4_load_launch(kv4_rows_call(k, v, k_stride, v_stride, slot_map, cache, T, n_kv, num_blocks, block_size),
                          stream);
 }
