@@ -490,9 +490,10 @@ int spc_mla_decode_attn(const void* q, const void* Wuk, const void* Wuv, const s
  * Table entries that are not needed (any more) are left as they were.
  * len, len_next int32 [B]; block_table int32 [B][max_blocks]; free_list int32
  * [num_blocks], its first n_free[0] entries the stack; n_free_next int32 [1],
- * the stack's new height (not the same address as n_free); cu_new int32
- * [B + 1], the cu_seqlens of the new tokens; slot_map int32 [n_slots];
- * status int32 [1], zeroed by the caller. If a length is outside [0,
+ * the stack's new height; cu_new int32 [B + 1], the cu_seqlens of the new
+ * tokens; slot_map int32 [n_slots]; status int32 [1], zeroed by the caller. The
+ * table, the stack and the four last must not overlap one another or an input
+ * (n_free_next is not n_free). If a length is outside [0,
  * max_blocks * block_size], the stack has too few blocks (or would pass
  * num_blocks), or the new positions pass n_slots, the status word becomes
  * SPC_ERR_OVERFLOW, tables and stack stay as they were, n_free_next = n_free,
@@ -538,7 +539,8 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
  * block_table int32 [B][max_blocks]; len int32 [B] (at most max_blocks *
  *            block_size positions count).
  * selected   int32 [B][n_kv][budget], or NULL with budget 0.
- * out        bf16 [B][n_q][d], 16-byte aligned; must not overlap q.
+ * out        bf16 [B][n_q][d], 16-byte aligned; neither it nor the workspace may
+ *            overlap anything else of the call.
  * workspace  spc_kv4_decode_attn_workspace_size() bytes, 256-byte aligned,
  *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
  *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
@@ -565,8 +567,9 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
  *            row's size (the three may lie in one fused projection's output).
  * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are an
  *            empty sequence.
- * out        bf16 [T][n_q][d], 16-byte aligned; must not overlap the memory from
- *            the first to the last element of q, k or v.
+ * out        bf16 [T][n_q][d], 16-byte aligned; neither it nor the workspace may
+ *            overlap the memory from the first to the last element of q, k or v,
+ *            cu_seqlens, or one another.
  * workspace  spc_prompt_attn_workspace_size() bytes, 256-byte aligned,
  *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
  *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls

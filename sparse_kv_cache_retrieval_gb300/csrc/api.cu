@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -415,6 +416,18 @@ static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_byt
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
+// whether one of the first n_out spans (which the call writes) overlaps any other
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+static bool outputs_overlap(std::initializer_list<Span> spans, size_t n_out) {
+  const Span* s = spans.begin();
+  for (size_t i = 0; i < n_out; ++i)
+    for (size_t j = i + 1; j < spans.size(); ++j)
+      if (s[i].p && s[j].p && overlap(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return true;
+  return false;
+}
 // the kernels take the scale times log2(e), which has to be finite as well
 static bool scale_ok(float scale) { return scale > 0.f && scale * kLog2e <= 3.4e38f; }
 constexpr int kMaxRows = 1 << 24;
@@ -431,6 +444,10 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
   if (B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, 1) || !table_ok(max_blocks, block_size))
     return SPC_ERR_SHAPE;
   if (n_slots < 1 || n_slots > kMaxRows) return SPC_ERR_SHAPE;
+  if (outputs_overlap({{block_table, (int64_t)B * max_blocks * 4}, {free_list, (int64_t)num_blocks * 4}, {n_free_next, 4},
+                       {cu_new, (B + 1) * 4}, {slot_map, (int64_t)n_slots * 4}, {status, 4}, {len, B * 4}, {len_next, B * 4},
+                       {n_free, 4}}, 6))
+    return SPC_ERR_INVALID_ARG;
   BlockMapCall c{};
   c.len = len; c.len_next = len_next; c.table = block_table; c.free_list = free_list; c.n_free = n_free;
   c.n_free_next = n_free_next; c.cu_new = cu_new; c.slot_map = slot_map; c.status = status;
@@ -528,7 +545,10 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
     return SPC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
   const int64_t io = (int64_t)B * n_q * d * 2;
-  if (overlap(out, io, q, io)) return SPC_ERR_INVALID_ARG;
+  if (outputs_overlap({{out, io}, {workspace, (int64_t)kv4_attn_workspace(B, n_q, n_kv, max_blocks, block_size, budget)}, {q, io},
+                       {cache, (int64_t)num_blocks * block_size * n_kv * SPC_KV4_RECORD}, {block_table, (int64_t)B * max_blocks * 4},
+                       {len, B * 4}, {selected, (int64_t)B * n_kv * budget * 4}}, 2))
+    return SPC_ERR_INVALID_ARG;
   Kv4AttnCall c{};
   c.q = static_cast<const uint16_t*>(q); c.cache = static_cast<const uint8_t*>(cache); c.table = block_table;
   c.len = len; c.selected = selected; c.out = static_cast<uint16_t*>(out);
@@ -559,9 +579,9 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
   if (q_stride < qr || k_stride < kr || v_stride < kr || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
       q_stride > (1ll << 32) || k_stride > (1ll << 32) || v_stride > (1ll << 32))
     return SPC_ERR_SHAPE;
-  const int64_t ob = T * qr * 2;
-  if (overlap(out, ob, q, ((T - 1) * q_stride + qr) * 2) || overlap(out, ob, k, ((T - 1) * k_stride + kr) * 2) ||
-      overlap(out, ob, v, ((T - 1) * v_stride + kr) * 2))
+  if (outputs_overlap({{out, T * qr * 2}, {workspace, (int64_t)prompt_attn_workspace(T, B, n_q, n_kv)},
+                       {q, ((T - 1) * q_stride + qr) * 2}, {k, ((T - 1) * k_stride + kr) * 2}, {v, ((T - 1) * v_stride + kr) * 2},
+                       {cu_seqlens, (B + 1) * 4}}, 2))
     return SPC_ERR_INVALID_ARG;
   PromptAttnCall c{};
   c.q = static_cast<const uint16_t*>(q); c.k = static_cast<const uint16_t*>(k); c.v = static_cast<const uint16_t*>(v);
