@@ -41,7 +41,9 @@ def small_weights_tol(c, n_q):
     tol = np.zeros((len(c.lens), n_q, 128))
     for b, n in enumerate(c.lens):
         pos = np.arange(n)
-        _, v = P.values(c.rec[c.table[b, pos // c.bs], :, pos % c.bs])          # [n][n_kv][128]
+        blk = c.table[b, pos // c.bs]
+        ok = (blk >= 0) & (blk < c.num_blocks)
+        _, v = P.values(c.rec[blk[ok], :, (pos % c.bs)[ok]])                    # [positions][n_kv][128]
         tol[b] = 2.0 ** -36 * np.repeat(np.abs(v).sum(0), n_q // c.n_kv, 0)
     return tol
 
