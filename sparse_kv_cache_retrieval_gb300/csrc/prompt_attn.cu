@@ -22,9 +22,9 @@
 // masked columns are replaced. In P V they meet P = 0, which a non-finite V
 // defeats: V rows behind the sequence's end are zeroed in shared memory before
 // they are used, and a row whose sum is finite but whose result is not, though
-// no V that it sees explains that (a non-finite V behind it, or weights above 1
-// on values near the type's largest), is computed again by a warp from global
-// memory over exactly the keys it sees. So is a row whose maximum passes 2^26 in
+// the V that it sees do not explain that (a non-finite V behind it, or weights
+// above 1 on values near the type's largest), is computed again by a warp from
+// global memory over exactly the keys it sees. So is a row whose maximum passes 2^26 in
 // base 2: a weight is 2^(s scale - m) with m rounded to fp32, and beyond 2^31 that
 // rounding alone passes the range of the weights.
 //
@@ -219,32 +219,44 @@ __device__ void pa_row_again(const PaArgs& a, int start, int qpos, int h, int g)
 }
 
 // The rows of a warp's lanes in `large` are computed again. Those in `again`
-// have results that are not finite: in the dims where a V that the row sees is
-// not finite they stay; a row with another such dim is computed again. One pass
-// over V tells each dim's first non-finite key, for all rows.
-__device__ void pa_rows_again(const PaArgs& a, uint32_t again, uint32_t large, int start, int qpos, int h, int g) {
+// have results that are not finite: a dim in which a V that the row sees is not
+// finite, and none behind it in the row's block of keys, stays; a row with
+// another such dim is computed again. One pass over V tells each dim's first
+// non-finite key, one over the block the last, for all rows.
+__device__ void pa_rows_again(const PaArgs& a, uint32_t again, uint32_t large, int start, int len, int qpos, int h, int g) {
   constexpr int U = 8;
   const PromptAttnCall& c = a.c;
   const int lane = threadIdx.x & 31;
   again &= ~large;
-  const int top = again ? __reduce_max_sync(0xffffffffu, again >> lane & 1 ? qpos : 0) : -1;
-  int first[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
-  for (int j = 0; j <= top; j += U) {
-    uint2 v[U];
+  int first[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX}, last[4] = {-1, -1, -1, -1};
+  // keys j0 .. j1 - 1, until `first` is known in every dim if that is all that is asked for
+  auto scan = [&](int j0, int j1, bool all) {
+    for (int j = j0; j < j1; j += U) {
+      uint2 v[U];
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      v[e] = make_uint2(0u, 0u);
-      if (j + e <= top)
-        v[e] = *reinterpret_cast<const uint2*>(c.v + (start + j + e) * c.v_stride + (size_t)g * kD + 4 * lane);
-    }
+      for (int e = 0; e < U; ++e) {
+        v[e] = make_uint2(0u, 0u);
+        if (j + e < j1)
+          v[e] = *reinterpret_cast<const uint2*>(c.v + (start + j + e) * c.v_stride + (size_t)g * kD + 4 * lane);
+      }
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      if (pa_not_finite(v[e].x)) first[0] = min(first[0], j + e);
-      if (pa_not_finite(v[e].x >> 16)) first[1] = min(first[1], j + e);
-      if (pa_not_finite(v[e].y)) first[2] = min(first[2], j + e);
-      if (pa_not_finite(v[e].y >> 16)) first[3] = min(first[3], j + e);
+      for (int e = 0; e < U; ++e) {
+        const bool bad[4] = {pa_not_finite(v[e].x), pa_not_finite(v[e].x >> 16), pa_not_finite(v[e].y), pa_not_finite(v[e].y >> 16)};
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if (!bad[d]) continue;
+          first[d] = min(first[d], j + e);
+          last[d] = max(last[d], j + e);
+        }
+      }
+      if (!all && __all_sync(0xffffffffu, max(max(first[0], first[1]), max(first[2], first[3])) < INT_MAX)) break;
     }
-    if (__all_sync(0xffffffffu, max(max(first[0], first[1]), max(first[2], first[3])) < INT_MAX)) break;
+  };
+  if (again) {
+    // the tokens of a warp's rows lie in one block of keys
+    const int top = __reduce_max_sync(0xffffffffu, again >> lane & 1 ? qpos : 0), b0 = top / kPaKeys * kPaKeys;
+    scan(0, b0, false);
+    scan(b0, min(b0 + kPaKeys, len), true);
   }
   __syncwarp();                                        // the rows' results are read and written by other lanes
   for (uint32_t rows = again | large; rows; rows &= rows - 1) {
@@ -255,9 +267,11 @@ __device__ void pa_rows_again(const PaArgs& a, uint32_t again, uint32_t large, i
       continue;
     }
     const uint2 o = __ldcg(reinterpret_cast<const uint2*>(c.out + ((size_t)(start + qp) * c.n_q + hh) * kD) + lane);
-    if (__any_sync(0xffffffffu, (pa_not_finite(o.x) && first[0] > qp) || (pa_not_finite(o.x >> 16) && first[1] > qp) ||
-                                    (pa_not_finite(o.y) && first[2] > qp) || (pa_not_finite(o.y >> 16) && first[3] > qp)))
-      pa_row_again(a, start, qp, hh, g);
+    const uint32_t w[4] = {o.x, o.x >> 16, o.y, o.y >> 16};
+    bool open = false;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) open = open || (pa_not_finite(w[d]) && (first[d] > qp || last[d] > qp));
+    if (__any_sync(0xffffffffu, open)) pa_row_again(a, start, qp, hh, g);
   }
 }
 
@@ -707,7 +721,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       }
       tc_fence_before();
       const uint32_t again = __ballot_sync(0xffffffffu, live && odd && (l < INFINITY || large));
-      if (again) pa_rows_again(a, again, __ballot_sync(0xffffffffu, large), start, qpos, h, g);
+      if (again) pa_rows_again(a, again, __ballot_sync(0xffffffffu, large), start, len, qpos, h, g);
     }
   } else if (warp == kPaWarpGate) {
     // ================= gate: passes the arrival of V_j and K_(j+1) on to the
