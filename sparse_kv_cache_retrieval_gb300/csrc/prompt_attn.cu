@@ -72,7 +72,9 @@ constexpr int kPaRegSoft = 208, kPaRegRest = 88;
 constexpr int kPaCtas = 152;
 constexpr float kPaHeadroom = 8.f;
 constexpr float kPaLarge = 67108864.f;                // 2^26
-constexpr long long kPaWait = 4000000000ll;           // clock cycles
+// clock cycles, some 4 s: a warp whose 32 rows are all computed again over 262144
+// keys takes 1.3 s, for which the other roles wait
+constexpr long long kPaWait = 8000000000ll;
 constexpr int kPaTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kPaColO = 256;
 constexpr uint32_t kPaIdescS = umma_idesc_bf16(128, kPaKeys, false);

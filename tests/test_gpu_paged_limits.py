@@ -63,3 +63,24 @@ def test_prompt_attention_of_the_most_rows():
             # long contexts of random values average to little: the rounding of the weights, in mag, is what is left
             assert np.all(np.abs(f64(out[i, 0]) - want) <= prompt_tol(want, mag)), (b, i - a)
     assert torch.all(out[int(cu[-1]):] == 7)
+
+
+def test_rows_computed_again_over_the_longest_sequence():
+    # an infinity in the last row's V: the rows of its block of keys that do not see it are computed again, which
+    # takes a second or so, and no wait gives up meanwhile
+    n = 262144
+    g = torch.Generator(device=DEV).manual_seed(122)
+    q, k, v = (torch.randn(n, m, 128, generator=g, device=DEV, dtype=torch.bfloat16) for m in (8, 1, 1))
+    v[n - 1, 0, 5] = float("inf")
+    out = torch.full((n, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(spc.spc_prompt_attn_workspace_size(n, 1, 8, 1, 128), dtype=torch.uint8, device=DEV)
+    spc.spc_prompt_attn(q, k, v, torch.tensor([0, n], dtype=torch.int32, device=DEV), n, 1, 8, 1, 128, SCALE, out, ws)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32).item()) == 0
+    odd = (~torch.isfinite(out[n - 300:].float())).nonzero()
+    assert odd[:, 0].unique().tolist() == [299] and odd[:, 2].unique().tolist() == [5] and len(odd) == 8
+    kd, vd = k[:, 0].double(), v[:, 0].double()
+    for i in (n - 2, n - 77, n - 128, n - 129):
+        w = torch.softmax(kd[:i + 1] @ q[i].double().T * SCALE, 0)
+        want, mag = (w.T @ vd[:i + 1]).cpu().numpy(), (w.T @ vd[:i + 1].abs()).cpu().numpy()
+        assert np.all(np.abs(f64(out[i]) - want) <= prompt_tol(want, mag)), i
