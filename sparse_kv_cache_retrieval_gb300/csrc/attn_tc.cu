@@ -162,14 +162,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
 }
 
-// 2^x for x <= 8 (and -inf -> 0): the MUFU approximation, relative error
-// ~2^-22, far inside what the bf16 split of the weights keeps
-__device__ __forceinline__ float ex2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Both index entries of kept index i (selected position, slot map entry),
 // fetched one tile ahead; i >= K reads nothing
 struct AtIdx {
@@ -628,7 +620,7 @@ __global__ void __maxnreg__(kAtMaxReg) attn_tc_kernel(const __grid_constant__ CU
       float alpha = 1.f;
       if (M > m + kAtHeadroom) {          // false for M = -inf; true for the first finite maximum
         if (m != -INFINITY) {
-          alpha = ex2_fast(m - M);
+          alpha = ex2_approx(m - M);
           l *= alpha;
           rescale = true;                 // O already holds this segment's earlier tiles
         }
@@ -640,7 +632,7 @@ __global__ void __maxnreg__(kAtMaxReg) attn_tc_kernel(const __grid_constant__ CU
         float ls4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kAtKT; ++j) {
-          s[j] = ex2_fast(fmaf(s[j], a.scale2, -m));
+          s[j] = ex2_approx(fmaf(s[j], a.scale2, -m));
           ls4[j & 3] += s[j];
         }
         lsum = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);

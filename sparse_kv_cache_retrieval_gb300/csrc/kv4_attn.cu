@@ -335,7 +335,7 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
         for (int k = 4; k <= 16; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], k));
         const float M = fmaxf(m[n][e], mx[e]);
         // a first finite maximum takes 0 of what was (nothing)
-        const float c = k4_ex2((m[n][e] - (M == -INFINITY ? 0.f : M)) * f[n][e]);
+        const float c = ex2_approx((m[n][e] - (M == -INFINITY ? 0.f : M)) * f[n][e]);
         m[n][e] = M;
         l[n][e] *= c;
 #pragma unroll
@@ -353,8 +353,8 @@ __device__ __forceinline__ void k4_step32(const uint8_t* rows, uint32_t valid, c
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float2 x = fma2(add2(make_float2(s[n][t][2 * e], s[n][t][2 * e + 1]), nm), ff, bias);
-        x.x = k4_ex2(x.x);
-        x.y = k4_ex2(x.y);
+        x.x = ex2_approx(x.x);
+        x.y = ex2_approx(x.y);
         ls = add2(ls, x);
         p[n][t][e] = movmatrix(pack_f16(x.x, x.y));
       }
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(K4Cfg<HT, SEL>::kThreads, 1) kv4_attn_kernel(K
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float* src = mrg + (size_t)(w * 8 + e) * kK4Part;
-          const float wt = k4_ex2((src[0] - Ms) * fh);
+          const float wt = ex2_approx((src[0] - Ms) * fh);
           const float4 x = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
           L += wt * src[1];
           v.x += wt * x.x; v.y += wt * x.y; v.z += wt * x.z; v.w += wt * x.w;

@@ -47,13 +47,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // q.K are multiples of 2^-34 below 2^20, so that at 2^100 the largest takes all
 // and nothing overflows.
 __device__ __forceinline__ float k4_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 1.26765060e30f); }
-// 2^x by the MUFU approximation (relative error about 2^-22); -inf gives 0
-__device__ __forceinline__ float k4_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // x / d for 0 <= x <= 2^21 (a request's tiles, or a segment's times the CTAs), d
 // >= 1. The approximate quotient is off by less than one there; an integer
 // division costs some 150 cycles each in a plan that every CTA waits for.
@@ -253,7 +246,7 @@ __device__ __forceinline__ void k4_merge(const Kv4Args& a, const K4Open& u, int 
       float L = 0.f;
       for (int q = lane; q < np; q += 32) {
         const float2 ml = wl[h * kK4Ctas + q];
-        const float wt = k4_ex2((ml.x - Ms) * f);
+        const float wt = ex2_approx((ml.x - Ms) * f);
         L += wt * ml.y;
         wl[h * kK4Ctas + q].x = wt;
       }

@@ -89,11 +89,6 @@ constexpr uint32_t kKtIdescS = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32
 template <int N>
 constexpr uint32_t kKtIdescO = kKtIdescS<N> | (1u << 15) | (1u << 16);         // both operands MN-major
 
-__device__ __forceinline__ bool kt_elect() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // barrier of the four softmax warps, plain and with the OR of a predicate
 __device__ __forceinline__ void kt_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool kt_any(bool x) {
@@ -242,7 +237,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     auto desc = [&](uint32_t addr, uint32_t lead) { return (uint64_t)hi << 32 | (addr >> 4) | (lead >> 4) << 16; };
     auto issue_s = [&](int i) {
       tc_fence_after();
-      if (kt_elect()) {
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk)
           umma_f16_tmem_a(tm + kKtColS + (i & 1) * 64, tm + (i & 1) * 64 + kk * 8,
@@ -254,7 +249,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
     };
     auto issue_pv = [&](int i, bool first) {
       tc_fence_after();
-      if (kt_elect()) {
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kKtTile / 16; ++kk)
           umma_f16(tm + kKtColO, desc(sm + kKtOffV + (uint32_t)(i & 1) * kKtV + (uint32_t)kk * 2048, kKtV / 2),
@@ -304,7 +299,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
       }
     }
     // every MMA has completed before tensor memory is released
-    if (kt_elect()) umma_commit(drain);
+    if (elect_one()) umma_commit(drain);
     __syncwarp();
     mbar_wait_bounded(drain, 0, a.wait_limit);
     __syncwarp();
@@ -456,8 +451,8 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
               const float2 x = fma2(add2(make_float2(s[h], s[h + 1]), make_float2(k.z, k.w)), make_float2(k.x, k.y),
                                     make_float2(kKtBias, kKtBias));
               mx = fmaxf(mx, fmaxf(x.x, x.y));
-              s[h] = k4_ex2(x.x);
-              s[h + 1] = k4_ex2(x.y);
+              s[h] = ex2_approx(x.x);
+              s[h + 1] = ex2_approx(x.y);
               p[j] = pack_f16(s[h], s[h + 1]);
             }
             asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(pb + (uint32_t)((n ^ (row & 7)) << 4)), "r"(p[0]),
@@ -481,7 +476,7 @@ __global__ void __launch_bounds__(kKtThreads, 1) kv4_attn_tc_kernel(Kv4Args a, K
             // (finite from the first position that counts on)
             const float tmx = fmaxf(fmaxf(fmaxf(red[row], red[64 + row]), fmaxf(red[128 + row], red[192 + row])), -3e38f);
             const float m = mrun[row], f = mf[mf_at(row)], M = (tmx - m) * f > kKtHeadroom ? tmx : m;
-            al[row] = M == m ? 1.f : k4_ex2((m - M) * f);
+            al[row] = M == m ? 1.f : ex2_approx((m - M) * f);
             mrun[row] = M;
             mf[mf_at(row) + 2] = -M;
           }
@@ -610,7 +605,7 @@ __global__ void __launch_bounds__(32 * kKmWarps) kt_merge_kernel(Kv4Args a, cons
   const float Ms = M == -INFINITY ? 0.f : M, f = __shfl_sync(0xffffffffu, ml[0].z, 0);
 #pragma unroll
   for (int k = 0; k < kMl; ++k) {
-    const float wt = k4_ex2((ml[k].x - Ms) * f);
+    const float wt = ex2_approx((ml[k].x - Ms) * f);
     L += wt * ml[k].y;
     if (lane + 32 * k < u.np) wl[warp][lane + 32 * k] = wt;
   }

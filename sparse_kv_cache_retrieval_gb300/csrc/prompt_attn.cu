@@ -106,11 +106,6 @@ struct PaItem {
 __device__ __forceinline__ bool pa_wait(const PaArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
 }
-__device__ __forceinline__ float pa_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // A shared-memory matrix descriptor (spc_tc.cuh) in two words: the low one
 // holds the address (in 16-byte units) and the leading byte offset, the high
 // one is the same for every operand here (1024 bytes between 8-row groups,
@@ -120,12 +115,6 @@ constexpr uint32_t kPaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kPaDescVLo = ((kPaBlock >> 4) - 1u) << 16;      // on top of a K-major low word
 __device__ __forceinline__ uint32_t pa_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ uint64_t pa_desc(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
-// one lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ float pa_max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -148,8 +137,8 @@ __device__ __forceinline__ void pa_weights(const float* s, float scale2, float m
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sc, nm);
-    x.x = pa_ex2(x.x);
-    x.y = pa_ex2(x.y);
+    x.x = ex2_approx(x.x);
+    x.y = ex2_approx(x.y);
     sum[e & 1] = add2(sum[e & 1], x);
     p[e] = pack_bf16(x.x, x.y);
   }
@@ -580,7 +569,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           float alpha = 1.f;
           const bool up = M > m + kPaHeadroom;
           if (up) {
-            alpha = m == -INFINITY ? 0.f : pa_ex2(m - M);
+            alpha = m == -INFINITY ? 0.f : ex2_approx(m - M);
             l *= alpha;
             m = M;
           }

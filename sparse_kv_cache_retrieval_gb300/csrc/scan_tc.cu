@@ -121,14 +121,6 @@ __device__ __forceinline__ int tc_len(const int32_t* len, int b, int append, int
   return (append && L < cap) ? L + 1 : L;
 }
 
-// 2^x by the MUFU approximation (relative error ~2^-22, far inside the
-// scores' tolerance); 2^-inf = 0
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // (max, sum of 2^(x - max)) merge with one exp2: the smaller maximum's sum is
 // scaled; an empty side is (-inf, 0)
 __device__ __forceinline__ void lse_merge(float& m, float& s, float m2, float s2) {
