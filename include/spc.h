@@ -28,9 +28,10 @@
  *   - Returns SPC_OK or a negative spc_status. An error raised by a kernel
  *     after launch surfaces at the caller's next synchronisation (CUDA error)
  *     or in the workspace status word (spc_score_select, spc_sparse_decode_attn,
- *     spc_mla_decode_attn): every bounded device-side wait that gives up
- *     records SPC_ERR_TIMEOUT there, lets its copies in flight land and
- *     returns, so the context stays usable.
+ *     spc_mla_decode_attn, spc_kv4_decode_attn, spc_prompt_attn): every bounded
+ *     device-side wait that gives up records SPC_ERR_TIMEOUT there, lets its
+ *     copies in flight land and returns, so the context stays usable.
+ *     (spc_block_map's status word is an argument of its own.)
  *   - Calls on the same stream may be captured into a CUDA graph once each
  *     entry point has been called once outside capture (the first call sets
  *     kernel attributes).
@@ -512,6 +513,11 @@ int spc_block_map(const int32_t* len, const int32_t* len_next, int32_t* block_ta
  *   s = e4m3(min(max|x| / 6, 448)),  code = e2m1(x / s)  (0 where s = 0),
  * both rounded to nearest, ties to even, of the exact quotients. Values beyond
  * 6 * 448 saturate (infinities too); a NaN makes its group's scale NaN.
+ * What 4 bits keep depends on a group's largest magnitude a. From 0.094 (6 *
+ * 2^-6) on the scale has 4 bits and normal values are off by about 9% (2-norm);
+ * below, its steps are 2^-9, and groups with a <= 0.0058 (6 * 2^-10) become
+ * zeros. Rows that small are kept by storing 2^n times them: with K so stored
+ * the attention's scale is divided by 2^n, with V its output.
  * k, v      bf16, row t at k + t * k_stride elements: [n_kv][d], 16-byte
  *           aligned; strides are multiples of 8 elements, at least n_kv * d and
  *           at most 2^37. Neither span, first to last row, may overlap the cache.
@@ -535,6 +541,11 @@ int spc_kv4_load(const void* cache, const int32_t* slot_map, void* k, void* v, i
  *   out[b,h,:] = sum_{p in R} softmax_p(scale * q[b,h] . K[g,p]) V[g,p]
  * Positions whose table entry is outside [0, num_blocks) are left out; zeros
  * where nothing is left.
+ * Precision: products, maxima and sums are fp32. Queries are taken in fp16 after a
+ * power of two per head (a value loses bits only below 2^-14 of the head's largest,
+ * at most 2^-25 of it); softmax weights are rounded to fp16 (2^-11) down to 2^-25 of
+ * the largest and are off by at most 2^-36 of it below; the output is rounded
+ * to bf16 once.
  * q          bf16 [B][n_q][d], 16-byte aligned.
  * block_table int32 [B][max_blocks]; len int32 [B] (at most max_blocks *
  *            block_size positions count).
@@ -562,6 +573,10 @@ int spc_kv4_decode_attn(const void* q, const void* cache, const int32_t* block_t
  *   out[i,h,:] = sum_{j <= i, j in the sequence} softmax_j(scale * q[i,h] . k[j,g]) v[j,g]
  * Rows outside every sequence are left as they were. What a row does not see
  * (later rows, other sequences) does not reach it, NaN and infinities included.
+ * Precision: products, maxima and sums are fp32; softmax weights are rounded to
+ * bf16 (2^-8 each) before they multiply v, not in their sum; the output is rounded
+ * to bf16 once. Rows beside non-finite v, and rows with logits beyond 2^26 in
+ * base 2, are computed one at a time, some 40 ms each over 262144 keys.
  * q, k, v    bf16, row t at q + t * q_stride elements: [n_q][d] (k, v: [n_kv][d]),
  *            16-byte aligned; strides are multiples of 8 elements, at least the
  *            row's size (the three may lie in one fused projection's output).
