@@ -629,10 +629,13 @@ bool paged_starve(long long* wait_limit) {
 }
 #endif
 
-// The whole context of groups of 32 and 64 heads goes to the tcgen05 kernel (8
-// requests of 65536 positions on one KV head, us there and here: 64 heads 48
-// and 89, 32 heads 39 and 62, but 16 heads 35 and 35, and on four KV heads 108
-// and 88). Selected positions stay here.
+// The whole context of groups of 32 and 64 heads goes to the tcgen05 kernel. Both
+// sides measured for 32 and 64 heads on 1, 4 and 8 KV heads, 1 to 64 requests of 16
+// to 65536 positions, equal and ragged: it is 1.17 to 3.8 times as fast in all 60
+// (us there and here: 64 heads on one, 8 x 65536 47 and 88, 1 x 2000 11 and 22, 64 of
+// 1-2000 21 and 63; 32 on one, 39 and 60, 9 and 22, 17 and 25; 32 on each of 8, 8 x
+// 65536 235 and 276, 32 of 16-200 12 and 21). 16 heads, 8 x 65536: 35 and 35 on one
+// KV head, 108 and 88 on four. Selected positions stay here.
 static bool k4_on_tc(int G, int budget) { return G >= 32 && budget == 0; }
 // head tiles a segment, and log2 of the segments a group is split into
 static int k4_head_tiles(int G, int budget) { return k4_on_tc(G, budget) ? G / 8 : G <= 8 ? 1 : G == 16 ? 2 : 4; }

@@ -20,20 +20,25 @@
 // times the weights against the running maximum, the top of fp16's range (see
 // kv4_attn.cu): 11 bits down to 2^-25 of the largest, off by at most 2^-36 of it
 // below. A raise costs about a tile here, which is why more of the range is left
-// to growth than there (8 x 65536, 64 heads on one: 47.5 us with a factor of 2^10,
-// 47.9 with 2^11, 49.7 with 2^12).
+// to growth than there (8 x 65536, 64 heads on one: 46.5 us with a factor of 2^10,
+// 46.7 with 2^11, 48.7 with 2^12).
 //
 // One CTA per SM, 16 warps:
 //   0-3    softmax and epilogue (one position, in the epilogue one dim, a thread)
 //   4-11   dequantisation, two groups of four that take the tiles by turns
 //   12     tensor memory, MMA issue: S(t + 1) ahead of PV(t)
 //   13     copies (cp.async.bulk, one a cache block), six tiles ahead
-// Bound: a tile's 18 KB are 800 cycles of an SM's share of HBM, its two products
-// about 720; the softmax warps' own path through a tile is longer (1800 cycles
-// at N = 64, 1000 at N = 32: logits 150, exponentials 64 N / 16, the stores of P
-// and their proxy fence, the barrier), and it is what bounds the kernel.
-// Measured (8 requests of 65536 positions on one KV head, 75 MB, floor 11 us):
-// N = 64 47 us, N = 32 38 us; the mma.sync kernel 89 and 62.
+// Bound: a tile is 1.26 us at N = 64 and 1.02 at N = 32 (from 8 requests of 32768
+// and of 131072 positions), of which its 18 KB are 0.41 us of an SM's share of HBM.
+// No unit is busy (tensor pipe 24%, ALU 26%): without the softmax's arithmetic it
+// is 0.99 and 0.82 us, without the conversions 1.21 and 0.97, without both 0.97
+// and 0.78. What is left is the chain of a tile, of which two are in flight: V
+// dequantised when the PV two tiles back has read its buffer, S, softmax, PV, a
+// barrier between each two. Beside its tiles a call has 13 us (N = 32: 11): launch,
+// plan, first tile, and 6 for the merge kernel; one request over 128 CTAs has
+// more in the merge (20 us) than here (14).
+// Measured (8 requests of 65536 positions on one KV head, 27 tiles a CTA, 75 MB,
+// floor 11 us): N = 64 46.7 us, N = 32 38.6 us; the mma.sync kernel 88 and 60.
 // Every wait is bounded; a warp whose wait gives up records SPC_ERR_TIMEOUT and
 // runs on without waiting, so that the softmax warps' barriers are reached.
 #include <cuda_runtime.h>
@@ -50,9 +55,9 @@ constexpr int kKtMasks = 16;                          // tiles whose masks are k
 constexpr float kKtBias = 11.f;                       // log2 of the factor of the weights
 constexpr float kKtHeadroom = 4.75f;                  // log2 growth allowed before a maximum is raised
 static_assert(kKtBias + kKtHeadroom <= 15.9f, "weights within fp16's range");
-// See k4_plan. A tile is 0.7 us of the CTA that has it, the merge some 3 us and
-// a little a piece: 64 heads on one, 1 x 2000: 10.6 us with these, 17.9 with 8
-// and 8; 1 x 65536 26.4 and 24.8.
+// See k4_plan. A tile is 1.0 to 1.3 us of the CTA that has it, the merge some 4 us
+// and a little a piece: 64 heads on one, 1 x 2000: 10.6 us with these, 17.9 with
+// 8 and 8; 1 x 65536 26.4 and 24.8.
 constexpr int kKtWhole = 4, kKtMinRun = 2, kKtSlack = 8;
 constexpr uint32_t kKtV = kKtTile * kRowBytes;        // 32 KB: V of a tile, fp16
 constexpr uint32_t kKtP = kKtTile * 128;              // 16 KB: P, 64 heads a row

@@ -38,9 +38,10 @@
 // of 512 cycles; a period was 2650 cycles in a clock trace, of which the chain
 // of one tile (its S, 1130 cycles from S to P, the MMA warp's wait, its PV) is
 // what is left. Measured, 32 heads on 8 KV heads: one sequence of 16384 tokens
-// (2199 GFLOP) 1.19-1.24 ms, 0.93-0.97 of the measured matrix rate, and 1.32-1.35
+// (2199 GFLOP) 1.20-1.31 ms, 0.88-0.96 of the measured matrix rate, and 1.32-1.35
 // ms in a long run, where the power limit lowers the clock (0.94-0.97 of the rate
-// measured so); 4096 tokens (137 GFLOP) 90 us, 0.80; 16 sequences of 1 to 700 tokens 41 us (their bytes alone are 17):
+// measured so); 4096 tokens (137 GFLOP) 91 us, 0.79; 16 sequences of 1 to 700 tokens
+// 41 us (their bytes alone are 17):
 // an item has one to six blocks, and its first S, its epilogue (about 3000
 // cycles) and the sixth item of a few CTAs weigh as much as the blocks.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
