@@ -72,13 +72,18 @@ constexpr float kK4Headroom = 1.75f;                 // log2 growth allowed befo
 static_assert(kK4Bias + kK4Headroom <= 15.9f, "weights within fp16's range");
 
 // The CTA of a kernel for HT head tiles; the last warps copy for the others:
-// one where the whole context is read, 5 (or 2 of 8) where positions are
-// gathered (64 segments of 4096: 2 warps 30 us, 3 25, 4 23, 5 22, 6 22).
+// one where the whole context is read, 5 of 15 (or 2 of 8) where positions are
+// gathered (64 segments of 4096: 5 for 10 that compute 21.4 us, 4 for 12 22.9, 3
+// for 12 25.3).
 template <int HT, bool SEL>
 struct K4Cfg {
-  static constexpr int kAll = HT == 1 ? 16 : 8;        // warps
+  static constexpr int kAll = HT > 1 ? 8 : SEL ? 15 : 16;      // warps
   static constexpr int kCopy = !SEL ? 1 : HT == 1 ? 5 : 2;
   static constexpr int kWarps = kAll - kCopy;          // warps that compute
+  // Copying warps take the tiles in turn, and a ring's tiles have to be one
+  // warp's: a wait on a stage's phase tells the phases of one parity from the
+  // other, so that who waits may be one phase ahead and not two.
+  static_assert(kWarps % kCopy == 0, "every ring is filled by one copying warp");
   static constexpr int kStages = HT == 1 ? 2 : 4;      // tiles in a warp's ring
   // Tiles up to which a segment is never split, and that a CTA takes at least
   // of one that is. A split costs about 2.5 us (8 segments of 10 tiles: 5.6 us

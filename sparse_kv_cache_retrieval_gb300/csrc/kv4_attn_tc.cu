@@ -51,6 +51,7 @@ namespace spc {
 constexpr int kKtTile = 128;                          // positions
 constexpr uint32_t kKtRaw = kKtTile * kKv4Rec;        // 18 KB: a tile's records
 constexpr int kKtStages = 6;
+static_assert(kKtStages % 2 == 0, "every stage is read by one of the two dequantising groups");
 constexpr int kKtMasks = 16;                          // tiles whose masks are kept
 constexpr float kKtBias = 11.f;                       // log2 of the factor of the weights
 constexpr float kKtHeadroom = 4.75f;                  // log2 growth allowed before a maximum is raised
