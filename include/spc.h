@@ -28,10 +28,11 @@
  *   - Returns SPC_OK or a negative spc_status. An error raised by a kernel
  *     after launch surfaces at the caller's next synchronisation (CUDA error)
  *     or in the workspace status word (spc_score_select, spc_sparse_decode_attn,
- *     spc_mla_decode_attn, spc_kv4_decode_attn, spc_prompt_attn): every bounded
+ *     spc_mla_decode_attn, spc_kv4_decode_attn, spc_prompt_attn,
+ *     spc_kv4_chunk_attn, spc_kv4_attn_mass): every bounded
  *     device-side wait that gives up records SPC_ERR_TIMEOUT there, lets its
  *     copies in flight land and returns, so the context stays usable.
- *     (spc_block_map's status word is an argument of its own.)
+ *     (The status words of spc_block_map and spc_kv4_evict are arguments of their own.)
  *   - Calls on the same stream may be captured into a CUDA graph once each
  *     entry point has been called once outside capture (the first call sets
  *     kernel attributes).
@@ -596,6 +597,98 @@ size_t spc_prompt_attn_workspace_size(int T, int B, int n_q, int n_kv, int d);
 int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int T, int B,
                     int n_q, int n_kv, int d, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                     float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of a chunk of new tokens over the paged 4-bit cache: a second turn,
+ * a prompt behind a shared prefix, one chunk of a long prompt, drafted tokens,
+ * single tokens, all in one batch. Request b's new tokens are rows
+ * [cu_seqlens[b], cu_seqlens[b + 1]) of q; their own K and V are in the cache
+ * already (spc_kv4_store), len[b] counts them, and token i of n sits at position
+ * P = len[b] - n + i. For its query head h (g = h / G):
+ *   R = { p : 0 <= p <= P }, without positions whose table entry is outside [0, num_blocks)
+ *   out[row,h,:] = sum_{p in R} softmax_p(scale * q[row,h] . K[g,p]) V[g,p]
+ *   lse[row,h]   = ln sum_{p in R} exp(scale * q[row,h] . K[g,p])
+ * Zeros and -infinity where R is empty (a token before position 0 among them).
+ * Rows outside every request are left as they were. What a row does not see
+ * does not reach it, NaN included; a query that is not finite makes its row NaN.
+ * Precision: as spc_kv4_decode_attn; lse is fp32.
+ * q          bf16, row t at q + t * q_stride elements: [n_q][d], 16-byte aligned;
+ *            the stride is a multiple of 8 elements, at least n_q * d and at most 2^32.
+ * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are a
+ *            request without new tokens.
+ * block_table int32 [B][max_blocks]; len int32 [B] (at most max_blocks *
+ *            block_size positions count).
+ * out        bf16 [T][n_q][d], 16-byte aligned. lse fp32 [T][n_q], or NULL. Neither they nor the
+ *            workspace may overlap anything else of the call.
+ * workspace  spc_kv4_chunk_attn_workspace_size() bytes, 256-byte aligned,
+ *            ZERO-FILLED BEFORE ITS FIRST USE (calls leave it ready); its
+ *            first int32 is the status word (0 or SPC_ERR_TIMEOUT). Calls
+ *            that may overlap must use distinct workspaces; calls of any
+ *            shapes may take turns on one that is large enough for each.
+ * Limits: d = 128, G in {1,2,4,8,16,32,64}, n_q <= 1024, 1 <= B <= 64,
+ *         0 <= T <= 2^24, scale > 0. */
+size_t spc_kv4_chunk_attn_workspace_size(int T, int B, int n_q, int n_kv, int d);
+
+int spc_kv4_chunk_attn(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                       const int32_t* cu_seqlens, int T, int B, int n_q, int n_kv, int d, int num_blocks,
+                       int block_size, int max_blocks, int64_t q_stride, float scale, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* The attention weight that each cached position receives from new tokens, added
+ * to what it had: with the rows, positions and sets R of spc_kv4_chunk_attn and
+ * its lse,
+ *   mass_next[b,g,p] = keep * mass_prev[b,g,p] + sum over the new tokens i and the heads h of
+ *                      group g whose R holds p of exp(scale * q[i,h] . K[g,p] - lse[i,h])
+ * for p < len[b]; other entries are left as they were. Rows with an lse of -infinity
+ * add nothing. The new tokens may be any of a request's last ones (the last 64
+ * of a prompt, say): q, cu_seqlens and lse then hold their rows, the last at
+ * position len[b] - 1. keep = 1 adds up, less than 1 lets older steps fade, and
+ * with 0 mass_prev is not read.
+ * Precision: products, exponentials and sums are fp32, in an order that is the
+ * same in every call of the same shapes and lengths.
+ * lse        fp32 [T][n_q].
+ * mass_prev, mass_next fp32 [B][n_kv][cap], cap >= max_blocks * block_size; mass_next may be
+ *            mass_prev; mass_prev may be NULL where keep = 0.
+ * The other arguments, the workspace and the limits are as for spc_kv4_chunk_attn;
+ * cap <= SPC_MAX_CAP, keep finite and >= 0. */
+size_t spc_kv4_attn_mass_workspace_size(int T, int B, int n_q, int n_kv, int d);
+
+int spc_kv4_attn_mass(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                      const int32_t* cu_seqlens, const float* lse, const float* mass_prev, float* mass_next, int T,
+                      int B, int n_q, int n_kv, int d, int num_blocks, int block_size, int max_blocks, int cap,
+                      int64_t q_stride, float scale, float keep, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Eviction from the paged 4-bit cache by accumulated attention weight: each KV
+ * head keeps its sinks, its recent window and the positions with the largest
+ * sums, and the kept records move to the front, in order. With L = len[b] (at
+ * most max_blocks * block_size), K = min(L, budget):
+ *   kept[b,g,:]      = the K positions of the spc_score_select rule with s_g[p] = mass[b,g,p]
+ *                      (sums that are NaN or negative count as 0), ascending, -1 padded
+ *   record of position i in block_table_next = record of position kept[b,g,i] in block_table, i < K
+ *   mass_next[b,g,i] = mass[b,g,kept[b,g,i]] for i < K, 0 for K <= i < L
+ *   len_next[b]      = K
+ * The blocks behind the kept ones go back with spc_block_map(len, len_next), and
+ * new positions then follow at K. Positions that later calls name are places in
+ * the shorter cache; kept says where they came from. With block_table_next =
+ * block_table the cache shrinks in place. A different table (its entries i < ceil(K /
+ * block_size) name blocks that no other row uses) leaves the old records as they
+ * were, where requests share them. A request with a table entry outside [0,
+ * num_blocks) among those is left as it was, with SPC_ERR_INVALID_ARG in the
+ * status word: len_next = L, kept = -1, mass_next = mass.
+ * cache      written; block_table, block_table_next int32 [B][max_blocks]. No block
+ *            that is written may occur twice in block_table_next, nor in another
+ *            request's row of block_table.
+ * mass, mass_next fp32 [B][n_kv][cap], cap >= max_blocks * block_size; entries p >= L are left as they
+ *            were. mass_next may be mass. len, len_next int32 [B], not the same.
+ * kept       int32 [B][n_kv][budget], or NULL. status int32 [1], zeroed by the caller.
+ * Beside block_table_next = block_table and mass_next = mass, nothing that is
+ * written may overlap anything else of the call.
+ * Limits: d = 128, 1 <= B <= 64, 1 <= n_kv <= 1024, 1 <= budget <= 4096, n_sink + n_recent <=
+ *         budget, cap <= SPC_MAX_CAP; 4-byte aligned addresses, the cache 16-byte. */
+int spc_kv4_evict(void* cache, const int32_t* block_table, const int32_t* block_table_next, const int32_t* len,
+                  int32_t* len_next, const float* mass, float* mass_next, int32_t* kept, int32_t* status, int B,
+                  int n_kv, int d, int num_blocks, int block_size, int max_blocks, int cap, int budget, int n_sink,
+                  int n_recent, void* stream);
 
 /* ------------------------------------------------------------------------
  * Helpers (no counterpart on the pages).

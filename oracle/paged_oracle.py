@@ -1,8 +1,10 @@
 """Float64 oracle of the paged 4-bit cache path -- TEST INFRASTRUCTURE ONLY.
 
 Plain numpy from the definitions: block tables and slot maps, the e2m1 / e4m3
-rounding of K and V rows, decode attention over a paged cache and causal
-attention over packed prompts. Shares no code with the CUDA path.
+rounding of K and V rows, decode attention over a paged cache, causal
+attention over packed prompts, and for chunks of new tokens over the cache their
+attention, the weights that its positions receive, and the eviction by those.
+Shares no code with the CUDA path.
 """
 from __future__ import annotations
 
@@ -144,5 +146,90 @@ def prompt_attention(q, k, v, cu, scale):
     return out, mag
 
 
+def _seen(cache, table_row, L, P):
+    """The positions 0 .. P of a request of L whose block is in the pool, with their blocks."""
+    pos = np.arange(max(0, min(L, P + 1)))
+    blk = table_row[pos // cache.shape[2]].astype(np.int64)
+    ok = (blk >= 0) & (blk < cache.shape[0])
+    return pos[ok], blk[ok]
+
+
+def chunk_attention(q, cache, table, lens, cu, scale):
+    """New tokens q [T][n_q][d] (float64), request b's last cu[b + 1] - cu[b]
+    positions. Returns (out, bound, lse, err): bound = sum w |v| and err = the
+    largest sum |q k| scale of a row's logits; NaN in rows of no request."""
+    num_blocks, n_kv, bs, _ = cache.shape
+    T, n_q, d = q.shape
+    G = n_q // n_kv
+    out, mag = np.full((T, n_q, d), np.nan), np.full((T, n_q, d), np.nan)
+    lse, err = np.full((T, n_q), np.nan), np.full((T, n_q), np.nan)
+    for b in range(len(lens)):
+        L, n = max(0, min(int(lens[b]), table.shape[1] * bs)), cu[b + 1] - cu[b]
+        for g in range(n_kv):
+            pos, blk = _seen(cache, table[b], L, L)
+            k, v = values(cache[blk, g, pos % bs])
+            for i in range(n):
+                m = int(np.searchsorted(pos, L - n + i, side="right"))
+                t, hs = cu[b] + i, slice(g * G, (g + 1) * G)
+                out[t, hs], mag[t, hs] = softmax_rows(q[t, hs], k[:m], v[:m], scale)
+                err[t, hs], lse[t, hs] = 0, -np.inf
+                if m:
+                    x = (q[t, hs] @ k[:m].T) * scale
+                    lse[t, hs] = x.max(-1) + np.log(np.exp(x - x.max(-1, keepdims=True)).sum(-1))
+                    err[t, hs] = (np.abs(q[t, hs]) @ np.abs(k[:m]).T).max(-1) * scale
+    return out, mag, lse, err
+
+
+def attn_mass(q, cache, table, lens, cu, lse, prev, keep, cap, scale):
+    """(mass [B][n_kv][cap], rel): what spc_kv4_attn_mass writes, NaN where it
+    writes nothing, and rel = the sum of weight * (sum |q k| scale + |lse|)."""
+    num_blocks, n_kv, bs, _ = cache.shape
+    G, B = q.shape[1] // n_kv, len(lens)
+    mass, rel = np.full((B, n_kv, cap), np.nan), np.zeros((B, n_kv, cap))
+    for b in range(B):
+        L, n = max(0, min(int(lens[b]), table.shape[1] * bs)), cu[b + 1] - cu[b]
+        for g in range(n_kv):
+            mass[b, g, :L] = keep * prev[b, g, :L] if keep else 0
+            for i in range(n):
+                pos, blk = _seen(cache, table[b], L, L - n + i)
+                k, _ = values(cache[blk, g, pos % bs])
+                for h in range(g * G, (g + 1) * G):
+                    y = lse[cu[b] + i, h]
+                    if len(pos) == 0 or y == -np.inf:
+                        continue
+                    row = q[cu[b] + i, h]
+                    w = np.exp((k @ row) * scale - y)
+                    mass[b, g, pos] += w
+                    rel[b, g, pos] += w * ((np.abs(k) @ np.abs(row)) * scale + abs(y))
+    return mass, rel
+
+
+def evict(cache, table, table_next, lens, mass, budget, n_sink, n_recent):
+    """(cache, kept, len_next, mass_next, ok) after the call, on copies."""
+    num_blocks, n_kv, bs, _ = cache.shape
+    new, B = cache.copy(), len(lens)
+    kept, after, len_next, ok = np.full((B, n_kv, budget), -1, np.int32), mass.copy(), np.zeros(B, np.int32), True
+    for b in range(B):
+        L = max(0, min(int(lens[b]), table.shape[1] * bs))
+        K = min(L, budget)
+        used = np.concatenate([table[b, :-(-L // bs)], table_next[b, :-(-K // bs)]])
+        if np.any((used < 0) | (used >= num_blocks)):
+            len_next[b], ok = L, False
+            continue
+        len_next[b] = K
+        for g in range(n_kv):
+            s = np.nan_to_num(np.maximum(mass[b, g, :L].astype(np.float64), 0), nan=0.0, posinf=np.inf)
+            s[:n_sink] = s[max(0, L - n_recent):] = np.inf
+            forced = np.zeros(L, bool)
+            forced[:n_sink] = forced[max(0, L - n_recent):] = True
+            order = np.lexsort((np.arange(L), -s, ~forced))
+            pos = np.sort(order[:K])
+            kept[b, g, :K] = pos
+            i = np.arange(K)
+            new[table_next[b, i // bs], g, i % bs] = cache[table[b, pos // bs], g, pos % bs]
+            after[b, g, :K], after[b, g, K:L] = mass[b, g, pos], 0
+    return new, kept, len_next, after, ok
+
+
 __all__ = ["RECORD", "E2M1", "E4M3", "quantise", "records", "values", "block_map", "decode_attention",
-           "prompt_attention", "softmax_rows"]
+           "prompt_attention", "softmax_rows", "chunk_attention", "attn_mass", "evict"]

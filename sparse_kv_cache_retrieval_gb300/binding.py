@@ -66,6 +66,12 @@ SIGNATURES = {
     "spc_prompt_attn_workspace_size": (ctypes.c_size_t, [_I] * 5),
     "spc_prompt_attn": (_I, [_P] * 4 + [_I] * 5 + [ctypes.c_int64] * 3 + [ctypes.c_float, _P, _P, ctypes.c_size_t,
                                                                          _P]),
+    "spc_kv4_chunk_attn_workspace_size": (ctypes.c_size_t, [_I] * 5),
+    "spc_kv4_chunk_attn": (_I, [_P] * 5 + [_I] * 8 + [ctypes.c_int64, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
+    "spc_kv4_attn_mass_workspace_size": (ctypes.c_size_t, [_I] * 5),
+    "spc_kv4_attn_mass": (_I, [_P] * 8 + [_I] * 9 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float, _P, ctypes.c_size_t,
+                                                    _P]),
+    "spc_kv4_evict": (_I, [_P] * 9 + [_I] * 10 + [_P]),
     "spc_mla_decode_attn_workspace_size": (ctypes.c_size_t, [_I] * 3),
     "spc_mla_decode_attn": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t,
                                  _P]),
@@ -287,7 +293,7 @@ def spc_mla_decode_attn(q, Wuk, Wuv, views, selected, slot_pos, n_layers, B, bud
 SPC_KV4_RECORD, SPC_KV4_GROUP = 144, 16
 
 # accepted dtypes, filled in by _device() (torch is imported on first use)
-_BF16, _I32, _BYTES = set(), set(), set()
+_BF16, _I32, _BYTES, _F32 = set(), set(), set(), set()
 
 
 _torch = None
@@ -301,6 +307,7 @@ def _device():
         _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
         _BYTES.update((torch.uint8, torch.int8))
         _I32.add(torch.int32)
+        _F32.add(torch.float32)
         _torch = torch
     return _torch.cuda.current_device() if _torch.cuda.is_initialized() else -2
 
@@ -431,6 +438,64 @@ def spc_prompt_attn(q, k, v, cu_seqlens, T, B, n_q, n_kv, d, scale, out, workspa
         q, k, v, _dev("cu_seqlens", cu_seqlens, _I32, B + 1, dev), T, B, n_q, n_kv, d, q_stride, k_stride, v_stride,
         float(scale), _dev("out", out, _BF16, T * n_q * d, dev),
         _dev("workspace", workspace, _BYTES, workspace_bytes, dev), workspace_bytes, _raw_stream(stream, dev)))
+
+
+def spc_kv4_chunk_attn_workspace_size(T, B, n_q, n_kv, d) -> int:
+    return int(lib().spc_kv4_chunk_attn_workspace_size(T, B, n_q, n_kv, d))
+
+
+def spc_kv4_chunk_attn(q, cache, block_table, len, cu_seqlens, T, B, n_q, n_kv, d, num_blocks, block_size, max_blocks,
+                       scale, out, lse, workspace, workspace_bytes=None, q_stride=None, stream=None) -> None:
+    """Attention of B requests' new tokens, packed, over the paged 4-bit cache
+    that holds them already, and (unless lse is None) the rows' log-sum-exp.
+    The row stride is q's own; it is given only with a plain address."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    dev = _device()
+    q, q_stride = _rows("q", q, T, n_q, d, q_stride, dev)
+    _check("spc_kv4_chunk_attn", lib().spc_kv4_chunk_attn(
+        q, _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev),
+        _dev("block_table", block_table, _I32, B * max_blocks, dev), _dev("len", len, _I32, B, dev),
+        _dev("cu_seqlens", cu_seqlens, _I32, B + 1, dev), T, B, n_q, n_kv, d, num_blocks, block_size, max_blocks, q_stride,
+        float(scale), _dev("out", out, _BF16, T * n_q * d, dev), _dev("lse", lse, _F32, T * n_q, dev),
+        _dev("workspace", workspace, _BYTES, workspace_bytes, dev), workspace_bytes, _raw_stream(stream, dev)))
+
+
+def spc_kv4_attn_mass_workspace_size(T, B, n_q, n_kv, d) -> int:
+    return int(lib().spc_kv4_attn_mass_workspace_size(T, B, n_q, n_kv, d))
+
+
+def spc_kv4_attn_mass(q, cache, block_table, len, cu_seqlens, lse, mass_prev, mass_next, T, B, n_q, n_kv, d, num_blocks,
+                      block_size, max_blocks, cap, scale, keep, workspace, workspace_bytes=None, q_stride=None,
+                      stream=None) -> None:
+    """The attention weight that the cached positions receive from new tokens
+    (spc_kv4_chunk_attn's rows and lse), added to keep * mass_prev."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    dev = _device()
+    q, q_stride = _rows("q", q, T, n_q, d, q_stride, dev)
+    _check("spc_kv4_attn_mass", lib().spc_kv4_attn_mass(
+        q, _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev),
+        _dev("block_table", block_table, _I32, B * max_blocks, dev), _dev("len", len, _I32, B, dev),
+        _dev("cu_seqlens", cu_seqlens, _I32, B + 1, dev), _dev("lse", lse, _F32, T * n_q, dev),
+        _dev("mass_prev", mass_prev, _F32, B * n_kv * cap, dev), _dev("mass_next", mass_next, _F32, B * n_kv * cap, dev),
+        T, B, n_q, n_kv, d, num_blocks, block_size, max_blocks, cap, q_stride, float(scale), float(keep),
+        _dev("workspace", workspace, _BYTES, workspace_bytes, dev), workspace_bytes, _raw_stream(stream, dev)))
+
+
+def spc_kv4_evict(cache, block_table, block_table_next, len, len_next, mass, mass_next, kept, status, B, n_kv, d,
+                  num_blocks, block_size, max_blocks, cap, budget, n_sink, n_recent, stream=None) -> None:
+    """Eviction by accumulated attention weight: each KV head's kept records to
+    the front of block_table_next's blocks (block_table's own to shrink in place)."""
+    dev = _device()
+    _check("spc_kv4_evict", lib().spc_kv4_evict(
+        _dev("cache", cache, _BYTES, num_blocks * n_kv * block_size * SPC_KV4_RECORD, dev),
+        _dev("block_table", block_table, _I32, B * max_blocks, dev),
+        _dev("block_table_next", block_table_next, _I32, B * max_blocks, dev), _dev("len", len, _I32, B, dev),
+        _dev("len_next", len_next, _I32, B, dev), _dev("mass", mass, _F32, B * n_kv * cap, dev),
+        _dev("mass_next", mass_next, _F32, B * n_kv * cap, dev), _dev("kept", kept, _I32, B * n_kv * budget, dev),
+        _dev("status", status, _I32, 1, dev), B, n_kv, d, num_blocks, block_size, max_blocks, cap, budget, n_sink, n_recent,
+        _raw_stream(stream, dev)))
 
 
 def spc_device_sm_count() -> int:

@@ -591,6 +591,113 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
   return prompt_attn_launch(c, workspace, stream);
 }
 
+size_t spc_kv4_chunk_attn_workspace_size(int T, int B, int n_q, int n_kv, int d) {
+  if (T < 0 || T > kMaxRows || B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024)
+    return 0;
+  return kv4_chunk_workspace(T, B, n_q, n_kv);
+}
+
+size_t spc_kv4_attn_mass_workspace_size(int T, int B, int n_q, int n_kv, int d) {
+  if (T < 0 || T > kMaxRows || B < 1 || B > SPC_MAX_BATCH || d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024)
+    return 0;
+  return kv4_mass_workspace(T, B, n_q, n_kv);
+}
+
+// what the two calls over new tokens have in common; fills the call
+static int kv4_chunk_check(Kv4ChunkCall& c, const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                           const int32_t* cu_seqlens, int T, int B, int n_q, int n_kv, int d, int num_blocks, int block_size,
+                           int max_blocks, int64_t q_stride, float scale, const void* workspace, size_t workspace_bytes,
+                           size_t need) {
+  if (d != SPC_HEAD_DIM || !group_ok(n_q, n_kv) || n_q > 1024) return SPC_ERR_SHAPE;
+  if (B < 1 || B > SPC_MAX_BATCH || T < 0 || T > kMaxRows) return SPC_ERR_SHAPE;
+  if (!pool_ok(num_blocks, block_size, n_kv) || !table_ok(max_blocks, block_size)) return SPC_ERR_SHAPE;
+  if (!scale_ok(scale)) return SPC_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return SPC_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPC_ERR_INVALID_ARG;
+  if (!cache || !block_table || !len || !cu_seqlens || !aligned16(cache) || !aligned4(block_table) || !aligned4(len) ||
+      !aligned4(cu_seqlens))
+    return SPC_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !aligned16(q))) return SPC_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)n_q * d || q_stride % 8 || q_stride > (1ll << 32)) return SPC_ERR_SHAPE;
+  c.q = static_cast<const uint16_t*>(q); c.cache = static_cast<const uint8_t*>(cache); c.table = block_table; c.len = len;
+  c.cu = cu_seqlens; c.q_stride = q_stride;
+  c.T = T; c.B = B; c.n_q = n_q; c.n_kv = n_kv; c.num_blocks = num_blocks; c.block_shift = block_shift_of(block_size);
+  c.max_blocks = max_blocks; c.scale = scale;
+  return SPC_OK;
+}
+static int64_t rows_span(int T, int64_t stride, int64_t row) { return T > 0 ? ((T - 1) * stride + row) * 2 : 0; }
+
+int spc_kv4_chunk_attn(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                       const int32_t* cu_seqlens, int T, int B, int n_q, int n_kv, int d, int num_blocks, int block_size,
+                       int max_blocks, int64_t q_stride, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const size_t need = spc_kv4_chunk_attn_workspace_size(T, B, n_q, n_kv, d);
+  Kv4ChunkCall c{};
+  const int bad = kv4_chunk_check(c, q, cache, block_table, len, cu_seqlens, T, B, n_q, n_kv, d, num_blocks, block_size,
+                                  max_blocks, q_stride, scale, workspace, workspace_bytes, need);
+  if (bad != SPC_OK || T == 0) return bad;
+  if (!out || !aligned16(out) || !aligned4(lse)) return SPC_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)n_q * d;
+  if (outputs_overlap({{out, T * row * 2}, {lse, (int64_t)T * n_q * 4}, {workspace, (int64_t)need}, {q, rows_span(T, q_stride, row)},
+                       {cache, (int64_t)num_blocks * block_size * n_kv * SPC_KV4_RECORD}, {block_table, (int64_t)B * max_blocks * 4},
+                       {len, B * 4}, {cu_seqlens, (B + 1) * 4}}, 3))
+    return SPC_ERR_INVALID_ARG;
+  c.out = static_cast<uint16_t*>(out); c.lse = lse;
+  return kv4_chunk_launch(c, workspace, stream);
+}
+
+int spc_kv4_attn_mass(const void* q, const void* cache, const int32_t* block_table, const int32_t* len,
+                      const int32_t* cu_seqlens, const float* lse, const float* mass_prev, float* mass_next, int T, int B,
+                      int n_q, int n_kv, int d, int num_blocks, int block_size, int max_blocks, int cap, int64_t q_stride,
+                      float scale, float keep, void* workspace, size_t workspace_bytes, void* stream) {
+  const size_t need = spc_kv4_attn_mass_workspace_size(T, B, n_q, n_kv, d);
+  Kv4ChunkCall c{};
+  const int bad = kv4_chunk_check(c, q, cache, block_table, len, cu_seqlens, T, B, n_q, n_kv, d, num_blocks, block_size,
+                                  max_blocks, q_stride, scale, workspace, workspace_bytes, need);
+  if (bad != SPC_OK) return bad;
+  if (cap > SPC_MAX_CAP || cap < max_blocks * block_size) return SPC_ERR_SHAPE;
+  if (!(keep >= 0.f && keep <= 3.4e38f)) return SPC_ERR_INVALID_ARG;
+  if (!mass_next || !aligned4(mass_next) || !aligned4(mass_prev) || (!mass_prev && keep != 0.f)) return SPC_ERR_INVALID_ARG;
+  if (T > 0 && (!lse || !aligned4(lse))) return SPC_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)n_q * d, mass = (int64_t)B * n_kv * cap * 4;
+  if (outputs_overlap({{mass_next, mass}, {workspace, (int64_t)need}, {mass_prev == mass_next ? nullptr : mass_prev, mass},
+                       {q, rows_span(T, q_stride, row)}, {lse, (int64_t)T * n_q * 4},
+                       {cache, (int64_t)num_blocks * block_size * n_kv * SPC_KV4_RECORD}, {block_table, (int64_t)B * max_blocks * 4},
+                       {len, B * 4}, {cu_seqlens, (B + 1) * 4}}, 2))
+    return SPC_ERR_INVALID_ARG;
+  c.lse = const_cast<float*>(lse); c.mass_prev = mass_prev; c.mass_next = mass_next; c.cap = cap; c.keep = keep;
+  return kv4_mass_launch(c, workspace, stream);
+}
+
+int spc_kv4_evict(void* cache, const int32_t* block_table, const int32_t* block_table_next, const int32_t* len,
+                  int32_t* len_next, const float* mass, float* mass_next, int32_t* kept, int32_t* status, int B, int n_kv,
+                  int d, int num_blocks, int block_size, int max_blocks, int cap, int budget, int n_sink, int n_recent,
+                  void* stream) {
+  if (!cache || !block_table || !block_table_next || !len || !len_next || !mass || !mass_next || !status)
+    return SPC_ERR_INVALID_ARG;
+  if (!aligned16(cache) || !aligned4(block_table) || !aligned4(block_table_next) || !aligned4(len) || !aligned4(len_next) ||
+      !aligned4(mass) || !aligned4(mass_next) || !aligned4(kept) || !aligned4(status))
+    return SPC_ERR_INVALID_ARG;
+  if (d != SPC_HEAD_DIM || B < 1 || B > SPC_MAX_BATCH || !pool_ok(num_blocks, block_size, n_kv) ||
+      !table_ok(max_blocks, block_size))
+    return SPC_ERR_SHAPE;
+  if (cap > SPC_MAX_CAP || cap < max_blocks * block_size) return SPC_ERR_SHAPE;
+  if (budget < 1 || budget > SPC_MAX_BUDGET || n_sink < 0 || n_recent < 0 || n_sink > budget || n_recent > budget - n_sink)
+    return SPC_ERR_SHAPE;
+  const int64_t sums = (int64_t)B * n_kv * cap * 4, table = (int64_t)B * max_blocks * 4;
+  if (outputs_overlap({{cache, (int64_t)num_blocks * block_size * n_kv * SPC_KV4_RECORD}, {len_next, B * 4}, {mass_next, sums},
+                       {kept, (int64_t)B * n_kv * budget * 4}, {status, 4}, {mass == mass_next ? nullptr : mass, sums},
+                       {block_table, table}, {block_table_next, table}, {len, B * 4}}, 5))
+    return SPC_ERR_INVALID_ARG;
+  if (block_table != block_table_next && overlap(block_table, table, block_table_next, table)) return SPC_ERR_INVALID_ARG;
+  Kv4EvictCall c{};
+  c.cache = static_cast<uint8_t*>(cache); c.table = block_table; c.table_next = block_table_next; c.len = len;
+  c.len_next = len_next; c.mass = mass; c.mass_next = mass_next; c.kept = kept; c.status = status;
+  c.B = B; c.n_kv = n_kv; c.num_blocks = num_blocks; c.block_shift = block_shift_of(block_size); c.max_blocks = max_blocks;
+  c.cap = cap; c.budget = budget; c.n_sink = n_sink; c.n_recent = n_recent;
+  return kv4_evict_launch(c, stream);
+}
+
 int spc_host_device_pointer(void* host_ptr, void** device_ptr) {
   if (!host_ptr || !device_ptr) return SPC_ERR_INVALID_ARG;
   void* p = nullptr;

@@ -200,6 +200,42 @@ struct PromptAttnCall {
 size_t prompt_attn_workspace(int T, int B, int n_q, int n_kv);
 int prompt_attn_launch(const PromptAttnCall& c, void* workspace, void* stream);
 
+// Chunks of new tokens over the paged 4-bit cache (kv4_chunk.cu), the weights
+// that its positions receive from them (kv4_mass.cu), and the eviction by those
+// (kv4_evict.cu).
+struct Kv4ChunkCall {
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int32_t* table;
+  const int32_t* len;
+  const int32_t* cu;
+  uint16_t* out;          // chunk attention
+  float* lse;             // chunk attention: written (may be null); mass: read
+  const float* mass_prev; // mass
+  float* mass_next;
+  int64_t q_stride;
+  int T, B, n_q, n_kv, num_blocks, block_shift, max_blocks, cap;
+  float scale, keep;
+};
+size_t kv4_chunk_workspace(int T, int B, int n_q, int n_kv);
+int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream);
+size_t kv4_mass_workspace(int T, int B, int n_q, int n_kv);
+int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream);
+
+struct Kv4EvictCall {
+  uint8_t* cache;
+  const int32_t* table;
+  const int32_t* table_next;
+  const int32_t* len;
+  int32_t* len_next;
+  const float* mass;
+  float* mass_next;
+  int32_t* kept;
+  int32_t* status;
+  int B, n_kv, num_blocks, block_shift, max_blocks, cap, budget, n_sink, n_recent;
+};
+int kv4_evict_launch(const Kv4EvictCall& c, void* stream);
+
 #ifdef SPC_TEST_HOOKS
 // Test builds only: whether the next launch of the two kernels above runs
 // starved (its copies are not issued), and the wait limit it then has.
