@@ -156,13 +156,14 @@ def _seen(cache, table_row, L, P):
 
 def chunk_attention(q, cache, table, lens, cu, scale):
     """New tokens q [T][n_q][d] (float64), request b's last cu[b + 1] - cu[b]
-    positions. Returns (out, bound, lse, err): bound = sum w |v| and err = the
-    largest sum |q k| scale of a row's logits; NaN in rows of no request."""
+    positions. Returns (out, bound, lse, err, vsum): bound = sum w |v|, err = the
+    largest sum |q k| scale of a row's logits, vsum = sum |v| of what a row sees;
+    NaN in rows of no request."""
     num_blocks, n_kv, bs, _ = cache.shape
     T, n_q, d = q.shape
     G = n_q // n_kv
     out, mag = np.full((T, n_q, d), np.nan), np.full((T, n_q, d), np.nan)
-    lse, err = np.full((T, n_q), np.nan), np.full((T, n_q), np.nan)
+    lse, err, vsum = np.full((T, n_q), np.nan), np.full((T, n_q), np.nan), np.full((T, n_q, d), np.nan)
     for b in range(len(lens)):
         L, n = max(0, min(int(lens[b]), table.shape[1] * bs)), cu[b + 1] - cu[b]
         for g in range(n_kv):
@@ -172,12 +173,12 @@ def chunk_attention(q, cache, table, lens, cu, scale):
                 m = int(np.searchsorted(pos, L - n + i, side="right"))
                 t, hs = cu[b] + i, slice(g * G, (g + 1) * G)
                 out[t, hs], mag[t, hs] = softmax_rows(q[t, hs], k[:m], v[:m], scale)
-                err[t, hs], lse[t, hs] = 0, -np.inf
+                err[t, hs], lse[t, hs], vsum[t, hs] = 0, -np.inf, np.abs(v[:m]).sum(0)
                 if m:
                     x = (q[t, hs] @ k[:m].T) * scale
                     lse[t, hs] = x.max(-1) + np.log(np.exp(x - x.max(-1, keepdims=True)).sum(-1))
                     err[t, hs] = (np.abs(q[t, hs]) @ np.abs(k[:m]).T).max(-1) * scale
-    return out, mag, lse, err
+    return out, mag, lse, err, vsum
 
 
 def attn_mass(q, cache, table, lens, cu, lse, prev, keep, cap, scale):

@@ -1,58 +1,909 @@
-// Attention of chunks of new tokens over the paged 4-bit cache:
-// out_i = sum_{p <= P_i} softmax_p(scale q_i.K_p) V_p, P_i = len - n + i.
-// One warp a (row, query head), one position at a time.
+// Attention of chunks of new tokens over the paged 4-bit cache, on the
+// 5th-generation tensor cores: out_i = sum_{p <= P_i} softmax_p(scale q_i.K_p) V_p,
+// P_i = len - n + i, and lse_i.
+//
+// Rows are (token, query head of the group) pairs: a 128-row tile holds 128/G
+// tokens x G heads of one KV head, so that a record that is dequantised serves
+// the whole group. An item is two such tiles (A and B, consecutive tokens) of one
+// (request, KV head) against that head's positions in blocks of 128:
+//   S[128][128] = Q K^T     Q, K in shared memory (128-byte swizzle)
+//   O[128][128] += P V      P in tensor memory over S's columns, V MN-major
+// The tensor cores work on one tile while the other one's softmax runs. A
+// request's last tile, if it has no partner (and with few new tokens it is the
+// only one), takes both places: A runs over the even blocks and B over the odd
+// ones, and their results are merged.
+//
+// Operands are fp16. A record's values are exact there; 11 bits of P instead of
+// bf16's 8; and e2m1 to fp16 is one conversion for two values. Queries are scaled
+// by a power of two a row (the largest to [2^14, 2^15): a value loses bits only
+// below 2^-28 of it), in place, by the softmax thread of the row. P and its sum
+// are kept 2^11 times the weights against the running maximum, the top of fp16's
+// range, so that weights keep 11 bits down to 2^-25 of the largest and are off by
+// 2^-36 of it below; the maximum (of the products q.K, before the scale, so that
+// a large logit's own rounding cannot pass the range) is raised when a logit
+// passes it by more than 4.75 in base 2, and only then is the row of O rescaled.
+// Sums, maxima, S and O are fp32; a weight's sum is that of the unrounded values.
+//
+// What a row does not see does not reach it. Masked columns of S are replaced. V
+// meets their weight of zero, which a value that is not finite would defeat:
+// records that are not there are zeros, and a V scale that is NaN (the only such
+// value a record can hold) is taken as zero in the product while the first
+// position that has it is noted for its 16 dims; rows at or behind that position
+// get NaN there.
+//
+// Work: the items' blocks (and one unit for an item's fixed part) form a line
+// that is cut into equal runs, one a CTA (persistent, one per SM). An item that
+// is cut, or whose tile took both places, leaves partials (O, maximum, sum) in
+// the workspace; of the warps that have the same 32 rows in their pieces the last
+// to arrive merges them, in the order of the positions, so that the result does
+// not depend on the order of arrival.
+//   warps 0-3, 4-7  softmax and epilogue of tile A, B
+//   warps 8-11      dequantisation into a ring of three 32 KB operands: K_j, V_j, K_j+1, ...
+//   warp 12         tensor memory, MMA issue
+//   warp 13         schedule, copies of the records (cp.async.bulk, one a cache block)
+//   warp 14         Q loads (TMA)
+// Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
+// and leaves, the others' waits then give up in turn; copies land and MMAs
+// complete before the CTA releases its tensor memory.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "kv4.cuh"
-#include "spc_device.cuh"
-#include "spc_internal.h"
+#include <climits>
+#include <type_traits>
+
+#include "kv4_attn.cuh"
+#include "kv4_chunk.cuh"
+#include "spc_tc.cuh"
 
 namespace spc {
 
-__global__ void __launch_bounds__(256) kv4_chunk_kernel(const Kv4ChunkCall c) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(w / c.n_q), h = (int)(w - (long long)t * c.n_q), g = h / (c.n_q / c.n_kv);
-  if (t >= c.T) return;
-  int b = 0;
-  while (b < c.B && !(t >= c.cu[b] && t < c.cu[b + 1])) ++b;
-  if (b == c.B) return;
-  const int L = max(0, min(c.len[b], c.max_blocks << c.block_shift)), P = L - (c.cu[b + 1] - t);
-  const uint2 qw = *reinterpret_cast<const uint2*>(c.q + t * c.q_stride + (size_t)h * kD + 4 * lane);
-  const float q[4] = {bf_lo(qw.x), bf_hi(qw.x), bf_lo(qw.y), bf_hi(qw.y)};
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  bool any = false;
-  for (int p = 0; p <= P; ++p) {
-    const int blk = c.table[(size_t)b * c.max_blocks + (p >> c.block_shift)];
-    if ((unsigned)blk >= (unsigned)c.num_blocks) continue;
-    const int bs = 1 << c.block_shift;
-    const uint8_t* r = c.cache + (((size_t)blk * c.n_kv + g) * bs + (p & (bs - 1))) * kKv4Rec;
-    uint32_t k[4], v[4];
-    e2m1x8_to_f16(*reinterpret_cast<const uint16_t*>(r + 2 * lane), k);
-    e2m1x8_to_f16(*reinterpret_cast<const uint16_t*>(r + kKv4V + 2 * lane), v);
-    const float ks = f16_lo(e4m3_dup_f16(r[kKv4Scale + lane / 4])), vs = f16_lo(e4m3_dup_f16(r[kKv4Scale + 8 + lane / 4]));
-    const float x = warp_sum(q[0] * (f16_lo(k[0]) * ks) + q[1] * (f16_hi(k[0]) * ks) + q[2] * (f16_lo(k[1]) * ks) +
-                             q[3] * (f16_hi(k[1]) * ks)) * c.scale * kLog2e;
-    any = true;
-    const float M = fmaxf(m, x), al = m == M ? 1.f : exp2f(m - M), e = exp2f(x - M);
-    m = M;
-    l = l * al + e;
-    o[0] = o[0] * al + e * (f16_lo(v[0]) * vs);
-    o[1] = o[1] * al + e * (f16_hi(v[0]) * vs);
-    o[2] = o[2] * al + e * (f16_lo(v[1]) * vs);
-    o[3] = o[3] * al + e * (f16_hi(v[1]) * vs);
-  }
-  const float r = any ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(c.out + ((size_t)t * c.n_q + h) * kD + 4 * lane) =
-      make_uint2(pack_bf16(o[0] * r, o[1] * r), pack_bf16(o[2] * r, o[3] * r));
-  if (c.lse && lane == 0) c.lse[(size_t)t * c.n_q + h] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
+constexpr int kKcRaw = 7;                             // stages of records, 64 positions each
+constexpr int kKcSlots = 3;                           // ring of dequantised operands
+constexpr int kKcItems = 2;                           // item ring
+constexpr int kKcMasks = 8;                           // blocks whose masks are kept: the copies are at most 5 ahead of the softmax
+constexpr int kKcWarpDeq = 8, kKcWarpMma = 12, kKcWarpCopy = 13, kKcWarpQ = 14;
+constexpr int kKcThreads = 512;
+// registers a thread: 128 at launch (512 threads); softmax 176 (two warpgroups),
+// dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128
+constexpr int kKcRegSoft = 176, kKcRegDeq = 88, kKcRegRest = 72;
+constexpr float kKcBias = 11.f;                       // log2 of the factor of the weights
+constexpr float kKcHeadroom = 4.75f;                  // log2 growth allowed before a maximum is raised
+constexpr int kKcFixed = 1;                           // units of an item's fixed part
+constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
+constexpr uint32_t kKcColO = 256;
+constexpr uint32_t kKcIdescS = (1u << 4) | ((uint32_t)(kKcKeys >> 3) << 17) | (8u << 24);
+constexpr uint32_t kKcIdescO = kKcIdescS | (1u << 16);
+constexpr uint32_t kKcDescVLo = umma_mn_lo(kKcBlock);
+
+// shared memory, from a 1024-byte aligned base
+constexpr uint32_t kKcOffQ = 0;                                       // [2] tiles
+constexpr uint32_t kKcOffKv = kKcOffQ + 2 * kKcTile;
+constexpr uint32_t kKcOffRaw = kKcOffKv + kKcSlots * kKcTile;
+constexpr uint32_t kKcOffItem = kKcOffRaw + kKcRaw * kKcStage;        // [kKcItems] KcItem
+constexpr uint32_t kKcOffNan = kKcOffItem + kKcItems * 64;            // [kKcItems][8] first position with a NaN V scale
+constexpr uint32_t kKcOffMask = kKcOffNan + kKcItems * 32;            // [kKcMasks][4 words]
+constexpr uint32_t kKcOffBar = kKcOffMask + kKcMasks * 16;
+constexpr int kKcBars = 2 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 1;
+constexpr size_t kKcSmem = 1024 + kKcOffBar + kKcBars * 8 + 16;
+static_assert(kKcSmem <= 227 * 1024, "shared memory of one CTA");
+
+// workspace: status; arrival counters (zero between calls), a warp's rows each,
+// per CTA of the items that are cut first there and of two whole items in turn;
+// partials, per CTA of its first and last piece and of two whole items, two tiles each
+constexpr size_t kKcOffCount = 256;
+constexpr size_t kKcOffPart = kKcOffCount + (size_t)kKcCtas * 3 * 8 * 4 + 256;
+constexpr int kKcPart = kD + 4;                       // a row's partial: O[128], m, l
+static_assert(kKcOffPart % 256 == 0, "aligned partials");
+
+struct KcArgs {
+  Kv4ChunkCall c;
+  int G, gshift, tpm;      // heads a group, its log2, tokens a tile
+  int part_rows;           // rows of a tile that can be new tokens'
+  int* status;
+  uint32_t* counters;
+  float* part;
+  long long wait_limit;
+  int starve;              // test builds: no copy is issued, so that every wait runs out
+};
+
+struct KcItem {
+  int row0, n;             // the request's first row and new tokens; n < 0: no more items
+  int len, g, t0;          // its positions, KV head, first token of tile A
+  int j0, j1;              // the piece's blocks
+  int n0, n1;              // how many of them tile A and B take
+  int single;              // one tile in both places
+  int pieces, piece, first;  // of the item, and its first CTA
+  int direct;              // nothing to merge
+  int pad[2];
+};
+static_assert(sizeof(KcItem) == 64, "item ring");
+
+__device__ __forceinline__ bool kc_wait(const KcArgs& a, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
 }
 
-size_t kv4_chunk_workspace(int, int, int, int) { return 256; }
+// 32 products of a row: weights 2^((s - m) f + bias) to 16 packed columns, and their sum
+__device__ __forceinline__ void kc_weights(const float* s, float f, float m, float2 (&sum)[2], uint32_t tp) {
+  const float2 nm = make_float2(-m, -m), ff = make_float2(f, f), bias = make_float2(kKcBias, kKcBias);
+  uint32_t p[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float2 x = fma2(add2(make_float2(s[2 * e], s[2 * e + 1]), nm), ff, bias);
+    x.x = ex2_approx(x.x);
+    x.y = ex2_approx(x.y);
+    sum[e & 1] = add2(sum[e & 1], x);
+    p[e] = pack_f16(x.x, x.y);
+  }
+  tmem_st16(tp, p);
+}
 
-int kv4_chunk_launch(const Kv4ChunkCall& c, void*, void* stream) {
-  const long long blocks = ((long long)c.T * c.n_q + 7) / 8;
-  kv4_chunk_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(c);
+// A row of 128 values of 64 bytes of codes (in shared memory) and 8 scales into
+// row r of a swizzled tile; zeros where there is no record.
+__device__ __forceinline__ void kc_row(uint32_t codes, uint2 sc, uint32_t tile, int r, bool there) {
+  const uint32_t dst = tile + (uint32_t)r * 128u, r7 = (uint32_t)r & 7u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 w = there ? lds_v4(codes + 16 * q) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t s2 = e4m3x2_to_f16(((q < 2 ? sc.x : sc.y) >> (16 * (q & 1))) & 0xffffu);
+    const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t h[4];
+      e2m1x8_to_f16(ww[e], h);
+      const uint32_t u = 4 * q + e;
+      sts_v4(dst + (u >> 3) * kKcBlock + (((u & 7u) ^ r7) << 4), hmul2(h[0], s[e >> 1]), hmul2(h[1], s[e >> 1]),
+             hmul2(h[2], s[e >> 1]), hmul2(h[3], s[e >> 1]));
+    }
+  }
+}
+
+// A row of queries, bf16 to fp16 times a power of two, in place; returns the
+// power's inverse. A row that is not finite becomes NaN: whatever it sees, its
+// softmax has no value.
+__device__ __forceinline__ float kc_query(uint32_t tile, int r) {
+  uint4 w[16];
+  uint32_t mx = 0u;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    w[u] = lds_v4(tile + (uint32_t)r * 128u + (u >> 3) * kKcBlock + (u & 7) * 16);
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu),
+                               __vmaxu2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu)));
+  }
+  const int E = (int)(max(mx & 0xffffu, mx >> 16) >> 7);       // exponent field of the largest
+  const bool odd = E == 255;
+  const int e = min(141 - E, 126);
+  const float up = __int_as_float((e + 127) << 23);
+  auto f16 = [&](uint32_t x) { return odd ? 0x7fff7fffu : pack_f16(bf_lo(x) * up, bf_hi(x) * up); };
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    sts_v4(tile + (uint32_t)r * 128u + (u >> 3) * kKcBlock + (u & 7) * 16, f16(w[u].x), f16(w[u].y), f16(w[u].z), f16(w[u].w));
+  return __int_as_float((127 - e) << 23);
+}
+
+// ---------------------------------------------------------------- the line of work
+// Pairs of tiles of a request: pair i holds tokens [i t, (i + 1) t), t = 2 tpm,
+// and sees ceil((ctx + (i + 1) t) / 128) blocks, ctx = len - n, at least one.
+struct KcShape {
+  int ctx, n, lt, pairs;   // lt: log2 of t
+};
+__device__ __forceinline__ int kc_blocks(const KcShape& s, int i) {
+  return max(1, (s.ctx + min(s.n, (i + 1) << s.lt) + kKcKeys - 1) >> 7);
+}
+// units of the pairs below k <= pairs - 1, all of them whole
+__device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
+  const int lt = s.lt;
+  // the first ones see one block (or nothing), from i0 on the sum of an arithmetic progression's quotients
+  const int i0 = max(0, min(k, (kKcKeys - s.ctx) >> lt)), m = k - i0;
+  long long u = (long long)k * kKcFixed + i0;
+  if (m == 0) return u;
+  const int c = s.ctx + (i0 << lt);
+  if (lt >= 7) return u + (long long)m * ((c + 127) >> 7) + ((long long)m * (m + 1) / 2 << (lt - 7));
+  const int ls = 7 - lt, w = (1 << ls) - 1 + ((c & ((1 << lt) - 1)) > 0 ? 1 : 0);
+  const long long a = (c >> lt) + w;                  // sum of floor((a + i) / 2^ls), i = 1 .. m
+  auto below = [&](long long x) {                     // sum of floor(j / 2^ls), j = 0 .. x
+    const long long q = (x + 1) >> ls, r = (x + 1) & ((1 << ls) - 1);
+    return (q * (q - 1) / 2 << ls) + r * q;
+  };
+  return u + below(a + m) - below(a);
+}
+// tiles of a request, and whether its pair i has one alone
+__device__ __forceinline__ int kc_tiles(const KcShape& s) { return (s.n + (1 << (s.lt - 1)) - 1) >> (s.lt - 1); }
+__device__ __forceinline__ int kc_item_units(const KcShape& s, int i) {
+  const int nb = kc_blocks(s, i);
+  return 2 * i + 2 > kc_tiles(s) ? (nb + 1) >> 1 : nb;
+}
+
+// The partials of a warp's 32 rows merged by the last of their pieces' warps.
+// Every lane has its own row's factor and inverse query scale.
+__device__ void kc_merge(const KcArgs& a, const KcItem& x, int slot0, int i, int w, int live, float f, float inv, int token,
+                         int h) {
+  const Kv4ChunkCall& c = a.c;
+  const int lane = threadIdx.x & 31, places = x.single ? 2 : 1, n = x.pieces * places;
+  auto part = [&](int k, int row) {                   // contribution k, in the order of the pieces
+    const int p = x.single ? k >> 1 : k, tile = x.single ? k & 1 : i;
+    const int cta = x.first + p, slot = x.pieces == 1 ? slot0 : p == 0 ? 1 : 0;
+    return a.part + ((((size_t)cta * 4 + slot) * 2 + tile) * a.part_rows + row) * kKcPart;
+  };
+  const int row = w * 32 + lane;
+  float M = -INFINITY, l = 0.f;
+  if (lane < live)
+    for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(part(k, row) + kD));
+  if (lane < live)
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(k, row) + kD));
+      if (ml.y != 0.f) l += ml.y * ex2_approx((ml.x - M) * f);
+    }
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  if (lane < live && c.lse)
+    c.lse[(size_t)(x.row0 + token) * c.n_q + h] =
+        l == 0.f ? -INFINITY : M * inv * c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
+  for (int rr = 0; rr < live; ++rr) {
+    const float Mr = __shfl_sync(0xffffffffu, M, rr), fr = __shfl_sync(0xffffffffu, f, rr), nr = __shfl_sync(0xffffffffu, r, rr);
+    const int tok = __shfl_sync(0xffffffffu, token, rr), hh = __shfl_sync(0xffffffffu, h, rr);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 4;
+    for (int k0 = 0; k0 < n; k0 += U) {
+      float2 ml[U];
+      float4 v[U];
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        ml[e] = make_float2(0.f, 0.f);
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + e < n) {
+          const float* p = part(k0 + e, w * 32 + rr);
+          ml[e] = __ldcg(reinterpret_cast<const float2*>(p + kD));
+          v[e] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        if (ml[e].y == 0.f) continue;                 // no position seen: O was not written
+        const float wt = ex2_approx((ml[e].x - Mr) * fr) * nr;
+        o[0] += wt * v[e].x;
+        o[1] += wt * v[e].y;
+        o[2] += wt * v[e].z;
+        o[3] += wt * v[e].w;
+      }
+    }
+    *reinterpret_cast<uint2*>(c.out + ((size_t)(x.row0 + tok) * c.n_q + hh) * kD + 4 * lane) =
+        make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+  }
+}
+
+__global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const KcArgs a) {
+  extern __shared__ uint8_t kc_raw[];
+  const uint32_t raw_addr = smem_u32(kc_raw);
+  uint8_t* base = kc_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  KcItem* items = reinterpret_cast<KcItem*>(base + kKcOffItem);
+  int* nans = reinterpret_cast<int*>(base + kKcOffNan);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(base + kKcOffMask);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kKcOffBar);
+  uint64_t* rfull = bars;                     // [kKcRaw] bytes of the records
+  uint64_t* rfree = rfull + kKcRaw;           // [kKcRaw] two dequantising warps have read them
+  uint64_t* kvfull = rfree + kKcRaw;          // [kKcSlots] four dequantising warps have written the operand
+  uint64_t* kvfree = kvfull + kKcSlots;       // [kKcSlots] commit after the last MMA that reads it
+  uint64_t* ifull = kvfree + kKcSlots;        // [kKcItems] item written
+  uint64_t* ifree = ifull + kKcItems;         // [kKcItems] every role has read it, the softmax warps are done with it
+  uint64_t* qfull = ifree + kKcItems;         // [2] TMA bytes
+  uint64_t* qready = qfull + 2;               // [2] four softmax warps have converted the tile
+  uint64_t* qfree = qready + 2;               // [2] commit after the tile's last S
+  uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
+  uint64_t* pfull = sfull + 2;                // [2] four softmax warps: P written, O rescaled
+  uint64_t* ofull = pfull + 2;                // [2] commit: the piece's last PV done
+  uint64_t* drain = ofull + 2;                // commit after the last MMA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const Kv4ChunkCall& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKcRaw; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rfree[s], 2);
+    }
+    for (int s = 0; s < kKcSlots; ++s) {
+      mbar_init(&kvfull[s], 4);
+      mbar_init(&kvfree[s], 1);
+    }
+    for (int s = 0; s < kKcItems; ++s) {
+      mbar_init(&ifull[s], 1);
+      mbar_init(&ifree[s], 4 + 8 + 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qready[s], 4);
+      mbar_init(&qfree[s], 1);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pfull[s], 4);
+      mbar_init(&ofull[s], 1);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kKcWarpMma) tmem_alloc<kKcTmemCols>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t qs = smem_u32(base + kKcOffQ), kvs = smem_u32(base + kKcOffKv);
+  bool dead = false;
+  auto acquire = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !kc_wait(a, bar, parity)) {
+      if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+      dead = true;
+    }
+  };
+
+  if (warp == kKcWarpCopy) {
+    // ================= schedule and copies of the records
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    KcRequests rq;
+    kc_requests(c, rq);
+    const int lt = 8 - a.gshift;                      // log2 of the tokens a pair
+    auto shape = [&](int len, int n) {
+      KcShape s;
+      s.ctx = len - n;
+      s.n = n;
+      s.lt = lt;
+      s.pairs = (n + (1 << lt) - 1) >> lt;
+      return s;
+    };
+    auto units = [&](const KcShape& s) {              // of one KV head
+      return s.n == 0 ? 0ll : kc_units(s, s.pairs - 1) + kKcFixed + kc_item_units(s, s.pairs - 1);
+    };
+    long long own[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) own[e] = units(shape(rq.len[e], rq.n[e]));
+    const long long total = kc_prefix(rq, own[0] * c.n_kv, own[1] * c.n_kv);
+    const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    const bool has = (int)blockIdx.x < ctas;
+    const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
+    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+    // the item at u0: request b, head g, pair i; `at` is its first unit
+    int b = 0, g = 0, i = 0, nb = 0;
+    long long at = 0, whole = 1;
+    KcShape s = shape(0, 0);
+    auto enter = [&](int request) {                   // its shape and units a head
+      b = request;
+      s = shape(kc_of(rq.len, b), kc_of(rq.n, b));
+      whole = __shfl_sync(0xffffffffu, b & 1 ? own[1] : own[0], b >> 1);
+    };
+    if (has) {
+      enter(kc_find(rq, u0));
+      long long r = u0 - (kc_of(rq.end, b) - whole * c.n_kv);
+      g = (int)(r / whole);
+      r -= (long long)g * whole;
+      int lo = 0, hi = s.pairs;                       // units(lo) <= r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (kc_units(s, mid) <= r) lo = mid; else hi = mid;
+      }
+      i = lo;
+      at = u0 - r + kc_units(s, i);
+    }
+    int it = 0, blocks = 0, nraw = 0;
+    for (;; ) {
+      KcItem x;
+      x.n = -1;
+      bool skip = false;
+      if (has && at < u1 && !dead) {
+        const int nu = kc_item_units(s, i);
+        nb = kc_blocks(s, i);
+        const long long first = at + kKcFixed;        // its first block's unit
+        const int lo = (int)max(0ll, u0 - first), hi = (int)min((long long)nu, u1 - first);
+        skip = hi <= lo;                              // only its fixed part is here
+        if (!skip) {
+          x.row0 = kc_of(rq.row0, b);
+          x.n = s.n;
+          x.len = s.ctx + s.n;
+          x.g = g;
+          x.t0 = i << lt;
+          x.single = 2 * i + 2 > kc_tiles(s);
+          x.j0 = x.single ? 2 * lo : lo;
+          x.j1 = x.single ? min(nb, 2 * hi) : hi;
+          if (x.single) {
+            x.n0 = (x.j1 - x.j0 + 1) >> 1;
+            x.n1 = (x.j1 - x.j0) >> 1;
+          } else {
+            // tile A sees the blocks up to its own last token
+            const int na = max(1, (s.ctx + min(s.n, x.t0 + a.tpm) + kKcKeys - 1) >> 7);
+            x.n0 = max(0, min(x.j1, na) - x.j0);
+            x.n1 = x.j1 - x.j0;
+          }
+          x.first = cta_of(first);
+          x.pieces = cta_of(first + nu - 1) - x.first + 1;
+          x.piece = (int)blockIdx.x - x.first;
+          x.direct = x.pieces == 1 && (!x.single || x.n1 == 0);
+        }
+      }
+      if (!skip) {
+        const int is = it % kKcItems;
+        acquire(&ifree[is], ((it / kKcItems) & 1) ^ 1);
+        if (lane == 0) items[is] = x;
+        if (lane < 8) nans[is * 8 + lane] = INT_MAX;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ifull[is]);
+        ++it;
+        if (x.n < 0) break;
+#ifdef SPC_TEST_HOOKS
+        if (a.starve) break;
+#endif
+        KcTable t;
+        t.start(c.table + (size_t)b * c.max_blocks, (x.len + (1 << c.block_shift) - 1) >> c.block_shift,
+                x.j0 * kKcKeys >> c.block_shift);
+        for (int j = x.j0; j < x.j1; ++j, ++blocks) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h, ++nraw) {
+            acquire(&rfree[nraw % kKcRaw], ((nraw / kKcRaw) & 1) ^ 1);
+            if (dead) break;
+            kc_copy(c, t, x.g, x.len, j * kKcKeys + h * kKcHalf, base + kKcOffRaw + (nraw % kKcRaw) * kKcStage,
+                    &rfull[nraw % kKcRaw], masks + (blocks % kKcMasks) * 4 + 2 * h);
+          }
+          if (dead) break;
+        }
+      }
+      // the next item
+      at += kKcFixed + kc_item_units(s, i);
+      if (++i == s.pairs) {
+        i = 0;
+        if (++g == c.n_kv) {
+          g = 0;
+          if (at < u1) enter(kc_find(rq, at));
+        }
+      }
+    }
+    // every copy lands before the CTA ends (they have, unless a role gave up)
+    if (lane == 0)
+      for (int k = max(0, nraw - kKcRaw); k < nraw; ++k) mbar_wait_bounded(&rfull[k % kKcRaw], (k / kKcRaw) & 1, a.wait_limit);
+    __syncwarp();
+  } else if (warp == kKcWarpQ) {
+    // ================= queries
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    int nq[2] = {0, 0};
+    for (int it = 0;; ++it) {
+      const int is = it % kKcItems;
+      acquire(&ifull[is], (it / kKcItems) & 1);
+      if (dead) break;
+      const int n = items[is].n, n0 = items[is].n0, n1 = items[is].n1, row = items[is].row0 + items[is].t0, g = items[is].g;
+      const int single = items[is].single;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (n < 0) break;
+#ifdef SPC_TEST_HOOKS
+      if (a.starve) break;
+#endif
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        if ((i ? n1 : n0) == 0) continue;
+        acquire(&qfree[i], (nq[i] & 1) ^ 1);
+        if (dead) break;
+        ++nq[i];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&qfull[i], kKcTile);
+          const int r = row + (single ? 0 : i * a.tpm);
+          tma_load_3d(qs + i * kKcTile, &qmap, 0, g << a.gshift, r, &qfull[i]);
+          tma_load_3d(qs + i * kKcTile + kKcBlock, &qmap, 64, g << a.gshift, r, &qfull[i]);
+        }
+        __syncwarp();
+      }
+      if (dead) break;
+    }
+    if (lane == 0)
+      for (int i = 0; i < 2; ++i)
+        if (nq[i] > 0) mbar_wait_bounded(&qfull[i], (nq[i] - 1) & 1, a.wait_limit);
+    __syncwarp();
+  } else if (warp == kKcWarpMma) {
+    // ================= MMA issue; the whole warp runs the loop, so that its values stay warp-uniform
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+    auto full = [&](int k) {                          // operand k has been written
+      acquire(&kvfull[k % kKcSlots], (k / kKcSlots) & 1);
+    };
+    // S of tile i against operand k; first: of the piece, last: no further one. `done`: nothing else reads k
+    auto issue_s = [&](auto tile, int k, bool first, bool last, bool done) {
+      constexpr int i = decltype(tile)::value;
+      if (first) acquire(&qready[i], nq[i]++ & 1);
+      if (dead) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t qd = umma_desc_lo(qs + i * kKcTile), kd = umma_desc_lo(kvs) + (uint32_t)(k % kKcSlots) * (kKcTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * (kKcBlock >> 4) + (uint32_t)(kk & 3) * 2;
+          umma_f16(tm + i * kKcKeys, umma_desc(qd + off), umma_desc(kd + off), kKcIdescS, kk ? 1u : 0u);
+        }
+        umma_commit(&sfull[i]);
+        if (last) umma_commit(&qfree[i]);
+        if (done) umma_commit(&kvfree[k % kKcSlots]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](auto tile, int k, bool first, bool last, bool done) {
+      constexpr int i = decltype(tile)::value;
+      if (!__all_sync(0xffffffffu, mbar_test(&pfull[i], np[i] & 1))) acquire(&pfull[i], np[i] & 1);
+      ++np[i];
+      if (dead) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t vd = umma_desc_lo(kvs) + (uint32_t)(k % kKcSlots) * (kKcTile >> 4) + kKcDescVLo;
+#pragma unroll
+        for (int kk = 0; kk < kKcKeys / 16; ++kk)
+          umma_f16_tmem_a(tm + kKcColO + i * kD, tm + i * kKcKeys + kk * 8, umma_desc(vd + (uint32_t)kk * 128), kKcIdescO,
+                          kk ? 1u : (first ? 0u : 1u));
+        if (done) umma_commit(&kvfree[k % kKcSlots]);
+        if (last) umma_commit(&ofull[i]);
+      }
+      __syncwarp();
+    };
+    constexpr std::integral_constant<int, 0> tA{};
+    constexpr std::integral_constant<int, 1> tB{};
+    for (int it = 0;; ++it) {
+      const int is = it % kKcItems;
+      acquire(&ifull[is], (it / kKcItems) & 1);
+      if (dead) break;
+      const int n = items[is].n, n0 = items[is].n0, n1 = items[is].n1, nb = items[is].j1 - items[is].j0;
+      const int single = items[is].single;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (n < 0) break;
+      // operand kv + 2 k is K of the piece's block k, kv + 2 k + 1 its V
+      full(kv);
+      if (single) {
+        issue_s(tA, kv, true, n0 == 1, true);
+        if (n1) {
+          full(kv + 2);
+          issue_s(tB, kv + 2, true, n1 == 1, true);
+        }
+#pragma unroll 1
+        for (int k = 0; k < nb && !dead; k += 2) {
+          full(kv + 2 * k + 1);
+          issue_pv(tA, kv + 2 * k + 1, k == 0, k + 2 >= nb, true);
+          if (k + 1 < nb) {
+            full(kv + 2 * k + 3);
+            issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
+          }
+          if (k + 2 < nb) {
+            full(kv + 2 * k + 4);
+            issue_s(tA, kv + 2 * k + 4, false, k + 4 >= nb, true);
+          }
+          if (k + 3 < nb) {
+            full(kv + 2 * k + 6);
+            issue_s(tB, kv + 2 * k + 6, false, k + 5 >= nb, true);
+          }
+        }
+      } else {
+        if (n0) issue_s(tA, kv, true, n0 == 1, n1 == 0);
+        if (n1) issue_s(tB, kv, true, n1 == 1, true);
+#pragma unroll 1
+        for (int k = 0; k < nb && !dead; ++k) {
+          const int v = kv + 2 * k + 1;
+          full(v);
+          if (k < n0) issue_pv(tA, v, k == 0, k + 1 == n0, k >= n1);
+          if (k + 1 < nb) full(v + 1);
+          if (k + 1 < n0) issue_s(tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
+          if (k < n1) issue_pv(tB, v, k == 0, k + 1 == n1, true);
+          if (k + 1 < n1) issue_s(tB, v + 1, false, k + 2 == n1, true);
+        }
+      }
+      kv += 2 * nb;
+      if (dead) break;
+    }
+    // tensor memory is released below: every MMA has completed (the softmax
+    // warps wait for each piece's last one, unless something gave up)
+    if (elect_one()) umma_commit(drain);
+    __syncwarp();
+    kc_wait(a, drain, 0);
+  } else if (warp >= kKcWarpDeq && warp < kKcWarpDeq + 4) {
+    // ================= dequantisation, a record a thread
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegDeq));
+    const int r = threadIdx.x & 127, h = r >> 6;
+    int blocks = 0, kv = 0;
+    for (int it = 0;; ++it) {
+      const int is = it % kKcItems;
+      acquire(&ifull[is], (it / kKcItems) & 1);
+      if (dead) break;
+      const int n = items[is].n, j0 = items[is].j0, j1 = items[is].j1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (n < 0) break;
+      for (int j = j0; j < j1; ++j, ++blocks) {
+        const int raw = 2 * blocks + h, st = raw % kKcRaw;
+        acquire(&rfull[st], (raw / kKcRaw) & 1);
+        if (dead) break;
+        const uint32_t rec = smem_u32(base + kKcOffRaw) + (uint32_t)st * kKcStage + (uint32_t)(r & 63) * kKv4Rec;
+        const bool there = masks[(blocks % kKcMasks) * 4 + (r >> 5)] >> lane & 1;
+#pragma unroll
+        for (int part = 0; part < 2; ++part, ++kv) {  // K, then V
+          const int slot = kv % kKcSlots;
+          acquire(&kvfree[slot], ((kv / kKcSlots) & 1) ^ 1);
+          if (dead) break;
+          uint2 sc = there ? lds_v2(rec + kKv4Scale + 8 * part) : make_uint2(0u, 0u);
+          if (part) {
+            // scales of V that are NaN: noted, and zero in the product
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint32_t& x = w ? sc.y : sc.x;
+              const uint32_t bad = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (bad) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (bad >> (8 * e + 7) & 1) {
+                    atomicMin(&nans[is * 8 + 4 * w + e], j * kKcKeys + r);
+                    x &= ~(0xffu << (8 * e));
+                  }
+              }
+            }
+          }
+          kc_row(rec + (part ? kKv4V : 0), sc, kvs + (uint32_t)slot * kKcTile, r, there);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&kvfull[slot]);
+            if (part) mbar_arrive(&rfree[st]);
+          }
+        }
+        if (dead) break;
+      }
+      if (dead) break;
+    }
+  } else if (warp < kKcWarpDeq) {
+    // ================= softmax and epilogue of tile i, one row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kKcRegSoft));
+    const int i = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * kKcKeys, to = tmem + lanes + kKcColO + i * kD;
+    int n_q = 0, n_s = 0, n_o = 0, blocks = 0;
+    for (int it = 0;; ++it) {
+      const int is = it % kKcItems;
+      acquire(&ifull[is], (it / kKcItems) & 1);
+      if (dead) break;
+      const KcItem x = items[is];
+      if (x.n < 0) break;
+      const int n = i ? x.n1 : x.n0, t0 = x.t0 + (x.single ? 0 : i * a.tpm);
+      const int token = t0 + (row >> a.gshift), qpos = x.len - x.n + token, qpos0 = x.len - x.n + t0;
+      const int hq = (x.g << a.gshift) + (row & (a.G - 1));
+      float m = -INFINITY, l = 0.f, inv = 1.f;
+      if (n > 0) {
+        acquire(&qfull[i], n_q & 1);
+        if (dead) break;
+        ++n_q;
+        inv = kc_query(qs + i * kKcTile, row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qready[i]);
+      } else if (!x.direct) {
+        // a piece without a block of this tile's: the rows' factors, for the merge
+        const int t = min(x.row0 + token, c.T - 1);
+        uint32_t mx = 0u;
+        for (int u = 0; u < 16; ++u) {
+          const uint4 w = *reinterpret_cast<const uint4*>(c.q + t * c.q_stride + (size_t)hq * kD + 8 * u);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                     __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+        inv = __int_as_float((127 - min(141 - (int)(max(mx & 0xffffu, mx >> 16) >> 7), 126)) << 23);
+      }
+      const float f = k4_factor(inv * c.scale * kLog2e);
+      for (int k = 0; k < n; ++k) {
+        const int j = x.single ? x.j0 + 2 * k + i : x.j0 + k;
+        acquire(&sfull[i], n_s & 1);
+        if (dead) break;
+        tc_fence_after();
+        const uint4 mask = *reinterpret_cast<const uint4*>(masks + ((blocks + j - x.j0) % kKcMasks) * 4);
+        const bool there = (mask.x & mask.y & mask.z & mask.w) == 0xffffffffu;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // raises the row's maximum to M where that is needed
+        auto raise = [&](float M) {
+          float alpha = 1.f;
+          const bool up = (M - m) * f > kKcHeadroom;
+          if (up) {
+            alpha = m == -INFINITY ? 0.f : ex2_approx((m - M) * f);
+            l *= alpha;
+            m = M;
+          }
+          if (k > 0 && __any_sync(0xffffffffu, up)) {
+            // O holds earlier blocks; their PV is done, for this block's S was
+            // issued behind it and the commit it came with covers both
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+              float o[16];
+              tmem_ld16(to + 16 * q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha;
+              tmem_st16(to + 16 * q, o);
+            }
+          }
+        };
+        if (there && (j + 1) * kKcKeys <= qpos0 + 1 && !__any_sync(0xffffffffu, m == -INFINITY)) {
+          // every row sees the whole block and has a maximum: weights against
+          // it at once, while the block's own maximum is being found
+          float s[128];
+          tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait32(s + 32 * q);
+            if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
+            max32(s + 32 * q, mx);
+            kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
+          }
+          const float M = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          if (__any_sync(0xffffffffu, (M - m) * f > kKcHeadroom)) {
+            // the weights go to the same columns again, and stores to tensor
+            // memory are asynchronous: the first ones have to be there
+            tmem_st_wait();
+            raise(M);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
+          }
+        } else {
+          // a piece's first block, a block with an end or a gap in it, and the
+          // last ones: S is read twice, in chunks of 32 columns, without the
+          // chunks behind the last column that a row of the warp sees
+          const int seen = qpos - j * kKcKeys, seen1 = qpos0 + ((wq * 32 + 31) >> a.gshift) - j * kKcKeys;
+          auto load = [&](int q, float (&v)[32]) {
+            tmem_ld32(ts + 32 * q, v);
+            tmem_ld_wait32(v);
+            const int cols = seen + 1 - 32 * q;
+            const uint32_t vis = (q == 0 ? mask.x : q == 1 ? mask.y : q == 2 ? mask.z : mask.w) &
+                                 (cols >= 32 ? 0xffffffffu : cols <= 0 ? 0u : (1u << cols) - 1u);
+            if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(vis >> e & 1)) v[e] = -INFINITY;
+            }
+          };
+          const int nq = seen1 < 0 ? 0 : min(4, seen1 / 32 + 1);
+#pragma unroll 1
+          for (int q = 0; q < nq; ++q) {
+            float v[32];
+            load(q, v);
+            max32(v, mx);
+          }
+          raise(max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int q = 0; q < nq; ++q) {
+            float v[32];
+            load(q, v);
+            kc_weights(v, f, mm, sum, ts + 16 * q);
+          }
+          const uint32_t none[16] = {};
+#pragma unroll 1
+          for (int q = nq; q < 4; ++q) tmem_st16(ts + 16 * q, none);
+        }
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[i]);
+        ++n_s;
+      }
+      if (dead) break;
+      blocks += x.j1 - x.j0;
+      // ---- epilogue
+      if (n > 0) {
+        acquire(&ofull[i], n_o & 1);
+        if (dead) break;
+        ++n_o;
+        tc_fence_after();
+      }
+      const bool live = token < x.n;
+      const int live_rows = max(0, min(32, (int)((long long)(x.n - t0) << a.gshift) - wq * 32));
+      if (x.direct) {
+        if (n > 0) {
+          const float r = l == 0.f ? 0.f : 1.f / l;
+          uint16_t* dst = c.out + ((size_t)(x.row0 + token) * c.n_q + hq) * kD;
+          const bool wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;   // whole sectors a store
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float o[32];
+            tmem_ld32(to + 32 * q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool nan = nans[is * 8 + 2 * q + e] <= qpos;
+              uint32_t w[8];
+#pragma unroll
+              for (int p = 0; p < 8; ++p)
+                w[p] = nan ? 0x7fff7fffu : pack_bf16(o[16 * e + 2 * p] * r, o[16 * e + 2 * p + 1] * r);
+              uint16_t* d = dst + 32 * q + 16 * e;
+              if (!live) continue;
+              if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                             "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+              } else {
+                stg_v4(d, make_uint4(w[0], w[1], w[2], w[3]));
+                stg_v4(d + 8, make_uint4(w[4], w[5], w[6], w[7]));
+              }
+            }
+          }
+          if (live && c.lse)
+            c.lse[(size_t)(x.row0 + token) * c.n_q + hq] =
+                l == 0.f ? -INFINITY : m * inv * c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
+        }
+        tc_fence_before();
+      } else if (live_rows > 0) {
+        const bool cut = x.pieces > 1;
+        const int slot = cut ? (x.piece == 0 ? 1 : 0) : 2 + (it & 1);
+        float* p = a.part + ((((size_t)blockIdx.x * 4 + slot) * 2 + i) * a.part_rows + row) * kKcPart;
+        if (n > 0) {
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            float o[16];
+            tmem_ld16(to + 16 * q, o);
+            tmem_ld_wait();
+            if (nans[is * 8 + q] <= qpos) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = NAN;
+            }
+            if (live && l != 0.f) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(p + 16 * q + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+          tc_fence_before();
+        }
+        if (live) *reinterpret_cast<float2*>(p + kD) = make_float2(m, l);
+        __threadfence();
+        __syncwarp();
+        const int tile = x.single ? 0 : i;
+        uint32_t* count = a.counters + ((size_t)(cut ? x.first * 3 : blockIdx.x * 3 + 1 + (it & 1)) * 2 + tile) * 4 + wq;
+        uint32_t before = 0u;
+        if (lane == 0) before = atomicAdd(count, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before + 1u == (uint32_t)(x.pieces * (x.single ? 2 : 1))) {
+          __threadfence();
+          kc_merge(a, x, 2 + (it & 1), i, wq, live_rows, f, inv, token, hq);
+          if (lane == 0) atomicExch(count, 0u);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kKcWarpMma) {
+    tc_fence_after();
+    tmem_dealloc<kKcTmemCols>(tmem);
+  }
+}
+
+static int kc_part_rows(int T, int G) { return (long long)T * G < 128 ? T * G : 128; }
+
+size_t kv4_chunk_workspace(int T, int, int n_q, int n_kv) {
+  return kKcOffPart + (size_t)kKcCtas * 4 * 2 * kc_part_rows(T, n_q / n_kv) * kKcPart * 4;
+}
+
+int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
+  KcArgs a{};
+  a.c = c;
+  a.G = c.n_q / c.n_kv;
+  while ((1 << a.gshift) < a.G) ++a.gshift;
+  a.tpm = 128 >> a.gshift;
+  a.part_rows = kc_part_rows(c.T, a.G);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<int*>(w);
+  a.counters = reinterpret_cast<uint32_t*>(w + kKcOffCount);
+  a.part = reinterpret_cast<float*>(w + kKcOffPart);
+  a.wait_limit = kKcWait;
+#ifdef SPC_TEST_HOOKS
+  a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
+#endif
+  CUtensorMap qmap;
+  const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)c.n_q, (uint64_t)c.T};
+  const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)c.q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
+  if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
+  if (set_func_attr((const void*)kv4_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKcSmem) != cudaSuccess)
+    return SPC_ERR_CUDA;
+  kv4_chunk_kernel<<<kKcCtas, kKcThreads, kKcSmem, static_cast<cudaStream_t>(stream)>>>(qmap, a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 

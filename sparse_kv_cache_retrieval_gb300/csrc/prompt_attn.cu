@@ -107,30 +107,7 @@ struct PaItem {
 __device__ __forceinline__ bool pa_wait(const PaArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
 }
-// A shared-memory matrix descriptor (spc_tc.cuh) in two words: the low one
-// holds the address (in 16-byte units) and the leading byte offset, the high
-// one is the same for every operand here (1024 bytes between 8-row groups,
-// 128-byte swizzle). K-major operands have leading offset 16, V's 64-value
-// blocks lie kPaBlock apart.
-constexpr uint32_t kPaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-constexpr uint32_t kPaDescVLo = ((kPaBlock >> 4) - 1u) << 16;      // on top of a K-major low word
-__device__ __forceinline__ uint32_t pa_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
-__device__ __forceinline__ uint64_t pa_desc(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
-__device__ __forceinline__ float pa_max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// tcgen05.wait::ld, with the values it makes valid passed through it
-__device__ __forceinline__ void pa_ld_wait(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
-               :: "memory");
-  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
-}
+constexpr uint32_t kPaDescVLo = umma_mn_lo(kPaBlock);              // on top of a K-major low word
 // 32 logits of a row: weights 2^(s scale - m) to 16 packed columns, their sum, their largest logit
 __device__ __forceinline__ void pa_weights(const float* s, float scale2, float m, float2 (&sum)[2], uint32_t tp) {
   const float2 sc = make_float2(scale2, scale2), nm = make_float2(-m, -m);
@@ -144,16 +121,6 @@ __device__ __forceinline__ void pa_weights(const float* s, float scale2, float m
     p[e] = pack_bf16(x.x, x.y);
   }
   tmem_st16(tp, p);
-}
-__device__ __forceinline__ void pa_max32(const float* s, float (&mx)[4]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 8)
-#pragma unroll
-    for (int f = 0; f < 4; ++f) mx[f] = pa_max3(mx[f], s[e + f], s[e + 4 + f]);
-}
-__device__ __forceinline__ void pa_tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ bool pa_not_finite(uint32_t bf) { return (bf & 0x7f80u) == 0x7f80u; }
@@ -395,13 +362,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
         if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[i], kPaTile);
           const int row = x.start + x.t0 + i * a.tpm;
-          pa_tma_3d(qs + i * kPaTile, &qmap, 0, x.g << a.gshift, row, &qfull[i]);
-          pa_tma_3d(qs + i * kPaTile + kPaBlock, &qmap, 64, x.g << a.gshift, row, &qfull[i]);
+          tma_load_3d(qs + i * kPaTile, &qmap, 0, x.g << a.gshift, row, &qfull[i]);
+          tma_load_3d(qs + i * kPaTile + kPaBlock, &qmap, 64, x.g << a.gshift, row, &qfull[i]);
         }
       };
       auto load = [&](const CUtensorMap* map, uint32_t dst, int j, uint64_t* bar) {
-        pa_tma_3d(dst, map, 0, x.g, x.start + j * kPaKeys, bar);
-        pa_tma_3d(dst + kPaBlock, map, 64, x.g, x.start + j * kPaKeys, bar);
+        tma_load_3d(dst, map, 0, x.g, x.start + j * kPaKeys, bar);
+        tma_load_3d(dst + kPaBlock, map, 64, x.g, x.start + j * kPaKeys, bar);
       };
       load_q(0);
       acquire(k0free, (nk0 & 1) ^ 1);
@@ -453,11 +420,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
     auto issue_s = [&](auto tile, uint32_t kd, bool last) {
       constexpr int i = decltype(tile)::value;
       if (elect_one()) {
-        const uint32_t qd = pa_desc_lo(qs + i * kPaTile);
+        const uint32_t qd = umma_desc_lo(qs + i * kPaTile);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t off = (uint32_t)(kk >> 2) * (kPaBlock >> 4) + (uint32_t)(kk & 3) * 2;
-          umma_f16(tm + i * kPaKeys, pa_desc(qd + off, kPaDescHi), pa_desc(kd + off, kPaDescHi), kPaIdescS, kk ? 1u : 0u);
+          umma_f16(tm + i * kPaKeys, umma_desc(qd + off), umma_desc(kd + off), kPaIdescS, kk ? 1u : 0u);
         }
         umma_commit(&sfull[i]);
         if (last) umma_commit(&qfree[i]);
@@ -474,16 +441,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       if (dead) return;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t vd = st + kPaDescVLo, kd = st + (kPaTile >> 4), qd = pa_desc_lo(qs + i * kPaTile);
+        const uint32_t vd = st + kPaDescVLo, kd = st + (kPaTile >> 4), qd = umma_desc_lo(qs + i * kPaTile);
 #pragma unroll
         for (int kk = 0; kk < kPaKeys / 16; ++kk)
-          umma_f16_tmem_a(tm + kPaColO + i * kD, tm + i * kPaKeys + kk * 8, pa_desc(vd + (uint32_t)kk * 128, kPaDescHi),
+          umma_f16_tmem_a(tm + kPaColO + i * kD, tm + i * kPaKeys + kk * 8, umma_desc(vd + (uint32_t)kk * 128),
                           kPaIdescO, kk ? 1u : (j ? 1u : 0u));
         if (j + 1 < n) {
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
             const uint32_t off = (uint32_t)(kk >> 2) * (kPaBlock >> 4) + (uint32_t)(kk & 3) * 2;
-            umma_f16(tm + i * kPaKeys, pa_desc(qd + off, kPaDescHi), pa_desc(kd + off, kPaDescHi), kPaIdescS, kk ? 1u : 0u);
+            umma_f16(tm + i * kPaKeys, umma_desc(qd + off), umma_desc(kd + off), kPaIdescS, kk ? 1u : 0u);
           }
           umma_commit(&sfull[i]);
           if (j + 2 == n) umma_commit(&qfree[i]);
@@ -505,7 +472,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (len < 0) break;
       const int n = max(nA, nB);
-      const uint32_t k0 = pa_desc_lo(qs + (kPaOffK0 - kPaOffQ));
+      const uint32_t k0 = umma_desc_lo(qs + (kPaOffK0 - kPaOffQ));
       acquire(k0full, nk0++ & 1);
       acquire(&qfull[0], nq[0]++ & 1);
       if (dead) break;
@@ -522,7 +489,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
       for (int j = 0; j < n; ++j) {
         const int st = nkv % kPaStages;
         ++nkv;
-        const uint32_t sd = pa_desc_lo(kvs) + (uint32_t)st * (2 * kPaTile >> 4);
+        const uint32_t sd = umma_desc_lo(kvs) + (uint32_t)st * (2 * kPaTile >> 4);
         if (j < nA) issue(tA, sd, j, nA, j < nB ? nullptr : &kvfree[st]);
         if (j < nB) issue(tB, sd, j, nB, &kvfree[st]);
       }
@@ -595,12 +562,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            pa_ld_wait(s + 32 * q);
+            tmem_ld_wait32(s + 32 * q);
             if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
-            pa_max32(s + 32 * q, mx);
+            max32(s + 32 * q, mx);
             pa_weights(s + 32 * q, c.scale2, m, sum, ts + 16 * q);
           }
-          const float M = pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
+          const float M = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2;
           if (__any_sync(0xffffffffu, M > m + kPaHeadroom)) {
             // the weights go to the same columns again, and stores to tensor
             // memory are asynchronous: the first ones have to be there
@@ -621,7 +588,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           const int seen = qpos - j * kPaKeys, seen0 = at + (w0 >> a.gshift), seen1 = at + ((w0 + 31) >> a.gshift);
           auto load = [&](int q, float (&v)[32]) {
             tmem_ld32(ts + 32 * q, v);
-            pa_ld_wait(v);
+            tmem_ld_wait32(v);
             if (seen0 < 32 * q + 31) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -633,9 +600,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attn_kernel(const __grid
           for (int q = 0; q < nq; ++q) {
             float v[32];
             load(q, v);
-            pa_max32(v, mx);
+            max32(v, mx);
           }
-          raise(pa_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2);
+          raise(max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c.scale2);
           const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
           for (int q = 0; q < nq; ++q) {

@@ -161,6 +161,46 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// tcgen05.wait::ld, with the 32 values it makes valid passed through it
+__device__ __forceinline__ void tmem_ld_wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+               :: "memory");
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
+}
+
+// A shared-memory matrix descriptor (above) in two words: the low one holds the
+// address (in 16-byte units) and the leading byte offset, the high one is the
+// same for every operand with 1024 bytes between 8-row groups and the 128-byte
+// swizzle. K-major operands have leading offset 16; umma_mn_lo goes on top of
+// their low word where 64-value MN blocks lie mn_block_bytes apart.
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t umma_mn_lo(uint32_t mn_block_bytes) { return ((mn_block_bytes >> 4) - 1u) << 16; }
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t umma_desc(uint32_t lo) { return (uint64_t)kUmmaDescHi << 32 | lo; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// four running maxima over 32 values
+__device__ __forceinline__ void max32(const float* s, float (&mx)[4]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) mx[f] = max3(mx[f], s[e + f], s[e + 4 + f]);
+}
+
+// a tiled TMA load of a 3-dimensional box
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+
 // N (16 or 32) consecutive columns, one lane per thread
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float (&v)[N]) {

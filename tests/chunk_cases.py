@@ -55,12 +55,14 @@ def mass(c, q, new, lse, prev, keep, out=None, ws=None, scale=SCALE, cache=None,
 # relatively, and the sum of the weights too, and by 2^-22 for the exponential.
 # Sums of weights run over at most 2^10 in a row (a thread's columns of a tile,
 # then the tiles), 2^-14 relatively. The weights that multiply V are rounded to
-# fp16, 2^-11, and the result to bf16, 2^-8 of it; a weight that is below 2^-25 of
-# the largest is off by 2^-36 of it, which is less than the above over fewer than
-# 2^20 positions.
-def chunk_tol(want, mag, err):
+# fp16, 2^-11, and the result to bf16, 2^-8 of it. Below 2^-25 of the largest
+# weight fp16 has steps of 2^-35 of it (they are kept 2^11 times as large, and the
+# type's last step is 2^-24): such a weight is off by up to 2^-36 of the largest,
+# which is at most 1, and a row's result by that times the sum of |v| over what it
+# sees. That sum counts where the weights that count meet zeros in V.
+def chunk_tol(want, mag, err, vsum):
     e = 128 * 2.0 ** -24 * err[..., None]
-    return 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -14 + 2 * e) * mag + 1e-30
+    return 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -14 + 2 * e) * mag + 2.0 ** -36 * vsum
 
 
 def lse_tol(want, err):
@@ -91,11 +93,11 @@ def check_chunk(c, q, new, out, lse, scale=SCALE, table=None, lens=None):
     """Both outputs of a call against the oracle; rows of no request are still 7."""
     cu = cu_of(new)
     with np.errstate(invalid="ignore", over="ignore"):
-        want, mag, want_lse, err = P.chunk_attention(f64(q), c.rec, c.table if table is None else table,
+        want, mag, want_lse, err, vsum = P.chunk_attention(f64(q), c.rec, c.table if table is None else table,
                                                      c.lens if lens is None else lens, cu, scale)
     n = cu[-1]
     assert np.all(f64(out[n:]) == 7)
-    close(out[:n], want[:n], chunk_tol(want, mag, err)[:n], "out")
+    close(out[:n], want[:n], chunk_tol(want, mag, err, vsum)[:n], "out")
     if lse is not None:
         assert np.all(f64(lse[n:]) == 7)
         close(lse[:n], want_lse[:n], lse_tol(want_lse, err)[:n], "lse")

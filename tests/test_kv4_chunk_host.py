@@ -38,7 +38,7 @@ def test_a_single_new_token_is_the_decode_attention():
     cache, table = _cache(rng, [70, 5], 2, 16)
     q = rng.standard_normal((2, 4, 128))
     want, _ = P.decode_attention(q, cache, table, [70, 5], None, 0.1)
-    out, _, lse, _ = P.chunk_attention(q, cache, table, [70, 5], [0, 1, 2], 0.1)
+    out, _, lse, *_ = P.chunk_attention(q, cache, table, [70, 5], [0, 1, 2], 0.1)
     assert np.allclose(out, want, rtol=1e-12)
     k, _ = P.values(cache[table[1, 0], 1, :5])
     assert np.allclose(lse[1, 2], np.log(np.exp(k @ q[1, 2] * 0.1).sum()), rtol=1e-12)
@@ -51,7 +51,7 @@ def test_a_whole_prompt_is_the_prompt_attention_of_the_cached_values():
     rows = cache[table[0]].transpose(0, 2, 1, 3).reshape(-1, 2, 144)[:40]
     k, v = P.values(rows)
     want, _ = P.prompt_attention(q, k, v, [0, 40], 0.1)
-    out, _, lse, _ = P.chunk_attention(q, cache, table, [40], [0, 40], 0.1)
+    out, _, lse, *_ = P.chunk_attention(q, cache, table, [40], [0, 40], 0.1)
     assert np.allclose(out, want, rtol=1e-12)
     # every row's weights are a distribution: the positions' sums add up to the rows
     mass, _ = P.attn_mass(q, cache, table, [40], [0, 40], lse, np.zeros((1, 2, 48)), 0.0, 48, 0.1)
@@ -65,11 +65,11 @@ def test_rows_before_position_zero_and_blocks_outside_the_pool():
     rng = np.random.default_rng(2)
     cache, table = _cache(rng, [33], 1, 16)
     q = rng.standard_normal((40, 1, 128))
-    out, _, lse, _ = P.chunk_attention(q, cache, table, [33], [0, 40], 0.1)
+    out, _, lse, *_ = P.chunk_attention(q, cache, table, [33], [0, 40], 0.1)
     assert np.all(out[:7] == 0) and np.all(lse[:7] == -np.inf) and np.all(np.isfinite(lse[7:]))
     cut = table.copy()
     cut[0, 0] = -1
-    out2, _, lse2, _ = P.chunk_attention(q, cache, cut, [33], [0, 40], 0.1)
+    out2, _, lse2, *_ = P.chunk_attention(q, cache, cut, [33], [0, 40], 0.1)
     assert np.all(out2[:23] == 0) and np.all(lse2[:23] == -np.inf) and np.all(lse2[23:] < lse[23:])
 
 
