@@ -610,7 +610,10 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
  * Zeros and -infinity where R is empty (a token before position 0 among them).
  * Rows outside every request are left as they were. What a row does not see
  * does not reach it, NaN included; a query that is not finite makes its row NaN.
- * Precision: as spc_kv4_decode_attn; lse is fp32.
+ * Precision: products, maxima and sums are fp32. Queries are taken in fp16 after a
+ * power of two per row (a value loses bits only below 2^-28 of the row's largest);
+ * softmax weights are rounded to fp16 (2^-11) down to 2^-22 of the largest and are
+ * off by at most 2^-33 of it below; the output is rounded to bf16 once. lse is fp32.
  * q          bf16, row t at q + t * q_stride elements: [n_q][d], 16-byte aligned;
  *            the stride is a multiple of 8 elements, at least n_q * d and at most 2^32.
  * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are a

@@ -17,11 +17,14 @@
 // bf16's 8; and e2m1 to fp16 is one conversion for two values. Queries are scaled
 // by a power of two a row (the largest to [2^14, 2^15): a value loses bits only
 // below 2^-28 of it), in place, by the softmax thread of the row. P and its sum
-// are kept 2^11 times the weights against the running maximum, the top of fp16's
-// range, so that weights keep 11 bits down to 2^-25 of the largest and are off by
-// 2^-36 of it below; the maximum (of the products q.K, before the scale, so that
-// a large logit's own rounding cannot pass the range) is raised when a logit
-// passes it by more than 4.75 in base 2, and only then is the row of O rescaled.
+// are kept 2^8 times the weights against the running maximum, so that weights keep
+// 11 bits down to 2^-22 of the largest and are off by 2^-33 of it below; the
+// maximum (of the products q.K, before the scale, so that a large logit's own
+// rounding cannot pass the range) is raised when a logit passes it by more than
+// 7.75 in base 2, and only then is the row of O rescaled. That costs some 2500
+// cycles, for which the other tile's products wait: with 2^11 and 4.75, where a raise
+// of some row came in a third of the blocks (logits of a deviation of 2), 64K x
+// 2048 tokens of 64 heads took 3.67 ms.
 // Sums, maxima, S and O are fp32; a weight's sum is that of the unrounded values.
 //
 // What a row does not see does not reach it. Masked columns of S are replaced. V
@@ -38,10 +41,12 @@
 // to arrive merges them, in the order of the positions, so that the result does
 // not depend on the order of arrival.
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
-//   warps 8-11      dequantisation into a ring of three 32 KB operands: K_j, V_j, K_j+1, ...
+//   warps 8-11      dequantisation into a ring of four 32 KB operands: K_j, V_j, K_j+1, ...
 //   warp 12         tensor memory, MMA issue
-//   warp 13         schedule, copies of the records (cp.async.bulk, one a cache block)
+//   warp 13         schedule, copies of the records (cp.async.bulk)
 //   warp 14         Q loads (TMA)
+//   warp 15         gate: passes the operands' arrival on to the P barriers, so that the MMA
+//                   warp waits once a batch
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
 // and leaves, the others' waits then give up in turn; copies land and MMAs
 // complete before the CTA releases its tensor memory.
@@ -57,8 +62,11 @@
 
 namespace spc {
 
-constexpr int kKcRaw = 7;                             // stages of records, 64 positions each
-constexpr int kKcSlots = 3;                           // ring of dequantised operands
+// Records: a ring for each dequantising warp (one reader, so that a wait on a phase's
+// parity is never two phases behind), stages of 16 positions, which lie in one cache block
+constexpr int kKcRaw = 3, kKcRun = 16;
+constexpr uint32_t kKcStage = kKcRun * kKv4Rec;
+constexpr int kKcSlots = 4;                           // ring of dequantised operands
 constexpr int kKcItems = 2;                           // item ring
 constexpr int kKcMasks = 8;                           // blocks whose masks are kept: the copies are at most 5 ahead of the softmax
 constexpr int kKcWarpDeq = 8, kKcWarpMma = 12, kKcWarpCopy = 13, kKcWarpQ = 14;
@@ -66,8 +74,8 @@ constexpr int kKcThreads = 512;
 // registers a thread: 128 at launch (512 threads); softmax 176 (two warpgroups),
 // dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128
 constexpr int kKcRegSoft = 176, kKcRegDeq = 88, kKcRegRest = 72;
-constexpr float kKcBias = 11.f;                       // log2 of the factor of the weights
-constexpr float kKcHeadroom = 4.75f;                  // log2 growth allowed before a maximum is raised
+constexpr float kKcBias = 8.f;                        // log2 of the factor of the weights
+constexpr float kKcHeadroom = 7.75f;                  // log2 growth allowed before a maximum is raised
 constexpr int kKcFixed = 1;                           // units of an item's fixed part
 constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kKcColO = 256;
@@ -79,11 +87,11 @@ constexpr uint32_t kKcDescVLo = umma_mn_lo(kKcBlock);
 constexpr uint32_t kKcOffQ = 0;                                       // [2] tiles
 constexpr uint32_t kKcOffKv = kKcOffQ + 2 * kKcTile;
 constexpr uint32_t kKcOffRaw = kKcOffKv + kKcSlots * kKcTile;
-constexpr uint32_t kKcOffItem = kKcOffRaw + kKcRaw * kKcStage;        // [kKcItems] KcItem
+constexpr uint32_t kKcOffItem = kKcOffRaw + 4 * kKcRaw * kKcStage;        // [kKcItems] KcItem
 constexpr uint32_t kKcOffNan = kKcOffItem + kKcItems * 64;            // [kKcItems][8] first position with a NaN V scale
 constexpr uint32_t kKcOffMask = kKcOffNan + kKcItems * 32;            // [kKcMasks][4 words]
 constexpr uint32_t kKcOffBar = kKcOffMask + kKcMasks * 16;
-constexpr int kKcBars = 2 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 1;
+constexpr int kKcBars = 8 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 1;
 constexpr size_t kKcSmem = 1024 + kKcOffBar + kKcBars * 8 + 16;
 static_assert(kKcSmem <= 227 * 1024, "shared memory of one CTA");
 
@@ -137,16 +145,14 @@ __device__ __forceinline__ void kc_weights(const float* s, float f, float m, flo
   tmem_st16(tp, p);
 }
 
-// A row of 128 values of 64 bytes of codes (in shared memory) and 8 scales into
-// row r of a swizzled tile; zeros where there is no record.
-__device__ __forceinline__ void kc_row(uint32_t codes, uint2 sc, uint32_t tile, int r, bool there) {
+// A row of 128 values of 64 bytes of codes and 8 scales into row r of a swizzled tile
+__device__ __forceinline__ void kc_row(const uint4* codes, uint32_t sc0, uint32_t sc1, uint32_t tile, int r) {
   const uint32_t dst = tile + (uint32_t)r * 128u, r7 = (uint32_t)r & 7u;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint4 w = there ? lds_v4(codes + 16 * q) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t s2 = e4m3x2_to_f16(((q < 2 ? sc.x : sc.y) >> (16 * (q & 1))) & 0xffffu);
+    const uint32_t s2 = e4m3x2_to_f16(((q < 2 ? sc0 : sc1) >> (16 * (q & 1))) & 0xffffu);
     const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t ww[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t h[4];
@@ -279,9 +285,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   int* nans = reinterpret_cast<int*>(base + kKcOffNan);
   uint32_t* masks = reinterpret_cast<uint32_t*>(base + kKcOffMask);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kKcOffBar);
-  uint64_t* rfull = bars;                     // [kKcRaw] bytes of the records
-  uint64_t* rfree = rfull + kKcRaw;           // [kKcRaw] two dequantising warps have read them
-  uint64_t* kvfull = rfree + kKcRaw;          // [kKcSlots] four dequantising warps have written the operand
+  uint64_t* rfull = bars;                     // [4 warps][kKcRaw] bytes of the records
+  uint64_t* rfree = rfull + 4 * kKcRaw;       // [4][kKcRaw] the warp has read them
+  uint64_t* kvfull = rfree + 4 * kKcRaw;      // [kKcSlots] four dequantising warps have written the operand
   uint64_t* kvfree = kvfull + kKcSlots;       // [kKcSlots] commit after the last MMA that reads it
   uint64_t* ifull = kvfree + kKcSlots;        // [kKcItems] item written
   uint64_t* ifree = ifull + kKcItems;         // [kKcItems] every role has read it, the softmax warps are done with it
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   uint64_t* qready = qfull + 2;               // [2] four softmax warps have converted the tile
   uint64_t* qfree = qready + 2;               // [2] commit after the tile's last S
   uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
-  uint64_t* pfull = sfull + 2;                // [2] four softmax warps: P written, O rescaled
+  uint64_t* pfull = sfull + 2;                // [2] four softmax warps: P written, O rescaled; gate: the batch's operands are there
   uint64_t* ofull = pfull + 2;                // [2] commit: the piece's last PV done
   uint64_t* drain = ofull + 2;                // commit after the last MMA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -297,9 +303,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   const Kv4ChunkCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKcRaw; ++s) {
+    for (int s = 0; s < 4 * kKcRaw; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rfree[s], 2);
+      mbar_init(&rfree[s], 1);
     }
     for (int s = 0; s < kKcSlots; ++s) {
       mbar_init(&kvfull[s], 4);
@@ -307,14 +313,14 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     }
     for (int s = 0; s < kKcItems; ++s) {
       mbar_init(&ifull[s], 1);
-      mbar_init(&ifree[s], 4 + 8 + 2);
+      mbar_init(&ifree[s], 4 + 8 + 3);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&qfull[s], 1);
       mbar_init(&qready[s], 4);
       mbar_init(&qfree[s], 1);
       mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], 4);
+      mbar_init(&pfull[s], 5);
       mbar_init(&ofull[s], 1);
     }
     mbar_init(drain, 1);
@@ -328,7 +334,8 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   const uint32_t qs = smem_u32(base + kKcOffQ), kvs = smem_u32(base + kKcOffKv);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !kc_wait(a, bar, parity)) {
+    // mostly over: tested before it is waited for (some 90 cycles against 190)
+    if (!dead && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !kc_wait(a, bar, parity)) {
       if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
       dead = true;
     }
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
     KcRequests rq;
     kc_requests(c, rq);
-    const int lt = 8 - a.gshift;                      // log2 of the tokens a pair
+    const int lt = 8 - a.gshift, bs = 1 << c.block_shift;   // lt: log2 of the tokens a pair
     auto shape = [&](int len, int n) {
       KcShape s;
       s.ctx = len - n;
@@ -429,17 +436,32 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         if (a.starve) break;
 #endif
         KcTable t;
-        t.start(c.table + (size_t)b * c.max_blocks, (x.len + (1 << c.block_shift) - 1) >> c.block_shift,
-                x.j0 * kKcKeys >> c.block_shift);
-        for (int j = x.j0; j < x.j1; ++j, ++blocks) {
+        t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.j0 * kKcKeys >> c.block_shift);
+        // lane w copies for dequantising warp w
+        for (int j = x.j0; j < x.j1 && !dead; ++j, ++blocks) {
+          uint32_t mask = 0u;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++nraw) {
-            acquire(&rfree[nraw % kKcRaw], ((nraw / kKcRaw) & 1) ^ 1);
-            if (dead) break;
-            kc_copy(c, t, x.g, x.len, j * kKcKeys + h * kKcHalf, base + kKcOffRaw + (nraw % kKcRaw) * kKcStage,
-                    &rfull[nraw % kKcRaw], masks + (blocks % kKcMasks) * 4 + 2 * h);
+            const int st = nraw % kKcRaw, p = j * kKcKeys + (lane & 3) * 32 + h * kKcRun;
+            const int blk = t.entry(j * kKcKeys >> c.block_shift, p >> c.block_shift);
+            const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kKcRun)) : 0;
+            mask |= ((1u << n) - 1u) << (h * kKcRun);
+            const uint32_t parity = ((nraw / kKcRaw) & 1) ^ 1;
+            uint64_t* bar = &rfull[(lane & 3) * kKcRaw + st];
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&rfree[(lane & 3) * kKcRaw + st], parity, a.wait_limit))) {
+              if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+              dead = true;
+              break;
+            }
+            if (lane < 4) {
+              if (h == 1) masks[(blocks % kKcMasks) * 4 + lane] = mask;
+              if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
+              if (n > 0)
+                bulk_g2s(base + kKcOffRaw + (lane * kKcRaw + st) * kKcStage,
+                         c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
+            }
+            __syncwarp();
           }
-          if (dead) break;
         }
       }
       // the next item
@@ -453,8 +475,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       }
     }
     // every copy lands before the CTA ends (they have, unless a role gave up)
-    if (lane == 0)
-      for (int k = max(0, nraw - kKcRaw); k < nraw; ++k) mbar_wait_bounded(&rfull[k % kKcRaw], (k / kKcRaw) & 1, a.wait_limit);
+    if (lane < 4)
+      for (int k = max(0, nraw - kKcRaw); k < nraw; ++k)
+        mbar_wait_bounded(&rfull[lane * kKcRaw + k % kKcRaw], (k / kKcRaw) & 1, a.wait_limit);
     __syncwarp();
   } else if (warp == kKcWarpQ) {
     // ================= queries
@@ -521,8 +544,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     };
     auto issue_pv = [&](auto tile, int k, bool first, bool last, bool done) {
       constexpr int i = decltype(tile)::value;
-      if (!__all_sync(0xffffffffu, mbar_test(&pfull[i], np[i] & 1))) acquire(&pfull[i], np[i] & 1);
-      ++np[i];
+      acquire(&pfull[i], np[i]++ & 1);
       if (dead) return;
       tc_fence_after();
       if (elect_one()) {
@@ -557,12 +579,8 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         }
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; k += 2) {
-          full(kv + 2 * k + 1);
           issue_pv(tA, kv + 2 * k + 1, k == 0, k + 2 >= nb, true);
-          if (k + 1 < nb) {
-            full(kv + 2 * k + 3);
-            issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
-          }
+          if (k + 1 < nb) issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
           if (k + 2 < nb) {
             full(kv + 2 * k + 4);
             issue_s(tA, kv + 2 * k + 4, false, k + 4 >= nb, true);
@@ -577,10 +595,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         if (n1) issue_s(tB, kv, true, n1 == 1, true);
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; ++k) {
+          // PV of block k, S of the next one; the tensor pipe queues only a few MMAs, so nothing waits between the two
           const int v = kv + 2 * k + 1;
-          full(v);
           if (k < n0) issue_pv(tA, v, k == 0, k + 1 == n0, k >= n1);
-          if (k + 1 < nb) full(v + 1);
           if (k + 1 < n0) issue_s(tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
           if (k < n1) issue_pv(tB, v, k == 0, k + 1 == n1, true);
           if (k + 1 < n1) issue_s(tB, v + 1, false, k + 2 == n1, true);
@@ -597,8 +614,8 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   } else if (warp >= kKcWarpDeq && warp < kKcWarpDeq + 4) {
     // ================= dequantisation, a record a thread
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegDeq));
-    const int r = threadIdx.x & 127, h = r >> 6;
-    int blocks = 0, kv = 0;
+    const int w = warp - kKcWarpDeq, r = threadIdx.x & 127;
+    int blocks = 0, kv = 0, nread = 0;
     for (int it = 0;; ++it) {
       const int is = it % kKcItems;
       acquire(&ifull[is], (it / kKcItems) & 1);
@@ -608,40 +625,48 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (n < 0) break;
       for (int j = j0; j < j1; ++j, ++blocks) {
-        const int raw = 2 * blocks + h, st = raw % kKcRaw;
-        acquire(&rfull[st], (raw / kKcRaw) & 1);
+        const int s0 = nread % kKcRaw, s1 = (nread + 1) % kKcRaw;
+        acquire(&rfull[w * kKcRaw + s0], (nread / kKcRaw) & 1);
+        acquire(&rfull[w * kKcRaw + s1], ((nread + 1) / kKcRaw) & 1);
         if (dead) break;
-        const uint32_t rec = smem_u32(base + kKcOffRaw) + (uint32_t)st * kKcStage + (uint32_t)(r & 63) * kKv4Rec;
-        const bool there = masks[(blocks % kKcMasks) * 4 + (r >> 5)] >> lane & 1;
+        nread += 2;
+        // the whole record into registers, so that its stage is free at once
+        const uint32_t rec = smem_u32(base + kKcOffRaw) + (uint32_t)(w * kKcRaw + (lane < kKcRun ? s0 : s1)) * kKcStage +
+                             (uint32_t)(lane & (kKcRun - 1)) * kKv4Rec;
+        const bool there = masks[(blocks % kKcMasks) * 4 + w] >> lane & 1;
+        uint4 v[9];
+#pragma unroll
+        for (int q = 0; q < 9; ++q) v[q] = lds_v4(rec + 16 * q);
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&rfree[w * kKcRaw + (lane ? s1 : s0)]);
+        if (!there) {
+#pragma unroll
+          for (int q = 0; q < 9; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // scales of V that are NaN: noted, and zero in the product
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t& x = e ? v[8].w : v[8].z;
+          const uint32_t bad = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+          if (bad) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              if (bad >> (8 * f + 7) & 1) {
+                atomicMin(&nans[is * 8 + 4 * e + f], j * kKcKeys + r);
+                x &= ~(0xffu << (8 * f));
+              }
+          }
+        }
 #pragma unroll
         for (int part = 0; part < 2; ++part, ++kv) {  // K, then V
           const int slot = kv % kKcSlots;
           acquire(&kvfree[slot], ((kv / kKcSlots) & 1) ^ 1);
           if (dead) break;
-          uint2 sc = there ? lds_v2(rec + kKv4Scale + 8 * part) : make_uint2(0u, 0u);
-          if (part) {
-            // scales of V that are NaN: noted, and zero in the product
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              uint32_t& x = w ? sc.y : sc.x;
-              const uint32_t bad = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (bad) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (bad >> (8 * e + 7) & 1) {
-                    atomicMin(&nans[is * 8 + 4 * w + e], j * kKcKeys + r);
-                    x &= ~(0xffu << (8 * e));
-                  }
-              }
-            }
-          }
-          kc_row(rec + (part ? kKv4V : 0), sc, kvs + (uint32_t)slot * kKcTile, r, there);
+          if (part) kc_row(v + 4, v[8].z, v[8].w, kvs + (uint32_t)slot * kKcTile, r);
+          else kc_row(v, v[8].x, v[8].y, kvs + (uint32_t)slot * kKcTile, r);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&kvfull[slot]);
-            if (part) mbar_arrive(&rfree[st]);
-          }
+          if (lane == 0) mbar_arrive(&kvfull[slot]);
         }
         if (dead) break;
       }
@@ -864,8 +889,36 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
     }
-  } else {
+  } else {                                    // warp 15
+    // ================= gate: one arrival a phase of the P barriers, when what the batch behind it reads is there
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    int kv = 0, np[2] = {0, 0};
+    for (int it = 0; !dead; ++it) {
+      const int is = it % kKcItems;
+      acquire(&ifull[is], (it / kKcItems) & 1);
+      if (dead) break;
+      const int n = items[is].n, n0 = items[is].n0, n1 = items[is].n1, nb = items[is].j1 - items[is].j0;
+      const int single = items[is].single;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (n < 0) break;
+      for (int k = 0; k < nb; ++k) {
+        // V of the block, and K of the next one where both tiles take it
+        const int v = kv + 2 * k + 1;
+        acquire(&kvfull[v % kKcSlots], (v / kKcSlots) & 1);
+        if (!single && k + 1 < nb) acquire(&kvfull[(v + 1) % kKcSlots], ((v + 1) / kKcSlots) & 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (single ? (k & 1) != i : k >= (i ? n1 : n0)) continue;
+          if (np[i] > 0) acquire(&pfull[i], (np[i] - 1) & 1);      // the phase before is over
+          if (dead) break;
+          ++np[i];
+          if (lane == 0) mbar_arrive(&pfull[i]);
+        }
+        if (dead) break;
+      }
+      kv += 2 * nb;
+    }
   }
   tc_fence_before();
   __syncthreads();

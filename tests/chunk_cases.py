@@ -55,14 +55,14 @@ def mass(c, q, new, lse, prev, keep, out=None, ws=None, scale=SCALE, cache=None,
 # relatively, and the sum of the weights too, and by 2^-22 for the exponential.
 # Sums of weights run over at most 2^10 in a row (a thread's columns of a tile,
 # then the tiles), 2^-14 relatively. The weights that multiply V are rounded to
-# fp16, 2^-11, and the result to bf16, 2^-8 of it. Below 2^-25 of the largest
-# weight fp16 has steps of 2^-35 of it (they are kept 2^11 times as large, and the
-# type's last step is 2^-24): such a weight is off by up to 2^-36 of the largest,
+# fp16, 2^-11, and the result to bf16, 2^-8 of it. Below 2^-22 of the largest
+# weight fp16 has steps of 2^-32 of it (they are kept 2^8 times as large, and the
+# type's last step is 2^-24): such a weight is off by up to 2^-33 of the largest,
 # which is at most 1, and a row's result by that times the sum of |v| over what it
 # sees. That sum counts where the weights that count meet zeros in V.
 def chunk_tol(want, mag, err, vsum):
     e = 128 * 2.0 ** -24 * err[..., None]
-    return 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -14 + 2 * e) * mag + 2.0 ** -36 * vsum
+    return 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -14 + 2 * e) * mag + 2.0 ** -33 * vsum
 
 
 def lse_tol(want, err):
