@@ -1,54 +1,697 @@
 // The attention weight that the positions of the paged 4-bit cache receive from
-// chunks of new tokens: mass_p = keep prev_p + sum_i exp(scale q_i.K_p - lse_i).
-// One warp a (request, KV head, position), one row at a time.
+// chunks of new tokens, on the 5th-generation tensor cores:
+// mass_p = keep prev_p + sum_i exp(scale q_i.K_p - lse_i) over the rows that see p.
+//
+// With the rows' lse known the weights need no second pass, so the positions
+// stay put and the rows stream past them. An item is two tiles (A and B) of 128
+// positions of one (request, KV head), dequantised once, against the 128-row
+// tiles of (token, query head of the group) pairs that see them:
+//   S^T[128 positions][N rows] = K Q^T     both in shared memory (128-byte swizzle)
+// A position is one thread's throughout: it reads its row of S^T from tensor
+// memory, takes the exponentials and adds them up, so that nothing is exchanged
+// between threads and every sum has one order. Operands are bf16, the queries'
+// own type, in which a record's values are exact: products are exact and their
+// sums fp32, so that the weights' errors are those of fp32. The exponent is
+// scale s - lse with one rounding, before the factor log2(e). A row tile's sums
+// go into the position's total by a compensated addition.
+//
+// Bound: the exponentials, 16 a clock and SM against 128 * 128 products in 512
+// clocks. See kMsPoly for the share of them that the FMA pipe takes.
+//
+// Work: the items' row tiles (and one unit for an item's fixed part) form a line
+// that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
+// an item that is cut leave their sums in the workspace; of the warps that have
+// the same 32 positions the last to arrive adds them in the order of the pieces.
+//   warps 0-3, 4-7  exponentials and sums of tile A, B
+//   warps 8-11      dequantisation, a record a thread
+//   warp 12         tensor memory, MMA issue
+//   warp 13         schedule, copies of the records (cp.async.bulk)
+//   warp 14         queries (TMA, or by hand where a tile has few rows) and lse
+// Every wait is bounded; see kv4_chunk.cu.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "kv4.cuh"
-#include "spc_device.cuh"
-#include "spc_internal.h"
+#include "kv4_chunk.cuh"
+#include "spc_tc.cuh"
 
 namespace spc {
 
-__global__ void __launch_bounds__(256) kv4_mass_kernel(const Kv4ChunkCall c) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y / c.n_kv, g = blockIdx.y - b * c.n_kv, G = c.n_q / c.n_kv;
-  const int L = max(0, min(c.len[b], c.max_blocks << c.block_shift)), bs = 1 << c.block_shift;
-  const int t0 = max(0, min(c.cu[b], c.T)), n = max(t0, min(c.cu[b + 1], c.T)) - t0;
-  for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < L; p += gridDim.x * 8) {
-    const int blk = c.table[(size_t)b * c.max_blocks + (p >> c.block_shift)];
-    float sum = 0.f;
-    if ((unsigned)blk < (unsigned)c.num_blocks) {
-      const uint8_t* r = c.cache + (((size_t)blk * c.n_kv + g) * bs + (p & (bs - 1))) * kKv4Rec;
-      uint32_t kw[4];
-      e2m1x8_to_f16(*reinterpret_cast<const uint16_t*>(r + 2 * lane), kw);
-      const float ks = f16_lo(e4m3_dup_f16(r[kKv4Scale + lane / 4]));
-      const float k[4] = {f16_lo(kw[0]) * ks, f16_hi(kw[0]) * ks, f16_lo(kw[1]) * ks, f16_hi(kw[1]) * ks};
-      float part = 0.f;                                // of 16 tokens
-      for (int i = max(0, p - (L - n)); i < n; ++i) {
-        for (int h = g * G; h < g * G + G; ++h) {
-          const float lse = c.lse[(size_t)(t0 + i) * c.n_q + h];
-          if (lse == -INFINITY) continue;
-          const uint2 qw = *reinterpret_cast<const uint2*>(c.q + (t0 + i) * c.q_stride + (size_t)h * kD + 4 * lane);
-          const float s = warp_sum(bf_lo(qw.x) * k[0] + bf_hi(qw.x) * k[1] + bf_lo(qw.y) * k[2] + bf_hi(qw.y) * k[3]);
-          part += expf(fmaf(s, c.scale, -lse));
-        }
-        if ((i & 15) == 15 || i == n - 1) {
-          sum += part;
-          part = 0.f;
-        }
-      }
+constexpr int kMsRaw = 3, kMsRun = 16;                // stages of each dequantising warp's ring of records, positions a stage
+constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
+constexpr int kMsK = 4;                               // ring of dequantised K tiles
+constexpr int kMsQ = 2;                               // ring of Q tiles
+constexpr int kMsL = 4;                               // ring of the rows' lse
+constexpr int kMsItems = 2;
+constexpr int kMsMasks = 16;                          // tiles whose masks are kept: the copies are at most 11 ahead of the sums
+constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
+constexpr int kMsWarpDeq = 8, kMsWarpMma = 12, kMsWarpPlan = 13, kMsWarpQ = 14;
+constexpr int kMsThreads = 512;
+constexpr int kMsRegSum = 176, kMsRegDeq = 88, kMsRegRest = 72;
+constexpr int kMsFixed = 1;                           // units of an item's fixed part
+constexpr int kMsTmemCols = 512;                      // S of A and B, two each
+constexpr int kMsPoly = 4;                            // of 16 pairs of columns, those whose exponentials are polynomials
+
+constexpr uint32_t kMsOffK = 0;
+constexpr uint32_t kMsOffQ = kMsOffK + kMsK * kKcTile;
+constexpr uint32_t kMsOffRaw = kMsOffQ + kMsQ * kKcTile;
+constexpr uint32_t kMsOffItem = kMsOffRaw + 4 * kMsRaw * kMsStage;    // [kMsItems] MsItem
+constexpr uint32_t kMsOffLse = kMsOffItem + kMsItems * 64;            // [kMsL][128] -lse
+constexpr uint32_t kMsOffOdd = kMsOffLse + kMsL * 512;                // [kMsL][4 words] rows that add nothing
+constexpr uint32_t kMsOffMask = kMsOffOdd + kMsL * 16;                // [kMsMasks][4 words]
+constexpr uint32_t kMsOffBar = kMsOffMask + kMsMasks * 16;
+constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * 4 + 1;
+constexpr size_t kMsSmem = 1024 + kMsOffBar + kMsBars * 8 + 16;
+static_assert(kMsSmem <= 227 * 1024, "shared memory of one CTA");
+
+// workspace: status; arrival counters (zero between calls) of the items that are
+// cut first in a CTA, [2 tiles][4 warps]; the sums of a CTA's first and last piece
+constexpr size_t kMsOffCount = 256;
+constexpr size_t kMsOffPart = kMsOffCount + (size_t)kKcCtas * 8 * 4;
+constexpr size_t kMsWorkspace = kMsOffPart + (size_t)kKcCtas * 2 * 256 * 4;
+static_assert(kMsOffPart % 256 == 0, "aligned partials");
+
+struct MsArgs {
+  Kv4ChunkCall c;
+  int G, gshift, tpm;      // heads a group, its log2, tokens a row tile
+  int* status;
+  uint32_t* counters;
+  float* part;
+  long long wait_limit;
+  int starve;              // test builds: no copy is issued, so that every wait runs out
+};
+
+struct MsItem {
+  int b, g, p0;            // request (-1: no more items), KV head, first position
+  int row0, n, len;        // the request's first row, new tokens and positions
+  int tiles;               // of positions: 1 or 2
+  int r0, r1;              // the piece's row tiles; none where the request has no new tokens
+  int pieces, piece, first;  // of the item, and its first CTA
+  int pad[4];
+};
+static_assert(sizeof(MsItem) == 64, "item ring");
+
+// ---------------------------------------------------------------- exponentials
+// 2^t of two values on the FMA pipe: t = i + r with i the nearest integer, 2^r by
+// its Taylor polynomial in r ln 2 up to the sixth power (|r| <= 1/2: off by less
+// than 2^-22), times 2^i put together from its bits. Below 2^-126 the result is 0, from
+// 2^128 on infinity; NaN stays NaN.
+__device__ __forceinline__ float2 ms_exp2_poly(float2 t) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(-127.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(128.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(128.f));
+  constexpr float kMagic = 12582912.f;                // 1.5 * 2^23: the integer ends up in the low bits
+  const float2 im = add2(t, make_float2(kMagic, kMagic));
+  const float2 i = add2(im, make_float2(-kMagic, -kMagic));
+  const float2 r = add2(t, make_float2(-i.x, -i.y));
+  constexpr float L = 0.6931471805599453f;
+  constexpr float c6 = L * L * L * L * L * L / 720.f, c5 = L * L * L * L * L / 120.f, c4 = L * L * L * L / 24.f,
+                  c3 = L * L * L / 6.f, c2 = L * L / 2.f;
+  float2 p = fma2(make_float2(c6, c6), r, make_float2(c5, c5));
+  p = fma2(p, r, make_float2(c4, c4));
+  p = fma2(p, r, make_float2(c3, c3));
+  p = fma2(p, r, make_float2(c2, c2));
+  p = fma2(p, r, make_float2(L, L));
+  p = fma2(p, r, make_float2(1.f, 1.f));
+  const float2 s = make_float2(__int_as_float((__float_as_int(im.x) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(im.y) << 23) + 0x3f800000));
+  return fma2(p, s, make_float2(0.f, 0.f));
+}
+
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A row of 128 K values of 64 bytes of codes and 8 scales as bf16 into row r of a
+// swizzled tile. A code as fp16 has at most one bit of mantissa; its bits three
+// places further down are bf16's of the value times 2^-112, which the scale, an
+// e4m3 number times 2^112, takes back: the product is exact.
+__device__ __forceinline__ void ms_row(const uint4* codes, uint2 sc, uint32_t tile, int r) {
+  const uint32_t dst = tile + (uint32_t)r * 128u, r7 = (uint32_t)r & 7u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t s2 = e4m3x2_to_f16(((q < 2 ? sc.x : sc.y) >> (16 * (q & 1))) & 0xffffu);
+    const float f0 = f16_lo(s2) * 5.192296858534828e33f, f1 = f16_hi(s2) * 5.192296858534828e33f;   // 2^112
+    const uint32_t s[2] = {pack_bf16(f0, f0), pack_bf16(f1, f1)};
+    const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t h[4];
+      e2m1x8_to_f16(w[e], h);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) h[f] = bmul2(((h[f] >> 3) & 0x0fff0fffu) | (h[f] & 0x80008000u), s[e >> 1]);
+      const uint32_t u = 4 * q + e;
+      sts_v4(dst + (u >> 3) * kKcBlock + (((u & 7u) ^ r7) << 4), h[0], h[1], h[2], h[3]);
     }
-    const size_t at = ((size_t)b * c.n_kv + g) * c.cap + p;
-    if (lane == 0) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, c.mass_prev[at], sum) : sum;
   }
 }
 
-size_t kv4_mass_workspace(int, int, int, int) { return 256; }
+// ---------------------------------------------------------------- the line of work
+// Item i of a request's head holds positions [256 i, 256 i + 256); its row tiles
+// are those from the first that sees one of them on, max(0, 2 G i - cd) of nt,
+// cd = ceil((len - n) / tpm). A request without new tokens has one unit an item.
+struct MsShape {
+  int n, len, nt, cd, items, G2;
+};
+__device__ __forceinline__ MsShape ms_shape(const MsArgs& a, int len, int n) {
+  const int lt = 7 - a.gshift;
+  MsShape s;
+  s.n = n;
+  s.len = len;
+  s.nt = (n + a.tpm - 1) >> lt;
+  s.cd = -((n - len) >> lt);
+  s.items = (len + 255) >> 8;
+  s.G2 = 2 * a.G;
+  return s;
+}
+__device__ __forceinline__ int ms_first(const MsShape& s, int i) { return max(0, s.G2 * i - s.cd); }
+__device__ __forceinline__ long long ms_units(const MsShape& s, int k) {   // of the items below k
+  if (s.n == 0) return k;
+  // the first item that some row tile does not see, and from there on an arithmetic progression
+  const int k0 = s.cd < 0 ? 0 : min(k, s.cd / s.G2 + 1);
+  const long long m = k - k0;
+  return (long long)k * (kMsFixed + s.nt) - ((long long)s.G2 * (k - 1 + k0) * m / 2 - (long long)s.cd * m);
+}
 
-int kv4_mass_launch(const Kv4ChunkCall& c, void*, void* stream) {
-  const int blocks = ((c.max_blocks << c.block_shift) + 7) / 8;
-  kv4_mass_kernel<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096), (unsigned)(c.B * c.n_kv)), 256, 0,
-                    static_cast<cudaStream_t>(stream)>>>(c);
+__global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_constant__ CUtensorMap qmap, const MsArgs a) {
+  extern __shared__ uint8_t ms_raw[];
+  const uint32_t raw_addr = smem_u32(ms_raw);
+  uint8_t* base = ms_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  MsItem* items = reinterpret_cast<MsItem*>(base + kMsOffItem);
+  float* neglse = reinterpret_cast<float*>(base + kMsOffLse);
+  uint32_t* odds = reinterpret_cast<uint32_t*>(base + kMsOffOdd);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(base + kMsOffMask);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kMsOffBar);
+  uint64_t* rfull = bars;                     // [4 warps][kMsRaw] bytes of the records
+  uint64_t* rfree = rfull + 4 * kMsRaw;       // [4][kMsRaw] the warp has read them
+  uint64_t* kfull = rfree + 4 * kMsRaw;       // [kMsK] four dequantising warps have written the tile
+  uint64_t* kfree = kfull + kMsK;             // [kMsK] commit after the last MMA that reads it
+  uint64_t* qfull = kfree + kMsK;             // [kMsQ] the tile's rows are there
+  uint64_t* qfree = qfull + kMsQ;             // [kMsQ] commit after the MMAs that read them
+  uint64_t* lfull = qfree + kMsQ;             // [kMsL] the rows' lse are there
+  uint64_t* lfree = lfull + kMsL;             // [kMsL] eight summing warps have read them
+  uint64_t* ifull = lfree + kMsL;             // [kMsItems]
+  uint64_t* ifree = ifull + kMsItems;         // [kMsItems]
+  uint64_t* sfull = ifree + kMsItems;         // [2 tiles][2] commit: S in tensor memory
+  uint64_t* sfree = sfull + 4;                // [2][2] four summing warps have read it
+  uint64_t* drain = sfree + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const Kv4ChunkCall& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4 * kMsRaw; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rfree[s], 1);
+    }
+    for (int s = 0; s < kMsK; ++s) {
+      mbar_init(&kfull[s], 4);
+      mbar_init(&kfree[s], 1);
+    }
+    for (int s = 0; s < kMsQ; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qfree[s], 1);
+    }
+    for (int s = 0; s < kMsL; ++s) {
+      mbar_init(&lfull[s], 1);
+      mbar_init(&lfree[s], 8);
+    }
+    for (int s = 0; s < kMsItems; ++s) {
+      mbar_init(&ifull[s], 1);
+      mbar_init(&ifree[s], 4 + 8 + 2);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sfree[s], 4);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMsWarpMma) tmem_alloc<kMsTmemCols>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t ks = smem_u32(base + kMsOffK), qs = smem_u32(base + kMsOffQ);
+  bool dead = false;
+  auto acquire = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !__all_sync(0xffffffffu, mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, a.wait_limit))) {
+      if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+      dead = true;
+    }
+  };
+
+  if (warp == kMsWarpPlan) {
+    // ================= schedule and copies of the records
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
+    const int bs = 1 << c.block_shift;
+    KcRequests rq;
+    kc_requests(c, rq);
+    long long own[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const MsShape s = ms_shape(a, rq.len[e], rq.n[e]);
+      own[e] = ms_units(s, s.items);
+    }
+    const long long total = kc_prefix(rq, own[0] * c.n_kv, own[1] * c.n_kv);
+    const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    const bool has = (int)blockIdx.x < ctas;
+    const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
+    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+    int b = 0, g = 0, i = 0;
+    long long at = 0, whole = 1;
+    MsShape s{};
+    auto enter = [&](int request) {
+      b = request;
+      s = ms_shape(a, kc_of(rq.len, b), kc_of(rq.n, b));
+      whole = __shfl_sync(0xffffffffu, b & 1 ? own[1] : own[0], b >> 1);
+    };
+    if (has) {
+      enter(kc_find(rq, u0));
+      long long r = u0 - (kc_of(rq.end, b) - whole * c.n_kv);
+      g = (int)(r / whole);
+      r -= (long long)g * whole;
+      int lo = 0, hi = s.items;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ms_units(s, mid) <= r) lo = mid; else hi = mid;
+      }
+      i = lo;
+      at = u0 - r + ms_units(s, i);
+    }
+    int it = 0, blocks = 0, nraw = 0;
+    for (;;) {
+      MsItem x;
+      x.b = -1;
+      bool skip = false;
+      int fixed = 0, nu = 1;
+      if (has && at < u1) {
+        const int q = ms_first(s, i);
+        fixed = s.n ? kMsFixed : 0;
+        nu = s.n ? s.nt - q : 1;
+      }
+      if (has && at < u1 && !dead) {
+        const long long first = at + fixed;
+        const int lo = (int)max(0ll, u0 - first), hi = (int)min((long long)nu, u1 - first);
+        skip = hi <= lo;
+        if (!skip) {
+          x.b = b;
+          x.g = g;
+          x.p0 = i << 8;
+          x.row0 = kc_of(rq.row0, b);
+          x.n = s.n;
+          x.len = s.len;
+          x.tiles = x.p0 + 128 < s.len ? 2 : 1;
+          x.r0 = s.n ? s.nt - nu + lo : 0;
+          x.r1 = s.n ? s.nt - nu + hi : 0;
+          x.first = cta_of(first);
+          x.pieces = cta_of(first + nu - 1) - x.first + 1;
+          x.piece = (int)blockIdx.x - x.first;
+        }
+      }
+      if (!skip) {
+        const int is = it % kMsItems;
+        acquire(&ifree[is], ((it / kMsItems) & 1) ^ 1);
+        if (lane == 0) {
+          items[is] = x;
+          mbar_arrive(&ifull[is]);
+        }
+        __syncwarp();
+        ++it;
+        if (x.b < 0) break;
+#ifdef SPC_TEST_HOOKS
+        if (a.starve) break;
+#endif
+        KcTable t;
+        if (x.n) t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
+        // lane w copies for dequantising warp w
+        for (int j = 0; x.n && j < x.tiles && !dead; ++j, ++blocks) {
+          uint32_t mask = 0u;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h, ++nraw) {
+            const int st = nraw % kMsRaw, p = x.p0 + j * 128 + (lane & 3) * 32 + h * kMsRun;
+            const int blk = t.entry((x.p0 + j * 128) >> c.block_shift, p >> c.block_shift);
+            const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kMsRun)) : 0;
+            mask |= ((1u << n) - 1u) << (h * kMsRun);
+            uint64_t* bar = &rfull[(lane & 3) * kMsRaw + st];
+            acquire(&rfree[(lane & 3) * kMsRaw + st], ((nraw / kMsRaw) & 1) ^ 1);
+            if (dead) break;
+            if (lane < 4) {
+              if (h == 1) masks[(blocks % kMsMasks) * 4 + lane] = mask;
+              if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
+              if (n > 0)
+                bulk_g2s(base + kMsOffRaw + (lane * kMsRaw + st) * kMsStage,
+                         c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // the next item
+      at += fixed + nu;
+      if (++i == s.items) {
+        i = 0;
+        if (++g == c.n_kv) {
+          g = 0;
+          if (at < u1) enter(kc_find(rq, at));
+        }
+      }
+    }
+    // every copy lands before the CTA ends (they have, unless a role gave up)
+    if (lane < 4)
+      for (int k = max(0, nraw - kMsRaw); k < nraw; ++k)
+        mbar_wait_bounded(&rfull[lane * kMsRaw + k % kMsRaw], (k / kMsRaw) & 1, a.wait_limit);
+    __syncwarp();
+  } else if (warp == kMsWarpQ) {
+    // ================= queries and lse of the row tiles
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
+    int nq = 0;
+    for (int it = 0;; ++it) {
+      const int is = it % kMsItems;
+      acquire(&ifull[is], (it / kMsItems) & 1);
+      if (dead) break;
+      const MsItem x = items[is];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (x.b < 0) break;
+#ifdef SPC_TEST_HOOKS
+      if (a.starve) break;
+#endif
+      // row r of a tile whose first token is tok
+      auto lse_of = [&](int tok, int r) {
+        const int t = tok + (r >> a.gshift);
+        return t < x.n ? c.lse[(size_t)(x.row0 + t) * c.n_q + (x.g << a.gshift) + (r & (a.G - 1))] : 0.f;
+      };
+      float next[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = lse_of(x.r0 * a.tpm, 32 * e + lane);
+      for (int r = x.r0; r < x.r1; ++r, ++nq) {
+        const int st = nq % kMsQ, tok = r * a.tpm, rows = min(128, (x.n - tok) << a.gshift);
+        acquire(&qfree[st], ((nq / kMsQ) & 1) ^ 1);
+        if (dead) break;
+        if (rows > kMsHand) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&qfull[st], kKcTile);
+            tma_load_3d(qs + st * kKcTile, &qmap, 0, x.g << a.gshift, x.row0 + tok, &qfull[st]);
+            tma_load_3d(qs + st * kKcTile + kKcBlock, &qmap, 64, x.g << a.gshift, x.row0 + tok, &qfull[st]);
+          }
+          __syncwarp();
+        } else {
+          // 16 pieces of 16 bytes a row; rows that are not there are zeros up to the MMA's multiple of 16
+          const int all = ((rows + 15) & ~15) * 16;
+#pragma unroll 1
+          for (int e0 = lane; e0 < all; e0 += 4 * 32) {
+            uint4 v[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int e = e0 + 32 * f, row = e >> 4;
+              v[f] = make_uint4(0u, 0u, 0u, 0u);
+              if (e < all && row < rows)
+                v[f] = *reinterpret_cast<const uint4*>(c.q + (x.row0 + tok + (row >> a.gshift)) * c.q_stride +
+                                                       (size_t)((x.g << a.gshift) + (row & (a.G - 1))) * kD + (e & 15) * 8);
+            }
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int e = e0 + 32 * f, row = e >> 4, u = e & 15;
+              if (e < all)
+                sts_v4(qs + st * kKcTile + (u >> 3) * kKcBlock + row * 128 + (((u & 7) ^ (row & 7)) << 4), v[f].x, v[f].y, v[f].z,
+                       v[f].w);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&qfull[st]);
+        }
+        const int ls = nq % kMsL;
+        acquire(&lfree[ls], ((nq / kMsL) & 1) ^ 1);
+        if (dead) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          neglse[ls * 128 + 32 * e + lane] = -next[e];
+          const uint32_t odd = __ballot_sync(0xffffffffu, next[e] == -INFINITY);
+          if (lane == 0) odds[ls * 4 + e] = odd;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lfull[ls]);
+        if (r + 1 < x.r1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) next[e] = lse_of(tok + a.tpm, 32 * e + lane);
+        }
+      }
+      if (dead) break;
+    }
+    if (lane == 0)
+      for (int k = max(0, nq - kMsQ); k < nq; ++k) mbar_wait_bounded(&qfull[k % kMsQ], (k / kMsQ) & 1, a.wait_limit);
+    __syncwarp();
+  } else if (warp == kMsWarpMma) {
+    // ================= MMA issue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int nk = 0, nq = 0, ns[2] = {0, 0};
+    for (int it = 0;; ++it) {
+      const int is = it % kMsItems;
+      acquire(&ifull[is], (it / kMsItems) & 1);
+      if (dead) break;
+      const int b = items[is].b, n = items[is].n, r0 = items[is].r0, r1 = items[is].r1, tiles = items[is].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (b < 0) break;
+      if (n == 0) continue;
+      for (int j = 0; j < tiles; ++j) acquire(&kfull[(nk + j) % kMsK], ((nk + j) / kMsK) & 1);
+      for (int r = r0; r < r1 && !dead; ++r, ++nq) {
+        const int st = nq % kMsQ, N = min(128, (((n - r * a.tpm) << a.gshift) + 15) & ~15);
+        acquire(&lfull[nq % kMsL], (nq / kMsL) & 1);
+        acquire(&qfull[st], (nq / kMsQ) & 1);
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          const int buf = ns[j] & 1;
+          acquire(&sfree[j * 2 + buf], ((ns[j] >> 1) & 1) ^ 1);
+          ++ns[j];
+          if (dead) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kd = umma_desc_lo(ks) + (uint32_t)((nk + j) % kMsK) * (kKcTile >> 4);
+            const uint32_t qd = umma_desc_lo(qs) + (uint32_t)st * (kKcTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kD / 16; ++kk) {
+              const uint32_t off = (uint32_t)(kk >> 2) * (kKcBlock >> 4) + (uint32_t)(kk & 3) * 2;
+              umma_f16(tm + (uint32_t)(j * 2 + buf) * 128, umma_desc(kd + off), umma_desc(qd + off), idesc, kk ? 1u : 0u);
+            }
+            umma_commit(&sfull[j * 2 + buf]);
+            if (j + 1 == tiles) umma_commit(&qfree[st]);
+            if (r + 1 == r1) umma_commit(&kfree[(nk + j) % kMsK]);
+          }
+          __syncwarp();
+        }
+      }
+      nk += tiles;
+      if (dead) break;
+    }
+    if (elect_one()) umma_commit(drain);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(drain, 0, a.wait_limit)) && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+  } else if (warp >= kMsWarpDeq && warp < kMsWarpDeq + 4) {
+    // ================= dequantisation, a record a thread
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegDeq));
+    const int w = warp - kMsWarpDeq, r = threadIdx.x & 127;
+    int nk = 0, nread = 0;
+    for (int it = 0;; ++it) {
+      const int is = it % kMsItems;
+      acquire(&ifull[is], (it / kMsItems) & 1);
+      if (dead) break;
+      const int b = items[is].b, tiles = items[is].n ? items[is].tiles : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (b < 0) break;
+      for (int j = 0; j < tiles; ++j, ++nk) {
+        const int s0 = nread % kMsRaw, s1 = (nread + 1) % kMsRaw;
+        acquire(&rfull[w * kMsRaw + s0], (nread / kMsRaw) & 1);
+        acquire(&rfull[w * kMsRaw + s1], ((nread + 1) / kMsRaw) & 1);
+        if (dead) break;
+        nread += 2;
+        const uint32_t rec = smem_u32(base + kMsOffRaw) + (uint32_t)(w * kMsRaw + (lane < kMsRun ? s0 : s1)) * kMsStage +
+                             (uint32_t)(lane & (kMsRun - 1)) * kKv4Rec;
+        const bool there = masks[(nk % kMsMasks) * 4 + w] >> lane & 1;
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = lds_v4(rec + 16 * q);
+        uint2 sc = lds_v2(rec + kKv4Scale);
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&rfree[w * kMsRaw + (lane ? s1 : s0)]);
+        if (!there) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
+          sc = make_uint2(0u, 0u);
+        }
+        const int slot = nk % kMsK;
+        acquire(&kfree[slot], ((nk / kMsK) & 1) ^ 1);
+        if (dead) break;
+        ms_row(v, sc, ks + (uint32_t)slot * kKcTile, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kfull[slot]);
+      }
+      if (dead) break;
+    }
+  } else if (warp < kMsWarpDeq) {
+    // ================= exponentials and sums of tile j, one position a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kMsRegSum));
+    const int j = warp >> 2, wq = warp & 3;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    int ns = 0, nq = 0, nk = 0;
+    for (int it = 0;; ++it) {
+      const int is = it % kMsItems;
+      acquire(&ifull[is], (it / kMsItems) & 1);
+      if (dead) break;
+      const MsItem x = items[is];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (x.b < 0) break;
+      const int p = x.p0 + j * 128 + wq * 32 + lane;
+      const size_t at = ((size_t)x.b * c.n_kv + x.g) * c.cap + p;
+      const bool mine = j < x.tiles && p < x.len;
+      const float prev = mine && c.keep != 0.f ? c.mass_prev[at] : 0.f;
+      float total = 0.f, lost = 0.f;
+      bool there = false;
+      for (int r = x.r0; r < x.r1; ++r, ++nq) {
+        if (j >= x.tiles) {                           // the item has no tile B
+          // its lse are read by nobody here, but only once they are there may they be released
+          acquire(&lfull[nq % kMsL], (nq / kMsL) & 1);
+          if (dead) break;
+          if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
+          continue;
+        }
+        const int buf = ns & 1;
+        acquire(&sfull[j * 2 + buf], (ns >> 1) & 1);
+        if (dead) break;
+        ++ns;
+        tc_fence_after();
+        there = masks[((nk + j) % kMsMasks) * 4 + wq] >> lane & 1;
+        const int tok = r * a.tpm, cols = min(128, (x.n - tok) << a.gshift);
+        const float* nl = neglse + (nq % kMsL) * 128;
+        const uint4 odd = *reinterpret_cast<const uint4*>(odds + (nq % kMsL) * 4);
+        const uint32_t ts = tmem + lanes + (uint32_t)(j * 2 + buf) * 128;
+        const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
+        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // columns from this one on are tokens at or behind the position
+        const long long from = (long long)(p - (x.len - x.n) - tok) << a.gshift;
+        if (cols == 128 && (odd.x | odd.y | odd.z | odd.w) == 0u && __all_sync(0xffffffffu, from <= 0)) {
+          float s[2][32];
+          tmem_ld32(ts, s[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait32(s[q & 1]);
+            if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * e);
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                float2 t = fma2(make_float2(s[q & 1][4 * e + 2 * f], s[q & 1][4 * e + 2 * f + 1]), sc,
+                                f ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                t = fma2(t, l2e, make_float2(0.f, 0.f));
+                if ((2 * e + f) * kMsPoly % 16 < kMsPoly) {
+                  t = ms_exp2_poly(t);
+                } else {
+                  t.x = ex2_approx(t.x);
+                  t.y = ex2_approx(t.y);
+                }
+                sum[(2 * e + f) & 3] = add2(sum[(2 * e + f) & 3], t);
+              }
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; 32 * q < cols; ++q) {
+            float s[32];
+            tmem_ld32(ts + 32 * q, s);
+            tmem_ld_wait32(s);
+            const long long lo = from - 32 * q;
+            const int hi = cols - 32 * q;
+            const uint32_t vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : 0xffffffffu << (int)lo) &
+                                 (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) &
+                                 ~(q == 0 ? odd.x : q == 1 ? odd.y : q == 2 ? odd.z : odd.w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float t = ex2_approx(fmaf(s[e], c.scale, nl[32 * q + e]) * kLog2e);
+              sum[e & 3].x += vis >> e & 1 ? t : 0.f;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sfree[j * 2 + buf]);
+          mbar_arrive(&lfree[nq % kMsL]);
+        }
+        // the tile's sum into the total, what the addition loses kept beside it
+        const float y = ((sum[0].x + sum[1].x) + (sum[2].x + sum[3].x)) + ((sum[0].y + sum[1].y) + (sum[2].y + sum[3].y));
+        const float u = total + y, v = u - total;
+        lost += (total - (u - v)) + (y - v);
+        total = u;
+      }
+      if (dead) break;
+      if (x.n) nk += x.tiles;
+      // infinities and NaN are the sum's own; their difference above is not
+      float sum = total + (fabsf(total) < INFINITY ? lost : 0.f);
+      if (!there) sum = 0.f;
+      if (j >= x.tiles) continue;
+      if (x.pieces > 1) {
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (x.piece == 0 ? 1 : 0)) * 256 + j * 128 + wq * 32 + lane;
+        *part = sum;
+        __threadfence();
+        __syncwarp();
+        uint32_t* count = a.counters + x.first * 8 + j * 4 + wq;
+        uint32_t before = 0u;
+        if (lane == 0) before = atomicAdd(count, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before + 1u != (uint32_t)x.pieces) continue;
+        __threadfence();
+        sum = 0.f;
+        for (int k = 0; k < x.pieces; ++k)
+          sum += __ldcg(a.part + ((size_t)(x.first + k) * 2 + (k == 0 ? 1 : 0)) * 256 + j * 128 + wq * 32 + lane);
+        if (lane == 0) atomicExch(count, 0u);
+      }
+      if (mine) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, prev, sum) : sum;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMsWarpMma) {
+    tc_fence_after();
+    tmem_dealloc<kMsTmemCols>(tmem);
+  }
+}
+
+size_t kv4_mass_workspace(int, int, int, int) { return kMsWorkspace; }
+
+int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
+  MsArgs a{};
+  a.c = c;
+  a.G = c.n_q / c.n_kv;
+  while ((1 << a.gshift) < a.G) ++a.gshift;
+  a.tpm = 128 >> a.gshift;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<int*>(w);
+  a.counters = reinterpret_cast<uint32_t*>(w + kMsOffCount);
+  a.part = reinterpret_cast<float*>(w + kMsOffPart);
+  a.wait_limit = kKcWait;
+#ifdef SPC_TEST_HOOKS
+  a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
+#endif
+  CUtensorMap qmap{};
+  const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)c.n_q, (uint64_t)c.T};
+  const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)c.q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
+  if (c.T > 0 && !tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
+  if (set_func_attr((const void*)kv4_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMsSmem) != cudaSuccess)
+    return SPC_ERR_CUDA;
+  kv4_mass_kernel<<<kKcCtas, kMsThreads, kMsSmem, static_cast<cudaStream_t>(stream)>>>(qmap, a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
