@@ -673,14 +673,14 @@ int spc_kv4_attn_mass(const void* q, const void* cache, const int32_t* block_tab
  * The blocks behind the kept ones go back with spc_block_map(len, len_next), and
  * new positions then follow at K. Positions that later calls name are places in
  * the shorter cache; kept says where they came from. With block_table_next =
- * block_table the cache shrinks in place. A different table (its entries i < ceil(K /
- * block_size) name blocks that no other row uses) leaves the old records as they
- * were, where requests share them. A request with a table entry outside [0,
+ * block_table the cache shrinks in place. A different table leaves the old records
+ * as they were, where requests share them; entry i < ceil(K / block_size) of its rows is
+ * entry i of block_table's row or a block of no row of block_table. A request with a table entry outside [0,
  * num_blocks) among those is left as it was, with SPC_ERR_INVALID_ARG in the
  * status word: len_next = L, kept = -1, mass_next = mass.
  * cache      written; block_table, block_table_next int32 [B][max_blocks]. No block
- *            that is written may occur twice in block_table_next, nor in another
- *            request's row of block_table.
+ *            that is written may occur twice in block_table_next, nor at another
+ *            place of block_table.
  * mass, mass_next fp32 [B][n_kv][cap], cap >= max_blocks * block_size; entries p >= L are left as they
  *            were. mass_next may be mass. len, len_next int32 [B], not the same.
  * kept       int32 [B][n_kv][budget], or NULL. status int32 [1], zeroed by the caller.

@@ -122,11 +122,11 @@ def test_into_other_blocks(budget):
 
 
 def test_into_blocks_that_are_partly_its_own():
-    """The next table may name the request's blocks in another order, beside new ones."""
+    """Some of the request's blocks keep their places, the others are new."""
     rng = np.random.default_rng(1)
     c = pool(rng, [1000, 600], 2, 16, spare=40)
     nxt = other_blocks(c, 300)
-    nxt[0, :10], nxt[1, :6] = c.table[0, 5:15][::-1], c.table[1, 30:36]
+    nxt[0, :10], nxt[1, 3:6] = c.table[0, :10], c.table[1, 3:6]
     Call(c, sums(rng, c), 300, 4, 16, table_next=nxt)().check()
 
 
@@ -136,6 +136,18 @@ def test_the_largest():
     Call(c, sums(rng, c), 4096, 4, 64)().check()
     c = pool(rng, [70000, 262144 // 4], 4, 64, max_blocks=4096)
     Call(c, sums(rng, c, kind="near"), 4096, 0, 0, in_place=True)().check()
+
+
+@pytest.mark.parametrize("n", [16384, 16385, 32768, 40000, 65536, 70000, 131072, 140000])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_every_number_of_ranks(n, in_place):
+    """A rank has 16384 positions: one to eight ranks, the last ones with little or nothing."""
+    rng = np.random.default_rng(n)
+    c = pool(rng, [n, n // 3], 1, 16)
+    m = sums(rng, c)
+    m[0, 0, n - 5000:] *= 1e6                                # most of what is kept lies behind
+    for budget in (100, 2100, 4096):
+        Call(c, m.copy(), budget, 4, 64, in_place=in_place)().check()
 
 
 def test_many_requests_and_heads():
