@@ -11,7 +11,8 @@
 // The tensor cores work on one tile while the other one's softmax runs. A
 // request's last tile, if it has no partner (and with few new tokens it is the
 // only one), takes both places: A runs over the even blocks and B over the odd
-// ones, and their results are merged.
+// ones, and A's warps merge what B's have found (a warp of B has the same tensor
+// memory lanes, so that only maxima and sums go through shared memory).
 //
 // Operands are fp16. A record's values are exact there; 11 bits of P instead of
 // bf16's 8; and e2m1 to fp16 is one conversion for two values. Queries are scaled
@@ -35,11 +36,9 @@
 // get NaN there.
 //
 // Work: the items' blocks (and one unit for an item's fixed part) form a line
-// that is cut into equal runs, one a CTA (persistent, one per SM). An item that
-// is cut, or whose tile took both places, leaves partials (O, maximum, sum) in
-// the workspace; of the warps that have the same 32 rows in their pieces the last
-// to arrive merges them, in the order of the positions, so that the result does
-// not depend on the order of arrival.
+// that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
+// an item that is cut leave partials (O, maximum, sum) in the workspace, which a
+// second kernel merges, a warp a row, in the order of the positions.
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
 //   warps 8-11      dequantisation into a ring of four 32 KB operands: K_j, V_j, K_j+1, ...
 //   warp 12         tensor memory, MMA issue
@@ -77,6 +76,7 @@ constexpr int kKcRegSoft = 176, kKcRegDeq = 88, kKcRegRest = 72;
 constexpr float kKcBias = 8.f;                        // log2 of the factor of the weights
 constexpr float kKcHeadroom = 7.75f;                  // log2 growth allowed before a maximum is raised
 constexpr int kKcFixed = 1;                           // units of an item's fixed part
+constexpr int kKcMinRun = 3;                          // units a CTA takes at least
 constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kKcColO = 256;
 constexpr uint32_t kKcIdescS = (1u << 4) | ((uint32_t)(kKcKeys >> 3) << 17) | (8u << 24);
@@ -90,29 +90,19 @@ constexpr uint32_t kKcOffRaw = kKcOffKv + kKcSlots * kKcTile;
 constexpr uint32_t kKcOffItem = kKcOffRaw + 4 * kKcRaw * kKcStage;        // [kKcItems] KcItem
 constexpr uint32_t kKcOffNan = kKcOffItem + kKcItems * 64;            // [kKcItems][8] first position with a NaN V scale
 constexpr uint32_t kKcOffMask = kKcOffNan + kKcItems * 32;            // [kKcMasks][4 words]
-constexpr uint32_t kKcOffBar = kKcOffMask + kKcMasks * 16;
-constexpr int kKcBars = 8 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 1;
+constexpr uint32_t kKcOffMl = kKcOffMask + kKcMasks * 16;              // [128] maximum and sum of tile B's row, for tile A
+constexpr uint32_t kKcOffBar = kKcOffMl + 128 * 8;
+constexpr int kKcBars = 8 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 2 * 4 + 1;
 constexpr size_t kKcSmem = 1024 + kKcOffBar + kKcBars * 8 + 16;
 static_assert(kKcSmem <= 227 * 1024, "shared memory of one CTA");
 
-// workspace: status; arrival counters (zero between calls), a warp's rows each,
-// per CTA of the items that are cut first there and of two whole items in turn;
-// partials, per CTA of its first and last piece and of two whole items, two tiles each
-constexpr size_t kKcOffCount = 256;
-constexpr size_t kKcOffPart = kKcOffCount + (size_t)kKcCtas * 3 * 8 * 4 + 256;
-constexpr int kKcPart = kD + 4;                       // a row's partial: O[128], m, l
-static_assert(kKcOffPart % 256 == 0, "aligned partials");
-
-struct KcArgs {
-  Kv4ChunkCall c;
-  int G, gshift, tpm;      // heads a group, its log2, tokens a tile
-  int part_rows;           // rows of a tile that can be new tokens'
-  int* status;
-  uint32_t* counters;
-  float* part;
-  long long wait_limit;
-  int starve;              // test builds: no copy is issued, so that every wait runs out
-};
+// workspace: status; for each CTA the item that is cut first there; partials, of
+// a CTA's first and last piece, two tiles each
+constexpr size_t kKcOffCut = 256;
+constexpr size_t kKcOffPart = kKcOffCut + (size_t)kKcCtas * 64;
+constexpr int kKcPart = kD + 4;                       // a row's partial: O[128], maximum, sum, their factor and the queries' scale
+static_assert(kKcOffPart % 128 == 0, "aligned partials");
+constexpr int kKcMergeThreads = 256;
 
 struct KcItem {
   int row0, n;             // the request's first row and new tokens; n < 0: no more items
@@ -121,10 +111,21 @@ struct KcItem {
   int n0, n1;              // how many of them tile A and B take
   int single;              // one tile in both places
   int pieces, piece, first;  // of the item, and its first CTA
-  int direct;              // nothing to merge
-  int pad[2];
+  int pad[3];
 };
 static_assert(sizeof(KcItem) == 64, "item ring");
+
+struct KcArgs {
+  Kv4ChunkCall c;
+  int G, gshift, tpm;      // heads a group, its log2, tokens a tile
+  int part_rows;           // rows of a tile that can be new tokens'
+  int* status;
+  KcItem* cut;
+  float* part;
+  long long wait_limit;
+  int starve;              // test builds: no copy is issued, so that every wait runs out
+};
+
 
 __device__ __forceinline__ bool kc_wait(const KcArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
@@ -220,60 +221,63 @@ __device__ __forceinline__ int kc_item_units(const KcShape& s, int i) {
   return 2 * i + 2 > kc_tiles(s) ? (nb + 1) >> 1 : nb;
 }
 
-// The partials of a warp's 32 rows merged by the last of their pieces' warps.
-// Every lane has its own row's factor and inverse query scale.
-__device__ void kc_merge(const KcArgs& a, const KcItem& x, int slot0, int i, int w, int live, float f, float inv, int token,
-                         int h) {
+__device__ __forceinline__ float kc_lse(const KcArgs& a, float m, float l, float inv) {
+  return l == 0.f ? -INFINITY : m * inv * a.c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
+}
+__device__ __forceinline__ float* kc_part(const KcArgs& a, int cta, int last, int tile, int row) {
+  return a.part + ((((size_t)cta * 2 + last) * 2 + tile) * a.part_rows + row) * kKcPart;
+}
+
+// The partials of the items that are cut, a warp a row.
+__global__ void __launch_bounds__(kKcMergeThreads) kv4_chunk_merge_kernel(const KcArgs a) {
   const Kv4ChunkCall& c = a.c;
-  const int lane = threadIdx.x & 31, places = x.single ? 2 : 1, n = x.pieces * places;
-  auto part = [&](int k, int row) {                   // contribution k, in the order of the pieces
-    const int p = x.single ? k >> 1 : k, tile = x.single ? k & 1 : i;
-    const int cta = x.first + p, slot = x.pieces == 1 ? slot0 : p == 0 ? 1 : 0;
-    return a.part + ((((size_t)cta * 4 + slot) * 2 + tile) * a.part_rows + row) * kKcPart;
-  };
-  const int row = w * 32 + lane;
-  float M = -INFINITY, l = 0.f;
-  if (lane < live)
-    for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(part(k, row) + kD));
-  if (lane < live)
-    for (int k = 0; k < n; ++k) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(k, row) + kD));
-      if (ml.y != 0.f) l += ml.y * ex2_approx((ml.x - M) * f);
-    }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  if (lane < live && c.lse)
-    c.lse[(size_t)(x.row0 + token) * c.n_q + h] =
-        l == 0.f ? -INFINITY : M * inv * c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
-  for (int rr = 0; rr < live; ++rr) {
-    const float Mr = __shfl_sync(0xffffffffu, M, rr), fr = __shfl_sync(0xffffffffu, f, rr), nr = __shfl_sync(0xffffffffu, r, rr);
-    const int tok = __shfl_sync(0xffffffffu, token, rr), hh = __shfl_sync(0xffffffffu, h, rr);
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int U = 4;
-    for (int k0 = 0; k0 < n; k0 += U) {
-      float2 ml[U];
-      float4 v[U];
+  const KcItem x = a.cut[blockIdx.x];
+  const int lane = threadIdx.x & 31, i = blockIdx.z;
+  if (x.pieces < 2 || (x.single && i)) return;
+  const int t0 = x.t0 + i * a.tpm;
+  const long long live = (long long)(x.n - t0) << a.gshift;
+  for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(live, (long long)blockIdx.y * 32 + 32) && row < 128;
+       row += kKcMergeThreads / 32) {
+    // piece k is its CTA's last one for k = 0, else its first
+    auto part = [&](int k) { return kc_part(a, x.first + k, k == 0, i, row); };
+    float M = -INFINITY, l = 0.f;
+    for (int k = lane; k < x.pieces; k += 32) M = fmaxf(M, part(k)[kD]);
+    M = warp_max(M);
+    const float f = part(0)[kD + 2], inv = part(0)[kD + 3];
+    float w[(kKcCtas + 31) / 32];                     // weights of pieces lane, lane + 32, ...; -1 where the row saw nothing
 #pragma unroll
-      for (int e = 0; e < U; ++e) {
-        ml[e] = make_float2(0.f, 0.f);
-        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + e < n) {
-          const float* p = part(k0 + e, w * 32 + rr);
-          ml[e] = __ldcg(reinterpret_cast<const float2*>(p + kD));
-          v[e] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+    for (int e = 0; e < (kKcCtas + 31) / 32; ++e) {
+      w[e] = -1.f;
+      const int k = lane + 32 * e;
+      if (k >= x.pieces) continue;
+      const float2 ml = *reinterpret_cast<const float2*>(part(k) + kD);
+      if (ml.y == 0.f) continue;
+      w[e] = ex2_approx((ml.x - M) * f);
+      l += ml.y * w[e];
+    }
+    l = warp_sum(l);
+    const float r = l == 0.f ? 0.f : 1.f / l;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 8;                              // pieces whose loads are in flight together
+#pragma unroll
+    for (int e = 0; e < (kKcCtas + 31) / 32; ++e)
+      for (int k0 = 32 * e; k0 < min(x.pieces, 32 * e + 32); k0 += U) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = k0 + u < x.pieces ? *(reinterpret_cast<const float4*>(part(k0 + u)) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float wt = __shfl_sync(0xffffffffu, w[e], (k0 + u) & 31);
+          if (wt < 0.f) continue;                     // its O was not written
+          o[0] += wt * v[u].x;
+          o[1] += wt * v[u].y;
+          o[2] += wt * v[u].z;
+          o[3] += wt * v[u].w;
         }
       }
-#pragma unroll
-      for (int e = 0; e < U; ++e) {
-        if (ml[e].y == 0.f) continue;                 // no position seen: O was not written
-        const float wt = ex2_approx((ml[e].x - Mr) * fr) * nr;
-        o[0] += wt * v[e].x;
-        o[1] += wt * v[e].y;
-        o[2] += wt * v[e].z;
-        o[3] += wt * v[e].w;
-      }
-    }
-    *reinterpret_cast<uint2*>(c.out + ((size_t)(x.row0 + tok) * c.n_q + hh) * kD + 4 * lane) =
-        make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+    const size_t at = (size_t)(x.row0 + t0 + (row >> a.gshift)) * c.n_q + (x.g << a.gshift) + (row & (a.G - 1));
+    *reinterpret_cast<uint2*>(c.out + at * kD + 4 * lane) = make_uint2(pack_bf16(o[0] * r, o[1] * r), pack_bf16(o[2] * r, o[3] * r));
+    if (c.lse && lane == 0) c.lse[at] = kc_lse(a, M, l, inv);
   }
 }
 
@@ -284,6 +288,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   KcItem* items = reinterpret_cast<KcItem*>(base + kKcOffItem);
   int* nans = reinterpret_cast<int*>(base + kKcOffNan);
   uint32_t* masks = reinterpret_cast<uint32_t*>(base + kKcOffMask);
+  float2* ml_b = reinterpret_cast<float2*>(base + kKcOffMl);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kKcOffBar);
   uint64_t* rfull = bars;                     // [4 warps][kKcRaw] bytes of the records
   uint64_t* rfree = rfull + 4 * kKcRaw;       // [4][kKcRaw] the warp has read them
@@ -297,7 +302,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   uint64_t* sfull = qfree + 2;                // [2] commit: S in tensor memory
   uint64_t* pfull = sfull + 2;                // [2] four softmax warps: P written, O rescaled; gate: the batch's operands are there
   uint64_t* ofull = pfull + 2;                // [2] commit: the piece's last PV done
-  uint64_t* drain = ofull + 2;                // commit after the last MMA
+  uint64_t* bdone = ofull + 2;                // [4] a warp of B: its rows' O, maxima and sums are there
+  uint64_t* bread = bdone + 4;                // [4] the warp of A with the same rows has read them
+  uint64_t* drain = bread + 4;                // commit after the last MMA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const Kv4ChunkCall& c = a.c;
@@ -322,6 +329,10 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 5);
       mbar_init(&ofull[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bdone[s], 1);
+      mbar_init(&bread[s], 1);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < 2; ++e) own[e] = units(shape(rq.len[e], rq.n[e]));
     const long long total = kc_prefix(rq, own[0] * c.n_kv, own[1] * c.n_kv);
-    const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    const int ctas = (int)max(min(total, 1ll), min(total / kKcMinRun, (long long)gridDim.x));
     const bool has = (int)blockIdx.x < ctas;
     const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
     auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
@@ -389,6 +400,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       at = u0 - r + kc_units(s, i);
     }
     int it = 0, blocks = 0, nraw = 0;
+    if (lane == 0) a.cut[blockIdx.x].pieces = 0;      // unless an item goes on in the next CTA
     for (;; ) {
       KcItem x;
       x.n = -1;
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
           x.first = cta_of(first);
           x.pieces = cta_of(first + nu - 1) - x.first + 1;
           x.piece = (int)blockIdx.x - x.first;
-          x.direct = x.pieces == 1 && (!x.single || x.n1 == 0);
+          if (x.pieces > 1 && x.piece == 0 && lane == 0) a.cut[blockIdx.x] = x;
         }
       }
       if (!skip) {
@@ -678,7 +690,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     const int i = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + i * kKcKeys, to = tmem + lanes + kKcColO + i * kD;
-    int n_q = 0, n_s = 0, n_o = 0, blocks = 0;
+    int n_q = 0, n_s = 0, n_o = 0, n_b = 0, blocks = 0;
     for (int it = 0;; ++it) {
       const int is = it % kKcItems;
       acquire(&ifull[is], (it / kKcItems) & 1);
@@ -697,7 +709,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qready[i]);
-      } else if (!x.direct) {
+      } else if (x.pieces > 1 && !x.single) {
         // a piece without a block of this tile's: the rows' factors, for the merge
         const int t = min(x.row0 + token, c.T - 1);
         uint32_t mx = 0u;
@@ -815,76 +827,85 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         ++n_o;
         tc_fence_after();
       }
-      const bool live = token < x.n;
-      const int live_rows = max(0, min(32, (int)((long long)(x.n - t0) << a.gshift) - wq * 32));
-      if (x.direct) {
+      if (i && x.single) {
+        // tile B: its warp's maxima and sums to the warp of A that has the same rows, which reads O as well
         if (n > 0) {
-          const float r = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* dst = c.out + ((size_t)(x.row0 + token) * c.n_q + hq) * kD;
-          const bool wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;   // whole sectors a store
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float o[32];
-            tmem_ld32(to + 32 * q, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool nan = nans[is * 8 + 2 * q + e] <= qpos;
-              uint32_t w[8];
-#pragma unroll
-              for (int p = 0; p < 8; ++p)
-                w[p] = nan ? 0x7fff7fffu : pack_bf16(o[16 * e + 2 * p] * r, o[16 * e + 2 * p + 1] * r);
-              uint16_t* d = dst + 32 * q + 16 * e;
-              if (!live) continue;
-              if (wide) {
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                             "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-              } else {
-                stg_v4(d, make_uint4(w[0], w[1], w[2], w[3]));
-                stg_v4(d + 8, make_uint4(w[4], w[5], w[6], w[7]));
-              }
-            }
-          }
-          if (live && c.lse)
-            c.lse[(size_t)(x.row0 + token) * c.n_q + hq] =
-                l == 0.f ? -INFINITY : m * inv * c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
+          ml_b[row] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bdone[wq]);
+          acquire(&bread[wq], n_b++ & 1);
+          if (dead) break;
         }
-        tc_fence_before();
-      } else if (live_rows > 0) {
+      } else if (n > 0 || x.pieces > 1) {
+        const bool live = token < x.n;
+        const bool both = x.single && x.n1 > 0;
+        float wa = 1.f, wb = 0.f;
+        if (both) {
+          acquire(&bdone[wq], n_b++ & 1);
+          if (dead) break;
+          tc_fence_after();
+          const float2 ml = ml_b[row];
+          const float M = fmaxf(m, ml.x);
+          wa = l == 0.f ? 0.f : ex2_approx((m - M) * f);
+          wb = ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * f);
+          m = M;
+          l = l * wa + ml.y * wb;
+        }
         const bool cut = x.pieces > 1;
-        const int slot = cut ? (x.piece == 0 ? 1 : 0) : 2 + (it & 1);
-        float* p = a.part + ((((size_t)blockIdx.x * 4 + slot) * 2 + i) * a.part_rows + row) * kKcPart;
+        float* p = kc_part(a, blockIdx.x, x.piece == 0, i, row);
+        const float r = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        wa *= r;
+        wb *= r;
+        uint16_t* dst = c.out + ((size_t)(x.row0 + token) * c.n_q + hq) * kD;
+        const bool wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;     // whole sectors a store
         if (n > 0) {
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < 8; ++q) {               // the 16 dims of a scale
             float o[16];
             tmem_ld16(to + 16 * q, o);
-            tmem_ld_wait();
+            if (both) {
+              float ob[16];
+              tmem_ld16(tmem + lanes + kKcColO + kD + 16 * q, ob);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = o[e] * wa + ob[e] * wb;
+            } else {
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= wa;
+            }
             if (nans[is * 8 + q] <= qpos) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = NAN;
             }
-            if (live && l != 0.f) {
+            if (!live) continue;
+            if (cut) {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<float4*>(p + 16 * q + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              continue;
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
+            uint16_t* d = dst + 16 * q;
+            if (wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                           "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+            } else {
+              stg_v4(d, make_uint4(w[0], w[1], w[2], w[3]));
+              stg_v4(d + 8, make_uint4(w[4], w[5], w[6], w[7]));
             }
           }
           tc_fence_before();
         }
-        if (live) *reinterpret_cast<float2*>(p + kD) = make_float2(m, l);
-        __threadfence();
-        __syncwarp();
-        const int tile = x.single ? 0 : i;
-        uint32_t* count = a.counters + ((size_t)(cut ? x.first * 3 : blockIdx.x * 3 + 1 + (it & 1)) * 2 + tile) * 4 + wq;
-        uint32_t before = 0u;
-        if (lane == 0) before = atomicAdd(count, 1u);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before + 1u == (uint32_t)(x.pieces * (x.single ? 2 : 1))) {
-          __threadfence();
-          kc_merge(a, x, 2 + (it & 1), i, wq, live_rows, f, inv, token, hq);
-          if (lane == 0) atomicExch(count, 0u);
+        if (both) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bread[wq]);
         }
+        if (live && cut) *reinterpret_cast<float4*>(p + kD) = make_float4(m, l, f, inv);
+        if (live && !cut && c.lse) c.lse[(size_t)(x.row0 + token) * c.n_q + hq] = kc_lse(a, m, l, inv);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
@@ -931,7 +952,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
 static int kc_part_rows(int T, int G) { return (long long)T * G < 128 ? T * G : 128; }
 
 size_t kv4_chunk_workspace(int T, int, int n_q, int n_kv) {
-  return kKcOffPart + (size_t)kKcCtas * 4 * 2 * kc_part_rows(T, n_q / n_kv) * kKcPart * 4;
+  return kKcOffPart + (size_t)kKcCtas * 2 * 2 * kc_part_rows(T, n_q / n_kv) * kKcPart * 4;
 }
 
 int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
@@ -943,7 +964,7 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   a.part_rows = kc_part_rows(c.T, a.G);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(w);
-  a.counters = reinterpret_cast<uint32_t*>(w + kKcOffCount);
+  a.cut = reinterpret_cast<KcItem*>(w + kKcOffCut);
   a.part = reinterpret_cast<float*>(w + kKcOffPart);
   a.wait_limit = kKcWait;
 #ifdef SPC_TEST_HOOKS
@@ -956,7 +977,9 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
   if (set_func_attr((const void*)kv4_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKcSmem) != cudaSuccess)
     return SPC_ERR_CUDA;
-  kv4_chunk_kernel<<<kKcCtas, kKcThreads, kKcSmem, static_cast<cudaStream_t>(stream)>>>(qmap, a);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  kv4_chunk_kernel<<<kKcCtas, kKcThreads, kKcSmem, st>>>(qmap, a);
+  kv4_chunk_merge_kernel<<<dim3(kKcCtas, (a.part_rows + 31) / 32, 2), kKcMergeThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
