@@ -6,17 +6,16 @@
 // stay put and the rows stream past them. An item is two tiles (A and B) of 128
 // positions of one (request, KV head), dequantised once, against the 128-row
 // tiles of (token, query head of the group) pairs that see them:
-//   S^T[128 positions][N rows] = K Q^T     both in shared memory (128-byte swizzle)
-// A position is one thread's throughout: it reads its row of S^T from tensor
-// memory, takes the exponentials and adds them up, so that nothing is exchanged
+//   S^T[128 positions][N rows] = K Q^T     K in tensor memory, Q in shared memory
+// A position is one thread's throughout: one dequantises its record into its own
+// tensor memory lane (no swizzle, and the shared memory is left to a ring of row
+// tiles that hides their loads), another reads its row of S^T into registers,
+// takes the exponentials and adds them up, so that nothing is exchanged
 // between threads and every sum has one order. Operands are bf16, the queries'
 // own type, in which a record's values are exact: products are exact and their
 // sums fp32, so that the weights' errors are those of fp32. The exponent is
 // scale s - lse with one rounding, before the factor log2(e). A row tile's sums
 // go into the position's total by a compensated addition.
-//
-// Bound: the exponentials, 16 a clock and SM against 128 * 128 products in 512
-// clocks. See kMsPoly for the share of them that the FMA pipe takes.
 //
 // Work: the items' row tiles (and one unit for an item's fixed part) form a line
 // that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
@@ -39,8 +38,8 @@ namespace spc {
 constexpr int kMsRaw = 3, kMsRun = 16;                // stages of each dequantising warp's ring of records, positions a stage
 constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
 constexpr int kMsK = 4;                               // ring of dequantised K tiles
-constexpr int kMsQ = 2;                               // ring of Q tiles
-constexpr int kMsL = 4;                               // ring of the rows' lse
+constexpr int kMsQ = 6;                               // ring of Q tiles
+constexpr int kMsL = 8;                               // ring of the rows' lse
 constexpr int kMsItems = 2;
 constexpr int kMsMasks = 16;                          // tiles whose masks are kept: the copies are at most 11 ahead of the sums
 constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
@@ -48,18 +47,17 @@ constexpr int kMsWarpDeq = 8, kMsWarpMma = 12, kMsWarpPlan = 13, kMsWarpQ = 14;
 constexpr int kMsThreads = 512;
 constexpr int kMsRegSum = 176, kMsRegDeq = 88, kMsRegRest = 72;
 constexpr int kMsFixed = 1;                           // units of an item's fixed part
-constexpr int kMsTmemCols = 512;                      // S of A and B, two each
-constexpr int kMsPoly = 4;                            // of 16 pairs of columns, those whose exponentials are polynomials
+constexpr int kMsTmemCols = 512;                      // S of A and B, four K tiles of 64 columns
+constexpr uint32_t kMsColK = 256;
 
-constexpr uint32_t kMsOffK = 0;
-constexpr uint32_t kMsOffQ = kMsOffK + kMsK * kKcTile;
+constexpr uint32_t kMsOffQ = 0;
 constexpr uint32_t kMsOffRaw = kMsOffQ + kMsQ * kKcTile;
 constexpr uint32_t kMsOffItem = kMsOffRaw + 4 * kMsRaw * kMsStage;    // [kMsItems] MsItem
 constexpr uint32_t kMsOffLse = kMsOffItem + kMsItems * 64;            // [kMsL][128] -lse
 constexpr uint32_t kMsOffOdd = kMsOffLse + kMsL * 512;                // [kMsL][4 words] rows that add nothing
 constexpr uint32_t kMsOffMask = kMsOffOdd + kMsL * 16;                // [kMsMasks][4 words]
 constexpr uint32_t kMsOffBar = kMsOffMask + kMsMasks * 16;
-constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * 4 + 1;
+constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * 2 + 1;
 constexpr size_t kMsSmem = 1024 + kMsOffBar + kMsBars * 8 + 16;
 static_assert(kMsSmem <= 227 * 1024, "shared memory of one CTA");
 
@@ -90,49 +88,21 @@ struct MsItem {
 };
 static_assert(sizeof(MsItem) == 64, "item ring");
 
-// ---------------------------------------------------------------- exponentials
-// 2^t of two values on the FMA pipe: t = i + r with i the nearest integer, 2^r by
-// its Taylor polynomial in r ln 2 up to the sixth power (|r| <= 1/2: off by less
-// than 2^-22), times 2^i put together from its bits. Below 2^-126 the result is 0, from
-// 2^128 on infinity; NaN stays NaN.
-__device__ __forceinline__ float2 ms_exp2_poly(float2 t) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(-127.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(-127.f));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(128.f));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(128.f));
-  constexpr float kMagic = 12582912.f;                // 1.5 * 2^23: the integer ends up in the low bits
-  const float2 im = add2(t, make_float2(kMagic, kMagic));
-  const float2 i = add2(im, make_float2(-kMagic, -kMagic));
-  const float2 r = add2(t, make_float2(-i.x, -i.y));
-  constexpr float L = 0.6931471805599453f;
-  constexpr float c6 = L * L * L * L * L * L / 720.f, c5 = L * L * L * L * L / 120.f, c4 = L * L * L * L / 24.f,
-                  c3 = L * L * L / 6.f, c2 = L * L / 2.f;
-  float2 p = fma2(make_float2(c6, c6), r, make_float2(c5, c5));
-  p = fma2(p, r, make_float2(c4, c4));
-  p = fma2(p, r, make_float2(c3, c3));
-  p = fma2(p, r, make_float2(c2, c2));
-  p = fma2(p, r, make_float2(L, L));
-  p = fma2(p, r, make_float2(1.f, 1.f));
-  const float2 s = make_float2(__int_as_float((__float_as_int(im.x) << 23) + 0x3f800000),
-                               __int_as_float((__float_as_int(im.y) << 23) + 0x3f800000));
-  return fma2(p, s, make_float2(0.f, 0.f));
-}
-
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// A row of 128 K values of 64 bytes of codes and 8 scales as bf16 into row r of a
-// swizzled tile. A code as fp16 has at most one bit of mantissa; its bits three
+// 64 K values of 32 bytes of codes and 4 scales as bf16 into 32 columns of this
+// thread's tensor memory lane. A code as fp16 has at most one bit of mantissa; its bits three
 // places further down are bf16's of the value times 2^-112, which the scale, an
 // e4m3 number times 2^112, takes back: the product is exact.
-__device__ __forceinline__ void ms_row(const uint4* codes, uint2 sc, uint32_t tile, int r) {
-  const uint32_t dst = tile + (uint32_t)r * 128u, r7 = (uint32_t)r & 7u;
+__device__ __forceinline__ void ms_half_row(const uint4* codes, uint32_t sc, uint32_t t) {
+  uint32_t k[32];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t s2 = e4m3x2_to_f16(((q < 2 ? sc.x : sc.y) >> (16 * (q & 1))) & 0xffffu);
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t s2 = e4m3x2_to_f16((sc >> (16 * q)) & 0xffffu);
     const float f0 = f16_lo(s2) * 5.192296858534828e33f, f1 = f16_hi(s2) * 5.192296858534828e33f;   // 2^112
     const uint32_t s[2] = {pack_bf16(f0, f0), pack_bf16(f1, f1)};
     const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
@@ -141,11 +111,11 @@ __device__ __forceinline__ void ms_row(const uint4* codes, uint2 sc, uint32_t ti
       uint32_t h[4];
       e2m1x8_to_f16(w[e], h);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) h[f] = bmul2(((h[f] >> 3) & 0x0fff0fffu) | (h[f] & 0x80008000u), s[e >> 1]);
-      const uint32_t u = 4 * q + e;
-      sts_v4(dst + (u >> 3) * kKcBlock + (((u & 7u) ^ r7) << 4), h[0], h[1], h[2], h[3]);
+      for (int f = 0; f < 4; ++f)
+        k[16 * q + 4 * e + f] = bmul2(((h[f] >> 3) & 0x0fff0fffu) | (h[f] & 0x80008000u), s[e >> 1]);
     }
   }
+  tmem_st32(t, k);
 }
 
 // ---------------------------------------------------------------- the line of work
@@ -194,9 +164,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   uint64_t* lfree = lfull + kMsL;             // [kMsL] eight summing warps have read them
   uint64_t* ifull = lfree + kMsL;             // [kMsItems]
   uint64_t* ifree = ifull + kMsItems;         // [kMsItems]
-  uint64_t* sfull = ifree + kMsItems;         // [2 tiles][2] commit: S in tensor memory
-  uint64_t* sfree = sfull + 4;                // [2][2] four summing warps have read it
-  uint64_t* drain = sfree + 4;
+  uint64_t* sfull = ifree + kMsItems;         // [2 tiles] commit: S in tensor memory
+  uint64_t* sfree = sfull + 2;                // [2] four summing warps have read it
+  uint64_t* drain = sfree + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const Kv4ChunkCall& c = a.c;
@@ -222,7 +192,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       mbar_init(&ifull[s], 1);
       mbar_init(&ifree[s], 4 + 8 + 2);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], 4);
     }
@@ -234,7 +204,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t ks = smem_u32(base + kMsOffK), qs = smem_u32(base + kMsOffQ);
+  const uint32_t qs = smem_u32(base + kMsOffQ);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
     if (!dead && !__all_sync(0xffffffffu, mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, a.wait_limit))) {
@@ -384,9 +354,12 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         const int t = tok + (r >> a.gshift);
         return t < x.n ? c.lse[(size_t)(x.row0 + t) * c.n_q + (x.g << a.gshift) + (r & (a.G - 1))] : 0.f;
       };
-      float next[4];
+      float next[4], after[4];                        // of this row tile and the one behind it
 #pragma unroll
-      for (int e = 0; e < 4; ++e) next[e] = lse_of(x.r0 * a.tpm, 32 * e + lane);
+      for (int e = 0; e < 4; ++e) {
+        next[e] = lse_of(x.r0 * a.tpm, 32 * e + lane);
+        after[e] = x.r0 + 1 < x.r1 ? lse_of((x.r0 + 1) * a.tpm, 32 * e + lane) : 0.f;
+      }
       for (int r = x.r0; r < x.r1; ++r, ++nq) {
         const int st = nq % kMsQ, tok = r * a.tpm, rows = min(128, (x.n - tok) << a.gshift);
         acquire(&qfree[st], ((nq / kMsQ) & 1) ^ 1);
@@ -435,9 +408,10 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&lfull[ls]);
-        if (r + 1 < x.r1) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) next[e] = lse_of(tok + a.tpm, 32 * e + lane);
+        for (int e = 0; e < 4; ++e) {
+          next[e] = after[e];
+          if (r + 2 < x.r1) after[e] = lse_of(tok + 2 * a.tpm, 32 * e + lane);
         }
       }
       if (dead) break;
@@ -467,20 +441,18 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          const int buf = ns[j] & 1;
-          acquire(&sfree[j * 2 + buf], ((ns[j] >> 1) & 1) ^ 1);
-          ++ns[j];
+          acquire(&sfree[j], (ns[j]++ & 1) ^ 1);
           if (dead) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t kd = umma_desc_lo(ks) + (uint32_t)((nk + j) % kMsK) * (kKcTile >> 4);
+            const uint32_t kt = tm + kMsColK + (uint32_t)((nk + j) % kMsK) * 64;
             const uint32_t qd = umma_desc_lo(qs) + (uint32_t)st * (kKcTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk) {
               const uint32_t off = (uint32_t)(kk >> 2) * (kKcBlock >> 4) + (uint32_t)(kk & 3) * 2;
-              umma_f16(tm + (uint32_t)(j * 2 + buf) * 128, umma_desc(kd + off), umma_desc(qd + off), idesc, kk ? 1u : 0u);
+              umma_f16_tmem_a(tm + (uint32_t)j * 128, kt + kk * 8, umma_desc(qd + off), idesc, kk ? 1u : 0u);
             }
-            umma_commit(&sfull[j * 2 + buf]);
+            umma_commit(&sfull[j]);
             if (j + 1 == tiles) umma_commit(&qfree[st]);
             if (r + 1 == r1) umma_commit(&kfree[(nk + j) % kMsK]);
           }
@@ -496,7 +468,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   } else if (warp >= kMsWarpDeq && warp < kMsWarpDeq + 4) {
     // ================= dequantisation, a record a thread
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegDeq));
-    const int w = warp - kMsWarpDeq, r = threadIdx.x & 127;
+    const int w = warp - kMsWarpDeq;
     int nk = 0, nread = 0;
     for (int it = 0;; ++it) {
       const int is = it % kMsItems;
@@ -529,8 +501,12 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         const int slot = nk % kMsK;
         acquire(&kfree[slot], ((nk / kMsK) & 1) ^ 1);
         if (dead) break;
-        ms_row(v, sc, ks + (uint32_t)slot * kKcTile, r);
-        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t t = tmem + ((uint32_t)(w * 32) << 16) + kMsColK + (uint32_t)slot * 64;
+        ms_half_row(v, sc.x, t);
+        ms_half_row(v + 2, sc.y, t + 32);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kfull[slot]);
       }
@@ -564,43 +540,40 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
           continue;
         }
-        const int buf = ns & 1;
-        acquire(&sfull[j * 2 + buf], (ns >> 1) & 1);
+        acquire(&sfull[j], ns++ & 1);
         if (dead) break;
-        ++ns;
         tc_fence_after();
         there = masks[((nk + j) % kMsMasks) * 4 + wq] >> lane & 1;
         const int tok = r * a.tpm, cols = min(128, (x.n - tok) << a.gshift);
         const float* nl = neglse + (nq % kMsL) * 128;
         const uint4 odd = *reinterpret_cast<const uint4*>(odds + (nq % kMsL) * 4);
-        const uint32_t ts = tmem + lanes + (uint32_t)(j * 2 + buf) * 128;
+        const uint32_t ts = tmem + lanes + (uint32_t)j * 128;
         const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
         float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // columns from this one on are tokens at or behind the position
         const long long from = (long long)(p - (x.len - x.n) - tok) << a.gshift;
         if (cols == 128 && (odd.x | odd.y | odd.z | odd.w) == 0u && __all_sync(0xffffffffu, from <= 0)) {
-          float s[2][32];
-          tmem_ld32(ts, s[0]);
+          // the whole row into registers, so that the next S can be written at once
+          float s[128];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait32(s[q & 1]);
-            if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
+          tmem_ld_wait32(s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * e);
+          for (int q = 1; q < 4; ++q) tmem_ld_wait32(s + 32 * q);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[j]);
 #pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                float2 t = fma2(make_float2(s[q & 1][4 * e + 2 * f], s[q & 1][4 * e + 2 * f + 1]), sc,
-                                f ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
-                t = fma2(t, l2e, make_float2(0.f, 0.f));
-                if ((2 * e + f) * kMsPoly % 16 < kMsPoly) {
-                  t = ms_exp2_poly(t);
-                } else {
-                  t.x = ex2_approx(t.x);
-                  t.y = ex2_approx(t.y);
-                }
-                sum[(2 * e + f) & 3] = add2(sum[(2 * e + f) & 3], t);
-              }
+          for (int e = 0; e < 32; ++e) {
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + 4 * e);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              float2 t = fma2(make_float2(s[4 * e + 2 * f], s[4 * e + 2 * f + 1]), sc,
+                              f ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+              t = fma2(t, l2e, make_float2(0.f, 0.f));
+              t.x = ex2_approx(t.x);
+              t.y = ex2_approx(t.y);
+              sum[(2 * e + f) & 3] = add2(sum[(2 * e + f) & 3], t);
             }
           }
         } else {
@@ -620,13 +593,12 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
               sum[e & 3].x += vis >> e & 1 ? t : 0.f;
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[j]);
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sfree[j * 2 + buf]);
-          mbar_arrive(&lfree[nq % kMsL]);
-        }
+        if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
         // the tile's sum into the total, what the addition loses kept beside it
         const float y = ((sum[0].x + sum[1].x) + (sum[2].x + sum[3].x)) + ((sum[0].y + sum[1].y) + (sum[2].y + sum[3].y));
         const float u = total + y, v = u - total;
