@@ -10,6 +10,8 @@
 
 namespace spc {
 
+constexpr int kK4Tile = 32;                          // positions a tile
+constexpr uint32_t kK4StageBytes = kK4Tile * kKv4Rec;
 constexpr int kK4Ctas = 152;                         // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kK4Part = kD + 4;                      // a head's partial: m, l, factor of m to base 2, unused, O[128]
 constexpr int kK4MaxKv = 128;                        // KV heads
@@ -112,6 +114,82 @@ __device__ __forceinline__ void k4_step(const Kv4AttnCall& c, const K4Line& ln, 
     }
   }
   k4_seg(c, ln, x);
+}
+
+// Whole context: the copying warp. Lane w serves warp w: tiles t0 + w, t0 + w
+// + W, ... go into its ring as its stages fall free, so that one instruction
+// stream computes the addresses of W tiles. A lane's table entries are fetched
+// one tile ahead.
+template <int W, int S>
+__device__ __forceinline__ void k4_copy(const Kv4Args& a, const K4Line& ln, int segs, int t0, int t1, uint8_t* ring,
+                                        uint64_t* full, uint64_t* empty, uint32_t* masks) {
+  const Kv4AttnCall& c = a.c;
+  const int lane = threadIdx.x & 31, bs = 1 << c.block_shift, sh = c.block_shift;
+  const bool mine = lane < W;
+  K4Cursor x = k4_at(c, ln, t0 + (mine ? lane : 0));
+  if (!mine) x.t = t1;
+  ring += lane * S * kK4StageBytes;
+  full += lane * S;
+  empty += lane * S;
+  masks += lane * S;
+  int k = 0, e0 = -1, e1 = -1;
+  auto fetch = [&]() {
+    if (x.t >= t1) return;
+    const int p = x.i * kK4Tile;
+    e0 = __ldg(x.table + (p >> sh));
+    e1 = (bs < kK4Tile && p + 16 < x.len) ? __ldg(x.table + (p >> sh) + 1) : -1;
+  };
+  fetch();
+  long long idle = clock64();
+  while (__any_sync(0xffffffffu, x.t < t1)) {
+    const int st = k % S;
+    const bool ready = x.t < t1 && (k < S || mbar_test(&empty[st], ((k / S) & 1) ^ 1));
+    if (ready) {
+      const int p = x.i * kK4Tile, n = min(kK4Tile, x.len - p), g = x.s >> a.hshift;
+      const bool ok0 = (unsigned)e0 < (unsigned)c.num_blocks;
+      uint8_t* dst = ring + st * kK4StageBytes;
+      if (bs >= kK4Tile) {
+        masks[st] = ok0 ? 0xffffffffu >> (32 - n) : 0u;
+        mbar_arrive_expect_tx(&full[st], ok0 ? (uint32_t)n * kKv4Rec : 0u);
+        if (ok0)
+          bulk_g2s(dst, c.cache + ((((size_t)e0 * c.n_kv + g) << sh) + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec,
+                   &full[st]);
+      } else {
+        // two blocks of 16
+        const bool ok1 = (unsigned)e1 < (unsigned)c.num_blocks;
+        const int n0 = ok0 ? min(16, n) : 0, n1 = ok1 ? max(0, n - 16) : 0;
+        masks[st] = ((1u << n0) - 1) | ((1u << n1) - 1) << 16;
+        mbar_arrive_expect_tx(&full[st], (uint32_t)(n0 + n1) * kKv4Rec);
+        if (n0 > 0)
+          bulk_g2s(dst, c.cache + (((size_t)e0 * c.n_kv + g) << sh) * kKv4Rec, (uint32_t)n0 * kKv4Rec, &full[st]);
+        if (n1 > 0)
+          bulk_g2s(dst + 16 * kKv4Rec, c.cache + (((size_t)e1 * c.n_kv + g) << sh) * kKv4Rec, (uint32_t)n1 * kKv4Rec,
+                   &full[st]);
+      }
+      ++k;
+      k4_step(c, ln, segs, x, W);
+      fetch();
+    }
+    if (__any_sync(0xffffffffu, ready)) {
+      idle = clock64();
+    } else {
+      if (__any_sync(0xffffffffu, clock64() - idle > a.wait_limit)) {   // a warp gave up: stop copying
+        set_status(a.status, SPC_ERR_TIMEOUT);
+        break;
+      }
+      __nanosleep(40);
+    }
+  }
+  // every copy lands before the CTA ends
+  for (int j = max(0, k - S); j < k; ++j) mbar_wait_bounded(&full[j % S], (j / S) & 1, a.wait_limit);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // One warp: the line of TILE-position tiles and this CTA's part of it.

@@ -30,6 +30,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "kv4_attn.cuh"
 #include "kv4_chunk.cuh"
 #include "spc_tc.cuh"
 
@@ -68,6 +69,8 @@ constexpr size_t kMsOffPart = kMsOffCount + (size_t)kKcCtas * 8 * 4;
 constexpr size_t kMsWorkspace = kMsOffPart + (size_t)kKcCtas * 2 * 256 * 4;
 static_assert(kMsOffPart % 256 == 0, "aligned partials");
 
+constexpr int kMfRows = 32;                           // rows up to which a request is the other kernel's
+
 struct MsArgs {
   Kv4ChunkCall c;
   int G, gshift, tpm;      // heads a group, its log2, tokens a row tile
@@ -82,7 +85,7 @@ struct MsItem {
   int b, g, p0;            // request (-1: no more items), KV head, first position
   int row0, n, len;        // the request's first row, new tokens and positions
   int tiles;               // of positions: 1 or 2
-  int r0, r1;              // the piece's row tiles; none where the request has no new tokens
+  int r0, r1;              // the piece's row tiles
   int pieces, piece, first;  // of the item, and its first CTA
   int pad[4];
 };
@@ -121,10 +124,11 @@ __device__ __forceinline__ void ms_half_row(const uint4* codes, uint32_t sc, uin
 // ---------------------------------------------------------------- the line of work
 // Item i of a request's head holds positions [256 i, 256 i + 256); its row tiles
 // are those from the first that sees one of them on, max(0, 2 G i - cd) of nt,
-// cd = ceil((len - n) / tpm). A request without new tokens has one unit an item.
+// cd = ceil((len - n) / tpm). Requests with few rows have no items here.
 struct MsShape {
   int n, len, nt, cd, items, G2;
 };
+__device__ __forceinline__ bool ms_few(const MsArgs& a, int n) { return ((long long)n << a.gshift) <= kMfRows; }
 __device__ __forceinline__ MsShape ms_shape(const MsArgs& a, int len, int n) {
   const int lt = 7 - a.gshift;
   MsShape s;
@@ -132,13 +136,12 @@ __device__ __forceinline__ MsShape ms_shape(const MsArgs& a, int len, int n) {
   s.len = len;
   s.nt = (n + a.tpm - 1) >> lt;
   s.cd = -((n - len) >> lt);
-  s.items = (len + 255) >> 8;
+  s.items = ms_few(a, n) ? 0 : (len + 255) >> 8;
   s.G2 = 2 * a.G;
   return s;
 }
 __device__ __forceinline__ int ms_first(const MsShape& s, int i) { return max(0, s.G2 * i - s.cd); }
 __device__ __forceinline__ long long ms_units(const MsShape& s, int k) {   // of the items below k
-  if (s.n == 0) return k;
   // the first item that some row tile does not see, and from there on an arithmetic progression
   const int k0 = s.cd < 0 ? 0 : min(k, s.cd / s.G2 + 1);
   const long long m = k - k0;
@@ -256,14 +259,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       MsItem x;
       x.b = -1;
       bool skip = false;
-      int fixed = 0, nu = 1;
-      if (has && at < u1) {
-        const int q = ms_first(s, i);
-        fixed = s.n ? kMsFixed : 0;
-        nu = s.n ? s.nt - q : 1;
-      }
+      const int nu = has && at < u1 ? s.nt - ms_first(s, i) : 0;
       if (has && at < u1 && !dead) {
-        const long long first = at + fixed;
+        const long long first = at + kMsFixed;
         const int lo = (int)max(0ll, u0 - first), hi = (int)min((long long)nu, u1 - first);
         skip = hi <= lo;
         if (!skip) {
@@ -274,8 +272,8 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           x.n = s.n;
           x.len = s.len;
           x.tiles = x.p0 + 128 < s.len ? 2 : 1;
-          x.r0 = s.n ? s.nt - nu + lo : 0;
-          x.r1 = s.n ? s.nt - nu + hi : 0;
+          x.r0 = s.nt - nu + lo;
+          x.r1 = s.nt - nu + hi;
           x.first = cta_of(first);
           x.pieces = cta_of(first + nu - 1) - x.first + 1;
           x.piece = (int)blockIdx.x - x.first;
@@ -295,9 +293,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         if (a.starve) break;
 #endif
         KcTable t;
-        if (x.n) t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
+        t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
         // lane w copies for dequantising warp w
-        for (int j = 0; x.n && j < x.tiles && !dead; ++j, ++blocks) {
+        for (int j = 0; j < x.tiles && !dead; ++j, ++blocks) {
           uint32_t mask = 0u;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++nraw) {
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         }
       }
       // the next item
-      at += fixed + nu;
+      at += kMsFixed + nu;
       if (++i == s.items) {
         i = 0;
         if (++g == c.n_kv) {
@@ -432,7 +430,6 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (b < 0) break;
-      if (n == 0) continue;
       for (int j = 0; j < tiles; ++j) acquire(&kfull[(nk + j) % kMsK], ((nk + j) / kMsK) & 1);
       for (int r = r0; r < r1 && !dead; ++r, ++nq) {
         const int st = nq % kMsQ, N = min(128, (((n - r * a.tpm) << a.gshift) + 15) & ~15);
@@ -474,7 +471,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       const int is = it % kMsItems;
       acquire(&ifull[is], (it / kMsItems) & 1);
       if (dead) break;
-      const int b = items[is].b, tiles = items[is].n ? items[is].tiles : 0;
+      const int b = items[is].b, tiles = items[is].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (b < 0) break;
@@ -606,7 +603,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         total = u;
       }
       if (dead) break;
-      if (x.n) nk += x.tiles;
+      nk += x.tiles;
       // infinities and NaN are the sum's own; their difference above is not
       float sum = total + (fabsf(total) < INFINITY ? lost : 0.f);
       if (!there) sum = 0.f;
@@ -640,6 +637,195 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   }
 }
 
+// ---------------------------------------------------------------- few rows
+// Requests with at most 32 rows (a decode step's token, a few drafted ones, none):
+// the records' bytes are what counts, so every warp streams positions for
+// itself. 15 warps each have a ring of stages of 32 records that a sixteenth
+// fills (k4_copy); the products run on mma.sync with 16 positions as M and 8 rows
+// as N. Lane (gid, tig) dequantises dims 32 tig .. 32 tig + 31 of positions gid
+// and gid + 8 to fp16, 16 bytes of codes each; the contraction's order is free,
+// so these are the fragments of the eight steps as they come, and the queries, in
+// registers, are in the same order: bf16 to fp16 times a power of two a row, as in
+// kv4_chunk.cu. Nothing is exchanged but a position's sum over four lanes.
+// Bound: HBM; see the figures at kv4_mass_launch.
+constexpr int kMfWarps = 15, kMfStages = 3, kMfTiles = kMfRows / 8;
+constexpr uint32_t kMfOffBar = kMfWarps * kMfStages * kK4StageBytes;
+constexpr uint32_t kMfOffMask = kMfOffBar + 2 * kMfWarps * kMfStages * 8;
+constexpr uint32_t kMfSmem = kMfOffMask + kMfWarps * kMfStages * 4;
+
+struct MfArgs {
+  Kv4Args k4;              // the cache, for k4_copy
+  MsArgs ms;
+};
+
+__global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(const MfArgs fa) {
+  extern __shared__ __align__(128) uint8_t mf_smem[];
+  __shared__ K4Line ln;
+  const MsArgs& a = fa.ms;
+  const Kv4ChunkCall& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  uint64_t* all_full = reinterpret_cast<uint64_t*>(mf_smem + kMfOffBar);
+  uint64_t* all_free = all_full + kMfWarps * kMfStages;
+  uint32_t* all_masks = reinterpret_cast<uint32_t*>(mf_smem + kMfOffMask);
+  if (warp == 1) {
+    for (int s = lane; s < kMfWarps * kMfStages; s += 32) {
+      mbar_init(&all_full[s], 1);
+      mbar_init(&all_free[s], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    // tiles of 32 positions of the requests with few rows, cut into equal runs
+    KcRequests rq;
+    kc_requests(c, rq);
+    int nt[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      nt[e] = ms_few(a, rq.n[e]) ? (rq.len[e] + kK4Tile - 1) / kK4Tile : 0;
+      ln.len[2 * lane + e] = rq.len[e];
+      ln.nt[2 * lane + e] = nt[e];
+      nt[e] *= c.n_kv;
+    }
+    const int incl = warp_incl_scan(nt[0] + nt[1]);
+    ln.pre[2 * lane] = incl - nt[0] - nt[1];
+    ln.pre[2 * lane + 1] = incl - nt[1];
+    if (lane == 31) {
+      ln.pre[SPC_MAX_BATCH] = incl;
+      ln.t0 = (int)((long long)incl * blockIdx.x / gridDim.x);
+      ln.t1 = (int)((long long)incl * (blockIdx.x + 1) / gridDim.x);
+    }
+  }
+  __syncthreads();
+  const int t0 = ln.t0, t1 = ln.t1;
+  if (t0 >= t1) return;
+  if (warp == kMfWarps) {
+#ifdef SPC_TEST_HOOKS
+    if (a.starve) return;
+#endif
+    k4_copy<kMfWarps, kMfStages>(fa.k4, ln, c.n_kv, t0, t1, mf_smem, all_full, all_free, all_masks);
+    return;
+  }
+  const uint32_t ring = smem_u32(mf_smem) + (uint32_t)warp * kMfStages * kK4StageBytes;
+  uint64_t* full = all_full + warp * kMfStages;
+  uint64_t* empty = all_free + warp * kMfStages;
+  const uint32_t* masks = all_masks + warp * kMfStages;
+  K4Cursor x = k4_at(fa.k4.c, ln, min(t0 + warp, t1 - 1));
+  int seg = -1, tiles = 0, ctx = 0;
+  uint32_t q[kMfTiles][16];                           // rows 8 i + gid, the lane's 32 dims
+  float inv[kMfTiles][2], nl[kMfTiles][2];            // of columns 8 i + 2 tig, + 1: the queries' scale, -lse
+  for (int t = t0 + warp, k = 0; t < t1; t += kMfWarps, ++k) {
+    const int b = x.b, g = x.s, p0 = x.i * kK4Tile;
+    if (seg != b * c.n_kv + g) {
+      seg = b * c.n_kv + g;
+      const int row0 = max(0, min(c.cu[b], c.T)), n = max(row0, min(c.cu[b + 1], c.T)) - row0, rows = n << a.gshift;
+      ctx = x.len - n;
+      tiles = (rows + 7) >> 3;
+#pragma unroll
+      for (int i = 0; i < kMfTiles; ++i) {
+        if (i >= tiles) continue;
+        const int r = 8 * i + gid;
+        const size_t tok = row0 + (r >> a.gshift);
+        const int h = (g << a.gshift) + (r & (a.G - 1));
+        const float lse = r < rows ? c.lse[tok * c.n_q + h] : -INFINITY;
+        uint4 w[4];
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // a row that adds nothing is zeros, whatever it holds
+          w[e] = lse != -INFINITY ? *reinterpret_cast<const uint4*>(c.q + tok * c.q_stride + (size_t)h * kD + 32 * tig + 8 * e)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu),
+                                     __vmaxu2(w[e].z & 0x7fff7fffu, w[e].w & 0x7fff7fffu)));
+        }
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int E = (int)(mx >> 7), e2 = min(141 - E, 126);
+        const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
+        auto f16 = [&](uint32_t v) { return E == 255 ? 0x7fff7fffu : pack_f16(bf_lo(v) * up, bf_hi(v) * up); };
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q[i][4 * e] = f16(w[e].x);
+          q[i][4 * e + 1] = f16(w[e].y);
+          q[i][4 * e + 2] = f16(w[e].z);
+          q[i][4 * e + 3] = f16(w[e].w);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          inv[i][e] = __shfl_sync(0xffffffffu, down, (2 * tig + e) * 4);
+          nl[i][e] = -__shfl_sync(0xffffffffu, lse == -INFINITY ? INFINITY : lse, (2 * tig + e) * 4);
+        }
+      }
+    }
+    // lane tig 0 writes position gid of each half, tig 1 position gid + 8
+    const size_t at = (size_t)seg * c.cap + p0 + gid + 8 * tig;
+    float prev[2] = {0.f, 0.f};
+    if (c.keep != 0.f && tig < 2) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (p0 + 16 * m + gid + 8 * tig < x.len) prev[m] = c.mass_prev[at + 16 * m];
+    }
+    const int st = k % kMfStages;
+    if (!__all_sync(0xffffffffu, mbar_test(&full[st], (k / kMfStages) & 1) ||
+                                     mbar_wait_bounded(&full[st], (k / kMfStages) & 1, a.wait_limit))) {
+      if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+      return;
+    }
+    const uint32_t mask = masks[st];
+    const bool seen = p0 + kK4Tile - 1 <= ctx;        // by every row
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint32_t rec = ring + (uint32_t)st * kK4StageBytes + (uint32_t)(16 * m + gid) * kKv4Rec;
+      const uint4 c0 = lds_v4(rec + 16 * tig), c1 = lds_v4(rec + 8 * kKv4Rec + 16 * tig);
+      const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+      uint32_t b0, b1;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(b0) : "r"(rec + kKv4Scale + 2 * tig));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(b1) : "r"(rec + 8 * kKv4Rec + kKv4Scale + 2 * tig));
+      const uint32_t h0 = e4m3x2_to_f16(b0), h1 = e4m3x2_to_f16(b1);
+      float d[kMfTiles][4] = {};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t s0 = __byte_perm(h0, h0, e < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(h1, h1, e < 2 ? 0x1010 : 0x3232);
+        uint32_t k0[4], k1[4];
+        e2m1x8_to_f16(w0[e], k0);
+        e2m1x8_to_f16(w1[e], k1);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t av[4] = {hmul2(k0[2 * f], s0), hmul2(k1[2 * f], s1), hmul2(k0[2 * f + 1], s0), hmul2(k1[2 * f + 1], s1)};
+#pragma unroll
+          for (int i = 0; i < kMfTiles; ++i)
+            if (i < tiles) mma_f16(d[i], av, q[i][4 * e + 2 * f], q[i][4 * e + 2 * f + 1]);
+        }
+      }
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kMfTiles; ++i) {
+        if (i >= tiles) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = ex2_approx(fmaf(d[i][e] * inv[i][e & 1], c.scale, nl[i][e & 1]) * kLog2e);
+          // column 8 i + 2 tig + (e & 1) is a token at or behind the position
+          const bool vis = seen || ctx + ((8 * i + 2 * tig + (e & 1)) >> a.gshift) >= p0 + 16 * m + gid + 8 * (e >> 1);
+          sum[e >> 1] += vis ? y : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+      }
+      const int j = 16 * m + gid + 8 * tig;
+      if (tig < 2 && p0 + j < x.len) {
+        const float y = mask >> j & 1 ? tig ? sum[1] : sum[0] : 0.f;
+        c.mass_next[at + 16 * m] = c.keep != 0.f ? fmaf(c.keep, prev[m], y) : y;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    if (t + kMfWarps < t1) k4_step(fa.k4.c, ln, c.n_kv, x, kMfWarps);
+  }
+}
+
 size_t kv4_mass_workspace(int, int, int, int) { return kMsWorkspace; }
 
 int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
@@ -656,14 +842,28 @@ int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
 #ifdef SPC_TEST_HOOKS
   a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
 #endif
-  CUtensorMap qmap{};
-  const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)c.n_q, (uint64_t)c.T};
-  const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)c.q_stride * 2};
-  const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
-  if (c.T > 0 && !tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
-  if (set_func_attr((const void*)kv4_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMsSmem) != cudaSuccess)
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MfArgs f{};
+  f.ms = a;
+  f.k4.c.cache = c.cache; f.k4.c.table = c.table; f.k4.c.len = c.len;
+  f.k4.c.B = c.B; f.k4.c.n_q = c.n_q; f.k4.c.n_kv = c.n_kv; f.k4.c.num_blocks = c.num_blocks;
+  f.k4.c.block_shift = c.block_shift; f.k4.c.max_blocks = c.max_blocks;
+  f.k4.status = a.status;
+  f.k4.wait_limit = a.wait_limit;
+  if (set_func_attr((const void*)kv4_mass_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMfSmem) != cudaSuccess)
     return SPC_ERR_CUDA;
-  kv4_mass_kernel<<<kKcCtas, kMsThreads, kMsSmem, static_cast<cudaStream_t>(stream)>>>(qmap, a);
+  kv4_mass_few_kernel<<<kKcCtas, 32 * (kMfWarps + 1), kMfSmem, st>>>(f);
+  // no request can have more rows than the call
+  if ((long long)c.T * a.G > kMfRows) {
+    CUtensorMap qmap{};
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)c.n_q, (uint64_t)c.T};
+    const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)c.q_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
+    if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
+    if (set_func_attr((const void*)kv4_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMsSmem) != cudaSuccess)
+      return SPC_ERR_CUDA;
+    kv4_mass_kernel<<<kKcCtas, kMsThreads, kMsSmem, st>>>(qmap, a);
+  }
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
 
