@@ -30,6 +30,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv4_attn.cuh"
 #include "kv4_chunk.cuh"
 #include "spc_tc.cuh"
@@ -722,8 +724,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
       tiles = (rows + 7) >> 3;
 #pragma unroll
       for (int i = 0; i < kMfTiles; ++i) {
-        if (i >= tiles) continue;
-        const int r = 8 * i + gid;
+        const int r = 8 * i + gid;                    // rows that are not there are zeros and add nothing
         const size_t tok = row0 + (r >> a.gshift);
         const int h = (g << a.gshift) + (r & (a.G - 1));
         const float lse = r < rows ? c.lse[tok * c.n_q + h] : -INFINITY;
@@ -773,8 +774,9 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
     }
     const uint32_t mask = masks[st];
     const bool seen = p0 + kK4Tile - 1 <= ctx;        // by every row
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    // 16 positions against NT row tiles
+    auto weigh = [&](auto count, int m) {
+      constexpr int NT = decltype(count)::value;
       const uint32_t rec = ring + (uint32_t)st * kK4StageBytes + (uint32_t)(16 * m + gid) * kKv4Rec;
       const uint4 c0 = lds_v4(rec + 16 * tig), c1 = lds_v4(rec + 8 * kKv4Rec + 16 * tig);
       const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
@@ -782,7 +784,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
       asm volatile("ld.shared.u16 %0, [%1];" : "=r"(b0) : "r"(rec + kKv4Scale + 2 * tig));
       asm volatile("ld.shared.u16 %0, [%1];" : "=r"(b1) : "r"(rec + 8 * kKv4Rec + kKv4Scale + 2 * tig));
       const uint32_t h0 = e4m3x2_to_f16(b0), h1 = e4m3x2_to_f16(b1);
-      float d[kMfTiles][4] = {};
+      float d[NT][4] = {};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t s0 = __byte_perm(h0, h0, e < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(h1, h1, e < 2 ? 0x1010 : 0x3232);
@@ -793,14 +795,12 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         for (int f = 0; f < 2; ++f) {
           const uint32_t av[4] = {hmul2(k0[2 * f], s0), hmul2(k1[2 * f], s1), hmul2(k0[2 * f + 1], s0), hmul2(k1[2 * f + 1], s1)};
 #pragma unroll
-          for (int i = 0; i < kMfTiles; ++i)
-            if (i < tiles) mma_f16(d[i], av, q[i][4 * e + 2 * f], q[i][4 * e + 2 * f + 1]);
+          for (int i = 0; i < NT; ++i) mma_f16(d[i], av, q[i][4 * e + 2 * f], q[i][4 * e + 2 * f + 1]);
         }
       }
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kMfTiles; ++i) {
-        if (i >= tiles) continue;
+      for (int i = 0; i < NT; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float y = ex2_approx(fmaf(d[i][e] * inv[i][e & 1], c.scale, nl[i][e & 1]) * kLog2e);
@@ -817,8 +817,14 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
       const int j = 16 * m + gid + 8 * tig;
       if (tig < 2 && p0 + j < x.len) {
         const float y = mask >> j & 1 ? tig ? sum[1] : sum[0] : 0.f;
-        c.mass_next[at + 16 * m] = c.keep != 0.f ? fmaf(c.keep, prev[m], y) : y;
+        c.mass_next[at + 16 * m] = c.keep != 0.f ? fmaf(c.keep, m ? prev[1] : prev[0], y) : y;
       }
+    };
+#pragma unroll 1
+    for (int m = 0; m < 2; ++m) {
+      if (tiles == 1) weigh(std::integral_constant<int, 1>{}, m);
+      else if (tiles == 2) weigh(std::integral_constant<int, 2>{}, m);
+      else weigh(std::integral_constant<int, kMfTiles>{}, m);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
