@@ -26,6 +26,7 @@
 //   warp 12         tensor memory, MMA issue
 //   warp 13         schedule, copies of the records (cp.async.bulk)
 //   warp 14         queries (TMA, or by hand where a tile has few rows) and lse
+//   warp 15         gate: waits for all that a product needs, so that the MMA warp waits once
 // Every wait is bounded; see kv4_chunk.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -40,27 +41,32 @@ namespace spc {
 
 constexpr int kMsRaw = 3, kMsRun = 16;                // stages of each dequantising warp's ring of records, positions a stage
 constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
-constexpr int kMsK = 4;                               // ring of dequantised K tiles
+constexpr int kMsK = 2;                               // ring of dequantised K tiles
 constexpr int kMsQ = 6;                               // ring of Q tiles
 constexpr int kMsL = 8;                               // ring of the rows' lse
 constexpr int kMsItems = 2;
+constexpr int kMsGo = 4;                              // products that the gate may be ahead by
 constexpr int kMsMasks = 16;                          // tiles whose masks are kept: the copies are at most 11 ahead of the sums
 constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
 constexpr int kMsWarpDeq = 8, kMsWarpMma = 12, kMsWarpPlan = 13, kMsWarpQ = 14;
 constexpr int kMsThreads = 512;
+// registers a thread: 128 at launch (512 threads); the two warpgroups that sum
+// 176, dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128
 constexpr int kMsRegSum = 176, kMsRegDeq = 88, kMsRegRest = 72;
 constexpr int kMsFixed = 1;                           // units of an item's fixed part
-constexpr int kMsTmemCols = 512;                      // S of A and B, four K tiles of 64 columns
-constexpr uint32_t kMsColK = 256;
+constexpr int kMsS = 3;                               // ring of S
+constexpr int kMsTmemCols = 512;                      // S, and K tiles of 64 columns
+constexpr uint32_t kMsColK = kMsS * 128;
+static_assert(kMsColK + kMsK * 64 <= kMsTmemCols, "tensor memory");
 
 constexpr uint32_t kMsOffQ = 0;
 constexpr uint32_t kMsOffRaw = kMsOffQ + kMsQ * kKcTile;
 constexpr uint32_t kMsOffItem = kMsOffRaw + 4 * kMsRaw * kMsStage;    // [kMsItems] MsItem
 constexpr uint32_t kMsOffLse = kMsOffItem + kMsItems * 64;            // [kMsL][128] -lse
-constexpr uint32_t kMsOffOdd = kMsOffLse + kMsL * 512;                // [kMsL][4 words] rows that add nothing
-constexpr uint32_t kMsOffMask = kMsOffOdd + kMsL * 16;                // [kMsMasks][4 words]
+constexpr uint32_t kMsOffOdd = kMsOffLse + kMsL * 512;                // [kMsL] whether a row adds nothing, [4 words] which
+constexpr uint32_t kMsOffMask = kMsOffOdd + kMsL * 32;                // [kMsMasks][4 words]
 constexpr uint32_t kMsOffBar = kMsOffMask + kMsMasks * 16;
-constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * 2 + 1;
+constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * kMsS + kMsGo + 1;
 constexpr size_t kMsSmem = 1024 + kMsOffBar + kMsBars * 8 + 16;
 static_assert(kMsSmem <= 227 * 1024, "shared memory of one CTA");
 
@@ -166,12 +172,13 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   uint64_t* qfull = kfree + kMsK;             // [kMsQ] the tile's rows are there
   uint64_t* qfree = qfull + kMsQ;             // [kMsQ] commit after the MMAs that read them
   uint64_t* lfull = qfree + kMsQ;             // [kMsL] the rows' lse are there
-  uint64_t* lfree = lfull + kMsL;             // [kMsL] eight summing warps have read them
+  uint64_t* lfree = lfull + kMsL;             // [kMsL] the summing warps have read them
   uint64_t* ifull = lfree + kMsL;             // [kMsItems]
   uint64_t* ifree = ifull + kMsItems;         // [kMsItems]
-  uint64_t* sfull = ifree + kMsItems;         // [2 tiles] commit: S in tensor memory
-  uint64_t* sfree = sfull + 2;                // [2] four summing warps have read it
-  uint64_t* drain = sfree + 2;
+  uint64_t* sfull = ifree + kMsItems;         // [kMsS] commit: S in tensor memory
+  uint64_t* sfree = sfull + kMsS;             // [kMsS] four summing warps have read it
+  uint64_t* go = sfree + kMsS;                // [kMsGo] gate: S may be written, its operands are there
+  uint64_t* drain = go + kMsGo;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const Kv4ChunkCall& c = a.c;
@@ -195,12 +202,13 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     }
     for (int s = 0; s < kMsItems; ++s) {
       mbar_init(&ifull[s], 1);
-      mbar_init(&ifree[s], 4 + 8 + 2);
+      mbar_init(&ifree[s], 4 + 8 + 3);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kMsS; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], 4);
     }
+    for (int s = 0; s < kMsGo; ++s) mbar_init(&go[s], 1);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -400,12 +408,15 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         const int ls = nq % kMsL;
         acquire(&lfree[ls], ((nq / kMsL) & 1) ^ 1);
         if (dead) break;
+        uint32_t any = 0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           neglse[ls * 128 + 32 * e + lane] = -next[e];
           const uint32_t odd = __ballot_sync(0xffffffffu, next[e] == -INFINITY);
-          if (lane == 0) odds[ls * 4 + e] = odd;
+          if (lane == 0) odds[ls * 8 + 1 + e] = odd;
+          any |= odd;
         }
+        if (lane == 0) odds[ls * 8] = any;
         __syncwarp();
         if (lane == 0) mbar_arrive(&lfull[ls]);
 #pragma unroll
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     // ================= MMA issue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    int nk = 0, nq = 0, ns[2] = {0, 0};
+    int nk = 0, nq = 0, ns = 0;
     for (int it = 0;; ++it) {
       const int is = it % kMsItems;
       acquire(&ifull[is], (it / kMsItems) & 1);
@@ -432,15 +443,14 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (b < 0) break;
-      for (int j = 0; j < tiles; ++j) acquire(&kfull[(nk + j) % kMsK], ((nk + j) / kMsK) & 1);
       for (int r = r0; r < r1 && !dead; ++r, ++nq) {
         const int st = nq % kMsQ, N = min(128, (((n - r * a.tpm) << a.gshift) + 15) & ~15);
-        acquire(&lfull[nq % kMsL], (nq / kMsL) & 1);
-        acquire(&qfull[st], (nq / kMsQ) & 1);
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          acquire(&sfree[j], (ns[j]++ & 1) ^ 1);
+          const int buf = ns % kMsS;
+          acquire(&go[ns % kMsGo], (ns / kMsGo) & 1);
+          ++ns;
           if (dead) break;
           tc_fence_after();
           if (elect_one()) {
@@ -449,9 +459,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk) {
               const uint32_t off = (uint32_t)(kk >> 2) * (kKcBlock >> 4) + (uint32_t)(kk & 3) * 2;
-              umma_f16_tmem_a(tm + (uint32_t)j * 128, kt + kk * 8, umma_desc(qd + off), idesc, kk ? 1u : 0u);
+              umma_f16_tmem_a(tm + (uint32_t)buf * 128, kt + kk * 8, umma_desc(qd + off), idesc, kk ? 1u : 0u);
             }
-            umma_commit(&sfull[j]);
+            umma_commit(&sfull[buf]);
             if (j + 1 == tiles) umma_commit(&qfree[st]);
             if (r + 1 == r1) umma_commit(&kfree[(nk + j) % kMsK]);
           }
@@ -531,6 +541,12 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       const float prev = mine && c.keep != 0.f ? c.mass_prev[at] : 0.f;
       float total = 0.f, lost = 0.f;
       bool there = false;
+      // Columns of row tile r from 0 on are tokens at or behind the warp's last
+      // position where r >= all; the last row tile may be short.
+      const long long need = (long long)(x.p0 + j * 128 + wq * 32 + 31 - (x.len - x.n));
+      const int all = (int)max(0ll, (need + a.tpm - 1) >> (7 - a.gshift));
+      const int whole = min(x.r1, x.n >> (7 - a.gshift));
+      const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
       for (int r = x.r0; r < x.r1; ++r, ++nq) {
         if (j >= x.tiles) {                           // the item has no tile B
           // its lse are read by nobody here, but only once they are there may they be released
@@ -539,43 +555,48 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
           continue;
         }
-        acquire(&sfull[j], ns++ & 1);
+        const int seq = ns + (r - x.r0) * x.tiles + j, buf = seq % kMsS;
+        acquire(&sfull[buf], (seq / kMsS) & 1);
         if (dead) break;
         tc_fence_after();
-        there = masks[((nk + j) % kMsMasks) * 4 + wq] >> lane & 1;
-        const int tok = r * a.tpm, cols = min(128, (x.n - tok) << a.gshift);
+        const uint32_t ts = tmem + lanes + (uint32_t)buf * 128;
         const float* nl = neglse + (nq % kMsL) * 128;
-        const uint4 odd = *reinterpret_cast<const uint4*>(odds + (nq % kMsL) * 4);
-        const uint32_t ts = tmem + lanes + (uint32_t)j * 128;
-        const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
-        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // columns from this one on are tokens at or behind the position
-        const long long from = (long long)(p - (x.len - x.n) - tok) << a.gshift;
-        if (cols == 128 && (odd.x | odd.y | odd.z | odd.w) == 0u && __all_sync(0xffffffffu, from <= 0)) {
-          // the whole row into registers, so that the next S can be written at once
-          float s[128];
+        float y;
+        const bool plain = r >= all && r < whole && odds[(nq % kMsL) * 8] == 0u;
+        if (plain) {
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float s[2][32];
+          tmem_ld32(ts, s[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
-          tmem_ld_wait32(s);
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait32(s[q & 1]);
+            if (q < 3) {
+              tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sfree[buf]);
+            }
 #pragma unroll
-          for (int q = 1; q < 4; ++q) tmem_ld_wait32(s + 32 * q);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[j]);
+            for (int e = 0; e < 8; ++e) {
+              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * q + 4 * e);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float4 l4 = *reinterpret_cast<const float4*>(nl + 4 * e);
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              float2 t = fma2(make_float2(s[4 * e + 2 * f], s[4 * e + 2 * f + 1]), sc,
-                              f ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
-              t = fma2(t, l2e, make_float2(0.f, 0.f));
-              t.x = ex2_approx(t.x);
-              t.y = ex2_approx(t.y);
-              sum[(2 * e + f) & 3] = add2(sum[(2 * e + f) & 3], t);
+              for (int f = 0; f < 2; ++f) {
+                float2 t = fma2(make_float2(s[q & 1][4 * e + 2 * f], s[q & 1][4 * e + 2 * f + 1]), sc,
+                                f ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                t = fma2(t, l2e, make_float2(0.f, 0.f));
+                t.x = ex2_approx(t.x);
+                t.y = ex2_approx(t.y);
+                sum[f] = add2(sum[f], t);
+              }
             }
           }
+          y = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         } else {
+          const int tok = r * a.tpm, cols = min(128, (x.n - tok) << a.gshift);
+          const long long from = (long long)(p - (x.len - x.n) - tok) << a.gshift;
+          const uint32_t* odd = odds + (nq % kMsL) * 8 + 1;
+          float sum[2] = {0.f, 0.f};
 #pragma unroll 1
           for (int q = 0; 32 * q < cols; ++q) {
             float s[32];
@@ -584,28 +605,29 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
             const long long lo = from - 32 * q;
             const int hi = cols - 32 * q;
             const uint32_t vis = (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : 0xffffffffu << (int)lo) &
-                                 (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) &
-                                 ~(q == 0 ? odd.x : q == 1 ? odd.y : q == 2 ? odd.z : odd.w);
+                                 (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & ~odd[q];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float t = ex2_approx(fmaf(s[e], c.scale, nl[32 * q + e]) * kLog2e);
-              sum[e & 3].x += vis >> e & 1 ? t : 0.f;
+              sum[e & 1] += vis >> e & 1 ? t : 0.f;
             }
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[j]);
+          if (lane == 0) mbar_arrive(&sfree[buf]);
+          y = sum[0] + sum[1];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
         // the tile's sum into the total, what the addition loses kept beside it
-        const float y = ((sum[0].x + sum[1].x) + (sum[2].x + sum[3].x)) + ((sum[0].y + sum[1].y) + (sum[2].y + sum[3].y));
         const float u = total + y, v = u - total;
         lost += (total - (u - v)) + (y - v);
         total = u;
       }
+      if (j < x.tiles) there = masks[((nk + j) % kMsMasks) * 4 + wq] >> lane & 1;
       if (dead) break;
       nk += x.tiles;
+      ns += (x.r1 - x.r0) * x.tiles;
       // infinities and NaN are the sum's own; their difference above is not
       float sum = total + (fabsf(total) < INFINITY ? lost : 0.f);
       if (!there) sum = 0.f;
@@ -628,8 +650,30 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       }
       if (mine) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, prev, sum) : sum;
     }
-  } else {
+  } else {                                    // warp 15
+    // ================= gate
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
+    int nk = 0, nq = 0, ns = 0;
+    for (int it = 0; !dead; ++it) {
+      const int is = it % kMsItems;
+      acquire(&ifull[is], (it / kMsItems) & 1);
+      if (dead) break;
+      const int b = items[is].b, steps = items[is].r1 - items[is].r0, tiles = items[is].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ifree[is]);
+      if (b < 0) break;
+      for (int j = 0; j < tiles; ++j) acquire(&kfull[(nk + j) % kMsK], ((nk + j) / kMsK) & 1);
+      for (int r = 0; r < steps && !dead; ++r, ++nq) {
+        acquire(&lfull[nq % kMsL], (nq / kMsL) & 1);
+        acquire(&qfull[nq % kMsQ], (nq / kMsQ) & 1);
+        for (int j = 0; j < tiles; ++j, ++ns) {
+          acquire(&sfree[ns % kMsS], ((ns / kMsS) & 1) ^ 1);
+          if (dead) break;
+          if (lane == 0) mbar_arrive(&go[ns % kMsGo]);
+        }
+      }
+      nk += tiles;
+    }
   }
   tc_fence_before();
   __syncthreads();
