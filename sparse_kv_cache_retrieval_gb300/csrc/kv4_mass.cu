@@ -21,12 +21,14 @@
 // that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
 // an item that is cut leave their sums in the workspace; of the warps that have
 // the same 32 positions the last to arrive adds them in the order of the pieces.
-//   warps 0-3, 4-7  exponentials and sums of tile A, B
-//   warps 8-11      dequantisation, a record a thread
-//   warp 12         tensor memory, MMA issue
-//   warp 13         schedule, copies of the records (cp.async.bulk)
-//   warp 14         queries (TMA, or by hand where a tile has few rows) and lse
-//   warp 15         gate: waits for all that a product needs, so that the MMA warp waits once
+//   warps 0-11      exponentials and sums: three groups take the products in turn, each
+//                   from an S of its own (a warp's way through one is some 2000 clocks,
+//                   of which it issues for 500: with two groups 904 us at 16K)
+//   warps 12-15     dequantisation, a record a thread
+//   warp 16         tensor memory, MMA issue
+//   warp 17         schedule, copies of the records (cp.async.bulk)
+//   warp 18         queries (TMA, or by hand where a tile has few rows) and lse
+//   warp 19         gate: waits for all that a product needs, so that the MMA warp waits once
 // Every wait is bounded; see kv4_chunk.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -43,18 +45,18 @@ constexpr int kMsRaw = 3, kMsRun = 16;                // stages of each dequanti
 constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
 constexpr int kMsK = 2;                               // ring of dequantised K tiles
 constexpr int kMsQ = 6;                               // ring of Q tiles
-constexpr int kMsL = 8;                               // ring of the rows' lse
+constexpr int kMsL = 6;                               // ring of the rows' lse
 constexpr int kMsItems = 2;
 constexpr int kMsGo = 4;                              // products that the gate may be ahead by
 constexpr int kMsMasks = 16;                          // tiles whose masks are kept: the copies are at most 11 ahead of the sums
 constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
-constexpr int kMsWarpDeq = 8, kMsWarpMma = 12, kMsWarpPlan = 13, kMsWarpQ = 14;
-constexpr int kMsThreads = 512;
-// registers a thread: 128 at launch (512 threads); the two warpgroups that sum
-// 176, dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128
-constexpr int kMsRegSum = 176, kMsRegDeq = 88, kMsRegRest = 72;
+constexpr int kMsWarpDeq = 12, kMsWarpMma = 16, kMsWarpPlan = 17, kMsWarpQ = 18;
+constexpr int kMsThreads = 640;
+// registers a thread: 96 at launch (640 threads); the three warpgroups that sum
+// 112, dequantisation 80, the rest 64: 3 * 112 + 80 + 64 = 5 * 96
+constexpr int kMsRegSum = 112, kMsRegDeq = 80, kMsRegRest = 64;
 constexpr int kMsFixed = 1;                           // units of an item's fixed part
-constexpr int kMsS = 3;                               // ring of S
+constexpr int kMsS = 3;                               // ring of S, and groups that sum
 constexpr int kMsTmemCols = 512;                      // S, and K tiles of 64 columns
 constexpr uint32_t kMsColK = kMsS * 128;
 static_assert(kMsColK + kMsK * 64 <= kMsTmemCols, "tensor memory");
@@ -65,8 +67,9 @@ constexpr uint32_t kMsOffItem = kMsOffRaw + 4 * kMsRaw * kMsStage;    // [kMsIte
 constexpr uint32_t kMsOffLse = kMsOffItem + kMsItems * 64;            // [kMsL][128] -lse
 constexpr uint32_t kMsOffOdd = kMsOffLse + kMsL * 512;                // [kMsL] whether a row adds nothing, [4 words] which
 constexpr uint32_t kMsOffMask = kMsOffOdd + kMsL * 32;                // [kMsMasks][4 words]
-constexpr uint32_t kMsOffBar = kMsOffMask + kMsMasks * 16;
-constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * kMsS + kMsGo + 1;
+constexpr uint32_t kMsOffComb = kMsOffMask + kMsMasks * 16;          // [2 tiles][2 other groups][128] sums
+constexpr uint32_t kMsOffBar = kMsOffComb + 2 * 2 * 512;
+constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsItems + 2 * kMsS + kMsGo + 2 * 8 + 1;
 constexpr size_t kMsSmem = 1024 + kMsOffBar + kMsBars * 8 + 16;
 static_assert(kMsSmem <= 227 * 1024, "shared memory of one CTA");
 
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   float* neglse = reinterpret_cast<float*>(base + kMsOffLse);
   uint32_t* odds = reinterpret_cast<uint32_t*>(base + kMsOffOdd);
   uint32_t* masks = reinterpret_cast<uint32_t*>(base + kMsOffMask);
+  float* comb = reinterpret_cast<float*>(base + kMsOffComb);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + kMsOffBar);
   uint64_t* rfull = bars;                     // [4 warps][kMsRaw] bytes of the records
   uint64_t* rfree = rfull + 4 * kMsRaw;       // [4][kMsRaw] the warp has read them
@@ -178,7 +182,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   uint64_t* sfull = ifree + kMsItems;         // [kMsS] commit: S in tensor memory
   uint64_t* sfree = sfull + kMsS;             // [kMsS] four summing warps have read it
   uint64_t* go = sfree + kMsS;                // [kMsGo] gate: S may be written, its operands are there
-  uint64_t* drain = go + kMsGo;
+  uint64_t* cdone = go + kMsGo;               // [2 tiles][4 warps] the other groups' sums are there
+  uint64_t* cread = cdone + 8;                // [2][4] and have been read
+  uint64_t* drain = cread + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const Kv4ChunkCall& c = a.c;
@@ -202,13 +208,17 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     }
     for (int s = 0; s < kMsItems; ++s) {
       mbar_init(&ifull[s], 1);
-      mbar_init(&ifree[s], 4 + 8 + 3);
+      mbar_init(&ifree[s], 4 + 12 + 3);
     }
     for (int s = 0; s < kMsS; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], 4);
     }
     for (int s = 0; s < kMsGo; ++s) mbar_init(&go[s], 1);
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&cdone[s], 2);
+      mbar_init(&cread[s], 1);
+    }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -522,11 +532,13 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       if (dead) break;
     }
   } else if (warp < kMsWarpDeq) {
-    // ================= exponentials and sums of tile j, one position a thread
+    // ================= exponentials and sums, one position a thread: group g takes the
+    // products whose number is g modulo 3, and ends up with tile g's sums
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kMsRegSum));
-    const int j = warp >> 2, wq = warp & 3;
-    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    int ns = 0, nq = 0, nk = 0;
+    const int grp = warp >> 2, wq = warp & 3, lt = 7 - a.gshift;
+    const uint32_t ts = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)grp * 128;
+    const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
+    int ns = 0, nq = 0, nk = 0, nc[2] = {0, 0};
     for (int it = 0;; ++it) {
       const int is = it % kMsItems;
       acquire(&ifull[is], (it / kMsItems) & 1);
@@ -535,35 +547,27 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (x.b < 0) break;
-      const int p = x.p0 + j * 128 + wq * 32 + lane;
-      const size_t at = ((size_t)x.b * c.n_kv + x.g) * c.cap + p;
-      const bool mine = j < x.tiles && p < x.len;
+      const int two = x.tiles - 1, count = (x.r1 - x.r0) << two, ctx = x.len - x.n;
+      const int at0 = x.p0 + wq * 32;                 // the warp's first position in tile A
+      const size_t at = ((size_t)x.b * c.n_kv + x.g) * c.cap + at0 + grp * 128 + lane;
+      const bool mine = grp < x.tiles && at0 + grp * 128 + lane < x.len;
       const float prev = mine && c.keep != 0.f ? c.mass_prev[at] : 0.f;
-      float total = 0.f, lost = 0.f;
-      bool there = false;
-      // Columns of row tile r from 0 on are tokens at or behind the warp's last
-      // position where r >= all; the last row tile may be short.
-      const long long need = (long long)(x.p0 + j * 128 + wq * 32 + 31 - (x.len - x.n));
-      const int all = (int)max(0ll, (need + a.tpm - 1) >> (7 - a.gshift));
-      const int whole = min(x.r1, x.n >> (7 - a.gshift));
-      const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
-      for (int r = x.r0; r < x.r1; ++r, ++nq) {
-        if (j >= x.tiles) {                           // the item has no tile B
-          // its lse are read by nobody here, but only once they are there may they be released
-          acquire(&lfull[nq % kMsL], (nq / kMsL) & 1);
-          if (dead) break;
-          if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
-          continue;
-        }
-        const int seq = ns + (r - x.r0) * x.tiles + j, buf = seq % kMsS;
-        acquire(&sfull[buf], (seq / kMsS) & 1);
+      float total[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
+      // Row tile r's columns are all tokens at or behind the warp's last position
+      // of tile j where r >= all[j]; the last row tile may be short.
+      int all[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        all[j] = (int)max(0ll, ((long long)at0 + j * 128 + 31 - ctx + a.tpm - 1) >> lt);
+      const int whole = x.n >> lt;
+      for (int k = (grp + kMsS - ns % kMsS) % kMsS; k < count; k += kMsS) {
+        const int r = x.r0 + (k >> two), j = k & two, ls = (nq + (k >> two)) % kMsL;
+        acquire(&sfull[grp], ((ns + k) / kMsS) & 1);
         if (dead) break;
         tc_fence_after();
-        const uint32_t ts = tmem + lanes + (uint32_t)buf * 128;
-        const float* nl = neglse + (nq % kMsL) * 128;
+        const float* nl = neglse + ls * 128;
         float y;
-        const bool plain = r >= all && r < whole && odds[(nq % kMsL) * 8] == 0u;
-        if (plain) {
+        if (r >= (j ? all[1] : all[0]) && r < whole && odds[ls * 8] == 0u) {
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           float s[2][32];
           tmem_ld32(ts, s[0]);
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
             } else {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sfree[buf]);
+              if (lane == 0) mbar_arrive(&sfree[grp]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -594,8 +598,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           y = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         } else {
           const int tok = r * a.tpm, cols = min(128, (x.n - tok) << a.gshift);
-          const long long from = (long long)(p - (x.len - x.n) - tok) << a.gshift;
-          const uint32_t* odd = odds + (nq % kMsL) * 8 + 1;
+          // columns from this one on are tokens at or behind the position
+          const long long from = ((long long)at0 + j * 128 + lane - ctx - tok) << a.gshift;
+          const uint32_t* odd = odds + ls * 8 + 1;
           float sum[2] = {0.f, 0.f};
 #pragma unroll 1
           for (int q = 0; 32 * q < cols; ++q) {
@@ -614,43 +619,67 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[buf]);
+          if (lane == 0) mbar_arrive(&sfree[grp]);
           y = sum[0] + sum[1];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&lfree[nq % kMsL]);
+        if (lane <= 1 - two) mbar_arrive(&lfree[ls]);   // eight arrivals a row tile, also where one tile reads it
         // the tile's sum into the total, what the addition loses kept beside it
-        const float u = total + y, v = u - total;
-        lost += (total - (u - v)) + (y - v);
-        total = u;
+        const float t0 = j ? total[1] : total[0], u = t0 + y, v = u - t0, w = (t0 - (u - v)) + (y - v);
+        if (j) {
+          total[1] = u;
+          lost[1] += w;
+        } else {
+          total[0] = u;
+          lost[0] += w;
+        }
       }
-      if (j < x.tiles) there = masks[((nk + j) % kMsMasks) * 4 + wq] >> lane & 1;
+      if (dead) break;
+      ns += count;
+      nq += x.r1 - x.r0;
+      // a tile's sums from the other two groups to the one that has its number
+      float sum[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // infinities and NaN are the sum's own; their difference above is not
+        sum[j] = total[j] + (fabsf(total[j]) < INFINITY ? lost[j] : 0.f);
+        if (j >= x.tiles || j == grp) continue;
+        acquire(&cread[j * 4 + wq], (nc[j]++ & 1) ^ 1);
+        if (dead) break;
+        comb[(j * 2 + (grp == 2 ? 1 : 0)) * 128 + wq * 32 + lane] = sum[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cdone[j * 4 + wq]);
+      }
       if (dead) break;
       nk += x.tiles;
-      ns += (x.r1 - x.r0) * x.tiles;
-      // infinities and NaN are the sum's own; their difference above is not
-      float sum = total + (fabsf(total) < INFINITY ? lost : 0.f);
-      if (!there) sum = 0.f;
-      if (j >= x.tiles) continue;
+      if (grp >= x.tiles) continue;
+      acquire(&cdone[grp * 4 + wq], nc[grp & 1]++ & 1);
+      if (dead) break;
+      float y = grp ? sum[1] : sum[0];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) y += comb[(grp * 2 + e) * 128 + wq * 32 + lane];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cread[grp * 4 + wq]);
+      if (!(masks[((nk - x.tiles + grp) % kMsMasks) * 4 + wq] >> lane & 1)) y = 0.f;
       if (x.pieces > 1) {
-        float* part = a.part + ((size_t)blockIdx.x * 2 + (x.piece == 0 ? 1 : 0)) * 256 + j * 128 + wq * 32 + lane;
-        *part = sum;
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (x.piece == 0 ? 1 : 0)) * 256 + grp * 128 + wq * 32 + lane;
+        *part = y;
         __threadfence();
         __syncwarp();
-        uint32_t* count = a.counters + x.first * 8 + j * 4 + wq;
+        uint32_t* arrived = a.counters + x.first * 8 + grp * 4 + wq;
         uint32_t before = 0u;
-        if (lane == 0) before = atomicAdd(count, 1u);
+        if (lane == 0) before = atomicAdd(arrived, 1u);
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before + 1u != (uint32_t)x.pieces) continue;
         __threadfence();
-        sum = 0.f;
+        y = 0.f;
         for (int k = 0; k < x.pieces; ++k)
-          sum += __ldcg(a.part + ((size_t)(x.first + k) * 2 + (k == 0 ? 1 : 0)) * 256 + j * 128 + wq * 32 + lane);
-        if (lane == 0) atomicExch(count, 0u);
+          y += __ldcg(a.part + ((size_t)(x.first + k) * 2 + (k == 0 ? 1 : 0)) * 256 + grp * 128 + wq * 32 + lane);
+        if (lane == 0) atomicExch(arrived, 0u);
       }
-      if (mine) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, prev, sum) : sum;
+      if (mine) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, prev, y) : y;
     }
-  } else {                                    // warp 15
+  } else {                                    // warp 19
     // ================= gate
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMsRegRest));
     int nk = 0, nq = 0, ns = 0;
