@@ -9,10 +9,12 @@
 //   S[128][128] = Q K^T     Q, K in shared memory (128-byte swizzle)
 //   O[128][128] += P V      P in tensor memory over S's columns, V MN-major
 // The tensor cores work on one tile while the other one's softmax runs. A
-// request's last tile, if it has no partner (and with few new tokens it is the
-// only one), takes both places: A runs over the even blocks and B over the odd
-// ones, and A's warps merge what B's have found (a warp of B has the same tensor
-// memory lanes, so that only maxima and sums go through shared memory).
+// request's last tile, if it has no partner, takes both places: A runs over the
+// even blocks and B over the odd ones, against the same Q, and A's warps merge
+// what B's have found (a warp of B has the same tensor memory lanes, so that only
+// maxima and sums go through shared memory). Where there are few new tokens all
+// tiles are such ones (LONE): there is one Q, and its partner's memory goes to the
+// rings of records, which then hold 3.5 blocks of the cache and not 1.5.
 //
 // Operands are fp16. A record's values are exact there; 11 bits of P instead of
 // bf16's 8; and e2m1 to fp16 is one conversion for two values. Queries are scaled
@@ -63,11 +65,11 @@ namespace spc {
 
 // Records: a ring for each dequantising warp (one reader, so that a wait on a phase's
 // parity is never two phases behind), stages of 16 positions, which lie in one cache block
-constexpr int kKcRaw = 3, kKcRun = 16;
+constexpr int kKcRun = 16;
 constexpr uint32_t kKcStage = kKcRun * kKv4Rec;
 constexpr int kKcSlots = 4;                           // ring of dequantised operands
 constexpr int kKcItems = 2;                           // item ring
-constexpr int kKcMasks = 8;                           // blocks whose masks are kept: the copies are at most 5 ahead of the softmax
+constexpr int kKcMasks = 16;                          // blocks whose masks are kept: the copies are at most 8 ahead of the softmax
 constexpr int kKcWarpDeq = 8, kKcWarpMma = 12, kKcWarpCopy = 13, kKcWarpQ = 14;
 constexpr int kKcThreads = 512;
 // registers a thread: 128 at launch (512 threads); softmax 176 (two warpgroups),
@@ -83,18 +85,25 @@ constexpr uint32_t kKcIdescS = (1u << 4) | ((uint32_t)(kKcKeys >> 3) << 17) | (8
 constexpr uint32_t kKcIdescO = kKcIdescS | (1u << 16);
 constexpr uint32_t kKcDescVLo = umma_mn_lo(kKcBlock);
 
-// shared memory, from a 1024-byte aligned base
-constexpr uint32_t kKcOffQ = 0;                                       // [2] tiles
-constexpr uint32_t kKcOffKv = kKcOffQ + 2 * kKcTile;
-constexpr uint32_t kKcOffRaw = kKcOffKv + kKcSlots * kKcTile;
-constexpr uint32_t kKcOffItem = kKcOffRaw + 4 * kKcRaw * kKcStage;        // [kKcItems] KcItem
-constexpr uint32_t kKcOffNan = kKcOffItem + kKcItems * 64;            // [kKcItems][8] first position with a NaN V scale
-constexpr uint32_t kKcOffMask = kKcOffNan + kKcItems * 32;            // [kKcMasks][4 words]
-constexpr uint32_t kKcOffMl = kKcOffMask + kKcMasks * 16;              // [128] maximum and sum of tile B's row, for tile A
-constexpr uint32_t kKcOffBar = kKcOffMl + 128 * 8;
-constexpr int kKcBars = 8 * kKcRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 2 * 4 + 1;
-constexpr size_t kKcSmem = 1024 + kKcOffBar + kKcBars * 8 + 16;
-static_assert(kKcSmem <= 227 * 1024, "shared memory of one CTA");
+// what differs between the kernel for few new tokens and the other one
+template <bool LONE>
+struct KcCfg {
+  static constexpr int kRaw = LONE ? 7 : 3;           // stages of a ring of records
+  static constexpr int kTiles = LONE ? 1 : 2;         // of Q
+  // shared memory, from a 1024-byte aligned base
+  static constexpr uint32_t kOffQ = 0;                                    // [kTiles]
+  static constexpr uint32_t kOffKv = kOffQ + kTiles * kKcTile;
+  static constexpr uint32_t kOffRaw = kOffKv + kKcSlots * kKcTile;        // [4 warps][kRaw]
+  static constexpr uint32_t kOffItem = kOffRaw + 4 * kRaw * kKcStage;     // [kKcItems] KcItem
+  static constexpr uint32_t kOffNan = kOffItem + kKcItems * 64;           // [kKcItems][8] first position with a NaN V scale
+  static constexpr uint32_t kOffMask = kOffNan + kKcItems * 32;           // [kKcMasks][4 words]
+  static constexpr uint32_t kOffMl = kOffMask + kKcMasks * 16;            // [128] maximum and sum of tile B's row, for tile A
+  static constexpr uint32_t kOffInv = kOffMl + 128 * 8;                   // [128] scale of tile A's row, for tile B
+  static constexpr uint32_t kOffBar = kOffInv + 128 * 4;
+  static constexpr int kBars = 8 * kRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 2 * 4 + 1;
+  static constexpr size_t kSmem = 1024 + kOffBar + kBars * 8 + 16;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
 
 // workspace: status; for each CTA the item that is cut first there; partials, of
 // a CTA's first and last piece, two tiles each
@@ -189,24 +198,25 @@ __device__ __forceinline__ float kc_query(uint32_t tile, int r) {
 }
 
 // ---------------------------------------------------------------- the line of work
-// Pairs of tiles of a request: pair i holds tokens [i t, (i + 1) t), t = 2 tpm,
-// and sees ceil((ctx + (i + 1) t) / 128) blocks, ctx = len - n, at least one.
+// Items of a request: item i holds tokens [i t, (i + 1) t), two tiles' or one's,
+// and sees ceil((ctx + (i + 1) t) / 128) blocks, ctx = len - n, at least one. A unit
+// is a block, or two of them where one tile takes both places.
 struct KcShape {
-  int ctx, n, lt, pairs;   // lt: log2 of t
+  int ctx, n, lt, lb, pairs;   // lt: log2 of t; lb: of a unit's positions; items
 };
 __device__ __forceinline__ int kc_blocks(const KcShape& s, int i) {
   return max(1, (s.ctx + min(s.n, (i + 1) << s.lt) + kKcKeys - 1) >> 7);
 }
-// units of the pairs below k <= pairs - 1, all of them whole
+// units of the items below k <= items - 1, none of them the last one
 __device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
-  const int lt = s.lt;
-  // the first ones see one block (or nothing), from i0 on the sum of an arithmetic progression's quotients
-  const int i0 = max(0, min(k, (kKcKeys - s.ctx) >> lt)), m = k - i0;
+  const int lt = s.lt, lb = s.lb, mask = (1 << lb) - 1;
+  // the first ones see one unit (or nothing), from i0 on the sum of an arithmetic progression's quotients
+  const int i0 = max(0, min(k, (mask + 1 - s.ctx) >> lt)), m = k - i0;
   long long u = (long long)k * kKcFixed + i0;
   if (m == 0) return u;
   const int c = s.ctx + (i0 << lt);
-  if (lt >= 7) return u + (long long)m * ((c + 127) >> 7) + ((long long)m * (m + 1) / 2 << (lt - 7));
-  const int ls = 7 - lt, w = (1 << ls) - 1 + ((c & ((1 << lt) - 1)) > 0 ? 1 : 0);
+  if (lt >= lb) return u + (long long)m * ((c + mask) >> lb) + ((long long)m * (m + 1) / 2 << (lt - lb));
+  const int ls = lb - lt, w = (1 << ls) - 1 + ((c & ((1 << lt) - 1)) > 0 ? 1 : 0);
   const long long a = (c >> lt) + w;                  // sum of floor((a + i) / 2^ls), i = 1 .. m
   auto below = [&](long long x) {                     // sum of floor(j / 2^ls), j = 0 .. x
     const long long q = (x + 1) >> ls, r = (x + 1) & ((1 << ls) - 1);
@@ -214,11 +224,15 @@ __device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
   };
   return u + below(a + m) - below(a);
 }
-// tiles of a request, and whether its pair i has one alone
-__device__ __forceinline__ int kc_tiles(const KcShape& s) { return (s.n + (1 << (s.lt - 1)) - 1) >> (s.lt - 1); }
+// whether item i is one tile, and its units
+template <bool LONE>
+__device__ __forceinline__ bool kc_single(const KcShape& s, int i) {
+  return LONE || 2 * i + 2 > (s.n + (1 << (s.lt - 1)) - 1) >> (s.lt - 1);
+}
+template <bool LONE>
 __device__ __forceinline__ int kc_item_units(const KcShape& s, int i) {
   const int nb = kc_blocks(s, i);
-  return 2 * i + 2 > kc_tiles(s) ? (nb + 1) >> 1 : nb;
+  return kc_single<LONE>(s, i) ? (nb + 1) >> 1 : nb;
 }
 
 __device__ __forceinline__ float kc_lse(const KcArgs& a, float m, float l, float inv) {
@@ -281,15 +295,19 @@ __global__ void __launch_bounds__(kKcMergeThreads) kv4_chunk_merge_kernel(const 
   }
 }
 
+template <bool LONE>
 __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const KcArgs a) {
+  using Cfg = KcCfg<LONE>;
+  constexpr int kKcRaw = Cfg::kRaw;
   extern __shared__ uint8_t kc_raw[];
   const uint32_t raw_addr = smem_u32(kc_raw);
   uint8_t* base = kc_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  KcItem* items = reinterpret_cast<KcItem*>(base + kKcOffItem);
-  int* nans = reinterpret_cast<int*>(base + kKcOffNan);
-  uint32_t* masks = reinterpret_cast<uint32_t*>(base + kKcOffMask);
-  float2* ml_b = reinterpret_cast<float2*>(base + kKcOffMl);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kKcOffBar);
+  KcItem* items = reinterpret_cast<KcItem*>(base + Cfg::kOffItem);
+  int* nans = reinterpret_cast<int*>(base + Cfg::kOffNan);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(base + Cfg::kOffMask);
+  float2* ml_b = reinterpret_cast<float2*>(base + Cfg::kOffMl);
+  float* inv_a = reinterpret_cast<float*>(base + Cfg::kOffInv);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::kOffBar);
   uint64_t* rfull = bars;                     // [4 warps][kKcRaw] bytes of the records
   uint64_t* rfree = rfull + 4 * kKcRaw;       // [4][kKcRaw] the warp has read them
   uint64_t* kvfull = rfree + 4 * kKcRaw;      // [kKcSlots] four dequantising warps have written the operand
@@ -342,7 +360,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t qs = smem_u32(base + kKcOffQ), kvs = smem_u32(base + kKcOffKv);
+  const uint32_t qs = smem_u32(base + Cfg::kOffQ), kvs = smem_u32(base + Cfg::kOffKv);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
     // mostly over: tested before it is waited for (some 90 cycles against 190)
@@ -357,17 +375,18 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
     KcRequests rq;
     kc_requests(c, rq);
-    const int lt = 8 - a.gshift, bs = 1 << c.block_shift;   // lt: log2 of the tokens a pair
+    const int lt = (LONE ? 7 : 8) - a.gshift, bs = 1 << c.block_shift;
     auto shape = [&](int len, int n) {
       KcShape s;
       s.ctx = len - n;
       s.n = n;
       s.lt = lt;
+      s.lb = LONE ? 8 : 7;
       s.pairs = (n + (1 << lt) - 1) >> lt;
       return s;
     };
     auto units = [&](const KcShape& s) {              // of one KV head
-      return s.n == 0 ? 0ll : kc_units(s, s.pairs - 1) + kKcFixed + kc_item_units(s, s.pairs - 1);
+      return s.n == 0 ? 0ll : kc_units(s, s.pairs - 1) + kKcFixed + kc_item_units<LONE>(s, s.pairs - 1);
     };
     long long own[2];
 #pragma unroll
@@ -406,7 +425,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       x.n = -1;
       bool skip = false;
       if (has && at < u1 && !dead) {
-        const int nu = kc_item_units(s, i);
+        const int nu = kc_item_units<LONE>(s, i);
         nb = kc_blocks(s, i);
         const long long first = at + kKcFixed;        // its first block's unit
         const int lo = (int)max(0ll, u0 - first), hi = (int)min((long long)nu, u1 - first);
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
           x.len = s.ctx + s.n;
           x.g = g;
           x.t0 = i << lt;
-          x.single = 2 * i + 2 > kc_tiles(s);
+          x.single = kc_single<LONE>(s, i);
           x.j0 = x.single ? 2 * lo : lo;
           x.j1 = x.single ? min(nb, 2 * hi) : hi;
           if (x.single) {
@@ -469,7 +488,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
               if (h == 1) masks[(blocks % kKcMasks) * 4 + lane] = mask;
               if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
               if (n > 0)
-                bulk_g2s(base + kKcOffRaw + (lane * kKcRaw + st) * kKcStage,
+                bulk_g2s(base + Cfg::kOffRaw + (lane * kKcRaw + st) * kKcStage,
                          c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
             }
             __syncwarp();
@@ -477,7 +496,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         }
       }
       // the next item
-      at += kKcFixed + kc_item_units(s, i);
+      at += kKcFixed + kc_item_units<LONE>(s, i);
       if (++i == s.pairs) {
         i = 0;
         if (++g == c.n_kv) {
@@ -509,13 +528,13 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
 #endif
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        if ((i ? n1 : n0) == 0) continue;
+        if (i ? single || n1 == 0 : n0 == 0) continue;  // one tile in both places has one Q
         acquire(&qfree[i], (nq[i] & 1) ^ 1);
         if (dead) break;
         ++nq[i];
         if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[i], kKcTile);
-          const int r = row + (single ? 0 : i * a.tpm);
+          const int r = row + i * a.tpm;
           tma_load_3d(qs + i * kKcTile, &qmap, 0, g << a.gshift, r, &qfull[i]);
           tma_load_3d(qs + i * kKcTile + kKcBlock, &qmap, 64, g << a.gshift, r, &qfull[i]);
         }
@@ -535,21 +554,21 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     auto full = [&](int k) {                          // operand k has been written
       acquire(&kvfull[k % kKcSlots], (k / kKcSlots) & 1);
     };
-    // S of tile i against operand k; first: of the piece, last: no further one. `done`: nothing else reads k
-    auto issue_s = [&](auto tile, int k, bool first, bool last, bool done) {
-      constexpr int i = decltype(tile)::value;
-      if (first) acquire(&qready[i], nq[i]++ & 1);
+    // S of tile i, of Q q, against operand k; first: use of q, last: no further one. `done`: nothing else reads k
+    auto issue_s = [&](auto tile, auto q, int k, bool first, bool last, bool done) {
+      constexpr int i = decltype(tile)::value, qi = decltype(q)::value;
+      if (first) acquire(&qready[qi], nq[qi]++ & 1);
       if (dead) return;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t qd = umma_desc_lo(qs + i * kKcTile), kd = umma_desc_lo(kvs) + (uint32_t)(k % kKcSlots) * (kKcTile >> 4);
+        const uint32_t qd = umma_desc_lo(qs + qi * kKcTile), kd = umma_desc_lo(kvs) + (uint32_t)(k % kKcSlots) * (kKcTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t off = (uint32_t)(kk >> 2) * (kKcBlock >> 4) + (uint32_t)(kk & 3) * 2;
           umma_f16(tm + i * kKcKeys, umma_desc(qd + off), umma_desc(kd + off), kKcIdescS, kk ? 1u : 0u);
         }
         umma_commit(&sfull[i]);
-        if (last) umma_commit(&qfree[i]);
+        if (last) umma_commit(&qfree[qi]);
         if (done) umma_commit(&kvfree[k % kKcSlots]);
       }
       __syncwarp();
@@ -583,11 +602,11 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       if (n < 0) break;
       // operand kv + 2 k is K of the piece's block k, kv + 2 k + 1 its V
       full(kv);
-      if (single) {
-        issue_s(tA, kv, true, n0 == 1, true);
+      if (LONE || single) {
+        issue_s(tA, tA, kv, true, nb == 1, true);
         if (n1) {
           full(kv + 2);
-          issue_s(tB, kv + 2, true, n1 == 1, true);
+          issue_s(tB, tA, kv + 2, false, nb == 2, true);
         }
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; k += 2) {
@@ -595,24 +614,24 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
           if (k + 1 < nb) issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
           if (k + 2 < nb) {
             full(kv + 2 * k + 4);
-            issue_s(tA, kv + 2 * k + 4, false, k + 4 >= nb, true);
+            issue_s(tA, tA, kv + 2 * k + 4, false, k + 3 == nb, true);
           }
           if (k + 3 < nb) {
             full(kv + 2 * k + 6);
-            issue_s(tB, kv + 2 * k + 6, false, k + 5 >= nb, true);
+            issue_s(tB, tA, kv + 2 * k + 6, false, k + 4 == nb, true);
           }
         }
-      } else {
-        if (n0) issue_s(tA, kv, true, n0 == 1, n1 == 0);
-        if (n1) issue_s(tB, kv, true, n1 == 1, true);
+      } else if constexpr (!LONE) {
+        if (n0) issue_s(tA, tA, kv, true, n0 == 1, n1 == 0);
+        if (n1) issue_s(tB, tB, kv, true, n1 == 1, true);
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; ++k) {
           // PV of block k, S of the next one; the tensor pipe queues only a few MMAs, so nothing waits between the two
           const int v = kv + 2 * k + 1;
           if (k < n0) issue_pv(tA, v, k == 0, k + 1 == n0, k >= n1);
-          if (k + 1 < n0) issue_s(tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
+          if (k + 1 < n0) issue_s(tA, tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
           if (k < n1) issue_pv(tB, v, k == 0, k + 1 == n1, true);
-          if (k + 1 < n1) issue_s(tB, v + 1, false, k + 2 == n1, true);
+          if (k + 1 < n1) issue_s(tB, tB, v + 1, false, k + 2 == n1, true);
         }
       }
       kv += 2 * nb;
@@ -643,7 +662,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         if (dead) break;
         nread += 2;
         // the whole record into registers, so that its stage is free at once
-        const uint32_t rec = smem_u32(base + kKcOffRaw) + (uint32_t)(w * kKcRaw + (lane < kKcRun ? s0 : s1)) * kKcStage +
+        const uint32_t rec = smem_u32(base + Cfg::kOffRaw) + (uint32_t)(w * kKcRaw + (lane < kKcRun ? s0 : s1)) * kKcStage +
                              (uint32_t)(lane & (kKcRun - 1)) * kKv4Rec;
         const bool there = masks[(blocks % kKcMasks) * 4 + w] >> lane & 1;
         uint4 v[9];
@@ -701,15 +720,16 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       const int token = t0 + (row >> a.gshift), qpos = x.len - x.n + token, qpos0 = x.len - x.n + t0;
       const int hq = (x.g << a.gshift) + (row & (a.G - 1));
       float m = -INFINITY, l = 0.f, inv = 1.f;
-      if (n > 0) {
+      if (n > 0 && !(i && x.single)) {
         acquire(&qfull[i], n_q & 1);
         if (dead) break;
         ++n_q;
         inv = kc_query(qs + i * kKcTile, row);
+        if (x.single) inv_a[row] = inv;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qready[i]);
-      } else if (x.pieces > 1 && !x.single) {
+      } else if (n == 0 && x.pieces > 1 && !x.single) {
         // a piece without a block of this tile's: the rows' factors, for the merge
         const int t = min(x.row0 + token, c.T - 1);
         uint32_t mx = 0u;
@@ -720,12 +740,16 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         }
         inv = __int_as_float((127 - min(141 - (int)(max(mx & 0xffffu, mx >> 16) >> 7), 126)) << 23);
       }
-      const float f = k4_factor(inv * c.scale * kLog2e);
+      float f = k4_factor(inv * c.scale * kLog2e);
       for (int k = 0; k < n; ++k) {
         const int j = x.single ? x.j0 + 2 * k + i : x.j0 + k;
         acquire(&sfull[i], n_s & 1);
         if (dead) break;
         tc_fence_after();
+        if (i && x.single && k == 0) {                // S is there, so are the rows' scales
+          inv = inv_a[row];
+          f = k4_factor(inv * c.scale * kLog2e);
+        }
         const uint4 mask = *reinterpret_cast<const uint4*>(masks + ((blocks + j - x.j0) % kKcMasks) * 4);
         const bool there = (mask.x & mask.y & mask.z & mask.w) == 0xffffffffu;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -955,6 +979,16 @@ size_t kv4_chunk_workspace(int T, int, int n_q, int n_kv) {
   return kKcOffPart + (size_t)kKcCtas * 2 * 2 * kc_part_rows(T, n_q / n_kv) * kKcPart * 4;
 }
 
+template <bool LONE>
+static int kc_launch(const CUtensorMap& qmap, const KcArgs& a, cudaStream_t st) {
+  constexpr size_t smem = KcCfg<LONE>::kSmem;
+  if (set_func_attr((const void*)kv4_chunk_kernel<LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return SPC_ERR_CUDA;
+  kv4_chunk_kernel<LONE><<<kKcCtas, kKcThreads, smem, st>>>(qmap, a);
+  kv4_chunk_merge_kernel<<<dim3(kKcCtas, (a.part_rows + 31) / 32, LONE ? 1 : 2), kKcMergeThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+}
+
 int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   KcArgs a{};
   a.c = c;
@@ -975,12 +1009,9 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)c.q_stride * 2};
   const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
   if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
-  if (set_func_attr((const void*)kv4_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKcSmem) != cudaSuccess)
-    return SPC_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  kv4_chunk_kernel<<<kKcCtas, kKcThreads, kKcSmem, st>>>(qmap, a);
-  kv4_chunk_merge_kernel<<<dim3(kKcCtas, (a.part_rows + 31) / 32, 2), kKcMergeThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+  // at most a tile's rows a request on average
+  return (long long)c.T * a.G <= 128ll * c.B ? kc_launch<true>(qmap, a, st) : kc_launch<false>(qmap, a, st);
 }
 
 }  // namespace spc
