@@ -9,12 +9,10 @@
 //   S[128][128] = Q K^T     Q, K in shared memory (128-byte swizzle)
 //   O[128][128] += P V      P in tensor memory over S's columns, V MN-major
 // The tensor cores work on one tile while the other one's softmax runs. A
-// request's last tile, if it has no partner, takes both places: A runs over the
-// even blocks and B over the odd ones, against the same Q, and A's warps merge
-// what B's have found (a warp of B has the same tensor memory lanes, so that only
-// maxima and sums go through shared memory). Where there are few new tokens all
-// tiles are such ones (LONE): there is one Q, and its partner's memory goes to the
-// rings of records, which then hold 3.5 blocks of the cache and not 1.5.
+// request's last tile, if it has no partner (and with few new tokens every one of
+// them), takes both places: A runs over the even blocks and B over the odd
+// ones, and A's warps merge what B's have found (a warp of B has the same tensor
+// memory lanes, so that only maxima and sums go through shared memory).
 //
 // Operands are fp16. A record's values are exact there; 11 bits of P instead of
 // bf16's 8; and e2m1 to fp16 is one conversion for two values. Queries are scaled
@@ -37,8 +35,8 @@
 // position that has it is noted for its 16 dims; rows at or behind that position
 // get NaN there.
 //
-// Work: the items' blocks (and one unit for an item's fixed part) form a line
-// that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
+// Work: the items' blocks (and an item's fixed part), in units of their time, form
+// a line that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
 // an item that is cut leave partials (O, maximum, sum) in the workspace, which a
 // second kernel merges, a warp a row, in the order of the positions.
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
@@ -63,44 +61,57 @@
 
 namespace spc {
 
-// Records: a ring for each dequantising warp (one reader, so that a wait on a phase's
-// parity is never two phases behind), stages of 16 positions, which lie in one cache block
-constexpr int kKcRun = 16;
-constexpr uint32_t kKcStage = kKcRun * kKv4Rec;
+// Records of the kernel for many new tokens: a ring for each dequantising warp (one
+// reader, so that a wait on a phase's parity is never two phases behind), stages of
+// 16 positions, which lie in one cache block
+constexpr int kKcRaw = 3, kKcRun = 16;
+constexpr uint32_t kKcRunBytes = kKcRun * kKv4Rec;
 constexpr int kKcSlots = 4;                           // ring of dequantised operands
 constexpr int kKcItems = 2;                           // item ring
 constexpr int kKcMasks = 16;                          // blocks whose masks are kept: the copies are at most 8 ahead of the softmax
-constexpr int kKcWarpDeq = 8, kKcWarpMma = 12, kKcWarpCopy = 13, kKcWarpQ = 14;
-constexpr int kKcThreads = 512;
-// registers a thread: 128 at launch (512 threads); softmax 176 (two warpgroups),
-// dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128
-constexpr int kKcRegSoft = 176, kKcRegDeq = 88, kKcRegRest = 72;
+constexpr int kKcWarpDeq = 8;
 constexpr float kKcBias = 8.f;                        // log2 of the factor of the weights
 constexpr float kKcHeadroom = 7.75f;                  // log2 growth allowed before a maximum is raised
-constexpr int kKcFixed = 1;                           // units of an item's fixed part
-constexpr int kKcMinRun = 3;                          // units a CTA takes at least
+// The line of work: units of a block for two tiles, for one in both places (2.3 and
+// 1.9 us), of an item's fixed part, and those a CTA takes at least (more than a
+// block's, so that every CTA between an item's first and last one has a piece of
+// it). 16 requests with up to 700 tokens take 932 us; with 6 for the fixed part
+// 1089. A run of 18 at least: 17 tokens behind 1000 take 29 us instead of 23.
+constexpr int kKcUnitsTwo = 6, kKcUnitsOne = 5, kKcFixed = 42, kKcMinRun = 11;
+static_assert(kKcMinRun >= kKcUnitsTwo, "a block begins in every run");
 constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kKcColO = 256;
 constexpr uint32_t kKcIdescS = (1u << 4) | ((uint32_t)(kKcKeys >> 3) << 17) | (8u << 24);
 constexpr uint32_t kKcIdescO = kKcIdescS | (1u << 16);
 constexpr uint32_t kKcDescVLo = umma_mn_lo(kKcBlock);
 
-// what differs between the kernel for few new tokens and the other one
+// What differs where there are few new tokens (LONE), so that every tile takes both
+// places and the cache's bytes count: one Q tile; a second group of dequantising
+// warps, the groups taking the blocks in turn, each with stages of its own of half a
+// block; and fewer registers for the softmax, which then reads S twice.
 template <bool LONE>
 struct KcCfg {
-  static constexpr int kRaw = LONE ? 7 : 3;           // stages of a ring of records
   static constexpr int kTiles = LONE ? 1 : 2;         // of Q
+  static constexpr int kDeq = LONE ? 2 : 1;           // groups of four dequantising warps
+  static constexpr int kRaw = LONE ? 2 * kDeq : 4 * kKcRaw;             // stages of records
+  static constexpr uint32_t kStage = LONE ? kKcHalf * kKv4Rec : kKcRunBytes;
+  static constexpr int kWarpMma = kKcWarpDeq + 4 * kDeq, kWarpCopy = kWarpMma + 1, kWarpQ = kWarpMma + 2;
+  static constexpr int kThreads = 32 * (kWarpMma + 4);
+  // registers a thread: 128 at launch (512 threads) or 96 (640). Softmax 176 (two
+  // warpgroups), dequantisation 88, the rest 72: 2 * 176 + 88 + 72 = 4 * 128; or 128,
+  // 72 (two) and 72: 2 * 128 + 2 * 72 + 72 < 5 * 96
+  static constexpr int kRegSoft = LONE ? 128 : 176, kRegDeq = LONE ? 72 : 88, kRegRest = 72;
   // shared memory, from a 1024-byte aligned base
   static constexpr uint32_t kOffQ = 0;                                    // [kTiles]
   static constexpr uint32_t kOffKv = kOffQ + kTiles * kKcTile;
-  static constexpr uint32_t kOffRaw = kOffKv + kKcSlots * kKcTile;        // [4 warps][kRaw]
-  static constexpr uint32_t kOffItem = kOffRaw + 4 * kRaw * kKcStage;     // [kKcItems] KcItem
+  static constexpr uint32_t kOffRaw = kOffKv + kKcSlots * kKcTile;        // [kRaw]
+  static constexpr uint32_t kOffItem = kOffRaw + kRaw * kStage;           // [kKcItems] KcItem
   static constexpr uint32_t kOffNan = kOffItem + kKcItems * 64;           // [kKcItems][8] first position with a NaN V scale
   static constexpr uint32_t kOffMask = kOffNan + kKcItems * 32;           // [kKcMasks][4 words]
   static constexpr uint32_t kOffMl = kOffMask + kKcMasks * 16;            // [128] maximum and sum of tile B's row, for tile A
   static constexpr uint32_t kOffInv = kOffMl + 128 * 8;                   // [128] scale of tile A's row, for tile B
   static constexpr uint32_t kOffBar = kOffInv + 128 * 4;
-  static constexpr int kBars = 8 * kRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 2 * 4 + 1;
+  static constexpr int kBars = 2 * kRaw + 2 * kKcSlots + 2 * kKcItems + 2 * 6 + 2 * 4 + 1;
   static constexpr size_t kSmem = 1024 + kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -199,42 +210,41 @@ __device__ __forceinline__ float kc_query(uint32_t tile, int r) {
 
 // ---------------------------------------------------------------- the line of work
 // Items of a request: item i holds tokens [i t, (i + 1) t), two tiles' or one's,
-// and sees ceil((ctx + (i + 1) t) / 128) blocks, ctx = len - n, at least one. A unit
-// is a block, or two of them where one tile takes both places.
+// and sees ceil((ctx + (i + 1) t) / 128) blocks, ctx = len - n, at least one. An
+// item's units are its fixed part's, then its blocks'.
 struct KcShape {
-  int ctx, n, lt, lb, pairs;   // lt: log2 of t; lb: of a unit's positions; items
+  int ctx, n, lt, pairs;       // lt: log2 of t; items
 };
 __device__ __forceinline__ int kc_blocks(const KcShape& s, int i) {
   return max(1, (s.ctx + min(s.n, (i + 1) << s.lt) + kKcKeys - 1) >> 7);
 }
+// units of a block of item i: it is one tile, or two
+template <bool LONE>
+__device__ __forceinline__ bool kc_single(const KcShape& s, int i) {
+  return LONE || 2 * i + 2 > (s.n + (1 << (s.lt - 1)) - 1) >> (s.lt - 1);
+}
+template <bool LONE>
+__device__ __forceinline__ int kc_unit(const KcShape& s, int i) { return kc_single<LONE>(s, i) ? kKcUnitsOne : kKcUnitsTwo; }
 // units of the items below k <= items - 1, none of them the last one
+template <bool LONE>
 __device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
-  const int lt = s.lt, lb = s.lb, mask = (1 << lb) - 1;
-  // the first ones see one unit (or nothing), from i0 on the sum of an arithmetic progression's quotients
+  constexpr int lb = 7, mask = kKcKeys - 1;
+  const int lt = s.lt;
+  // the first ones see one block (or nothing), from i0 on the sum of an arithmetic progression's quotients
   const int i0 = max(0, min(k, (mask + 1 - s.ctx) >> lt)), m = k - i0;
-  long long u = (long long)k * kKcFixed + i0;
+  const int each = LONE ? kKcUnitsOne : kKcUnitsTwo;
+  const long long u = (long long)k * kKcFixed + (long long)i0 * each;
   if (m == 0) return u;
   const int c = s.ctx + (i0 << lt);
-  if (lt >= lb) return u + (long long)m * ((c + mask) >> lb) + ((long long)m * (m + 1) / 2 << (lt - lb));
+  if (lt >= lb) return u + each * ((long long)m * ((c + mask) >> lb) + ((long long)m * (m + 1) / 2 << (lt - lb)));
   const int ls = lb - lt, w = (1 << ls) - 1 + ((c & ((1 << lt) - 1)) > 0 ? 1 : 0);
   const long long a = (c >> lt) + w;                  // sum of floor((a + i) / 2^ls), i = 1 .. m
   auto below = [&](long long x) {                     // sum of floor(j / 2^ls), j = 0 .. x
     const long long q = (x + 1) >> ls, r = (x + 1) & ((1 << ls) - 1);
     return (q * (q - 1) / 2 << ls) + r * q;
   };
-  return u + below(a + m) - below(a);
+  return u + each * (below(a + m) - below(a));
 }
-// whether item i is one tile, and its units
-template <bool LONE>
-__device__ __forceinline__ bool kc_single(const KcShape& s, int i) {
-  return LONE || 2 * i + 2 > (s.n + (1 << (s.lt - 1)) - 1) >> (s.lt - 1);
-}
-template <bool LONE>
-__device__ __forceinline__ int kc_item_units(const KcShape& s, int i) {
-  const int nb = kc_blocks(s, i);
-  return kc_single<LONE>(s, i) ? (nb + 1) >> 1 : nb;
-}
-
 __device__ __forceinline__ float kc_lse(const KcArgs& a, float m, float l, float inv) {
   return l == 0.f ? -INFINITY : m * inv * a.c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
 }
@@ -296,9 +306,9 @@ __global__ void __launch_bounds__(kKcMergeThreads) kv4_chunk_merge_kernel(const 
 }
 
 template <bool LONE>
-__global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const KcArgs a) {
+__global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const KcArgs a) {
   using Cfg = KcCfg<LONE>;
-  constexpr int kKcRaw = Cfg::kRaw;
+  constexpr int kDeqWarps = 4 * Cfg::kDeq;
   extern __shared__ uint8_t kc_raw[];
   const uint32_t raw_addr = smem_u32(kc_raw);
   uint8_t* base = kc_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -308,9 +318,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   float2* ml_b = reinterpret_cast<float2*>(base + Cfg::kOffMl);
   float* inv_a = reinterpret_cast<float*>(base + Cfg::kOffInv);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::kOffBar);
-  uint64_t* rfull = bars;                     // [4 warps][kKcRaw] bytes of the records
-  uint64_t* rfree = rfull + 4 * kKcRaw;       // [4][kKcRaw] the warp has read them
-  uint64_t* kvfull = rfree + 4 * kKcRaw;      // [kKcSlots] four dequantising warps have written the operand
+  uint64_t* rfull = bars;                     // [kRaw] bytes of the records ([4 warps][kKcRaw], LONE: [group][half block])
+  uint64_t* rfree = rfull + Cfg::kRaw;        // [kRaw] the warp, or the group's four, have read them
+  uint64_t* kvfull = rfree + Cfg::kRaw;       // [kKcSlots] four dequantising warps have written the operand
   uint64_t* kvfree = kvfull + kKcSlots;       // [kKcSlots] commit after the last MMA that reads it
   uint64_t* ifull = kvfree + kKcSlots;        // [kKcItems] item written
   uint64_t* ifree = ifull + kKcItems;         // [kKcItems] every role has read it, the softmax warps are done with it
@@ -328,9 +338,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   const Kv4ChunkCall& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4 * kKcRaw; ++s) {
+    for (int s = 0; s < Cfg::kRaw; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rfree[s], 1);
+      mbar_init(&rfree[s], LONE ? 4 : 1);
     }
     for (int s = 0; s < kKcSlots; ++s) {
       mbar_init(&kvfull[s], 4);
@@ -338,7 +348,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     }
     for (int s = 0; s < kKcItems; ++s) {
       mbar_init(&ifull[s], 1);
-      mbar_init(&ifree[s], 4 + 8 + 3);
+      mbar_init(&ifree[s], kDeqWarps + 8 + 3);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&qfull[s], 1);
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == kKcWarpMma) tmem_alloc<kKcTmemCols>(tmem_slot);
+  if (warp == Cfg::kWarpMma) tmem_alloc<kKcTmemCols>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -370,9 +380,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     }
   };
 
-  if (warp == kKcWarpCopy) {
+  if (warp == Cfg::kWarpCopy) {
     // ================= schedule and copies of the records
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cfg::kRegRest));
     KcRequests rq;
     kc_requests(c, rq);
     const int lt = (LONE ? 7 : 8) - a.gshift, bs = 1 << c.block_shift;
@@ -381,12 +391,12 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       s.ctx = len - n;
       s.n = n;
       s.lt = lt;
-      s.lb = LONE ? 8 : 7;
       s.pairs = (n + (1 << lt) - 1) >> lt;
       return s;
     };
     auto units = [&](const KcShape& s) {              // of one KV head
-      return s.n == 0 ? 0ll : kc_units(s, s.pairs - 1) + kKcFixed + kc_item_units<LONE>(s, s.pairs - 1);
+      return s.n == 0 ? 0ll : kc_units<LONE>(s, s.pairs - 1) + kKcFixed +
+                              (long long)kc_blocks(s, s.pairs - 1) * kc_unit<LONE>(s, s.pairs - 1);
     };
     long long own[2];
 #pragma unroll
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
     auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
     // the item at u0: request b, head g, pair i; `at` is its first unit
-    int b = 0, g = 0, i = 0, nb = 0;
+    int b = 0, g = 0, i = 0;
     long long at = 0, whole = 1;
     KcShape s = shape(0, 0);
     auto enter = [&](int request) {                   // its shape and units a head
@@ -413,10 +423,10 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       int lo = 0, hi = s.pairs;                       // units(lo) <= r
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (kc_units(s, mid) <= r) lo = mid; else hi = mid;
+        if (kc_units<LONE>(s, mid) <= r) lo = mid; else hi = mid;
       }
       i = lo;
-      at = u0 - r + kc_units(s, i);
+      at = u0 - r + kc_units<LONE>(s, i);
     }
     int it = 0, blocks = 0, nraw = 0;
     if (lane == 0) a.cut[blockIdx.x].pieces = 0;      // unless an item goes on in the next CTA
@@ -425,11 +435,12 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       x.n = -1;
       bool skip = false;
       if (has && at < u1 && !dead) {
-        const int nu = kc_item_units<LONE>(s, i);
-        nb = kc_blocks(s, i);
+        const int nb = kc_blocks(s, i);
         const long long first = at + kKcFixed;        // its first block's unit
-        const int lo = (int)max(0ll, u0 - first), hi = (int)min((long long)nu, u1 - first);
-        skip = hi <= lo;                              // only its fixed part is here
+        const int each = kc_unit<LONE>(s, i);         // a block is the CTA's in whose run it begins
+        const int lo = (int)((max(0ll, u0 - first) + each - 1) / each);
+        const int hi = (int)min((long long)nb, (max(0ll, u1 - first) + each - 1) / each);
+        skip = hi <= lo;                              // no block begins here
         if (!skip) {
           x.row0 = kc_of(rq.row0, b);
           x.n = s.n;
@@ -437,8 +448,8 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
           x.g = g;
           x.t0 = i << lt;
           x.single = kc_single<LONE>(s, i);
-          x.j0 = x.single ? 2 * lo : lo;
-          x.j1 = x.single ? min(nb, 2 * hi) : hi;
+          x.j0 = lo;
+          x.j1 = hi;
           if (x.single) {
             x.n0 = (x.j1 - x.j0 + 1) >> 1;
             x.n1 = (x.j1 - x.j0) >> 1;
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
             x.n1 = x.j1 - x.j0;
           }
           x.first = cta_of(first);
-          x.pieces = cta_of(first + nu - 1) - x.first + 1;
+          x.pieces = cta_of(first + (long long)(nb - 1) * each) - x.first + 1;
           x.piece = (int)blockIdx.x - x.first;
           if (x.pieces > 1 && x.piece == 0 && lane == 0) a.cut[blockIdx.x] = x;
         }
@@ -468,35 +479,48 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
 #endif
         KcTable t;
         t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.j0 * kKcKeys >> c.block_shift);
-        // lane w copies for dequantising warp w
-        for (int j = x.j0; j < x.j1 && !dead; ++j, ++blocks) {
-          uint32_t mask = 0u;
+        if constexpr (LONE) {
+          for (int j = x.j0; j < x.j1 && !dead; ++j, ++blocks) {
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h, ++nraw) {
-            const int st = nraw % kKcRaw, p = j * kKcKeys + (lane & 3) * 32 + h * kKcRun;
-            const int blk = t.entry(j * kKcKeys >> c.block_shift, p >> c.block_shift);
-            const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kKcRun)) : 0;
-            mask |= ((1u << n) - 1u) << (h * kKcRun);
-            const uint32_t parity = ((nraw / kKcRaw) & 1) ^ 1;
-            uint64_t* bar = &rfull[(lane & 3) * kKcRaw + st];
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&rfree[(lane & 3) * kKcRaw + st], parity, a.wait_limit))) {
-              if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
-              dead = true;
-              break;
+            for (int h = 0; h < 2; ++h) {
+              const int st = (blocks & 1) * 2 + h;
+              acquire(&rfree[st], ((blocks >> 1) & 1) ^ 1);
+              if (dead) break;
+              kc_copy(c, t, x.g, x.len, j * kKcKeys + h * kKcHalf, base + Cfg::kOffRaw + st * Cfg::kStage, &rfull[st],
+                      masks + (blocks % kKcMasks) * 4 + 2 * h);
             }
-            if (lane < 4) {
-              if (h == 1) masks[(blocks % kKcMasks) * 4 + lane] = mask;
-              if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
-              if (n > 0)
-                bulk_g2s(base + Cfg::kOffRaw + (lane * kKcRaw + st) * kKcStage,
-                         c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
+          }
+        } else {
+          // lane w copies for dequantising warp w
+          for (int j = x.j0; j < x.j1 && !dead; ++j, ++blocks) {
+            uint32_t mask = 0u;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h, ++nraw) {
+              const int st = nraw % kKcRaw, p = j * kKcKeys + (lane & 3) * 32 + h * kKcRun;
+              const int blk = t.entry(j * kKcKeys >> c.block_shift, p >> c.block_shift);
+              const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kKcRun)) : 0;
+              mask |= ((1u << n) - 1u) << (h * kKcRun);
+              const uint32_t parity = ((nraw / kKcRaw) & 1) ^ 1;
+              uint64_t* bar = &rfull[(lane & 3) * kKcRaw + st];
+              if (!__all_sync(0xffffffffu, mbar_wait_bounded(&rfree[(lane & 3) * kKcRaw + st], parity, a.wait_limit))) {
+                if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+                dead = true;
+                break;
+              }
+              if (lane < 4) {
+                if (h == 1) masks[(blocks % kKcMasks) * 4 + lane] = mask;
+                if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
+                if (n > 0)
+                  bulk_g2s(base + Cfg::kOffRaw + (lane * kKcRaw + st) * kKcRunBytes,
+                           c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }
       // the next item
-      at += kKcFixed + kc_item_units<LONE>(s, i);
+      at += kKcFixed + (long long)kc_blocks(s, i) * kc_unit<LONE>(s, i);
       if (++i == s.pairs) {
         i = 0;
         if (++g == c.n_kv) {
@@ -506,13 +530,18 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       }
     }
     // every copy lands before the CTA ends (they have, unless a role gave up)
-    if (lane < 4)
+    if constexpr (LONE) {
+      if (lane == 0)
+        for (int k = max(0, 2 * blocks - Cfg::kRaw); k < 2 * blocks; ++k)     // each stage's last use
+          mbar_wait_bounded(&rfull[(k >> 1 & 1) * 2 + (k & 1)], (k >> 2) & 1, a.wait_limit);
+    } else if (lane < 4) {
       for (int k = max(0, nraw - kKcRaw); k < nraw; ++k)
         mbar_wait_bounded(&rfull[lane * kKcRaw + k % kKcRaw], (k / kKcRaw) & 1, a.wait_limit);
+    }
     __syncwarp();
-  } else if (warp == kKcWarpQ) {
+  } else if (warp == Cfg::kWarpQ) {
     // ================= queries
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cfg::kRegRest));
     int nq[2] = {0, 0};
     for (int it = 0;; ++it) {
       const int is = it % kKcItems;
@@ -528,13 +557,13 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
 #endif
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        if (i ? single || n1 == 0 : n0 == 0) continue;  // one tile in both places has one Q
+        if (i ? LONE || n1 == 0 : n0 == 0) continue;
         acquire(&qfree[i], (nq[i] & 1) ^ 1);
         if (dead) break;
         ++nq[i];
         if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[i], kKcTile);
-          const int r = row + i * a.tpm;
+          const int r = row + (single ? 0 : i * a.tpm);
           tma_load_3d(qs + i * kKcTile, &qmap, 0, g << a.gshift, r, &qfull[i]);
           tma_load_3d(qs + i * kKcTile + kKcBlock, &qmap, 64, g << a.gshift, r, &qfull[i]);
         }
@@ -546,17 +575,17 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       for (int i = 0; i < 2; ++i)
         if (nq[i] > 0) mbar_wait_bounded(&qfull[i], (nq[i] - 1) & 1, a.wait_limit);
     __syncwarp();
-  } else if (warp == kKcWarpMma) {
+  } else if (warp == Cfg::kWarpMma) {
     // ================= MMA issue; the whole warp runs the loop, so that its values stay warp-uniform
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cfg::kRegRest));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
     auto full = [&](int k) {                          // operand k has been written
       acquire(&kvfull[k % kKcSlots], (k / kKcSlots) & 1);
     };
-    // S of tile i, of Q q, against operand k; first: use of q, last: no further one. `done`: nothing else reads k
-    auto issue_s = [&](auto tile, auto q, int k, bool first, bool last, bool done) {
-      constexpr int i = decltype(tile)::value, qi = decltype(q)::value;
+    // S of tile i against operand k; first: of its Q, last: no further one. `done`: nothing else reads k
+    auto issue_s = [&](auto tile, int k, bool first, bool last, bool done) {
+      constexpr int i = decltype(tile)::value, qi = LONE ? 0 : i;
       if (first) acquire(&qready[qi], nq[qi]++ & 1);
       if (dead) return;
       tc_fence_after();
@@ -603,35 +632,36 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       // operand kv + 2 k is K of the piece's block k, kv + 2 k + 1 its V
       full(kv);
       if (LONE || single) {
-        issue_s(tA, tA, kv, true, nb == 1, true);
+        // LONE: the two have one Q, whose last use is the last block's
+        issue_s(tA, kv, true, LONE ? nb == 1 : n0 == 1, true);
         if (n1) {
           full(kv + 2);
-          issue_s(tB, tA, kv + 2, false, nb == 2, true);
+          issue_s(tB, kv + 2, !LONE, LONE ? nb == 2 : n1 == 1, true);
         }
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; k += 2) {
           issue_pv(tA, kv + 2 * k + 1, k == 0, k + 2 >= nb, true);
-          if (k + 1 < nb) issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
           if (k + 2 < nb) {
             full(kv + 2 * k + 4);
-            issue_s(tA, tA, kv + 2 * k + 4, false, k + 3 == nb, true);
+            issue_s(tA, kv + 2 * k + 4, false, LONE ? k + 3 == nb : k + 4 >= nb, true);
           }
+          if (k + 1 < nb) issue_pv(tB, kv + 2 * k + 3, k == 0, k + 3 >= nb, true);
           if (k + 3 < nb) {
             full(kv + 2 * k + 6);
-            issue_s(tB, tA, kv + 2 * k + 6, false, k + 4 == nb, true);
+            issue_s(tB, kv + 2 * k + 6, false, LONE ? k + 4 == nb : k + 5 >= nb, true);
           }
         }
-      } else if constexpr (!LONE) {
-        if (n0) issue_s(tA, tA, kv, true, n0 == 1, n1 == 0);
-        if (n1) issue_s(tB, tB, kv, true, n1 == 1, true);
+      } else {
+        if (n0) issue_s(tA, kv, true, n0 == 1, n1 == 0);
+        if (n1) issue_s(tB, kv, true, n1 == 1, true);
 #pragma unroll 1
         for (int k = 0; k < nb && !dead; ++k) {
           // PV of block k, S of the next one; the tensor pipe queues only a few MMAs, so nothing waits between the two
           const int v = kv + 2 * k + 1;
           if (k < n0) issue_pv(tA, v, k == 0, k + 1 == n0, k >= n1);
-          if (k + 1 < n0) issue_s(tA, tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
+          if (k + 1 < n0) issue_s(tA, v + 1, false, k + 2 == n0, k + 1 >= n1);
           if (k < n1) issue_pv(tB, v, k == 0, k + 1 == n1, true);
-          if (k + 1 < n1) issue_s(tB, tB, v + 1, false, k + 2 == n1, true);
+          if (k + 1 < n1) issue_s(tB, v + 1, false, k + 2 == n1, true);
         }
       }
       kv += 2 * nb;
@@ -642,9 +672,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     if (elect_one()) umma_commit(drain);
     __syncwarp();
     kc_wait(a, drain, 0);
-  } else if (warp >= kKcWarpDeq && warp < kKcWarpDeq + 4) {
+  } else if (warp >= kKcWarpDeq && warp < Cfg::kWarpMma) {
     // ================= dequantisation, a record a thread
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegDeq));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cfg::kRegDeq));
     const int w = warp - kKcWarpDeq, r = threadIdx.x & 127;
     int blocks = 0, kv = 0, nread = 0;
     for (int it = 0;; ++it) {
@@ -655,21 +685,33 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
       if (n < 0) break;
-      for (int j = j0; j < j1; ++j, ++blocks) {
-        const int s0 = nread % kKcRaw, s1 = (nread + 1) % kKcRaw;
-        acquire(&rfull[w * kKcRaw + s0], (nread / kKcRaw) & 1);
-        acquire(&rfull[w * kKcRaw + s1], ((nread + 1) / kKcRaw) & 1);
-        if (dead) break;
-        nread += 2;
+      for (int j = j0; j < j1; ++j, ++blocks, kv += 2) {
         // the whole record into registers, so that its stage is free at once
-        const uint32_t rec = smem_u32(base + Cfg::kOffRaw) + (uint32_t)(w * kKcRaw + (lane < kKcRun ? s0 : s1)) * kKcStage +
-                             (uint32_t)(lane & (kKcRun - 1)) * kKv4Rec;
-        const bool there = masks[(blocks % kKcMasks) * 4 + w] >> lane & 1;
+        int s0, s1;
+        uint32_t rec;
+        if constexpr (LONE) {
+          if ((blocks & 1) != w >> 2) continue;
+          s0 = (blocks & 1) * 2;
+          s1 = s0 + 1;
+          acquire(&rfull[s0], (blocks >> 1) & 1);
+          acquire(&rfull[s1], (blocks >> 1) & 1);
+          rec = smem_u32(base + Cfg::kOffRaw) + (uint32_t)s0 * Cfg::kStage + (uint32_t)r * kKv4Rec;   // the two lie one behind the other
+        } else {
+          s0 = w * kKcRaw + nread % kKcRaw;
+          s1 = w * kKcRaw + (nread + 1) % kKcRaw;
+          acquire(&rfull[s0], (nread / kKcRaw) & 1);
+          acquire(&rfull[s1], ((nread + 1) / kKcRaw) & 1);
+          nread += 2;
+          rec = smem_u32(base + Cfg::kOffRaw) + (uint32_t)(lane < kKcRun ? s0 : s1) * Cfg::kStage +
+                (uint32_t)(lane & (kKcRun - 1)) * kKv4Rec;
+        }
+        if (dead) break;
+        const bool there = masks[(blocks % kKcMasks) * 4 + (w & 3)] >> lane & 1;
         uint4 v[9];
 #pragma unroll
         for (int q = 0; q < 9; ++q) v[q] = lds_v4(rec + 16 * q);
         __syncwarp();
-        if (lane < 2) mbar_arrive(&rfree[w * kKcRaw + (lane ? s1 : s0)]);
+        if (lane < 2) mbar_arrive(&rfree[lane ? s1 : s0]);
         if (!there) {
 #pragma unroll
           for (int q = 0; q < 9; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -689,9 +731,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
           }
         }
 #pragma unroll
-        for (int part = 0; part < 2; ++part, ++kv) {  // K, then V
-          const int slot = kv % kKcSlots;
-          acquire(&kvfree[slot], ((kv / kKcSlots) & 1) ^ 1);
+        for (int part = 0; part < 2; ++part) {        // K, then V
+          const int slot = (kv + part) % kKcSlots;
+          acquire(&kvfree[slot], (((kv + part) / kKcSlots) & 1) ^ 1);
           if (dead) break;
           if (part) kc_row(v + 4, v[8].z, v[8].w, kvs + (uint32_t)slot * kKcTile, r);
           else kc_row(v, v[8].x, v[8].y, kvs + (uint32_t)slot * kKcTile, r);
@@ -705,7 +747,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
     }
   } else if (warp < kKcWarpDeq) {
     // ================= softmax and epilogue of tile i, one row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kKcRegSoft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(Cfg::kRegSoft));
     const int i = warp >> 2, wq = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + i * kKcKeys, to = tmem + lanes + kKcColO + i * kD;
@@ -720,16 +762,22 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       const int token = t0 + (row >> a.gshift), qpos = x.len - x.n + token, qpos0 = x.len - x.n + t0;
       const int hq = (x.g << a.gshift) + (row & (a.G - 1));
       float m = -INFINITY, l = 0.f, inv = 1.f;
-      if (n > 0 && !(i && x.single)) {
+      if (LONE && i) {
+        if (n > 0) {                                  // tile A's rows: their scales are there when an S is
+          acquire(&sfull[i], n_s & 1);
+          if (dead) break;
+          inv = inv_a[row];
+        }
+      } else if (n > 0) {
         acquire(&qfull[i], n_q & 1);
         if (dead) break;
         ++n_q;
         inv = kc_query(qs + i * kKcTile, row);
-        if (x.single) inv_a[row] = inv;
+        if (LONE) inv_a[row] = inv;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qready[i]);
-      } else if (n == 0 && x.pieces > 1 && !x.single) {
+      } else if (x.pieces > 1 && !x.single) {
         // a piece without a block of this tile's: the rows' factors, for the merge
         const int t = min(x.row0 + token, c.T - 1);
         uint32_t mx = 0u;
@@ -740,16 +788,12 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
         }
         inv = __int_as_float((127 - min(141 - (int)(max(mx & 0xffffu, mx >> 16) >> 7), 126)) << 23);
       }
-      float f = k4_factor(inv * c.scale * kLog2e);
+      const float f = k4_factor(inv * c.scale * kLog2e);
       for (int k = 0; k < n; ++k) {
         const int j = x.single ? x.j0 + 2 * k + i : x.j0 + k;
         acquire(&sfull[i], n_s & 1);
         if (dead) break;
         tc_fence_after();
-        if (i && x.single && k == 0) {                // S is there, so are the rows' scales
-          inv = inv_a[row];
-          f = k4_factor(inv * c.scale * kLog2e);
-        }
         const uint4 mask = *reinterpret_cast<const uint4*>(masks + ((blocks + j - x.j0) % kKcMasks) * 4);
         const bool there = (mask.x & mask.y & mask.z & mask.w) == 0xffffffffu;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -777,27 +821,49 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
             }
           }
         };
-        if (there && (j + 1) * kKcKeys <= qpos0 + 1 && !__any_sync(0xffffffffu, m == -INFINITY)) {
-          // every row sees the whole block and has a maximum: weights against
-          // it at once, while the block's own maximum is being found
-          float s[128];
-          tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
+        // every row sees the whole block
+        if (there && (j + 1) * kKcKeys <= qpos0 + 1 && (LONE || !__any_sync(0xffffffffu, m == -INFINITY))) {
+          if constexpr (LONE) {
+            // twice from tensor memory: there are not the registers to keep a row
+            float s[2][32];
+            tmem_ld32(ts, s[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait32(s + 32 * q);
-            if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
-            max32(s + 32 * q, mx);
-            kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
-          }
-          const float M = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          if (__any_sync(0xffffffffu, (M - m) * f > kKcHeadroom)) {
-            // the weights go to the same columns again, and stores to tensor
-            // memory are asynchronous: the first ones have to be there
-            tmem_st_wait();
-            raise(M);
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld_wait32(s[q & 1]);
+              if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+              max32(s[q & 1], mx);
+            }
+            raise(max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
+            const float mm = m == -INFINITY ? 0.f : m;
+            tmem_ld32(ts, s[0]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld_wait32(s[q & 1]);
+              if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+              kc_weights(s[q & 1], f, mm, sum, ts + 16 * q);
+            }
+          } else {
+            // every row has a maximum, too: weights against
+            // it at once, while the block's own maximum is being found
+            float s[128];
+            tmem_ld32(ts, *reinterpret_cast<float (*)[32]>(s));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld_wait32(s + 32 * q);
+              if (q < 3) tmem_ld32(ts + 32 * (q + 1), *reinterpret_cast<float (*)[32]>(s + 32 * (q + 1)));
+              max32(s + 32 * q, mx);
+              kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
+            }
+            const float M = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            if (__any_sync(0xffffffffu, (M - m) * f > kKcHeadroom)) {
+              // the weights go to the same columns again, and stores to tensor
+              // memory are asynchronous: the first ones have to be there
+              tmem_st_wait();
+              raise(M);
+              sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) kc_weights(s + 32 * q, f, m, sum, ts + 16 * q);
+            }
           }
         } else {
           // a piece's first block, a block with an end or a gap in it, and the
@@ -934,9 +1000,9 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&ifree[is]);
     }
-  } else {                                    // warp 15
+  } else {                                    // the last warp
     // ================= gate: one arrival a phase of the P barriers, when what the batch behind it reads is there
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKcRegRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cfg::kRegRest));
     int kv = 0, np[2] = {0, 0};
     for (int it = 0; !dead; ++it) {
       const int is = it % kKcItems;
@@ -967,7 +1033,7 @@ __global__ void __launch_bounds__(kKcThreads, 1) kv4_chunk_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kKcWarpMma) {
+  if (warp == Cfg::kWarpMma) {
     tc_fence_after();
     tmem_dealloc<kKcTmemCols>(tmem);
   }
@@ -984,7 +1050,7 @@ static int kc_launch(const CUtensorMap& qmap, const KcArgs& a, cudaStream_t st) 
   constexpr size_t smem = KcCfg<LONE>::kSmem;
   if (set_func_attr((const void*)kv4_chunk_kernel<LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SPC_ERR_CUDA;
-  kv4_chunk_kernel<LONE><<<kKcCtas, kKcThreads, smem, st>>>(qmap, a);
+  kv4_chunk_kernel<LONE><<<kKcCtas, KcCfg<LONE>::kThreads, smem, st>>>(qmap, a);
   kv4_chunk_merge_kernel<<<dim3(kKcCtas, (a.part_rows + 31) / 32, LONE ? 1 : 2), kKcMergeThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
 }
@@ -1010,7 +1076,9 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpm};
   if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // at most a tile's rows a request on average
+  // One Q tile where a request has at most a tile's rows on average. G = 4, the one
+  // way and the other: 8 requests of 32K, 32 tokens (a tile) 171 and 204 us, 33
+  // tokens (two) 306 and 242; one of 32K, 55 and 60, 70 and 67; 1 token 33 and 38
   return (long long)c.T * a.G <= 128ll * c.B ? kc_launch<true>(qmap, a, st) : kc_launch<false>(qmap, a, st);
 }
 

@@ -7,11 +7,13 @@
 #include "kv4.cuh"
 #include "spc_device.cuh"
 #include "spc_internal.h"
+#include "spc_tc.cuh"
 
 namespace spc {
 
 constexpr int kKcCtas = 152;                          // one per SM; a constant, so that the workspace depends on shapes alone
 constexpr int kKcKeys = 128;                          // positions a block
+constexpr int kKcHalf = 64;                           // positions of half a block
 constexpr uint32_t kKcTile = kKcKeys * kRowBytes;     // 32 KB: 128 rows of 16-bit values
 constexpr uint32_t kKcBlock = kKcTile / 2;            // its 64-value half
 constexpr long long kKcWait = 4000000000ll;           // clock cycles, some 2 s
@@ -79,6 +81,52 @@ struct KcTable {
     return __shfl_sync(0xffffffffu, cur, i & 31);
   }
 };
+
+// One warp: the records of positions p0 .. p0 + 63 (p0 a multiple of 64) of a
+// request with `len` positions, KV head g, into a stage, one bulk copy a cache
+// block (a copy costs its warp some 200 clocks); the positions there are, as
+// bits. The stage's barrier has one arrival.
+__device__ __forceinline__ void kc_copy(const Kv4ChunkCall& c, KcTable& t, int g, int len, int p0, uint8_t* stage,
+                                        uint64_t* bar, uint32_t* mask) {
+  const int lane = threadIdx.x & 31, bs = 1 << c.block_shift, run = min(bs, kKcHalf), runs = kKcHalf / run;
+  const int p = p0 + lane * run;
+  const int blk = t.entry(p0 >> c.block_shift, p >> c.block_shift);
+  int n = 0;
+  if (lane < runs && (unsigned)blk < (unsigned)c.num_blocks) n = max(0, min(len - p, run));
+  if (runs == 1) {
+    // one copy: by an elected lane, from uniform values
+    const int one = __shfl_sync(0xffffffffu, blk, 0), cnt = __shfl_sync(0xffffffffu, n, 0);
+    if (elect_one()) {
+      *reinterpret_cast<uint2*>(mask) = make_uint2(cnt >= 32 ? 0xffffffffu : (1u << cnt) - 1u,
+                                                   cnt >= 64 ? 0xffffffffu : cnt > 32 ? (1u << (cnt - 32)) - 1u : 0u);
+      if (cnt > 0) {
+        mbar_arrive_expect_tx(bar, (uint32_t)cnt * kKv4Rec);
+        bulk_g2s(stage, c.cache + (((size_t)one * c.n_kv + g) * bs + (p0 & (bs - 1))) * kKv4Rec, (uint32_t)cnt * kKv4Rec, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    __syncwarp();
+    return;
+  }
+  uint32_t m[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int lo = max(0, lane * run - 32 * h), hi = min(32, lane * run + n - 32 * h);   // bits of word h
+    m[h] = n > 0 && hi > lo ? (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1u)) << lo : 0u;
+    m[h] = __reduce_or_sync(0xffffffffu, m[h]);
+  }
+  const uint32_t bytes = __reduce_add_sync(0xffffffffu, (uint32_t)n) * kKv4Rec;
+  if (lane == 0) {
+    *reinterpret_cast<uint2*>(mask) = make_uint2(m[0], m[1]);
+    if (bytes) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
+  }
+  __syncwarp();
+  if (n > 0)
+    bulk_g2s(stage + lane * run * kKv4Rec, c.cache + (((size_t)blk * c.n_kv + g) * bs + (p & (bs - 1))) * kKv4Rec,
+             (uint32_t)n * kKv4Rec, bar);
+  __syncwarp();
+}
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
   uint4 r;
