@@ -17,7 +17,7 @@
 // scale s - lse with one rounding, before the factor log2(e). A row tile's sums
 // go into the position's total by a compensated addition.
 //
-// Work: the items' row tiles (and one unit for an item's fixed part) form a line
+// Work: the items' row tiles (and an item's fixed part) form a line
 // that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
 // an item that is cut leave their sums in the workspace; of the warps that have
 // the same 32 positions the last to arrive adds them in the order of the pieces.
@@ -41,21 +41,23 @@
 
 namespace spc {
 
-constexpr int kMsRaw = 3, kMsRun = 16;                // stages of each dequantising warp's ring of records, positions a stage
+// stages of each dequantising warp's ring of records, and positions a stage: three
+// tiles, where with 1.5 (and six Q tiles) 64 rows' look back took 95 us, not 83
+constexpr int kMsRaw = 6, kMsRun = 16;
 constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
 constexpr int kMsK = 2;                               // ring of dequantised K tiles
-constexpr int kMsQ = 6;                               // ring of Q tiles
+constexpr int kMsQ = 5;                               // ring of Q tiles
 constexpr int kMsL = 6;                               // ring of the rows' lse
 constexpr int kMsItems = 2;
 constexpr int kMsGo = 4;                              // products that the gate may be ahead by
-constexpr int kMsMasks = 16;                          // tiles whose masks are kept: the copies are at most 11 ahead of the sums
+constexpr int kMsMasks = 2 * kMsItems;                // tiles whose masks are kept: the items' in the ring
 constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
 constexpr int kMsWarpDeq = 12, kMsWarpMma = 16, kMsWarpPlan = 17, kMsWarpQ = 18;
 constexpr int kMsThreads = 640;
 // registers a thread: 96 at launch (640 threads); the three warpgroups that sum
 // 112, dequantisation 80, the rest 64: 3 * 112 + 80 + 64 = 5 * 96
 constexpr int kMsRegSum = 112, kMsRegDeq = 80, kMsRegRest = 64;
-constexpr int kMsFixed = 1;                           // units of an item's fixed part
+constexpr int kMsFixed = 12;                          // units (of two products) of an item's fixed part; with 1 a 16K prompt took 823 us, not 804
 constexpr int kMsS = 3;                               // ring of S, and groups that sum
 constexpr int kMsTmemCols = 512;                      // S, and K tiles of 64 columns
 constexpr uint32_t kMsColK = kMsS * 128;
@@ -230,7 +232,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   const uint32_t qs = smem_u32(base + kMsOffQ);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !__all_sync(0xffffffffu, mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, a.wait_limit))) {
+    // mostly over: tested before it is waited for
+    if (!dead && !__all_sync(0xffffffffu, mbar_test(bar, parity)) &&
+        !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit))) {
       if (lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
       dead = true;
     }
