@@ -611,9 +611,9 @@ int kv4_attn_launch(const Kv4AttnCall& c, void* workspace, void* stream) {
 }  // namespace spc
 
 #ifdef SPC_TEST_HOOKS
-// Test builds only: the next `calls` launches of the 4-bit decode attention or
-// the prompt attention issue no copies and give up waiting after `wait_cycles`
-// clock cycles.
+// Test builds only: the next `calls` calls of the 4-bit decode attention, the
+// prompt's, a chunk's or the accumulated weight issue no copies and give up
+// waiting after `wait_cycles` clock cycles.
 extern "C" int spc_test_starve_paged(int calls, long long wait_cycles) {
   if (calls < 0 || wait_cycles < 1) return SPC_ERR_INVALID_ARG;
   spc::g_starve_wait.store(wait_cycles);

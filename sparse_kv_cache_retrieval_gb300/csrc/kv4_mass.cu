@@ -50,7 +50,8 @@ constexpr int kMsQ = 5;                               // ring of Q tiles
 constexpr int kMsL = 6;                               // ring of the rows' lse
 constexpr int kMsItems = 2;
 constexpr int kMsGo = 4;                              // products that the gate may be ahead by
-constexpr int kMsMasks = 2 * kMsItems;                // tiles whose masks are kept: the items' in the ring
+constexpr int kMsMasks = 8;                           // tiles whose masks are kept: the ring's items' and those of the one being summed up
+static_assert(kMsMasks >= 2 * (kMsItems + 1), "masks of three items");
 constexpr int kMsHand = 32;                           // rows up to which a Q tile is loaded without TMA
 constexpr int kMsWarpDeq = 12, kMsWarpMma = 16, kMsWarpPlan = 17, kMsWarpQ = 18;
 constexpr int kMsThreads = 640;
@@ -75,7 +76,7 @@ constexpr int kMsBars = 8 * kMsRaw + 2 * kMsK + 2 * kMsQ + 2 * kMsL + 2 * kMsIte
 constexpr size_t kMsSmem = 1024 + kMsOffBar + kMsBars * 8 + 16;
 static_assert(kMsSmem <= 227 * 1024, "shared memory of one CTA");
 
-// workspace: status; arrival counters (zero between calls) of the items that are
+// workspace: status; arrival counters (zeroed by the call's first kernel) of the items that are
 // cut first in a CTA, [2 tiles][4 warps]; the sums of a CTA's first and last piece
 constexpr size_t kMsOffCount = 256;
 constexpr size_t kMsOffPart = kMsOffCount + (size_t)kKcCtas * 8 * 4;
@@ -679,7 +680,6 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         y = 0.f;
         for (int k = 0; k < x.pieces; ++k)
           y += __ldcg(a.part + ((size_t)(x.first + k) * 2 + (k == 0 ? 1 : 0)) * 256 + grp * 128 + wq * 32 + lane);
-        if (lane == 0) atomicExch(arrived, 0u);
       }
       if (mine) c.mass_next[at] = c.keep != 0.f ? fmaf(c.keep, prev, y) : y;
     }
@@ -776,6 +776,8 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
   }
   __syncthreads();
   const int t0 = ln.t0, t1 = ln.t1;
+  // the other kernel's counters, whatever a call that ran out of time has left there
+  if (threadIdx.x < 8) a.counters[blockIdx.x * 8 + threadIdx.x] = 0u;
   if (t0 >= t1) return;
   if (warp == kMfWarps) {
 #ifdef SPC_TEST_HOOKS

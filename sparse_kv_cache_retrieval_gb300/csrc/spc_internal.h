@@ -237,8 +237,9 @@ struct Kv4EvictCall {
 int kv4_evict_launch(const Kv4EvictCall& c, void* stream);
 
 #ifdef SPC_TEST_HOOKS
-// Test builds only: whether the next launch of the two kernels above runs
-// starved (its copies are not issued), and the wait limit it then has.
+// Test builds only: whether this call of the 4-bit decode attention, the prompt's,
+// a chunk's or the accumulated weight runs starved (its copies are not issued),
+// and the wait limit it then has.
 bool paged_starve(long long* wait_limit);
 #endif
 
