@@ -38,7 +38,7 @@
 // Work: the items' blocks (and an item's fixed part), in units of their time, form
 // a line that is cut into equal runs, one a CTA (persistent, one per SM). The pieces of
 // an item that is cut leave partials (O, maximum, sum) in the workspace, which a
-// second kernel merges, a warp a row, in the order of the positions.
+// second kernel merges in the order of the positions.
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
 //   warps 8-11      dequantisation into a ring of four 32 KB operands: K_j, V_j, K_j+1, ...
 //   warp 12         tensor memory, MMA issue
@@ -120,7 +120,7 @@ struct KcCfg {
 // a CTA's first and last piece, two tiles each
 constexpr size_t kKcOffCut = 256;
 constexpr size_t kKcOffPart = kKcOffCut + (size_t)kKcCtas * 64;
-constexpr int kKcPart = kD + 4;                       // a row's partial: O[128], maximum, sum, their factor and the queries' scale
+constexpr int kKcPart = kD + 4;                       // a row's partial: O[128], and maximum, sum, their factor and the queries' scale
 static_assert(kKcOffPart % 128 == 0, "aligned partials");
 constexpr int kKcMergeThreads = 256;
 
@@ -146,6 +146,11 @@ struct KcArgs {
   int starve;              // test builds: no copy is issued, so that every wait runs out
 };
 
+
+// a / b of 64 bits each, mostly small: a division of 64 bits takes some 400 cycles, and the plan has a chain of them
+__device__ __forceinline__ long long kc_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 __device__ __forceinline__ bool kc_wait(const KcArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
@@ -248,62 +253,69 @@ __device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
 __device__ __forceinline__ float kc_lse(const KcArgs& a, float m, float l, float inv) {
   return l == 0.f ? -INFINITY : m * inv * a.c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
 }
-__device__ __forceinline__ float* kc_part(const KcArgs& a, int cta, int last, int tile, int row) {
-  return a.part + ((((size_t)cta * 2 + last) * 2 + tile) * a.part_rows + row) * kKcPart;
+// A piece's partials of a tile: four dims of O of each row, [32][rows][4], then the
+// rows' maxima and so on, [rows][4]: the lanes of a warp have consecutive rows,
+// where they are written and where they are read
+__device__ __forceinline__ float4* kc_part(const KcArgs& a, int cta, int last, int tile) {
+  return reinterpret_cast<float4*>(a.part) + (((size_t)cta * 2 + last) * 2 + tile) * a.part_rows * (kKcPart / 4);
 }
 
-// The partials of the items that are cut, a warp a row.
+// The partials of the items that are cut. A warp has 16 dims of 32 rows, a row a
+// lane, and goes through the pieces once, with the running maximum: nothing that
+// it loads depends on what it has loaded but the number of pieces. (A warp a row,
+// maxima first, then the weights, then O, and four rows in turn: 8.4 us of the 23
+// that 17 tokens behind 1000 took.)
 __global__ void __launch_bounds__(kKcMergeThreads) kv4_chunk_merge_kernel(const KcArgs a) {
   const Kv4ChunkCall& c = a.c;
   const KcItem x = a.cut[blockIdx.x];
-  const int lane = threadIdx.x & 31, i = blockIdx.z;
+  const int warp = threadIdx.x >> 5, row = blockIdx.y * 32 + (threadIdx.x & 31), i = blockIdx.z;
   if (x.pieces < 2 || (x.single && i)) return;
   const int t0 = x.t0 + i * a.tpm;
-  const long long live = (long long)(x.n - t0) << a.gshift;
-  for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(live, (long long)blockIdx.y * 32 + 32) && row < 128;
-       row += kKcMergeThreads / 32) {
-    // piece k is its CTA's last one for k = 0, else its first
-    auto part = [&](int k) { return kc_part(a, x.first + k, k == 0, i, row); };
-    float M = -INFINITY, l = 0.f;
-    for (int k = lane; k < x.pieces; k += 32) M = fmaxf(M, part(k)[kD]);
-    M = warp_max(M);
-    const float f = part(0)[kD + 2], inv = part(0)[kD + 3];
-    float w[(kKcCtas + 31) / 32];                     // weights of pieces lane, lane + 32, ...; -1 where the row saw nothing
+  if (row >= min((long long)(x.n - t0) << a.gshift, 128ll)) return;
+  float m = -INFINITY, l = 0.f, f = 0.f, inv = 0.f, o[16];
 #pragma unroll
-    for (int e = 0; e < (kKcCtas + 31) / 32; ++e) {
-      w[e] = -1.f;
-      const int k = lane + 32 * e;
-      if (k >= x.pieces) continue;
-      const float2 ml = *reinterpret_cast<const float2*>(part(k) + kD);
-      if (ml.y == 0.f) continue;
-      w[e] = ex2_approx((ml.x - M) * f);
-      l += ml.y * w[e];
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+  constexpr int U = 4;                                // pieces whose loads are in flight together
+  for (int k0 = 0; k0 < x.pieces; k0 += U) {
+    float4 ml[U], v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= x.pieces) continue;
+      // piece k is its CTA's last one for k = 0, else its first
+      const float4* p = kc_part(a, x.first + k0 + u, k0 + u == 0, i) + row;
+      ml[u] = p[(size_t)(kD / 4) * a.part_rows];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = p[(size_t)(4 * warp + e) * a.part_rows];
     }
-    l = warp_sum(l);
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int U = 8;                              // pieces whose loads are in flight together
 #pragma unroll
-    for (int e = 0; e < (kKcCtas + 31) / 32; ++e)
-      for (int k0 = 32 * e; k0 < min(x.pieces, 32 * e + 32); k0 += U) {
-        float4 v[U];
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= x.pieces) continue;
+      f = ml[u].z;
+      inv = ml[u].w;
+      if (ml[u].y == 0.f) continue;                   // the row saw nothing, and its O may not have been written
+      const float M = fmaxf(m, ml[u].x), wo = l == 0.f ? 0.f : ex2_approx((m - M) * f), wn = ex2_approx((ml[u].x - M) * f);
+      m = M;
+      l = l * wo + ml[u].y * wn;
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = k0 + u < x.pieces ? *(reinterpret_cast<const float4*>(part(k0 + u)) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float wt = __shfl_sync(0xffffffffu, w[e], (k0 + u) & 31);
-          if (wt < 0.f) continue;                     // its O was not written
-          o[0] += wt * v[u].x;
-          o[1] += wt * v[u].y;
-          o[2] += wt * v[u].z;
-          o[3] += wt * v[u].w;
-        }
+      for (int e = 0; e < 4; ++e) {
+        o[4 * e] = o[4 * e] * wo + v[u][e].x * wn;
+        o[4 * e + 1] = o[4 * e + 1] * wo + v[u][e].y * wn;
+        o[4 * e + 2] = o[4 * e + 2] * wo + v[u][e].z * wn;
+        o[4 * e + 3] = o[4 * e + 3] * wo + v[u][e].w * wn;
       }
-    const size_t at = (size_t)(x.row0 + t0 + (row >> a.gshift)) * c.n_q + (x.g << a.gshift) + (row & (a.G - 1));
-    *reinterpret_cast<uint2*>(c.out + at * kD + 4 * lane) = make_uint2(pack_bf16(o[0] * r, o[1] * r), pack_bf16(o[2] * r, o[3] * r));
-    if (c.lse && lane == 0) c.lse[at] = kc_lse(a, M, l, inv);
+    }
   }
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  const size_t at = (size_t)(x.row0 + t0 + (row >> a.gshift)) * c.n_q + (x.g << a.gshift) + (row & (a.G - 1));
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[2 * e] * r, o[2 * e + 1] * r);
+  uint16_t* d = c.out + at * kD + 16 * warp;
+  stg_v4(d, make_uint4(w[0], w[1], w[2], w[3]));
+  stg_v4(d + 8, make_uint4(w[4], w[5], w[6], w[7]));
+  if (c.lse && warp == 0) c.lse[at] = kc_lse(a, m, l, inv);
 }
+static_assert(kKcMergeThreads == 32 * (kD / 16), "a warp for 16 dims");
 
 template <bool LONE>
 __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const KcArgs a) {
@@ -404,8 +416,8 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
     const long long total = kc_prefix(rq, own[0] * c.n_kv, own[1] * c.n_kv);
     const int ctas = (int)max(min(total, 1ll), min(total / kKcMinRun, (long long)gridDim.x));
     const bool has = (int)blockIdx.x < ctas;
-    const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
-    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+    const long long u0 = has ? kc_div(total * blockIdx.x, ctas) : 0, u1 = has ? kc_div(total * (blockIdx.x + 1), ctas) : 0;
+    auto cta_of = [&](long long u) { return (int)kc_div((u + 1) * ctas - 1, total); };
     // the item at u0: request b, head g, pair i; `at` is its first unit
     int b = 0, g = 0, i = 0;
     long long at = 0, whole = 1;
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
     if (has) {
       enter(kc_find(rq, u0));
       long long r = u0 - (kc_of(rq.end, b) - whole * c.n_kv);
-      g = (int)(r / whole);
+      g = (int)kc_div(r, whole);
       r -= (long long)g * whole;
       int lo = 0, hi = s.pairs;                       // units(lo) <= r
       while (hi - lo > 1) {
@@ -943,7 +955,7 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
           l = l * wa + ml.y * wb;
         }
         const bool cut = x.pieces > 1;
-        float* p = kc_part(a, blockIdx.x, x.piece == 0, i, row);
+        float4* p = kc_part(a, blockIdx.x, x.piece == 0, i) + row;
         const float r = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
         wa *= r;
         wb *= r;
@@ -972,8 +984,8 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
             if (!live) continue;
             if (cut) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(p + 16 * q + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 4; ++e)
+                p[(size_t)(4 * q + e) * a.part_rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
               continue;
             }
             uint32_t w[8];
@@ -994,7 +1006,7 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
           __syncwarp();
           if (lane == 0) mbar_arrive(&bread[wq]);
         }
-        if (live && cut) *reinterpret_cast<float4*>(p + kD) = make_float4(m, l, f, inv);
+        if (live && cut) p[(size_t)(kD / 4) * a.part_rows] = make_float4(m, l, f, inv);
         if (live && !cut && c.lse) c.lse[(size_t)(x.row0 + token) * c.n_q + hq] = kc_lse(a, m, l, inv);
       }
       __syncwarp();
