@@ -76,8 +76,8 @@ constexpr float kKcHeadroom = 7.75f;                  // log2 growth allowed bef
 // 1.9 us), of an item's fixed part, and those a CTA takes at least (more than a
 // block's, so that every CTA between an item's first and last one has a piece of
 // it). 16 requests with up to 700 tokens take 932 us; with 6 for the fixed part
-// 1089. A run of 18 at least: 17 tokens behind 1000 take 29 us instead of 23.
-constexpr int kKcUnitsTwo = 6, kKcUnitsOne = 5, kKcFixed = 42, kKcMinRun = 11;
+// 1089. A run of 18 at least: 17 tokens behind 1000 took 29 us instead of 23.
+constexpr int kKcUnitsTwo = 6, kKcUnitsOne = 5, kKcFixed = 42, kKcMinRun = 9;
 static_assert(kKcMinRun >= kKcUnitsTwo, "a block begins in every run");
 constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
 constexpr uint32_t kKcColO = 256;
