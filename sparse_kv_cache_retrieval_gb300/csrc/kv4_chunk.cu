@@ -40,12 +40,18 @@
 // an item that is cut leave partials (O, maximum, sum) in the workspace, which a
 // second kernel merges in the order of the positions.
 //   warps 0-3, 4-7  softmax and epilogue of tile A, B
-//   warps 8-11      dequantisation into a ring of four 32 KB operands: K_j, V_j, K_j+1, ...
+//   warps 8-11      dequantisation (few new tokens: 8-15, and four more below) into a ring of four 32 KB operands: K_j, V_j, K_j+1, ...
 //   warp 12         tensor memory, MMA issue
 //   warp 13         schedule, copies of the records (cp.async.bulk)
 //   warp 14         Q loads (TMA)
 //   warp 15         gate: passes the operands' arrival on to the P barriers, so that the MMA
 //                   warp waits once a batch
+// Bound: 2048 tokens of 64 heads behind 64K take 3.2 ms, 1.34 PFLOP/s, a block of two
+// tiles 1.9 us. Its products are 1 024 cycles of the tensor pipe (53% busy), but S reads both
+// operands from shared memory, which takes twice that long, and with the operands'
+// own 64 KB shared memory is some 65% busy; the rest is the chain S, softmax, P of a
+// tile where the other one does not cover it. With few rows (LONE) a block costs
+// what 128 rows cost: 8 x 64K, 32 rows, 287 us, 2.1 TB/s of records.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
 // and leaves, the others' waits then give up in turn; copies land and MMAs
 // complete before the CTA releases its tensor memory.

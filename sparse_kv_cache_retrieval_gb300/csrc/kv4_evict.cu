@@ -16,9 +16,13 @@
 //     cache that shrinks in place needs no more: row i comes from a place >= i, so
 //     that a batch overwrites no source of a later one.
 // Ranks: one for each 16384 positions, and while there are few heads more of them, until
-// the kept rows are one batch each (measured: see kv4_evict_launch).
-// Bound: the sums' bytes and the kept records', 144 in and out; small calls by
-// the chain of dependent steps.
+// the kept rows are one batch each (both sides at kv4_evict_launch).
+// Bound: 8 requests of 65536 positions cut to 4096, 8 heads, take 45 us: 20 of
+// them move 38 MB each way (65 MB of DRAM reads, for a record of 144 bytes begins
+// at any multiple of 16; 5.4 TB/s with the writes), the others are the select's
+// chain, which every cluster goes through at the same time: sums 7 us, three levels
+// 10 (a barrier of the cluster, the other ranks' counts, two scans), the list 5. Small
+// calls are that chain alone: 1088 positions cut to 1024 take 10.7 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -84,6 +88,10 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
   float* mass_next = c.mass_next + (size_t)seg * c.cap;
   int32_t* kept = c.kept ? c.kept + (size_t)seg * c.budget : nullptr;
 
+  // the tables' entries are checked below, where the first of them have arrived
+  const int nfrom = (L + bs - 1) >> c.block_shift, nto = (K + bs - 1) >> c.block_shift;
+  const int from0 = tid < nfrom ? from[tid] : 0, to0 = tid < nto ? to[tid] : 0;
+
   // ---- order keys of the slice, padded to whole runs of 128 by keys that are never kept
   const int slice = min(a.slice, ((L + C - 1) / C + 127) & ~127), p0 = min(L, rank * slice), n = min(L, p0 + slice) - p0;
   const int whole = (n + 127) & ~127;
@@ -132,9 +140,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
   }
   for (int i = tid; i < kEvBins / 4; i += kEvThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   // the request is left as it was if a block that it uses is not in the pool
-  bool bad = false;
-  for (int i = tid; i < (L + bs - 1) >> c.block_shift; i += kEvThreads) bad |= (unsigned)from[i] >= (unsigned)c.num_blocks;
-  for (int i = tid; i < (K + bs - 1) >> c.block_shift; i += kEvThreads) bad |= (unsigned)to[i] >= (unsigned)c.num_blocks;
+  bool bad = (tid < nfrom && (unsigned)from0 >= (unsigned)c.num_blocks) || (tid < nto && (unsigned)to0 >= (unsigned)c.num_blocks);
+  for (int i = tid + kEvThreads; i < nfrom; i += kEvThreads) bad |= (unsigned)from[i] >= (unsigned)c.num_blocks;
+  for (int i = tid + kEvThreads; i < nto; i += kEvThreads) bad |= (unsigned)to[i] >= (unsigned)c.num_blocks;
   if (__syncthreads_or(bad)) {                        // the same in every rank
     const int t = rank * kEvThreads + tid;
     if (kept)
@@ -232,12 +240,19 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
   }
 
   // ---- the kept positions, to the ranks that move them
+  const uint32_t below = (1u << lane) - 1u;
   for (int i = w0 + 4 * lane; i < w1; i += 128) {
     const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    const uint32_t m = count(k4);
-    const uint32_t incl = (uint32_t)warp_incl_scan((int)m), all_of = __shfl_sync(0xffffffffu, incl, 31);
-    uint32_t x = gt + ((incl - m) & 0xffffu), e = eq + ((incl - m) >> 16);
+    uint32_t x = gt, e = eq;                          // before the lane's four
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const uint32_t above = __ballot_sync(0xffffffffu, k[f] > thr), tie = __ballot_sync(0xffffffffu, k[f] == thr);
+      x += __popc(above & below);
+      e += __popc(tie & below);
+      gt += __popc(above);
+      eq += __popc(tie);
+    }
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const bool above = k[f] > thr, tie = k[f] == thr;
@@ -245,13 +260,10 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
         // place at: batch at / (256 C), rank (at / 256) % C
         const uint32_t at = x + min(e, ties);
         *ev_at<C>(&list[at / (kEvBatch * C) * kEvBatch + at % kEvBatch], at / kEvBatch % C) = (uint32_t)(p0 + i + f);
-        if (kept) kept[at] = p0 + i + f;
       }
       x += above;
       e += tie;
     }
-    gt += all_of & 0xffffu;
-    eq += all_of >> 16;
   }
   if (kept)
     for (int i = K + rank * kEvThreads + tid; i < c.budget; i += C * kEvThreads) kept[i] = -1;
@@ -271,6 +283,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
     if (i >= batches * kEvBatch || at >= K) continue;
     const int p = (int)list[i];
     sums[e] = mass[p];
+    if (kept) kept[at] = p;
     list[i] = record(from, p);
     dst[i] = record(to, at);
   }
@@ -353,6 +366,9 @@ int kv4_evict_launch(const Kv4EvictCall& c, void* stream) {
   a.c = c;
   const int most = c.max_blocks << c.block_shift, budget = most < c.budget ? most : c.budget;
   int C = 1;
+  // us with 1, 2, 4 and 8 ranks, 8 heads: one request of 8000 positions to 2048 19.9, 17.9,
+  // 13.8, 14.0; four of 12000 22.6, 19.7, 15.5, 23.1; sixteen of 8000 23.9, 28.4, 38.9,
+  // 84.0; one of 1088 to 1024 11.4, 12.2, 11.3, 13.5
   while (C < kEvCluster && C * kEvSlice < most) C *= 2;
   while (C < kEvCluster && C * kEvBatch < budget && 2 * C * c.B * c.n_kv <= 152) C *= 2;
   switch (C) {

@@ -30,6 +30,10 @@
 //   warp 18         queries (TMA, or by hand where a tile has few rows) and lse
 //   warp 19         gate: waits for all that a product needs, so that the MMA warp waits once
 // Every wait is bounded; see kv4_chunk.cu.
+// Bound: exponentials and products, 58% of their pipes each, and 62% of the issue
+// slots (8192 tokens): 16384 tokens of 32 heads take 794-817 us, 1.35-1.38 PFLOP/s.
+// Where an item has few row tiles (64 tokens look back over five prompts: two for
+// 256 positions, 83 us), the copies and conversions of K and an item's ends.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -726,7 +730,9 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
 // so these are the fragments of the eight steps as they come, and the queries, in
 // registers, are in the same order: bf16 to fp16 times a power of two a row, as in
 // kv4_chunk.cu. Nothing is exchanged but a position's sum over four lanes.
-// Bound: HBM; see the figures at kv4_mass_launch.
+// Bound: HBM. 8 x 65536 positions, 64 heads on 8: 604 MB of records (K's 72 bytes of
+// 144 are in every line that is read) and 34 MB of sums in 124 us, 5.1 TB/s; 32768:
+// 67 us alone, 4.8 TB/s, the ALU pipe 39% busy with conversions.
 constexpr int kMfWarps = 15, kMfStages = 3, kMfTiles = kMfRows / 8;
 constexpr uint32_t kMfOffBar = kMfWarps * kMfStages * kK4StageBytes;
 constexpr uint32_t kMfOffMask = kMfOffBar + 2 * kMfWarps * kMfStages * 8;
@@ -938,7 +944,11 @@ int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   if (set_func_attr((const void*)kv4_mass_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMfSmem) != cudaSuccess)
     return SPC_ERR_CUDA;
   kv4_mass_few_kernel<<<kKcCtas, 32 * (kMfWarps + 1), kMfSmem, st>>>(f);
-  // no request can have more rows than the call
+  // The request's rows decide, up to 32 of them here and more there. us, the one way and the
+  // other, G = 4: 8 x 65536 positions, 4 rows 121 and 492, 8 rows 126 and 492, 16 rows
+  // 138 and 493, 32 rows 173 and 513; 1 x 1000, 4 rows 4.4 and 10.6, 32 rows 6.1 and
+  // 11.0. 64 rows are eight tiles of 8, with 128 registers of queries a lane: not here.
+  // No request can have more rows than the call.
   if ((long long)c.T * a.G > kMfRows) {
     CUtensorMap qmap{};
     const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)c.n_q, (uint64_t)c.T};
