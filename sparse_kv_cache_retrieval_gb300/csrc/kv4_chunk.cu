@@ -153,11 +153,6 @@ struct KcArgs {
 };
 
 
-// a / b of 64 bits each, mostly small: a division of 64 bits takes some 400 cycles, and the plan has a chain of them
-__device__ __forceinline__ long long kc_div(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 __device__ __forceinline__ bool kc_wait(const KcArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.wait_limit));
 }
@@ -477,8 +472,9 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
             x.n0 = max(0, min(x.j1, na) - x.j0);
             x.n1 = x.j1 - x.j0;
           }
-          x.first = cta_of(first);
-          x.pieces = cta_of(first + (long long)(nb - 1) * each) - x.first + 1;
+          const bool cut = lo > 0 || hi < nb;
+          x.first = lo > 0 ? cta_of(first) : (int)blockIdx.x;
+          x.pieces = cut ? cta_of(first + (long long)(nb - 1) * each) - x.first + 1 : 1;
           x.piece = (int)blockIdx.x - x.first;
           if (x.pieces > 1 && x.piece == 0 && lane == 0) a.cut[blockIdx.x] = x;
         }

@@ -58,6 +58,11 @@ __device__ __forceinline__ int kc_find(const KcRequests& r, long long u) {
   return __popc(__ballot_sync(0xffffffffu, r.end[0] <= u)) + __popc(__ballot_sync(0xffffffffu, r.end[1] <= u));
 }
 
+// a / b of 64 bits each, mostly small: a division of 64 bits takes some 400 cycles, and the plans have chains of them
+__device__ __forceinline__ long long kc_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The table entries of a request, a window of 32 at a time and the next one on
 // its way: lane l holds entry `at` + l, -1 behind the last one.
 struct KcTable {
@@ -70,6 +75,11 @@ struct KcTable {
     at = first & ~31;
     cur = get(at + (threadIdx.x & 31));
     next = get(at + 32 + (threadIdx.x & 31));
+  }
+  // the same, where what is there may do: the same row, at its window or the one behind it
+  __device__ __forceinline__ void move(const int32_t* table_row, int entries, int first) {
+    const int to = first & ~31;
+    if (row != table_row || (to != at && to != at + 32)) start(table_row, entries, first);
   }
   // entry i of this lane's choice, all of them in the window of `first` (a warp-uniform index)
   __device__ __forceinline__ int entry(int first, int i) {

@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     const long long total = kc_prefix(rq, own[0] * c.n_kv, own[1] * c.n_kv);
     const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
     const bool has = (int)blockIdx.x < ctas;
-    const long long u0 = has ? total * blockIdx.x / ctas : 0, u1 = has ? total * (blockIdx.x + 1) / ctas : 0;
-    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+    const long long u0 = has ? kc_div(total * blockIdx.x, ctas) : 0, u1 = has ? kc_div(total * (blockIdx.x + 1), ctas) : 0;
+    auto cta_of = [&](long long u) { return (int)kc_div((u + 1) * ctas - 1, total); };
     int b = 0, g = 0, i = 0;
     long long at = 0, whole = 1;
     MsShape s{};
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     if (has) {
       enter(kc_find(rq, u0));
       long long r = u0 - (kc_of(rq.end, b) - whole * c.n_kv);
-      g = (int)(r / whole);
+      g = (int)kc_div(r, whole);
       r -= (long long)g * whole;
       int lo = 0, hi = s.items;
       while (hi - lo > 1) {
@@ -284,6 +284,8 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
       at = u0 - r + ms_units(s, i);
     }
     int it = 0, blocks = 0, nraw = 0;
+    KcTable t;
+    t.row = nullptr;
     for (;;) {
       MsItem x;
       x.b = -1;
@@ -303,8 +305,8 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
           x.tiles = x.p0 + 128 < s.len ? 2 : 1;
           x.r0 = s.nt - nu + lo;
           x.r1 = s.nt - nu + hi;
-          x.first = cta_of(first);
-          x.pieces = cta_of(first + nu - 1) - x.first + 1;
+          x.first = lo > 0 ? cta_of(first) : (int)blockIdx.x;
+          x.pieces = lo > 0 || hi < nu ? cta_of(first + nu - 1) - x.first + 1 : 1;
           x.piece = (int)blockIdx.x - x.first;
         }
       }
@@ -321,8 +323,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
 #ifdef SPC_TEST_HOOKS
         if (a.starve) break;
 #endif
-        KcTable t;
-        t.start(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
+        t.move(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
         // lane w copies for dequantising warp w
         for (int j = 0; j < x.tiles && !dead; ++j, ++blocks) {
           uint32_t mask = 0u;
