@@ -268,6 +268,7 @@ __device__ __forceinline__ float4* kc_part(const KcArgs& a, int cta, int last, i
 // that 17 tokens behind 1000 took.)
 __global__ void __launch_bounds__(kKcMergeThreads) kv4_chunk_merge_kernel(const KcArgs a) {
   const Kv4ChunkCall& c = a.c;
+  kc_wait_first();
   const KcItem x = a.cut[blockIdx.x];
   const int warp = threadIdx.x >> 5, row = blockIdx.y * 32 + (threadIdx.x & 31), i = blockIdx.z;
   if (x.pieces < 2 || (x.single && i)) return;
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  kc_let_next();
   const uint32_t qs = smem_u32(base + Cfg::kOffQ), kvs = smem_u32(base + Cfg::kOffKv);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
@@ -1065,8 +1067,9 @@ static int kc_launch(const CUtensorMap& qmap, const KcArgs& a, cudaStream_t st) 
   if (set_func_attr((const void*)kv4_chunk_kernel<LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SPC_ERR_CUDA;
   kv4_chunk_kernel<LONE><<<kKcCtas, KcCfg<LONE>::kThreads, smem, st>>>(qmap, a);
-  kv4_chunk_merge_kernel<<<dim3(kKcCtas, (a.part_rows + 31) / 32, LONE ? 1 : 2), kKcMergeThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return SPC_ERR_CUDA;
+  const dim3 grid(kKcCtas, (a.part_rows + 31) / 32, LONE ? 1 : 2);
+  return kc_launch_next(kv4_chunk_merge_kernel, grid, kKcMergeThreads, 0, st, a) ? SPC_OK : SPC_ERR_CUDA;
 }
 
 int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {

@@ -58,6 +58,27 @@ __device__ __forceinline__ int kc_find(const KcRequests& r, long long u) {
   return __popc(__ballot_sync(0xffffffffu, r.end[0] <= u)) + __popc(__ballot_sync(0xffffffffu, r.end[1] <= u));
 }
 
+// The second of a call's two kernels is launched while the first one runs: the
+// first one lets it, once each of its CTAs is there, and the second one waits for
+// the end of it before anything else (18.7 us instead of 20.5 for 17 tokens behind 1000,
+// call after call in a stream; no difference in a graph).
+__device__ __forceinline__ void kc_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void kc_wait_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P, class... A>
+static bool kc_launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // a / b of 64 bits each, mostly small: a division of 64 bits takes some 400 cycles, and the plans have chains of them
 __device__ __forceinline__ long long kc_div(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;

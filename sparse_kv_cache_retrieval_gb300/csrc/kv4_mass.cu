@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  kc_wait_first();
   const uint32_t qs = smem_u32(base + kMsOffQ);
   bool dead = false;
   auto acquire = [&](uint64_t* bar, uint32_t parity) {
@@ -785,6 +786,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
   const int t0 = ln.t0, t1 = ln.t1;
   // the other kernel's counters, whatever a call that ran out of time has left there
   if (threadIdx.x < 8) a.counters[blockIdx.x * 8 + threadIdx.x] = 0u;
+  kc_let_next();
   if (t0 >= t1) return;
   if (warp == kMfWarps) {
 #ifdef SPC_TEST_HOOKS
@@ -945,6 +947,7 @@ int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   if (set_func_attr((const void*)kv4_mass_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMfSmem) != cudaSuccess)
     return SPC_ERR_CUDA;
   kv4_mass_few_kernel<<<kKcCtas, 32 * (kMfWarps + 1), kMfSmem, st>>>(f);
+  if (cudaGetLastError() != cudaSuccess) return SPC_ERR_CUDA;
   // The request's rows decide, up to 32 of them here and more there. us, the one way and the
   // other, G = 4: 8 x 65536 positions, 4 rows 121 and 492, 8 rows 126 and 492, 16 rows
   // 138 and 493, 32 rows 173 and 513; 1 x 1000, 4 rows 4.4 and 10.6, 32 rows 6.1 and
@@ -958,9 +961,9 @@ int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
     if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
     if (set_func_attr((const void*)kv4_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMsSmem) != cudaSuccess)
       return SPC_ERR_CUDA;
-    kv4_mass_kernel<<<kKcCtas, kMsThreads, kMsSmem, st>>>(qmap, a);
+    if (!kc_launch_next(kv4_mass_kernel, dim3(kKcCtas), kMsThreads, kMsSmem, st, qmap, a)) return SPC_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? SPC_OK : SPC_ERR_CUDA;
+  return SPC_OK;
 }
 
 }  // namespace spc
