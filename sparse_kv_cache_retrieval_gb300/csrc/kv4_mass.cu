@@ -33,7 +33,7 @@
 // Bound: exponentials and products, 58% of their pipes each, and 62% of the issue
 // slots (8192 tokens): 16384 tokens of 32 heads take 794-817 us, 1.35-1.38 PFLOP/s.
 // Where an item has few row tiles (64 tokens look back over five prompts: two for
-// 256 positions, 83 us), the copies and conversions of K and an item's ends.
+// 256 positions, 79 us), the copies and conversions of K and an item's ends.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +46,7 @@
 namespace spc {
 
 // stages of each dequantising warp's ring of records, and positions a stage: three
-// tiles, where with 1.5 (and six Q tiles) 64 rows' look back took 95 us, not 83
+// tiles, where with 1.5 (and six Q tiles) 64 tokens' look back took 95 us, not 83
 constexpr int kMsRaw = 6, kMsRun = 16;
 constexpr uint32_t kMsStage = kMsRun * kKv4Rec;
 constexpr int kMsK = 2;                               // ring of dequantised K tiles
@@ -115,28 +115,24 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// 64 K values of 32 bytes of codes and 4 scales as bf16 into 32 columns of this
+// 32 K values of 16 bytes of codes and two scales as bf16 into 16 columns of this
 // thread's tensor memory lane. A code as fp16 has at most one bit of mantissa; its bits three
 // places further down are bf16's of the value times 2^-112, which the scale, an
 // e4m3 number times 2^112, takes back: the product is exact.
-__device__ __forceinline__ void ms_half_row(const uint4* codes, uint32_t sc, uint32_t t) {
-  uint32_t k[32];
+__device__ __forceinline__ void ms_quarter_row(const uint4& codes, uint32_t sc, uint32_t t) {
+  uint32_t k[16];
+  const uint32_t s2 = e4m3x2_to_f16(sc & 0xffffu);
+  const float f0 = f16_lo(s2) * 5.192296858534828e33f, f1 = f16_hi(s2) * 5.192296858534828e33f;   // 2^112
+  const uint32_t s[2] = {pack_bf16(f0, f0), pack_bf16(f1, f1)};
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t s2 = e4m3x2_to_f16((sc >> (16 * q)) & 0xffffu);
-    const float f0 = f16_lo(s2) * 5.192296858534828e33f, f1 = f16_hi(s2) * 5.192296858534828e33f;   // 2^112
-    const uint32_t s[2] = {pack_bf16(f0, f0), pack_bf16(f1, f1)};
-    const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
+  for (int e = 0; e < 4; ++e) {
+    uint32_t h[4];
+    e2m1x8_to_f16(w[e], h);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t h[4];
-      e2m1x8_to_f16(w[e], h);
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        k[16 * q + 4 * e + f] = bmul2(((h[f] >> 3) & 0x0fff0fffu) | (h[f] & 0x80008000u), s[e >> 1]);
-    }
+    for (int f = 0; f < 4; ++f) k[4 * e + f] = bmul2(((h[f] >> 3) & 0x0fff0fffu) | (h[f] & 0x80008000u), s[e >> 1]);
   }
-  tmem_st32(t, k);
+  tmem_st16(t, k);
 }
 
 // ---------------------------------------------------------------- the line of work
@@ -325,27 +321,28 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         if (a.starve) break;
 #endif
         t.move(c.table + (size_t)b * c.max_blocks, (x.len + bs - 1) >> c.block_shift, x.p0 >> c.block_shift);
-        // lane w copies for dequantising warp w
-        for (int j = 0; j < x.tiles && !dead; ++j, ++blocks) {
-          uint32_t mask = 0u;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h, ++nraw) {
-            const int st = nraw % kMsRaw, p = x.p0 + j * 128 + (lane & 3) * 32 + h * kMsRun;
-            const int blk = t.entry((x.p0 + j * 128) >> c.block_shift, p >> c.block_shift);
-            const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kMsRun)) : 0;
-            mask |= ((1u << n) - 1u) << (h * kMsRun);
-            uint64_t* bar = &rfull[(lane & 3) * kMsRaw + st];
-            acquire(&rfree[(lane & 3) * kMsRaw + st], ((nraw / kMsRaw) & 1) ^ 1);
-            if (dead) break;
-            if (lane < 4) {
-              if (h == 1) masks[(blocks % kMsMasks) * 4 + lane] = mask;
-              if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)n * kKv4Rec); else mbar_arrive(bar);
-              if (n > 0)
-                bulk_g2s(base + kMsOffRaw + (lane * kMsRaw + st) * kMsStage,
-                         c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, bar);
+        // lane w + 4 h copies half h of dequantising warp w's positions
+        const int w = lane & 3, h = lane >> 2 & 1;
+        for (int j = 0; j < x.tiles && !dead; ++j, ++blocks, nraw += 2) {
+          const int use = nraw + h, st = w * kMsRaw + use % kMsRaw, p = x.p0 + j * 128 + w * 32 + h * kMsRun;
+          const int blk = t.entry((x.p0 + j * 128) >> c.block_shift, p >> c.block_shift);
+          const int n = (unsigned)blk < (unsigned)c.num_blocks ? max(0, min(x.len - p, kMsRun)) : 0;
+          uint32_t mask = ((1u << n) - 1u) << (h * kMsRun);
+          mask |= __shfl_xor_sync(0xffffffffu, mask, 4);
+          acquire(&rfree[st], ((use / kMsRaw) & 1) ^ 1);
+          if (dead) break;
+          if (lane < 4) masks[(blocks % kMsMasks) * 4 + lane] = mask;
+          __syncwarp();                               // before the arrivals that let them be read
+          if (lane < 8) {
+            if (n > 0) {
+              mbar_arrive_expect_tx(&rfull[st], (uint32_t)n * kKv4Rec);
+              bulk_g2s(base + kMsOffRaw + st * kMsStage,
+                       c.cache + (((size_t)blk * c.n_kv + x.g) * bs + (p & (bs - 1))) * kKv4Rec, (uint32_t)n * kKv4Rec, &rfull[st]);
+            } else {
+              mbar_arrive(&rfull[st]);
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
       }
       // the next item
@@ -517,24 +514,24 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         const uint32_t rec = smem_u32(base + kMsOffRaw) + (uint32_t)(w * kMsRaw + (lane < kMsRun ? s0 : s1)) * kMsStage +
                              (uint32_t)(lane & (kMsRun - 1)) * kKv4Rec;
         const bool there = masks[(nk % kMsMasks) * 4 + w] >> lane & 1;
-        uint4 v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = lds_v4(rec + 16 * q);
-        uint2 sc = lds_v2(rec + kKv4Scale);
-        __syncwarp();
-        if (lane < 2) mbar_arrive(&rfree[w * kMsRaw + (lane ? s1 : s0)]);
-        if (!there) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
-          sc = make_uint2(0u, 0u);
-        }
         const int slot = nk % kMsK;
         acquire(&kfree[slot], ((nk / kMsK) & 1) ^ 1);
         if (dead) break;
         tc_fence_after();
         const uint32_t t = tmem + ((uint32_t)(w * 32) << 16) + kMsColK + (uint32_t)slot * 64;
-        ms_half_row(v, sc.x, t);
-        ms_half_row(v + 2, sc.y, t + 32);
+        // in a loop: one warp an SM's quarter runs this code, and unrolled it waits for its own instructions
+        // (64 tokens' look back 79 us, unrolled 83)
+        const uint2 sc = lds_v2(rec + kKv4Scale);
+        uint4 v = lds_v4(rec);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const uint4 next = q < 3 ? lds_v4(rec + 16 * (q + 1)) : v;
+          if (!there) v = make_uint4(0u, 0u, 0u, 0u);
+          ms_quarter_row(v, there ? (q < 2 ? sc.x : sc.y) >> (16 * (q & 1)) : 0u, t + 16 * q);
+          v = next;
+        }
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&rfree[w * kMsRaw + (lane ? s1 : s0)]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
