@@ -23,9 +23,9 @@
 // maximum (of the products q.K, before the scale, so that a large logit's own
 // rounding cannot pass the range) is raised when a logit passes it by more than
 // 7.75 in base 2, and only then is the row of O rescaled. That costs some 2500
-// cycles, for which the other tile's products wait: with 2^11 and 4.75, where a raise
-// of some row came in a third of the blocks (logits of a deviation of 2), 64K x
-// 2048 tokens of 64 heads took 3.67 ms.
+// cycles, for which the other tile's products wait: an earlier state with 2^11 and 4.75, where a raise
+// of some row came in a third of the blocks (logits of a deviation of 2), took 3.67 ms
+// for 64K x 2048 tokens of 64 heads.
 // Sums, maxima, S and O are fp32; a weight's sum is that of the unrounded values.
 //
 // What a row does not see does not reach it. Masked columns of S are replaced. V
@@ -46,12 +46,12 @@
 //   warp 14         Q loads (TMA)
 //   warp 15         gate: passes the operands' arrival on to the P barriers, so that the MMA
 //                   warp waits once a batch
-// Bound: 2048 tokens of 64 heads behind 64K take 3.2 ms, 1.34 PFLOP/s, a block of two
-// tiles 1.9 us. Its products are 1 024 cycles of the tensor pipe (53% busy), but S reads both
-// operands from shared memory, which takes twice that long, and with the operands'
-// own 64 KB shared memory is some 65% busy; the rest is the chain S, softmax, P of a
+// Bound: 2048 tokens of 64 heads behind 64K take 2.93 ms, 1.48 PFLOP/s, a block of two
+// tiles 1.7 us. Its products are 1 024 cycles of the tensor pipe, but S reads both
+// operands from shared memory, which takes its half twice as long, and with the operands'
+// own 64 KB shared memory is some 70% busy; the rest is the chain S, softmax, P of a
 // tile where the other one does not cover it. With few rows (LONE) a block costs
-// what 128 rows cost: 8 x 64K, 32 rows, 287 us, 2.1 TB/s of records.
+// what 128 rows cost: 8 x 64K, 32 rows, 265 us, 2.3 TB/s of records.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
 // and leaves, the others' waits then give up in turn; copies land and MMAs
 // complete before the CTA releases its tensor memory.
@@ -78,11 +78,12 @@ constexpr int kKcMasks = 16;                          // blocks whose masks are 
 constexpr int kKcWarpDeq = 8;
 constexpr float kKcBias = 8.f;                        // log2 of the factor of the weights
 constexpr float kKcHeadroom = 7.75f;                  // log2 growth allowed before a maximum is raised
-// The line of work: units of a block for two tiles, for one in both places (2.3 and
-// 1.9 us), of an item's fixed part, and those a CTA takes at least (more than a
-// block's, so that every CTA between an item's first and last one has a piece of
-// it). 16 requests with up to 700 tokens take 932 us; with 6 for the fixed part
-// 1089. A run of 18 at least: 17 tokens behind 1000 took 29 us instead of 23.
+// The line of work: units of a block for two tiles, for one in both places, of an
+// item's fixed part, and those a CTA takes at least (more than a block's, so that
+// every CTA between an item's first and last one has a piece of it). 16 requests
+// with up to 700 tokens take 755 us; with 4 or 6 for a block of one tile 814 or 767;
+// with 6 for the fixed part 1.17 times as long. A run of 18 at least: 17 tokens behind
+// 1000 took 29 us where a run of 11 took 23.
 constexpr int kKcUnitsTwo = 6, kKcUnitsOne = 5, kKcFixed = 42, kKcMinRun = 9;
 static_assert(kKcMinRun >= kKcUnitsTwo, "a block begins in every run");
 constexpr int kKcTmemCols = 512;                      // S_A, S_B, O_A, O_B
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(KcCfg<LONE>::kThreads, 1) kv4_chunk_kernel(con
               kc_weights(v, f, mm, sum, ts + 16 * q);
             }
           } else {
-            // once (2.93 ms for 2048 tokens behind 64K, in two passes 3.16)
+            // once (2.93 ms for 2048 tokens behind 64K, in two passes in loops 3.25)
             float s[128];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, *reinterpret_cast<float (*)[32]>(s + 32 * q));
@@ -1095,8 +1096,8 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   if (!tensor_map_bf16_sw128(&qmap, c.q, 3, dims, strides, box)) return SPC_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // One Q tile where a request has at most a tile's rows on average. G = 4, the one
-  // way and the other: 8 requests of 32K, 32 tokens (a tile) 171 and 204 us, 33
-  // tokens (two) 306 and 242; one of 32K, 55 and 60, 70 and 67; 1 token 33 and 38
+  // way and the other: 8 requests of 32K, 32 tokens (a tile) 144 and 176 us, 33
+  // tokens (two) 271 and 210; one of 32K, 35 and 40, 48 and 46; 1 token 32 and 37
   return (long long)c.T * a.G <= 128ll * c.B ? kc_launch<true>(qmap, a, st) : kc_launch<false>(qmap, a, st);
 }
 
