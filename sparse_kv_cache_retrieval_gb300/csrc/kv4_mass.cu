@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
   K4Cursor x = k4_at(fa.k4.c, ln, min(t0 + warp, t1 - 1));
   int seg = -1, tiles = 0, ctx = 0;
   uint32_t q[kMfTiles][16];                           // rows 8 i + gid, the lane's 32 dims
-  float inv[kMfTiles][2], nl[kMfTiles][2];            // of columns 8 i + 2 tig, + 1: the queries' scale, -lse
+  float inv[kMfTiles][2], nl[kMfTiles][2];            // of columns 8 i + 2 tig, + 1: the queries' scale (0: adds nothing), -lse
   for (int t = t0 + warp, k = 0; t < t1; t += kMfWarps, ++k) {
     const int b = x.b, g = x.s, p0 = x.i * kK4Tile;
     if (seg != b * c.n_kv + g) {
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
       tiles = (rows + 7) >> 3;
 #pragma unroll
       for (int i = 0; i < kMfTiles; ++i) {
-        const int r = 8 * i + gid;                    // rows that are not there are zeros and add nothing
+        const int r = 8 * i + gid;                    // rows that are not there are as those that add nothing
         const size_t tok = row0 + (r >> a.gshift);
         const int h = (g << a.gshift) + (r & (a.G - 1));
         const float lse = r < rows ? c.lse[tok * c.n_q + h] : -INFINITY;
@@ -817,7 +817,8 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         uint32_t mx = 0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // a row that adds nothing is zeros, whatever it holds
+          // a row that adds nothing is zeros, whatever it holds, and left out of the sums: a
+          // K scale that is NaN makes its products NaN
           w[e] = lse != -INFINITY ? *reinterpret_cast<const uint4*>(c.q + tok * c.q_stride + (size_t)h * kD + 32 * tig + 8 * e)
                                   : make_uint4(0u, 0u, 0u, 0u);
           mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu),
@@ -838,8 +839,8 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          inv[i][e] = __shfl_sync(0xffffffffu, down, (2 * tig + e) * 4);
-          nl[i][e] = -__shfl_sync(0xffffffffu, lse == -INFINITY ? INFINITY : lse, (2 * tig + e) * 4);
+          inv[i][e] = __shfl_sync(0xffffffffu, lse == -INFINITY ? 0.f : down, (2 * tig + e) * 4);
+          nl[i][e] = -__shfl_sync(0xffffffffu, lse, (2 * tig + e) * 4);
         }
       }
     }
@@ -889,8 +890,9 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float y = ex2_approx(fmaf(d[i][e] * inv[i][e & 1], c.scale, nl[i][e & 1]) * kLog2e);
-          // column 8 i + 2 tig + (e & 1) is a token at or behind the position
-          const bool vis = seen || ctx + ((8 * i + 2 * tig + (e & 1)) >> a.gshift) >= p0 + 16 * m + gid + 8 * (e >> 1);
+          // column 8 i + 2 tig + (e & 1) adds something and is a token at or behind the position
+          const bool vis = inv[i][e & 1] != 0.f &&
+                           (seen || ctx + ((8 * i + 2 * tig + (e & 1)) >> a.gshift) >= p0 + 16 * m + gid + 8 * (e >> 1));
           sum[e >> 1] += vis ? y : 0.f;
         }
       }
