@@ -56,6 +56,17 @@ struct EvArgs {
   uint32_t list;           // offset in shared memory of the lists, behind the keys that become batches of rows
 };
 
+// Whether the cluster's other ranks have started: none of them may touch the shared
+// memory of one that has not. Requests that select nothing (not longer than the
+// budget, or all of it forced) meet no other barrier before they write to each other.
+template <int C>
+__device__ __forceinline__ void ev_started() {
+  if constexpr (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+template <int C>
+__device__ __forceinline__ void ev_wait_started() {
+  if constexpr (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // a barrier of the cluster, or of the CTA where it is one
 template <int C>
 __device__ __forceinline__ void ev_sync() {
@@ -70,6 +81,7 @@ __device__ __forceinline__ T* ev_at(T* p, int r) {
 template <int C>
 __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a) {
   extern __shared__ __align__(16) uint8_t ev_raw[];
+  ev_started<C>();
   const Kv4EvictCall& c = a.c;
   EvShared& sm = *reinterpret_cast<EvShared*>(ev_raw);
   uint8_t* rows = ev_raw + sizeof(EvShared);                                  // [2][kEvBatch][144]; before that
@@ -143,6 +155,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv4_evict_kernel(const EvArgs a
   bool bad = (tid < nfrom && (unsigned)from0 >= (unsigned)c.num_blocks) || (tid < nto && (unsigned)to0 >= (unsigned)c.num_blocks);
   for (int i = tid + kEvThreads; i < nfrom; i += kEvThreads) bad |= (unsigned)from[i] >= (unsigned)c.num_blocks;
   for (int i = tid + kEvThreads; i < nto; i += kEvThreads) bad |= (unsigned)to[i] >= (unsigned)c.num_blocks;
+  ev_wait_started<C>();
   if (__syncthreads_or(bad)) {                        // the same in every rank
     const int t = rank * kEvThreads + tid;
     if (kept)
