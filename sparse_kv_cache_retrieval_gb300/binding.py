@@ -351,8 +351,8 @@ def _rows(name, t, T, n, d, stride, dev):
     if len(shape) != 3 or shape[0] < T or shape[1] != n or shape[2] != d:
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [{T}][{n}][{d}]")
     s0, s1, s2 = t.stride()
-    # a dimension of one element may carry any stride
-    if (s2 != 1 and d > 1) or (s1 != d and n > 1):
+    # a dimension of one element may carry any stride, and a tensor of none has none
+    if shape[0] and ((s2 != 1 and d > 1) or (s1 != d and n > 1)):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     if shape[0] <= 1:
         s0 = n * d
