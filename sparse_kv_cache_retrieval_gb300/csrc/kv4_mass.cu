@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int E = (int)(mx >> 7), e2 = min(141 - E, 126);
         const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
-        auto f16 = [&](uint32_t v) { return E == 255 ? 0x7fff7fffu : pack_f16(bf_lo(v) * up, bf_hi(v) * up); };
+        auto f16 = [&](uint32_t v) { return pack_f16(bf_lo(v) * up, bf_hi(v) * up); };   // infinities and NaN stay what they are
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           q[i][4 * e] = f16(w[e].x);

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.paged_oracle as P
 from tests.chunk_cases import chunk, mass
 from tests.paged_cases import DEV, SCALE, Cache, bf16, f64
 from tests.test_gpu_kv4_mass import check, prev_of
@@ -97,6 +98,27 @@ def test_nan_scales_and_queries(n_q, n_kv, n):
     z[n - 1, 0] = -INF                                      # and none of it from a row that adds nothing
     got, _ = mass(c, x, [n], z, prev, 1.0)
     check(c, q, [n], z, prev, 1.0, got)
+
+
+@pytest.mark.parametrize("n_q,n_kv,n", SIZES)
+def test_infinite_queries(n_q, n_kv, n):
+    """A weight is exp(inf), exp(-inf) or, where K is zero, NaN, as the formula has it."""
+    rng = np.random.default_rng(5 * n_q + n)
+    c = Cache(rng, [290], n_kv, 16)
+    q = bf16(rng, n, n_q, 128).to(DEV)
+    _, lse, _ = chunk(c, q, [n])
+    prev, z = prev_of(rng, c), lse.clone()
+    z[n - 1, 0] = -INF
+    rest, _ = mass(c, q, [n], z, prev, 1.0)                 # without the last token's head 0
+    k = np.array([P.values(c.rec[c.table[0, p // 16], 0, p % 16])[0][7] for p in range(290)])
+    for odd in (INF, -INF):
+        x = q.clone()
+        x[n - 1, 0, 7] = odd
+        got, _ = mass(c, x, [n], lse, prev, 1.0)
+        s = torch.from_numpy(k * np.sign(odd)).to(DEV)
+        want = rest.clone()
+        want[0, 0, :290] = torch.where(s == 0, NAN, torch.where(s > 0, INF, rest[0, 0, :290]))
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
 
 
 @pytest.mark.parametrize("n_q,n_kv,n", SIZES)
