@@ -263,8 +263,10 @@ __device__ __forceinline__ long long kc_units(const KcShape& s, int k) {
   };
   return u + each * (below(a + m) - below(a));
 }
+// a row's log-sum-exp; the queries' factor goes to the scale, for q.K itself may be beyond fp32's range (and
+// where the two are, a product of zero stays one)
 __device__ __forceinline__ float kc_lse(const KcArgs& a, float m, float l, float inv) {
-  return l == 0.f ? -INFINITY : m * inv * a.c.scale + (log2f(l) - kKcBias) * 0.6931471805599453f;
+  return l == 0.f ? -INFINITY : m * fminf(inv * a.c.scale, 3.40282347e38f) + (log2f(l) - kKcBias) * 0.6931471805599453f;
 }
 // A piece's partials of a tile: four dims of O of each row, [32][rows][4], then the
 // rows' maxima and so on, [rows][4]: the lanes of a warp have consecutive rows,
