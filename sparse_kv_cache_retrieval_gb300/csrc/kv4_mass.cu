@@ -95,6 +95,7 @@ struct MsArgs {
   int* status;
   uint32_t* counters;
   float* part;
+  float up, scale;         // of K's scales in tensor memory; of the products
   long long wait_limit;
   int starve;              // test builds: no copy is issued, so that every wait runs out
 };
@@ -118,11 +119,14 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
 // 32 K values of 16 bytes of codes and two scales as bf16 into 16 columns of this
 // thread's tensor memory lane. A code as fp16 has at most one bit of mantissa; its bits three
 // places further down are bf16's of the value times 2^-112, which the scale, an
-// e4m3 number times 2^112, takes back: the product is exact.
-__device__ __forceinline__ void ms_quarter_row(const uint4& codes, uint32_t sc, uint32_t t) {
+// e4m3 number times `up`, takes back: the product is exact. `up` is 2^112, or 2^92 where the
+// scale is at most 1 and takes the 2^20 (MsArgs): sums of 128 products of any finite queries,
+// up to 2^147, then stay within fp32's range, and what is lost below 2^-126 is nothing in the logit.
+// With a larger scale a sum beyond fp32's range is a logit beyond it.
+__device__ __forceinline__ void ms_quarter_row(const uint4& codes, uint32_t sc, float up, uint32_t t) {
   uint32_t k[16];
   const uint32_t s2 = e4m3x2_to_f16(sc & 0xffffu);
-  const float f0 = f16_lo(s2) * 5.192296858534828e33f, f1 = f16_hi(s2) * 5.192296858534828e33f;   // 2^112
+  const float f0 = f16_lo(s2) * up, f1 = f16_hi(s2) * up;
   const uint32_t s[2] = {pack_bf16(f0, f0), pack_bf16(f1, f1)};
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
@@ -527,7 +531,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
         for (int q = 0; q < 4; ++q) {
           const uint4 next = q < 3 ? lds_v4(rec + 16 * (q + 1)) : v;
           if (!there) v = make_uint4(0u, 0u, 0u, 0u);
-          ms_quarter_row(v, there ? (q < 2 ? sc.x : sc.y) >> (16 * (q & 1)) : 0u, t + 16 * q);
+          ms_quarter_row(v, there ? (q < 2 ? sc.x : sc.y) >> (16 * (q & 1)) : 0u, a.up, t + 16 * q);
           v = next;
         }
         __syncwarp();
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kMsRegSum));
     const int grp = warp >> 2, wq = warp & 3, lt = 7 - a.gshift;
     const uint32_t ts = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)grp * 128;
-    const float2 sc = make_float2(c.scale, c.scale), l2e = make_float2(kLog2e, kLog2e);
+    const float2 sc = make_float2(a.scale, a.scale), l2e = make_float2(kLog2e, kLog2e);
     int ns = 0, nq = 0, nk = 0, nc[2] = {0, 0};
     for (int it = 0;; ++it) {
       const int is = it % kMsItems;
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
                                  (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & ~odd[q];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float t = ex2_approx(fmaf(s[e], c.scale, nl[32 * q + e]) * kLog2e);
+              const float t = ex2_approx(fmaf(s[e], a.scale, nl[32 * q + e]) * kLog2e);
               sum[e & 1] += vis >> e & 1 ? t : 0.f;
             }
           }
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
   K4Cursor x = k4_at(fa.k4.c, ln, min(t0 + warp, t1 - 1));
   int seg = -1, tiles = 0, ctx = 0;
   uint32_t q[kMfTiles][16];                           // rows 8 i + gid, the lane's 32 dims
-  float inv[kMfTiles][2], nl[kMfTiles][2];            // of columns 8 i + 2 tig, + 1: the queries' scale (0: adds nothing), -lse
+  float f[kMfTiles][2], nl[kMfTiles][2];              // of columns 8 i + 2 tig, + 1: a logit's factor (0: adds nothing), -lse
   for (int t = t0 + warp, k = 0; t < t1; t += kMfWarps, ++k) {
     const int b = x.b, g = x.s, p0 = x.i * kK4Tile;
     if (seg != b * c.n_kv + g) {
@@ -828,7 +832,10 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int E = (int)(mx >> 7), e2 = min(141 - E, 126);
-        const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
+        const float up = __int_as_float((e2 + 127) << 23);
+        // the scale over the power of two (q.K itself may be beyond fp32's range), kept from zero and from infinity: a
+        // row that adds nothing is told by it, and a product of zero stays one
+        const float factor = fminf(fmaxf(__int_as_float((127 - e2) << 23) * c.scale, 1.17549435e-38f), 3.40282347e38f);
         auto f16 = [&](uint32_t v) { return pack_f16(bf_lo(v) * up, bf_hi(v) * up); };   // infinities and NaN stay what they are
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -839,7 +846,7 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          inv[i][e] = __shfl_sync(0xffffffffu, lse == -INFINITY ? 0.f : down, (2 * tig + e) * 4);
+          f[i][e] = __shfl_sync(0xffffffffu, lse == -INFINITY ? 0.f : factor, (2 * tig + e) * 4);
           nl[i][e] = -__shfl_sync(0xffffffffu, lse, (2 * tig + e) * 4);
         }
       }
@@ -878,10 +885,10 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
         e2m1x8_to_f16(w0[e], k0);
         e2m1x8_to_f16(w1[e], k1);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const uint32_t av[4] = {hmul2(k0[2 * f], s0), hmul2(k1[2 * f], s1), hmul2(k0[2 * f + 1], s0), hmul2(k1[2 * f + 1], s1)};
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t av[4] = {hmul2(k0[2 * h], s0), hmul2(k1[2 * h], s1), hmul2(k0[2 * h + 1], s0), hmul2(k1[2 * h + 1], s1)};
 #pragma unroll
-          for (int i = 0; i < NT; ++i) mma_f16(d[i], av, q[i][4 * e + 2 * f], q[i][4 * e + 2 * f + 1]);
+          for (int i = 0; i < NT; ++i) mma_f16(d[i], av, q[i][4 * e + 2 * h], q[i][4 * e + 2 * h + 1]);
         }
       }
       float sum[2] = {0.f, 0.f};
@@ -889,9 +896,9 @@ __global__ void __launch_bounds__(32 * (kMfWarps + 1), 1) kv4_mass_few_kernel(co
       for (int i = 0; i < NT; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = ex2_approx(fmaf(d[i][e] * inv[i][e & 1], c.scale, nl[i][e & 1]) * kLog2e);
+          const float y = ex2_approx(fmaf(d[i][e], f[i][e & 1], nl[i][e & 1]) * kLog2e);
           // column 8 i + 2 tig + (e & 1) adds something and is a token at or behind the position
-          const bool vis = inv[i][e & 1] != 0.f &&
+          const bool vis = f[i][e & 1] != 0.f &&
                            (seen || ctx + ((8 * i + 2 * tig + (e & 1)) >> a.gshift) >= p0 + 16 * m + gid + 8 * (e >> 1));
           sum[e >> 1] += vis ? y : 0.f;
         }
@@ -931,6 +938,8 @@ int kv4_mass_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   a.status = reinterpret_cast<int*>(w);
   a.counters = reinterpret_cast<uint32_t*>(w + kMsOffCount);
   a.part = reinterpret_cast<float*>(w + kMsOffPart);
+  a.up = c.scale <= 1.f ? 4.951760157141521e27f : 5.192296858534828e33f;   // 2^92, 2^112
+  a.scale = c.scale <= 1.f ? c.scale * 1048576.f : c.scale;
   a.wait_limit = kKcWait;
 #ifdef SPC_TEST_HOOKS
   a.starve = paged_starve(&a.wait_limit) ? 1 : 0;
