@@ -50,7 +50,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // and nothing overflows.
 __device__ __forceinline__ float k4_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 1.26765060e30f); }
 // x / d for 0 <= x <= 2^21 (a request's tiles, or a segment's times the CTAs), d
-// >= 1. The approximate quotient is off by less than one there; an integer
+// >= 1, or for x < 2^24 with a quotient of at most 2^10 (the tiles of a request of 1024 KV
+// heads). The approximate quotient is off by less than one there; an integer
 // division costs some 150 cycles each in a plan that every CTA waits for.
 __device__ __forceinline__ int k4_div(int x, int d) {
   const int q = (int)__fdividef((float)x, (float)d), r = x - q * d;

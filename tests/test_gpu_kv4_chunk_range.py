@@ -14,7 +14,7 @@ CASES = [(4, 1, [500], [20]), (8, 2, [700, 300], [150, 60]), (4, 1, [20000], [3]
 
 
 @pytest.mark.parametrize("n_q,n_kv,lens,new", CASES)
-@pytest.mark.parametrize("power", [125, 110, -110])
+@pytest.mark.parametrize("power", [125, 110, -110, -128])
 def test_products_of_any_size(n_q, n_kv, lens, new, power):
     rng = np.random.default_rng(sum(lens) + power)
     c = Cache(rng, lens, n_kv, 16)

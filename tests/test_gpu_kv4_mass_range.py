@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("n_q,n_kv,n", SIZES + [(8, 2, 200)])
-@pytest.mark.parametrize("power", [125, 110, -110])
+@pytest.mark.parametrize("power", [125, 110, -110, -128])
 def test_products_of_any_size(n_q, n_kv, n, power):
     rng = np.random.default_rng(n_q + n + power + 200)
     c = Cache(rng, [700], n_kv, 16)
