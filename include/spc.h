@@ -613,7 +613,8 @@ int spc_prompt_attn(const void* q, const void* k, const void* v, const int32_t* 
  * Precision: products, maxima and sums are fp32. Queries are taken in fp16 after a
  * power of two per row (a value loses bits only below 2^-28 of the row's largest);
  * softmax weights are rounded to fp16 (2^-11) down to 2^-22 of the largest and are
- * off by at most 2^-33 of it below; the output is rounded to bf16 once. lse is fp32.
+ * off by at most 2^-33 of it below; the output is rounded to bf16 once. lse is fp32:
+ * infinite where the logits pass its range (q . K alone may).
  * q          bf16, row t at q + t * q_stride elements: [n_q][d], 16-byte aligned;
  *            the stride is a multiple of 8 elements, at least n_q * d and at most 2^32.
  * cu_seqlens int32 [B + 1], ascending, within [0, T]; equal neighbours are a
@@ -647,7 +648,11 @@ int spc_kv4_chunk_attn(const void* q, const void* cache, const int32_t* block_ta
  * position len[b] - 1. keep = 1 adds up, less than 1 lets older steps fade, and
  * with 0 mass_prev is not read.
  * Precision: products, exponentials and sums are fp32, in an order that is the
- * same in every call of the same shapes and lengths.
+ * same in every call of the same shapes and lengths. A request with at most 32 rows
+ * of a KV head (new tokens * G) has its queries in fp16 after a power of two per row, as
+ * spc_kv4_chunk_attn; any other one as they are. The logits scale * q . K and lse have to be
+ * within fp32's range (q . K alone may pass it), and what fp32 rounds off them, some 2^-24
+ * of |lse| and of scale * sum |q K|, is the relative error of a weight.
  * lse        fp32 [T][n_q].
  * mass_prev, mass_next fp32 [B][n_kv][cap], cap >= max_blocks * block_size; mass_next may be
  *            mass_prev; mass_prev may be NULL where keep = 0.
