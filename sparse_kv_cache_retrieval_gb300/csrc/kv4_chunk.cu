@@ -49,7 +49,7 @@
 // Bound: 2048 tokens of 64 heads behind 64K take 2.93 ms, 1.48 PFLOP/s, a block of two
 // tiles 1.7 us. Its products are 1 024 cycles of the tensor pipe, but S reads both
 // operands from shared memory, which takes its half twice as long, and with the operands'
-// own 64 KB shared memory is some 70% busy; the rest is the chain S, softmax, P of a
+// own 64 KB shared memory is some 70% busy (counted, 2340 of 3250 cycles); the rest is the chain S, softmax, P of a
 // tile where the other one does not cover it. With few rows (LONE) a block costs
 // what 128 rows cost: 8 x 64K, 32 rows, 265 us, 2.3 TB/s of records.
 // Every wait is bounded: a role whose wait gives up records SPC_ERR_TIMEOUT
@@ -1099,7 +1099,9 @@ int kv4_chunk_launch(const Kv4ChunkCall& c, void* workspace, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // One Q tile where a request has at most a tile's rows on average. G = 4, the one
   // way and the other: 8 requests of 32K, 32 tokens (a tile) 144 and 176 us, 33
-  // tokens (two) 271 and 210; one of 32K, 35 and 40, 48 and 46; 1 token 32 and 37
+  // tokens (two) 271 and 210; one of 32K, 35 and 40, 48 and 46; 1 token 32 and 37. One
+  // rule for the whole call, measured with requests that are alike: in a batch of many single
+  // tokens and one long chunk either kind may take the kernel that is slower for it
   return (long long)c.T * a.G <= 128ll * c.B ? kc_launch<true>(qmap, a, st) : kc_launch<false>(qmap, a, st);
 }
 

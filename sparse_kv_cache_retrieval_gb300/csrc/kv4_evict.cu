@@ -17,12 +17,13 @@
 //     that a batch overwrites no source of a later one.
 // Ranks: one for each 16384 positions, and while there are few heads more of them, until
 // the kept rows are one batch each (both sides at kv4_evict_launch).
-// Bound: 8 requests of 65536 positions cut to 4096, 8 heads, take 45 us: 20 of
+// Bound: 8 requests of 65536 positions cut to 4096, 8 heads, take 45 us: 15 of
 // them move 38 MB each way (65 MB of DRAM reads, for a record of 144 bytes begins
-// at any multiple of 16; 5.4 TB/s with the writes), the others are the select's
-// chain, which every cluster goes through at the same time: sums 7 us, three levels
-// 10 (a barrier of the cluster, the other ranks' counts, two scans), the list 5. Small
-// calls are that chain alone: 1088 positions cut to 1024 take 10.7 us.
+// at any multiple of 16: 4.3 TB/s), the others are the select's chain, which every
+// cluster goes through at the same time: sums and tables 7 us, three levels 11 (a
+// barrier of the cluster, the other ranks' counts, two scans), the ranks' counts 3, the list
+// 6, the records' places 3. Small calls are that chain alone: 1088 positions cut to
+// 1024 take 10.8 us. (Times from a clock trace of the slowest ranks.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

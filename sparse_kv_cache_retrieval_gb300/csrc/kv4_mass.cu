@@ -31,7 +31,7 @@
 //   warp 19         gate: waits for all that a product needs, so that the MMA warp waits once
 // Every wait is bounded; see kv4_chunk.cu.
 // Bound: exponentials and products, 58% of their pipes each, and 62% of the issue
-// slots (8192 tokens): 16384 tokens of 32 heads take 794-817 us, 1.35-1.38 PFLOP/s.
+// slots (8192 tokens): 16384 tokens of 32 heads take 783-807 us, 1.36-1.40 PFLOP/s.
 // Where an item has few row tiles (64 tokens look back over five prompts: two for
 // 256 positions, 79 us), the copies and conversions of K and an item's ends.
 #include <cuda.h>
@@ -732,10 +732,11 @@ __global__ void __launch_bounds__(kMsThreads, 1) kv4_mass_kernel(const __grid_co
 // and gid + 8 to fp16, 16 bytes of codes each; the contraction's order is free,
 // so these are the fragments of the eight steps as they come, and the queries, in
 // registers, are in the same order: bf16 to fp16 times a power of two a row, as in
-// kv4_chunk.cu. Nothing is exchanged but a position's sum over four lanes.
+// kv4_chunk.cu (11 bits down to 2^-28 of the row's largest, so that a bf16 value is
+// exact there). Nothing is exchanged but a position's sum over four lanes.
 // Bound: HBM. 8 x 65536 positions, 64 heads on 8: 604 MB of records (K's 72 bytes of
-// 144 are in every line that is read) and 34 MB of sums in 124 us, 5.1 TB/s; 32768:
-// 67 us alone, 4.8 TB/s, the ALU pipe 39% busy with conversions.
+// 144 are in every line that is read) and 34 MB of sums in 126 us, 5.1 TB/s; 32768:
+// 69 us alone, 4.7 TB/s, the ALU pipe 41% busy with conversions.
 constexpr int kMfWarps = 15, kMfStages = 3, kMfTiles = kMfRows / 8;
 constexpr uint32_t kMfOffBar = kMfWarps * kMfStages * kK4StageBytes;
 constexpr uint32_t kMfOffMask = kMfOffBar + 2 * kMfWarps * kMfStages * 8;
